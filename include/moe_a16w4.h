@@ -281,6 +281,132 @@ moe_status mxfp4_to_int4g32_requant(const uint8_t* w, const uint8_t* scale_e8m0,
                                     int K, int expert_lo, int expert_hi, uint8_t* w_int4,
                                     uint16_t* scale_bf16, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Dense operators around the routed experts: the norm that makes the layer's
+ * input, the projection (router logits; per-request low-rank adapters) and
+ * the shared expert, a gated feed-forward block with its backward pass.
+ *
+ * Common to these calls: matrices are row-major with their last dimension
+ * contiguous; a `stride` argument is the distance of two rows in elements, at
+ * least the row's length. T == 0 is a no-op (the backward call then writes
+ * zero weight gradients). Sizes and strides of at most 2^18 columns (2^20 for
+ * strides) and 2^24 tokens, else MOE_ERR_UNSUPPORTED. Sums are fp32. Calls
+ * that need a workspace take one of the size that their query returns (-1 for
+ * invalid sizes), 256-byte aligned; it is scratch for that call alone. Unless
+ * stated otherwise, outputs must not overlap inputs or each other.
+ * ------------------------------------------------------------------------ */
+typedef enum { MOE_DT_BF16 = 0, MOE_DT_F32 = 1 } moe_dtype;
+
+/* Residual addition and RMS norm of token rows:
+ *   s = x + residual (s = x when residual is NULL)
+ *   v = s / sqrt(mean(s^2) + eps) * (weight_offset + weight)
+ *   residual_out = s;  y = bf16(v);  (q, q_scale) = MXFP8(v).
+ * MXFP8 holds each 32 consecutive elements of a row as e4m3 codes q and one
+ * e8m0 byte: the smallest power of two s with max|v| / s <= 448 (at least
+ * 2^-127), q = e4m3(v / s), rounded to nearest even. NaN and infinite
+ * elements become NaN codes and do not take part in the maximum.
+ *   x             bf16 [T, H]; residual [T, H] of residual_type, or NULL.
+ *   weight        [H] of weight_type.
+ *   residual_out  out [T, H] of residual_type, or NULL.
+ *   y             out bf16 [T, H], or NULL.
+ *   q, q_scale    out uint8 [T, H] and [T, H/32], both or neither; H % 32 == 0.
+ * At least one output is required. 1 <= H <= 65536 (any H without q). Pointers
+ * need their element's alignment only (rows that are 16-byte aligned are
+ * faster). An output may be an input's own buffer with the same row stride and
+ * element size (y = x, residual_out = residual). eps must be >= 0 and finite. */
+moe_status moe_rms_norm(const uint16_t* x, int64_t x_stride, const void* residual,
+                        int64_t residual_stride, moe_dtype residual_type, const void* weight,
+                        moe_dtype weight_type, float eps, float weight_offset, int T, int H,
+                        void* residual_out, int64_t residual_out_stride, uint16_t* y,
+                        int64_t y_stride, uint8_t* q, int64_t q_stride, uint8_t* q_scale,
+                        int64_t q_scale_stride, void* stream);
+
+/* Low-rank adapters of many requests beside one projection [N, K]: token t
+ * adds scale[i] * B[i] (A[i] x[t]) for i = index[t]; an index outside [0, n)
+ * adds nothing.
+ *   a       bf16 [n, rank, K];  b bf16 [n, N, rank].
+ *   index   int32 [T].
+ *   ranks   int32 [n] or NULL: adapter i uses the first ranks[i] rows of A[i]
+ *           and columns of B[i] (what lies beyond is not read as numbers;
+ *           values outside [0, rank] are clamped).
+ *   scale   fp32 [n] or NULL (1).
+ *   n >= 1, rank a multiple of 8 in [8, 256]. a and b 16-byte aligned. */
+typedef struct {
+    const uint16_t* a;
+    const uint16_t* b;
+    const int32_t* index;
+    const int32_t* ranks;
+    const float* scale;
+    int n;
+    int rank;
+} moe_lora;
+
+/* Projection out[t] = W x[t] (+ the token's adapter): the router's logits
+ * (fp32 output, no adapter) or a dense projection whose requests carry
+ * adapters. A x and the sum W x + B (A x) stay in fp32 (A x enters the second
+ * product as a pair of bf16 numbers).
+ *   x  bf16 [T, K];  w bf16 [N, K];  lora NULL or as above.
+ *   out  [T, N] of out_type.
+ * K and N multiples of 8, >= 8; strides multiples of 8; pointers 16-byte
+ * aligned. */
+int64_t moe_lora_linear_workspace_size(int T, int K, int N, int rank);
+moe_status moe_lora_linear(const uint16_t* x, int64_t x_stride, const uint16_t* w,
+                           const moe_lora* lora, int T, int K, int N, void* out, int64_t out_stride,
+                           moe_dtype out_type, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/* Gated feed-forward block (the shared expert beside the routed ones):
+ *   [gate; up] = W13 x (+ adapter);  h = silu(gate) * up, rounded to bf16;
+ *   out = W2 h (+ adapter) (+ addend).
+ *   x        bf16 [T, H];  w13 bf16 [2I, H] (gate rows [0, I), up rows
+ *            [I, 2I));  w2 bf16 [H, I].
+ *   addend   bf16 [T, H] or NULL, added before the one rounding of out (the
+ *            routed experts' output); may be out itself.
+ *   lora13   adapters of w13 (K = H, N = 2I) or NULL; lora2 of w2 (K = I,
+ *            N = H; its input is h) or NULL.
+ *   gate_up  out bf16 [T, 2I] or NULL: gate and up, for moe_ffn_backward.
+ * H and I multiples of 8, >= 8; strides multiples of 8; pointers 16-byte
+ * aligned. Only MOE_ACT_SWIGLU is implemented. The workspace query takes the
+ * two stacks' ranks (0: none). */
+int64_t moe_ffn_workspace_size(int T, int H, int I, int rank13, int rank2);
+moe_status moe_ffn_forward(const uint16_t* x, int64_t x_stride, const uint16_t* w13,
+                           const uint16_t* w2, moe_act act, const uint16_t* addend,
+                           int64_t addend_stride, const moe_lora* lora13, const moe_lora* lora2,
+                           int T, int H, int I, uint16_t* out, int64_t out_stride,
+                           uint16_t* gate_up, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/* The same block with MXFP8 activations and weights (moe_rms_norm's q and
+ * q_scale; weights in the same format along K), on the scaled matrix
+ * instructions; h goes from its fp32 value to MXFP8.
+ *   x uint8 [T, H] e4m3, x_scale uint8 [T, H/32] e8m0; w13 [2I, H], w13_scale
+ *   [2I, H/32]; w2 [H, I], w2_scale [H, I/32]; addend, out as above.
+ * H and I multiples of 32. Codes and scales pointers 16-byte aligned. */
+int64_t moe_ffn_mxfp8_workspace_size(int T, int H, int I);
+moe_status moe_ffn_forward_mxfp8(const uint8_t* x, const uint8_t* x_scale, const uint8_t* w13,
+                                 const uint8_t* w13_scale, const uint8_t* w2,
+                                 const uint8_t* w2_scale, moe_act act, const uint16_t* addend,
+                                 int64_t addend_stride, int T, int H, int I, uint16_t* out,
+                                 int64_t out_stride, void* workspace, size_t workspace_bytes,
+                                 void* stream);
+
+/* Backward of moe_ffn_forward (without adapters) from its saved gate_up:
+ *   s = 1 / (1 + exp(-gate));  dh = W2^T dout;
+ *   dgate = dh up s (1 + gate (1 - s));  dup = dh gate s;
+ *   dx = W13^T [dgate; dup];  dw13 = [dgate; dup]^T x;  dw2 = dout^T h.
+ * h, dgate and dup are rounded to bf16 (they are operands of the second
+ * products); the gradient of addend is dout itself.
+ *   dout, x  bf16 [T, H];  gate_up bf16 [T, 2I];  w13, w2 as above.
+ *   dx       out bf16 [T, H], dw13 bf16 [2I, H], dw2 bf16 [H, I]; each may be
+ *            NULL (not computed), at least one is required. dw13 and dw2 are
+ *            overwritten, and no sum depends on the order of atomics. */
+int64_t moe_ffn_backward_workspace_size(int T, int H, int I);
+moe_status moe_ffn_backward(const uint16_t* dout, int64_t dout_stride, const uint16_t* x,
+                            int64_t x_stride, const uint16_t* gate_up, const uint16_t* w13,
+                            const uint16_t* w2, moe_act act, int T, int H, int I, uint16_t* dx,
+                            int64_t dx_stride, uint16_t* dw13, uint16_t* dw2, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -12,8 +12,12 @@ Functions mirror the C ABI names:
   moe_align_sort, moe_route_align, moe_a16w4_workspace_size, moe_a16w4_forward,
   moe_a16w4_forward_stages, moe_a16w4_forward_ex, moe_a16w4_forward_monolithic,
   moe_a16w4_forward_noalloc,
-  mxfp4_to_int4g32_requant, moe_last_error
-plus two compositions: moe_a16w4_layer (route -> sort -> forward, the
+  mxfp4_to_int4g32_requant, moe_last_error,
+  moe_rms_norm, moe_lora_linear, moe_ffn_forward, moe_ffn_forward_mxfp8,
+  moe_ffn_backward (the dense operators around the routed experts)
+plus compositions: moe_ffn (the shared expert as a differentiable function),
+moe_a16w4_block (norm -> router -> routed experts + shared expert),
+moe_a16w4_layer (route -> sort -> forward, the
 in-kernel routing path of apply_monolithic on the vLLM mxfp4 API page) and
 requantize_mxfp4_experts (the chunked MXFP4 -> int4-g32 load-time
 conversion, eight experts per call).
@@ -22,6 +26,7 @@ import contextlib
 import ctypes
 import os
 import warnings
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -31,6 +36,7 @@ LIB_PATH = os.path.join(HERE, "libmoe_a16w4.so")
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_HIP = 0, 1, 2, 3
 MOE_W_MXFP4, MOE_W_INT4G32 = 0, 1
 MOE_ACT_SWIGLU = 0
+MOE_DT_BF16, MOE_DT_F32 = 0, 1
 MOE_STAGE_GATE_UP, MOE_STAGE_DOWN, MOE_STAGE_COMBINE, MOE_STAGE_ALL = 1, 2, 4, 7
 
 # Every symbol include/moe_a16w4.h declares.
@@ -40,9 +46,18 @@ EXPORTS = (
     "moe_a16w4_forward_stages", "moe_a16w4_forward_ex", "moe_a16w4_forward_monolithic",
     "moe_a16w4_forward_noalloc",
     "mxfp4_to_int4g32_requant",
+    "moe_rms_norm", "moe_lora_linear_workspace_size", "moe_lora_linear", "moe_ffn_workspace_size",
+    "moe_ffn_forward", "moe_ffn_mxfp8_workspace_size", "moe_ffn_forward_mxfp8",
+    "moe_ffn_backward_workspace_size", "moe_ffn_backward",
 )
 # Scratch of the allocation-free forward (MOE_NOALLOC_SCRATCH_BYTES).
 NOALLOC_SCRATCH_BYTES = 64 << 20
+
+
+class _CLora(ctypes.Structure):
+    _fields_ = [("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("index", ctypes.c_void_p),
+                ("ranks", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("n", ctypes.c_int),
+                ("rank", ctypes.c_int)]
 
 
 class MoeError(RuntimeError):
@@ -87,6 +102,25 @@ def _load():
     L.moe_a16w4_forward_noalloc.argtypes = [p, p, p, p, p, i, i, p, p, p, p, p, i, i, i, i, i, i, p, p]
     L.mxfp4_to_int4g32_requant.restype = i
     L.mxfp4_to_int4g32_requant.argtypes = [p, p, i, i, i, i, i, p, p, p]
+    f, lo = ctypes.c_float, ctypes.POINTER(_CLora)
+    L.moe_rms_norm.restype = i
+    L.moe_rms_norm.argtypes = [p, i64, p, i64, i, p, i, f, f, i, i, p, i64, p, i64, p, i64, p, i64, p]
+    L.moe_lora_linear_workspace_size.restype = i64
+    L.moe_lora_linear_workspace_size.argtypes = [i, i, i, i]
+    L.moe_lora_linear.restype = i
+    L.moe_lora_linear.argtypes = [p, i64, p, lo, i, i, i, p, i64, i, p, sz, p]
+    L.moe_ffn_workspace_size.restype = i64
+    L.moe_ffn_workspace_size.argtypes = [i, i, i, i, i]
+    L.moe_ffn_forward.restype = i
+    L.moe_ffn_forward.argtypes = [p, i64, p, p, i, p, i64, lo, lo, i, i, i, p, i64, p, p, sz, p]
+    L.moe_ffn_mxfp8_workspace_size.restype = i64
+    L.moe_ffn_mxfp8_workspace_size.argtypes = [i, i, i]
+    L.moe_ffn_forward_mxfp8.restype = i
+    L.moe_ffn_forward_mxfp8.argtypes = [p, p, p, p, p, p, i, p, i64, i, i, i, p, i64, p, sz, p]
+    L.moe_ffn_backward_workspace_size.restype = i64
+    L.moe_ffn_backward_workspace_size.argtypes = [i, i, i]
+    L.moe_ffn_backward.restype = i
+    L.moe_ffn_backward.argtypes = [p, i64, p, i64, p, p, p, i, i, i, i, p, i64, p, p, p, sz, p]
     return L
 
 
@@ -414,3 +448,343 @@ def requantize_mxfp4_experts(w, scale_e8m0, chunk=8, stream=None):
     for lo in range(0, E, chunk):
         mxfp4_to_int4g32_requant(w, scale_e8m0, lo, min(lo + chunk, E), codes, scales, stream=stream)
     return codes, scales
+
+
+# ---------------------------------------------------------------------------
+# Dense operators around the routed experts.
+
+class LoraAdapters(NamedTuple):
+    """A stack of low-rank adapters beside one projection [N, K]: token t adds
+    scale[i] * B[i] (A[i] x[t]) for i = index[t] (outside [0, n): nothing).
+    a bf16 [n, rank, K]; b bf16 [n, N, rank]; index int32 [T]; ranks int32 [n]
+    (adapter i uses its first ranks[i]) and scale fp32 [n], each optional."""
+    a: torch.Tensor
+    b: torch.Tensor
+    index: torch.Tensor
+    ranks: Optional[torch.Tensor] = None
+    scale: Optional[torch.Tensor] = None
+
+
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+_SCALES = (torch.uint8, torch.float8_e8m0fnu)
+
+
+def _fail_tensor(t, name, dtype, shape, device):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must live on the GPU")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+        raise ValueError(f"{name} must have dtype {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _full(t, name, dtype, shape, device):
+    """A contiguous tensor of this type, shape and device."""
+    if (not isinstance(t, torch.Tensor) or t.device != device or not t.is_cuda or t.shape != shape
+            or not (t.dtype in dtype if isinstance(dtype, tuple) else t.dtype == dtype)
+            or not t.is_contiguous()):
+        _fail_tensor(t, name, dtype, shape, device)
+    return t.data_ptr()
+
+
+def _rows(t, name, dtype, shape, device):
+    """A matrix whose rows are contiguous -> (pointer, row stride)."""
+    if (not isinstance(t, torch.Tensor) or t.device != device or not t.is_cuda or t.shape != shape
+            or not (t.dtype in dtype if isinstance(dtype, tuple) else t.dtype == dtype)):
+        _fail_tensor(t, name, dtype, shape, device)
+    T, cols = shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows, got strides {t.stride()}")
+    return t.data_ptr(), t.stride(0) if T > 1 else cols
+
+
+def _matrix(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must live on the GPU")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D, got shape {tuple(t.shape)}")
+    return t.shape
+
+
+def _run(device, stream, call):
+    """call(stream pointer) with `device` current, on `stream` or that
+    device's current stream."""
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    if torch.cuda.current_device() != device.index:
+        with torch.cuda.device(device):
+            return _run(device, stream, call)
+    _check(call((torch.cuda.current_stream() if stream is None else stream).cuda_stream))
+
+
+def _empty(shape, dtype, device, stream):
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _workspace(given, need, device, stream):
+    if need < 0:
+        raise MoeError(MOE_ERR_INVALID_ARG, "invalid sizes")
+    if given is None:
+        return _empty(max(need, 256), torch.uint8, device, stream) if need else None
+    if given.dtype != torch.uint8 or not given.is_contiguous() or given.device != device:
+        raise ValueError("workspace must be a contiguous uint8 tensor on the inputs' device")
+    return given
+
+
+def _lora(lora, name, T, K, N, device):
+    """-> (ctypes struct or None, rank)."""
+    if lora is None:
+        return None, 0
+    lora = LoraAdapters(*lora)
+    a = lora.a
+    if not isinstance(a, torch.Tensor) or a.dim() != 3:
+        raise ValueError(f"{name}.a must be a tensor [n, rank, {K}]")
+    n, rank, _ = a.shape
+    s = _CLora(_full(a, name + ".a", torch.bfloat16, (n, rank, K), device),
+               _full(lora.b, name + ".b", torch.bfloat16, (n, N, rank), device),
+               _full(lora.index, name + ".index", torch.int32, (T,), device),
+               None if lora.ranks is None else _full(lora.ranks, name + ".ranks", torch.int32, (n,), device),
+               None if lora.scale is None else _full(lora.scale, name + ".scale", torch.float32, (n,), device),
+               n, rank)
+    return s, rank
+
+
+def moe_rms_norm(x, weight, residual=None, eps=1e-6, weight_offset=0.0, mxfp8=False, y=None,
+                 residual_out=None, q=None, q_scale=None, stream=None):
+    """Residual addition and RMS norm of x bf16 [T, H]:
+    s = x + residual, v = s / sqrt(mean(s^2) + eps) * (weight_offset + weight).
+    residual bf16 or fp32 [T, H] (None: s = x, and no residual_out unless a
+    buffer is given); weight bf16 or fp32 [H]. mxfp8: also the MXFP8 output,
+    for moe_ffn_forward_mxfp8. -> (y bf16, residual_out of residual's type or
+    None, q float8_e4m3fn or None, q_scale float8_e8m0fnu [T, H/32] or None).
+    Buffers may be given; y=x and residual_out=residual work in place."""
+    T, H = _matrix(x, "x")
+    device = x.device
+    px, ldx = _rows(x, "x", torch.bfloat16, (T, H), device)
+    pr, ldr, rdt = None, H, None
+    if residual is not None:
+        pr, ldr = _rows(residual, "residual", (torch.bfloat16, torch.float32), (T, H), device)
+        rdt = residual.dtype
+    pw = _full(weight, "weight", (torch.bfloat16, torch.float32), (H,), device)
+    if y is None:
+        y = _empty((T, H), torch.bfloat16, device, stream)
+    if residual_out is None and residual is not None:
+        residual_out = _empty((T, H), rdt, device, stream)
+    py, ldy = _rows(y, "y", torch.bfloat16, (T, H), device)
+    po, ldo = None, H
+    if residual_out is not None:
+        po, ldo = _rows(residual_out, "residual_out", rdt or (torch.bfloat16, torch.float32), (T, H), device)
+        rdt = residual_out.dtype
+    pq, ldq, ps, lds = None, H, None, max(H // 32, 1)
+    if mxfp8 or q is not None or q_scale is not None:
+        if H % 32:
+            raise ValueError(f"H={H} must be a multiple of 32 for the MXFP8 output")
+        if q is None:
+            q = _empty((T, H), torch.float8_e4m3fn, device, stream)
+        if q_scale is None:
+            q_scale = _empty((T, H // 32), torch.float8_e8m0fnu, device, stream)
+        pq, ldq = _rows(q, "q", _CODES, (T, H), device)
+        ps, lds = _rows(q_scale, "q_scale", _SCALES, (T, H // 32), device)
+    _run(device, stream, lambda s: lib.moe_rms_norm(
+        px, ldx, pr, ldr, MOE_DT_F32 if rdt == torch.float32 else MOE_DT_BF16, pw,
+        MOE_DT_F32 if weight.dtype == torch.float32 else MOE_DT_BF16, eps, weight_offset, T, H, po, ldo,
+        py, ldy, pq, ldq, ps, lds, s))
+    return y, residual_out, q, q_scale
+
+
+def moe_lora_linear_workspace_size(T, K, N, rank=0) -> int:
+    return int(lib.moe_lora_linear_workspace_size(T, K, N, rank))
+
+
+def moe_lora_linear(x, w, lora=None, out_dtype=torch.bfloat16, out=None, workspace=None, stream=None):
+    """x bf16 [T, K] times w bf16 [N, K] transposed, plus each token's low-rank
+    adapter (LoraAdapters, or a tuple of its fields) -> out [T, N] in bf16 or
+    fp32 (without adapters and in fp32: a router's logits)."""
+    T, K = _matrix(x, "x")
+    N = _matrix(w, "w")[0]
+    device = x.device
+    px, ldx = _rows(x, "x", torch.bfloat16, (T, K), device)
+    pw = _full(w, "w", torch.bfloat16, (N, K), device)
+    cl, rank = _lora(lora, "lora", T, K, N, device)
+    if out is None:
+        if out_dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError(f"out_dtype must be bfloat16 or float32, got {out_dtype}")
+        out = _empty((T, N), out_dtype, device, stream)
+    po, ldo = _rows(out, "out", (torch.bfloat16, torch.float32), (T, N), device)
+    ws = _workspace(workspace, lib.moe_lora_linear_workspace_size(T, K, N, rank), device, stream)
+    _run(device, stream, lambda s: lib.moe_lora_linear(
+        px, ldx, pw, cl, T, K, N, po, ldo, MOE_DT_F32 if out.dtype == torch.float32 else MOE_DT_BF16,
+        ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0, s))
+    return out
+
+
+def moe_ffn_workspace_size(T, H, I, rank13=0, rank2=0) -> int:
+    return int(lib.moe_ffn_workspace_size(T, H, I, rank13, rank2))
+
+
+def _ffn_sizes(x, w13, w2):
+    T, H = _matrix(x, "x")
+    I2 = _matrix(w13, "w13")[0]
+    if I2 % 2:
+        raise ValueError(f"w13 must have 2I rows (gate rows, then up rows), got {I2}")
+    return T, H, I2 // 2
+
+
+def moe_ffn_forward(x, w13, w2, addend=None, lora13=None, lora2=None, save_gate_up=False, gate_up=None,
+                    act=MOE_ACT_SWIGLU, out=None, workspace=None, stream=None):
+    """Gated feed-forward block (the shared expert): [gate; up] = w13 x,
+    h = silu(gate) * up, out = w2 h (+ addend). x bf16 [T, H], w13 bf16
+    [2I, H], w2 bf16 [H, I], addend bf16 [T, H]; lora13 / lora2: adapters of
+    the two projections. save_gate_up (or a gate_up buffer): -> (out, gate_up
+    bf16 [T, 2I], what moe_ffn_backward needs), else out."""
+    T, H, I = _ffn_sizes(x, w13, w2)
+    device = x.device
+    px, ldx = _rows(x, "x", torch.bfloat16, (T, H), device)
+    p13 = _full(w13, "w13", torch.bfloat16, (2 * I, H), device)
+    p2 = _full(w2, "w2", torch.bfloat16, (H, I), device)
+    pa, lda = (None, H) if addend is None else _rows(addend, "addend", torch.bfloat16, (T, H), device)
+    c13, r13 = _lora(lora13, "lora13", T, H, 2 * I, device)
+    c2, r2 = _lora(lora2, "lora2", T, I, H, device)
+    if out is None:
+        out = _empty((T, H), torch.bfloat16, device, stream)
+    po, ldo = _rows(out, "out", torch.bfloat16, (T, H), device)
+    if gate_up is None and save_gate_up:
+        gate_up = _empty((T, 2 * I), torch.bfloat16, device, stream)
+    pg = None if gate_up is None else _full(gate_up, "gate_up", torch.bfloat16, (T, 2 * I), device)
+    ws = _workspace(workspace, lib.moe_ffn_workspace_size(T, H, I, r13, r2), device, stream)
+    _run(device, stream, lambda s: lib.moe_ffn_forward(
+        px, ldx, p13, p2, act, pa, lda, c13, c2, T, H, I, po, ldo, pg,
+        ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0, s))
+    return out if gate_up is None else (out, gate_up)
+
+
+def moe_ffn_mxfp8_workspace_size(T, H, I) -> int:
+    return int(lib.moe_ffn_mxfp8_workspace_size(T, H, I))
+
+
+def moe_ffn_forward_mxfp8(x, x_scale, w13, w13_scale, w2, w2_scale, addend=None, act=MOE_ACT_SWIGLU,
+                          out=None, workspace=None, stream=None):
+    """moe_ffn_forward with MXFP8 activations and weights: codes e4m3 x [T, H],
+    w13 [2I, H], w2 [H, I] (float8_e4m3fn or uint8) and e8m0 scales [rows,
+    columns / 32] (float8_e8m0fnu or uint8) -> out bf16 [T, H]."""
+    T, H, I = _ffn_sizes(x, w13, w2)
+    device = x.device
+    if H % 32 or I % 32:
+        raise ValueError(f"H={H} and I={I} must be multiples of 32")
+    px = _full(x, "x", _CODES, (T, H), device)
+    pxs = _full(x_scale, "x_scale", _SCALES, (T, H // 32), device)
+    p13 = _full(w13, "w13", _CODES, (2 * I, H), device)
+    p13s = _full(w13_scale, "w13_scale", _SCALES, (2 * I, H // 32), device)
+    p2 = _full(w2, "w2", _CODES, (H, I), device)
+    p2s = _full(w2_scale, "w2_scale", _SCALES, (H, I // 32), device)
+    pa, lda = (None, H) if addend is None else _rows(addend, "addend", torch.bfloat16, (T, H), device)
+    if out is None:
+        out = _empty((T, H), torch.bfloat16, device, stream)
+    po, ldo = _rows(out, "out", torch.bfloat16, (T, H), device)
+    ws = _workspace(workspace, lib.moe_ffn_mxfp8_workspace_size(T, H, I), device, stream)
+    _run(device, stream, lambda s: lib.moe_ffn_forward_mxfp8(
+        px, pxs, p13, p13s, p2, p2s, act, pa, lda, T, H, I, po, ldo,
+        ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0, s))
+    return out
+
+
+def moe_ffn_backward_workspace_size(T, H, I) -> int:
+    return int(lib.moe_ffn_backward_workspace_size(T, H, I))
+
+
+def moe_ffn_backward(dout, x, gate_up, w13, w2, need_dx=True, need_dw13=True, need_dw2=True, dx=None,
+                     dw13=None, dw2=None, act=MOE_ACT_SWIGLU, workspace=None, stream=None):
+    """Backward of moe_ffn_forward (without adapters) from its gate_up ->
+    (dx bf16 [T, H], dw13 bf16 [2I, H], dw2 bf16 [H, I]); a gradient that is
+    not needed is None. The gradient of addend is dout itself."""
+    T, H, I = _ffn_sizes(x, w13, w2)
+    device = x.device
+    pd, ldd = _rows(dout, "dout", torch.bfloat16, (T, H), device)
+    px, ldx = _rows(x, "x", torch.bfloat16, (T, H), device)
+    pg = _full(gate_up, "gate_up", torch.bfloat16, (T, 2 * I), device)
+    p13 = _full(w13, "w13", torch.bfloat16, (2 * I, H), device)
+    p2 = _full(w2, "w2", torch.bfloat16, (H, I), device)
+    if not (need_dx or need_dw13 or need_dw2):
+        return None, None, None
+    if need_dx and dx is None:
+        dx = _empty((T, H), torch.bfloat16, device, stream)
+    if need_dw13 and dw13 is None:
+        dw13 = _empty((2 * I, H), torch.bfloat16, device, stream)
+    if need_dw2 and dw2 is None:
+        dw2 = _empty((H, I), torch.bfloat16, device, stream)
+    pdx, lddx = (None, H) if not need_dx else _rows(dx, "dx", torch.bfloat16, (T, H), device)
+    pd13 = None if not need_dw13 else _full(dw13, "dw13", torch.bfloat16, (2 * I, H), device)
+    pd2 = None if not need_dw2 else _full(dw2, "dw2", torch.bfloat16, (H, I), device)
+    ws = _workspace(workspace, lib.moe_ffn_backward_workspace_size(T, H, I), device, stream)
+    _run(device, stream, lambda s: lib.moe_ffn_backward(
+        pd, ldd, px, ldx, pg, p13, p2, act, T, H, I, pdx, lddx, pd13, pd2,
+        ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0, s))
+    return dx if need_dx else None, dw13 if need_dw13 else None, dw2 if need_dw2 else None
+
+
+class _Ffn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w13, w2, addend):
+        needs = any(ctx.needs_input_grad[:3])
+        r = moe_ffn_forward(x, w13, w2, addend=addend, save_gate_up=needs)
+        out, gate_up = r if needs else (r, None)
+        ctx.save_for_backward(x, w13, w2, gate_up)
+        return out
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dout):
+        x, w13, w2, gate_up = ctx.saved_tensors
+        nx, n13, n2, na = ctx.needs_input_grad
+        if not (nx or n13 or n2):
+            return None, None, None, dout
+        # A gradient may come expanded or transposed.
+        dense = dout.contiguous()
+        if dense.data_ptr() % 16:
+            dense = dense.clone()
+        dx, dw13, dw2 = moe_ffn_backward(dense, x, gate_up, w13, w2, nx, n13, n2)
+        return dx, dw13, dw2, dout if na else None
+
+
+def moe_ffn(x, w13, w2, addend=None):
+    """The shared expert as a differentiable function of bf16 x [T, H], w13
+    [2I, H], w2 [H, I] and addend [T, H]: moe_ffn_forward, with
+    moe_ffn_backward for the gradients that are asked for."""
+    return _Ffn.apply(x, w13, w2, addend)
+
+
+def moe_a16w4_block(x, norm_weight, router_w, w13, w13_scale, w2, w2_scale, topk, residual=None, eps=1e-6,
+                    weight_offset=0.0, shared=None, shared_mxfp8=None, lora13=None, lora2=None,
+                    renormalize=True, fmt=MOE_W_MXFP4, block_m=None, stream=None):
+    """The feed-forward half of a decoder layer on one stream: residual
+    addition and norm (moe_rms_norm), router logits (moe_lora_linear in fp32
+    with router_w bf16 [E, H]), the routed experts (moe_a16w4_layer) and the
+    shared expert added to their output: shared = (w13, w2) in bf16
+    (moe_ffn_forward, with its adapters), or shared_mxfp8 = (w13, w13_scale,
+    w2, w2_scale) (moe_ffn_forward_mxfp8 on the norm's MXFP8 output).
+    -> (out bf16 [T, H], the residual for the next layer)."""
+    if shared is not None and shared_mxfp8 is not None:
+        raise ValueError("shared and shared_mxfp8 exclude each other")
+    if shared is None and (lora13 is not None or lora2 is not None):
+        raise ValueError("lora13 and lora2 belong to the bf16 shared expert")
+    with torch.cuda.device(x.device), _on(stream):
+        y, res, q, qs = moe_rms_norm(x, norm_weight, residual=residual, eps=eps, weight_offset=weight_offset,
+                                     mxfp8=shared_mxfp8 is not None, stream=stream)
+        logits = moe_lora_linear(y, router_w, out_dtype=torch.float32, stream=stream)
+        out = moe_a16w4_layer(y, logits, w13, w13_scale, w2, w2_scale, topk, fmt=fmt, renormalize=renormalize,
+                              block_m=block_m, stream=stream)
+        if shared is not None:
+            out = moe_ffn_forward(y, *shared, addend=out, out=out, lora13=lora13, lora2=lora2, stream=stream)
+        elif shared_mxfp8 is not None:
+            out = moe_ffn_forward_mxfp8(q, qs, *shared_mxfp8, addend=out, out=out, stream=stream)
+    return out, x if residual is None else res

@@ -11,11 +11,13 @@
 #include <mutex>
 
 #include "../../include/moe_a16w4.h"
+#include "abi_common.hpp"
 #include "launch.hpp"
 
-namespace {
+namespace moe {
+namespace abi {
 
-thread_local char g_err[512] = "no error";
+static thread_local char g_err[512] = "no error";
 
 moe_status fail(moe_status st, const char* fmt, ...) {
     va_list ap;
@@ -30,7 +32,15 @@ moe_status hip_status(hipError_t e, const char* what) {
     return fail(MOE_ERR_HIP, "%s: HIP error %d (%s)", what, (int)e, hipGetErrorString(e));
 }
 
-bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
+}  // namespace abi
+}  // namespace moe
+
+using moe::abi::align_up;
+using moe::abi::aligned;
+using moe::abi::fail;
+using moe::abi::hip_status;
+
+namespace {
 
 // Largest activation buffer (x or h) the GEMM kernels address with 32-bit
 // buffer offsets, keeping kOob (2^31) past the end of every record.
@@ -49,8 +59,6 @@ int64_t capacity(int T, int topk, int E, int bm) {
     const int64_t cap = P + groups * (bm - 1);
     return (cap + bm - 1) / bm * bm;
 }
-
-int64_t align_up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
 
 struct WsLayout {
     int64_t h_off, h_bytes, y_off, y_bytes, list_off, list_bytes, total;
@@ -210,7 +218,7 @@ moe_status launch_forward(const moe::MoeGemmArgs& a, const WsLayout& L, void* wo
 
 extern "C" {
 
-const char* moe_last_error(void) { return g_err; }
+const char* moe_last_error(void) { return moe::abi::g_err; }
 
 int64_t moe_align_sort_capacity(int T, int topk, int E, int block_m) {
     if (T < 0 || topk < 1 || E < 1 || !valid_bm(block_m)) return -1;

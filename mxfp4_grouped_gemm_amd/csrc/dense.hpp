@@ -1,0 +1,94 @@
+// Arguments and launchers of the dense operators around the routed experts:
+// residual RMS norm, gated feed-forward block (forward and backward) and the
+// projection with low-rank adapters.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace moe {
+
+// A stack of low-rank adapters beside one projection [N, K]: token t adds
+// scale[a] * B[a] (A[a] x[t]) for a = index[t]; an index outside [0, n) adds
+// nothing. v [T, vld] (fp32) receives scale * A x from the narrow product and
+// is read by the projection's kernels.
+struct LoraArgs {
+    const uint16_t* a;       // bf16 [n, rank, K]
+    const uint16_t* b;       // bf16 [n, N, rank]
+    const int32_t* index;    // [T]
+    const int32_t* ranks;    // [n] or null (all `rank`)
+    const float* scale;      // [n] or null (all 1)
+    float* v;                // fp32 [T, vld], vld = rank rounded up to 32
+    int n, rank, vld;
+};
+
+// Epilogues of the dense products.
+constexpr int kEpiOut = 0;      // out = acc (+ addend), bf16 or fp32
+constexpr int kEpiGated = 1;    // h = silu(gate) * up, bf16; optional gate_up
+constexpr int kEpiGatedMx = 2;  // the same, h in MXFP8
+constexpr int kEpiGatedBwd = 3; // acc = dh: dgate_up and h from the saved gate_up
+
+// One product C[m, n] = sum_k X[m, k] W[n, k]. Strides in elements. For the
+// gated epilogues W holds 2N rows (gate rows, then up rows) and n counts pairs.
+struct DenseArgs {
+    const void* x;
+    const void* w;
+    const uint8_t* xs;  // e8m0 [M, K/32] (MXFP8)
+    const uint8_t* ws;
+    int64_t ldx, ldw;
+    int M, N, K;
+    void* out;              // kEpiOut: C; kEpiGated: h; kEpiGatedMx: h codes; kEpiGatedBwd: dgate_up
+    int64_t ldo;
+    int out_f32;
+    const uint16_t* addend; // bf16 [M, N], stride ldadd
+    int64_t ldadd;
+    uint16_t* gate_up;      // kEpiGated: saved (may be null); kEpiGatedBwd: read
+    uint16_t* h;            // kEpiGatedBwd: h
+    uint8_t* hs;            // kEpiGatedMx: e8m0 scales of h
+    float* partial;         // split K: fp32 [splits, M, N or 2N]
+    int splits;             // 1: the epilogue runs in the product's kernel
+    LoraArgs lora;          // lora.n == 0: none
+};
+
+// Operand orders: K-major rows, or K as the row index ("transposed").
+enum DenseOrder { kNT = 0, kNN = 1, kTN = 2 };  // (X K-major, W K-major), (X K-major, W transposed), (both transposed)
+
+// splits the launcher would take for this product, and the bytes of `partial`
+// that they need.
+int dense_splits(const DenseArgs& a, int order, int elt, int epi);
+inline int64_t dense_partial_bytes(const DenseArgs& a, int splits, int epi) {
+    return splits <= 1 ? 0 : (int64_t)splits * a.M * a.N * (epi == kEpiOut || epi == kEpiGatedBwd ? 1 : 2) * 4;
+}
+bool dense_big_tiles(const DenseArgs& a, int epi);
+hipError_t launch_join(const DenseArgs& a, int epi, hipStream_t s);
+hipError_t launch_dense(const DenseArgs& a, int order, int elt, int epi, hipStream_t s);
+hipError_t launch_dense_nt(const DenseArgs& a, int epi, hipStream_t s);
+hipError_t launch_dense_mx(const DenseArgs& a, int epi, hipStream_t s);
+hipError_t launch_dense_bwd(const DenseArgs& a, int order, int epi, hipStream_t s);
+
+// Up to this many tokens the products stream the weights without LDS tiles.
+constexpr int kSkinnyMaxTokens = 64;
+// elt 0: bf16; 1: MXFP8 activations and weights. h_f32: the fp32 h of the
+// MXFP8 block between its two products (written by kEpiGated, and read and
+// quantised by the second product).
+hipError_t launch_skinny(const DenseArgs& a, int elt, int epi, const float* h_f32, hipStream_t s);
+
+// v[t] = scale * A[index[t]] x[t].
+hipError_t launch_lora_shrink(const uint16_t* x, int64_t ldx, int T, int K, const LoraArgs& l, hipStream_t s);
+
+struct NormArgs {
+    const uint16_t* x;
+    const void* residual;
+    const void* weight;
+    void* residual_out;
+    uint16_t* y;
+    uint8_t* q;
+    uint8_t* qs;
+    int64_t ldx, ldr, ldro, ldy, ldq, ldqs;
+    int T, H;
+    float eps, offset;
+    int res_f32, weight_f32;
+};
+hipError_t launch_rms_norm(const NormArgs& a, hipStream_t s);
+
+}  // namespace moe

@@ -1,0 +1,22 @@
+// Instances of the LDS-tiled product for the backward of the gated block:
+// dh = dout W2 with the activation's backward as its epilogue, dx, and the two
+// weight gradients.
+#include "dense_tile.hpp"
+
+namespace moe {
+
+using namespace dense;
+
+template <bool XT, int EPI>
+static hipError_t launch_epi(const DenseArgs& a, hipStream_t s) {
+    if (dense_big_tiles(a, EPI))
+        return launch_tile<Tile<256, 256, 2, 4, XT, true, kEltBf16, EPI, false, false>>(a, s);
+    return launch_tile<Tile<128, 128, 2, 2, XT, true, kEltBf16, EPI, false, false>>(a, s);
+}
+
+hipError_t launch_dense_bwd(const DenseArgs& a, int order, int epi, hipStream_t s) {
+    if (order == kTN) return launch_epi<true, kEpiOut>(a, s);
+    return epi == kEpiOut ? launch_epi<false, kEpiOut>(a, s) : launch_epi<false, kEpiGatedBwd>(a, s);
+}
+
+}  // namespace moe

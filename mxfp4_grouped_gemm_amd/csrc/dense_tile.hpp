@@ -1,0 +1,548 @@
+// LDS-tiled dense product C[m, n] = sum_k X[m, k] W[n, k] with the epilogues
+// of the dense operators, on v_mfma_f32_16x16x32_bf16 or, for MXFP8 operands,
+// v_mfma_scale_f32_16x16x128_f8f6f4.
+//
+// A workgroup owns a BM x BN tile of C and its waves a WM x WN grid of it.
+// Both operands go to LDS in steps of 128 bytes of K (64 bf16 or 128 e4m3
+// elements) with loads straight into LDS, one buffer ahead of the one that is
+// multiplied (two buffers, one barrier a step; the buffers are separate
+// __shared__ objects, so that the compiler sees that reads of one need not
+// wait for loads into the other).
+//
+// W is the MFMA's first operand, so a lane's four results are four
+// consecutive n of one m. The rows of W are dealt to the fragments such that
+// a lane's fragments are consecutive too (`n = 4 F q + 4 f + p` for fragment f
+// of F, MFMA row i = 4 q + p): a lane owns 4 F consecutive outputs of a token.
+//
+// LDS layouts, in 16-byte pieces (the granule of a load into LDS, whose
+// destination is fixed, so the piece that a lane fetches is permuted):
+//  * K-major operand: 128-byte rows; piece c of row r sits at c ^ key(r),
+//    key chosen such that the 16 rows of an operand read, two of which share
+//    the 64 banks, touch every bank once.
+//  * K as the row index (the other operand order of a backward product): rows
+//    of BM or BN elements; the operand is read through the transposing LDS
+//    read (four rows of 16 elements -> each lane four elements of one column).
+//    Piece c of row k sits at c ^ (2 ((k & 3) | (k >> 3 & 1) << 2)).
+#pragma once
+
+#include "common.hpp"
+#include "dense.hpp"
+#include "mx8.hpp"
+
+namespace moe {
+namespace dense {
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kEltBf16 = 0, kEltMx8 = 1;
+constexpr int kRowBytes = 128;  // bytes of K a step
+constexpr int kGroupM = 4;      // tiles of M that share a column of W tiles
+// Every load's record: masked lanes carry kOob, the others stay inside the
+// tensor by construction (the tile's base is a 64-bit address).
+constexpr uint32_t kRecord = 0x7fff0000u;
+
+typedef __attribute__((address_space(3))) void* lds_ptr;
+
+__device__ __forceinline__ void load_lds16(rsrc_t r, uint8_t* dst, uint32_t voff, uint32_t soff) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)dst, 16, voff, soff, 0, 0);
+}
+
+// e^x / (1 + e^x) and friends with the accurate expf: the epilogue runs once
+// per output.
+__device__ __forceinline__ float sigmoid(float g) { return 1.0f / (1.0f + expf(-g)); }
+
+template <int BM_, int BN_, int WM_, int WN_, bool XT_, bool WT_, int ELT_, int EPI_, bool SPLIT_, bool LORA_>
+struct Tile {
+    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, ELT = ELT_, EPI = EPI_;
+    static constexpr bool XT = XT_, WT = WT_, SPLIT = SPLIT_, LORA = LORA_;
+    static constexpr bool GATED = EPI == kEpiGated || EPI == kEpiGatedMx;
+    static constexpr int NW = WM * WN, THREADS = NW * 64;
+    static constexpr int FM = BM / WM / 16, FN = BN / WN / 16;
+    static constexpr int F = GATED ? FN / 2 : FN;      // fragments of one column set
+    static constexpr int BNC = GATED ? BN / 2 : BN;    // output columns (pairs) of a tile
+    static constexpr int BK = ELT == kEltBf16 ? 64 : 128;
+    static constexpr int ESZ = ELT == kEltBf16 ? 2 : 1;
+    static constexpr int XBYTES = BM * kRowBytes, WBYTES = BN * kRowBytes;
+    static constexpr int SBYTES = ELT == kEltMx8 ? (BM + BN) * 4 : 0;  // scales of a step
+    static constexpr int BUF = XBYTES + WBYTES + SBYTES;
+    static constexpr int XL = XBYTES / 1024 / NW, WL = WBYTES / 1024 / NW;  // loads a wave issues per step
+    static_assert(XBYTES % (1024 * NW) == 0 && WBYTES % (1024 * NW) == 0, "whole loads");
+    static_assert(ELT == kEltBf16 || (!XT && !WT), "MXFP8 operands are K-major");
+};
+
+// Swizzle keys (see the top).
+__device__ __forceinline__ int key_x(int r) { return (r >> 1) & 7; }
+template <int F>
+__device__ __forceinline__ int key_w(int r) {
+    constexpr int s = F == 4 ? 4 : F == 2 ? 3 : 2;
+    return ((r >> 1) & 1) | (((r >> s) & 3) << 1);
+}
+__device__ __forceinline__ int key_t(int k) { return 2 * ((k & 3) | (((k >> 3) & 1) << 2)); }
+
+// The low-rank term of a wave's accumulators: for each adapter that one of
+// the wave's rows uses, acc += B[a] v over its rank, with v (fp32) split into
+// two bf16 (hi + lo: 16 bits of it) and zero in the other adapters' rows.
+// n_of(f, lane) gives the W row (of the stack's N rows) of fragment f's MFMA
+// row lane % 16, or -1; m_of(fm) the token of this lane's column, or -1.
+// Adapters whose turn is not `turn` of `turns` are left to other waves.
+template <int FN, int FM, class NOF, class MOF>
+__device__ __forceinline__ void lora_accumulate(const LoraArgs& l, int64_t brows, f32x4 (&acc)[FN][FM], NOF n_of,
+                                                MOF m_of, int turn, int turns) {
+    const int lane = (int)threadIdx.x & 63;
+    const int g = lane >> 4;
+    int idx[FM];
+    int64_t mrow[FM];
+#pragma unroll
+    for (int fm = 0; fm < FM; ++fm) {
+        const int m = m_of(fm);
+        mrow[fm] = m;
+        const int i = m >= 0 ? l.index[m] : -1;
+        idx[fm] = (unsigned)i < (unsigned)l.n ? i : 0x7fffffff;
+    }
+    int last = -1;
+    for (int seen = 0;; ++seen) {
+        // The smallest adapter above `last` among the wave's rows.
+        int next = 0x7fffffff;
+#pragma unroll
+        for (int fm = 0; fm < FM; ++fm) next = idx[fm] > last && idx[fm] < next ? idx[fm] : next;
+#pragma unroll
+        for (int d = 1; d < 16; d *= 2) {
+            const int o = __shfl_xor(next, d);
+            next = o < next ? o : next;
+        }
+        next = __builtin_amdgcn_readfirstlane(next);
+        if (next == 0x7fffffff) break;
+        last = next;
+        if (seen % turns != turn) continue;
+        int rank = l.ranks ? l.ranks[next] : l.rank;
+        rank = rank < l.rank ? rank : l.rank;
+        const uint16_t* bp = l.b + (int64_t)next * brows * l.rank;
+        for (int k0 = 0; k0 < rank; k0 += 32) {
+            const int k = k0 + 8 * g;
+            bf16x8 bf[FN];
+#pragma unroll
+            for (int f = 0; f < FN; ++f) {
+                const int n = n_of(f);
+                u32x4 u = {0, 0, 0, 0};
+                if (n >= 0 && k < rank) {
+                    u = *(const u32x4*)(bp + (int64_t)n * l.rank + k);
+                    if (k + 8 > rank) {  // columns beyond the adapter's rank are not read as numbers
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            if (k + 2 * e >= rank) u[e] = 0;
+                            else if (k + 2 * e + 1 >= rank) u[e] &= 0xffffu;
+                        }
+                    }
+                }
+                bf[f] = __builtin_bit_cast(bf16x8, u);
+            }
+#pragma unroll
+            for (int fm = 0; fm < FM; ++fm) {
+                if (!__any(idx[fm] == next)) continue;
+                float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                if (idx[fm] == next) {
+                    const float* vp = l.v + mrow[fm] * l.vld + k;
+                    const f32x4 a = *(const f32x4*)vp, b = *(const f32x4*)(vp + 4);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        v[e] = a[e];
+                        v[4 + e] = b[e];
+                    }
+                }
+                u32x4 hi, lo;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    hi[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
+                    lo[e] = pack_bf16x2(v[2 * e] - __uint_as_float(hi[e] << 16),
+                                        v[2 * e + 1] - __uint_as_float(hi[e] & 0xffff0000u));
+                }
+                // A lane's results are one token's: only those of this adapter
+                // are kept (a NaN in its factors stays with its own tokens).
+                const bool mine = idx[fm] == next;
+#pragma unroll
+                for (int f = 0; f < FN; ++f) {
+                    f32x4 d = mfma16x16x32(bf[f], __builtin_bit_cast(bf16x8, hi), acc[f][fm]);
+                    d = mfma16x16x32(bf[f], __builtin_bit_cast(bf16x8, lo), d);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) acc[f][fm][r] = mine ? d[r] : acc[f][fm][r];
+                }
+            }
+        }
+    }
+}
+
+template <class C>
+__global__ __launch_bounds__(C::THREADS, C::THREADS == 256 ? 1 : 2) void dense_kernel(DenseArgs a) {
+    __shared__ __align__(1024) uint8_t s0[C::BUF];
+    __shared__ __align__(1024) uint8_t s1[C::BUF];
+    const int tid = (int)threadIdx.x, lane = tid & 63;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = w / C::WN, wn = w % C::WN;
+    const int g = lane >> 4, l16 = lane & 15;
+
+    // Tile of this workgroup. Consecutive workgroups go round-robin over the 8
+    // XCDs; giving an XCD a contiguous run of tiles, in columns of kGroupM
+    // tiles of M, keeps its W tiles in its own L2.
+    const int tm = (a.M + C::BM - 1) / C::BM, tn = (a.N + C::BNC - 1) / C::BNC;
+    int id = (int)blockIdx.x;
+    const int total = tm * tn;
+    {
+        const int q = total / 8, r = total % 8, xcd = id % 8, i = id / 8;
+        id = xcd * q + (xcd < r ? xcd : r) + i;
+    }
+    const int per = kGroupM * tn, grp = id / per, rest = id % per;
+    const int gm = tm - grp * kGroupM < kGroupM ? tm - grp * kGroupM : kGroupM;
+    const int m0 = (grp * kGroupM + rest % gm) * C::BM, n0 = rest / gm * C::BNC;
+
+    const int steps = (a.K + C::BK - 1) / C::BK;
+    int kt0 = 0, kt1 = steps;
+    if constexpr (C::SPLIT) {
+        const int z = (int)blockIdx.y;
+        kt0 = (int)((int64_t)steps * z / a.splits);
+        kt1 = (int)((int64_t)steps * (z + 1) / a.splits);
+    }
+
+    // Loads: offsets of this lane's pieces from the tile's first element.
+    const char* xb = (const char*)a.x + (C::XT ? (int64_t)m0 : (int64_t)m0 * a.ldx) * C::ESZ;
+    const char* wb = (const char*)a.w + (C::WT ? (int64_t)n0 : (int64_t)n0 * a.ldw) * C::ESZ;
+    uint32_t xo[C::XL], wo[C::WL];
+    int xk[C::XL], wk[C::WL];  // K of the piece in its step (elements)
+#pragma unroll
+    for (int i = 0; i < C::XL; ++i) {
+        const int p = (w * C::XL + i) * 64 + lane;  // piece of the tile
+        if constexpr (C::XT) {
+            constexpr int PR = C::BM / 8;  // pieces a row
+            const int k = p / PR, c = (p % PR) ^ key_t(k);
+            xk[i] = k;
+            xo[i] = m0 + c * 8 < a.M ? (uint32_t)(k * a.ldx * 2 + c * 16) : kOob;
+        } else {
+            const int r = p >> 3, c = (p & 7) ^ key_x(r);
+            xk[i] = c * (16 / C::ESZ);
+            xo[i] = m0 + r < a.M ? (uint32_t)(r * a.ldx * C::ESZ + c * 16) : kOob;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < C::WL; ++i) {
+        const int p = (w * C::WL + i) * 64 + lane;
+        if constexpr (C::WT) {
+            constexpr int PR = C::BN / 8;
+            const int k = p / PR, c = (p % PR) ^ key_t(k);
+            wk[i] = k;
+            wo[i] = n0 + c * 8 < a.N ? (uint32_t)(k * a.ldw * 2 + c * 16) : kOob;
+        } else {
+            const int r = p >> 3, c = (p & 7) ^ key_w<C::F>(r);
+            wk[i] = c * (16 / C::ESZ);
+            if constexpr (C::GATED) {
+                // Rows [0, BNC) of the tile are gate rows, the others the up
+                // rows, N rows further on: their own base (wo is 32 bits).
+                const int col = r % C::BNC;
+                wo[i] = n0 + col < a.N ? (uint32_t)(col * a.ldw * C::ESZ + c * 16) : kOob;
+            } else {
+                wo[i] = n0 + r < a.N ? (uint32_t)(r * a.ldw * C::ESZ + c * 16) : kOob;
+            }
+        }
+    }
+    const int64_t up = C::GATED ? (int64_t)a.N * a.ldw * C::ESZ : 0;
+
+    auto issue = [&](uint8_t* buf, int kt) {
+        const bool tail = (kt + 1) * C::BK > a.K;
+        const rsrc_t rx = make_rsrc(xb + (C::XT ? (int64_t)kt * C::BK * a.ldx * 2 : (int64_t)kt * kRowBytes), kRecord);
+        const int64_t wadv = C::WT ? (int64_t)kt * C::BK * a.ldw * 2 : (int64_t)kt * kRowBytes;
+        const rsrc_t rw = make_rsrc(wb + wadv, kRecord);
+        const rsrc_t ru = make_rsrc(wb + wadv + up, kRecord);
+        const int left = a.K - kt * C::BK;
+#pragma unroll
+        for (int i = 0; i < C::XL; ++i)
+            load_lds16(rx, buf + (w * C::XL + i) * 1024, tail && xk[i] >= left ? kOob : xo[i], 0);
+#pragma unroll
+        for (int i = 0; i < C::WL; ++i) {
+            const bool second = C::GATED && (w * C::WL + i) * 8 >= C::BNC;  // 8 rows a load: uniform
+            load_lds16(second ? ru : rw, buf + C::XBYTES + (w * C::WL + i) * 1024,
+                       tail && wk[i] >= left ? kOob : wo[i], 0);
+        }
+    };
+
+    // MXFP8 scales: thread t carries row t's four bytes of a step (and row
+    // t + THREADS's), in registers until its buffer is free.
+    constexpr int SR = C::ELT == kEltMx8 ? (C::BM + C::BN + C::THREADS - 1) / C::THREADS : 0;
+    uint32_t sv[SR > 0 ? SR : 1];
+    const int kb = a.K / 32;
+    auto load_scales = [&](int kt) {
+        if constexpr (C::ELT == kEltMx8) {
+#pragma unroll
+            for (int i = 0; i < SR; ++i) {
+                const int r = tid + i * C::THREADS;
+                const uint8_t* p = nullptr;
+                if (r < C::BM) {
+                    if (m0 + r < a.M) p = a.xs + (int64_t)(m0 + r) * kb;
+                } else if (r < C::BM + C::BN) {
+                    const int rw = r - C::BM, col = C::GATED ? rw % C::BNC : rw;
+                    if (n0 + col < a.N) p = a.ws + (int64_t)(n0 + col + (C::GATED && rw >= C::BNC ? a.N : 0)) * kb;
+                }
+                uint32_t v = 0;
+                if (p) {
+                    if (kb % 4 == 0) {
+                        v = *(const uint32_t*)(p + kt * 4);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (kt * 4 + e < kb) v |= (uint32_t)p[kt * 4 + e] << (8 * e);
+                    }
+                }
+                sv[i] = v;
+            }
+        }
+    };
+    auto store_scales = [&](uint8_t* buf) {
+        if constexpr (C::ELT == kEltMx8) {
+#pragma unroll
+            for (int i = 0; i < SR; ++i) {
+                const int r = tid + i * C::THREADS;
+                if (r < C::BM + C::BN) *(uint32_t*)(buf + C::XBYTES + C::WBYTES + r * 4) = sv[i];
+            }
+        }
+    };
+
+    f32x4 acc[C::FN][C::FM];
+#pragma unroll
+    for (int i = 0; i < C::FN; ++i)
+#pragma unroll
+        for (int j = 0; j < C::FM; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+
+    // LDS row of W for fragment f, MFMA row i (K-major).
+    auto wrow = [&](int f, int i) {
+        const int half = C::GATED ? f / C::F : 0, ff = f % C::F;
+        return half * C::BNC + wn * 16 * C::F + (i >> 2) * 4 * C::F + ff * 4 + (i & 3);
+    };
+    const int xr0 = wm * C::FM * 16;
+    auto read_x = [&](const uint8_t* buf, int fm, int piece) -> u32x4 {
+        const int r = xr0 + fm * 16 + l16;
+        return *(const u32x4*)(buf + r * kRowBytes + ((piece ^ key_x(r)) << 4));
+    };
+    auto read_w = [&](const uint8_t* buf, int f, int piece) -> u32x4 {
+        const int r = wrow(f, l16);
+        return *(const u32x4*)(buf + C::XBYTES + r * kRowBytes + ((piece ^ key_w<C::F>(r)) << 4));
+    };
+    // Transposed operand: columns c0 + 0..15 of K rows 32 s + 8 g + 0..7.
+    auto read_t = [&](const uint8_t* base, int pitch, int c0, int s) -> bf16x8 {
+        bf16x4 v[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int k = 32 * s + 8 * g + 4 * h + (l16 >> 2);
+            const int col = c0 + (l16 & 3) * 4;
+            const uint8_t* p = base + k * pitch + ((((col >> 3) ^ key_t(k)) << 4) | ((col & 4) << 1));
+            typedef __attribute__((address_space(3))) bf16x4* tp;
+            v[h] = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((tp)p);
+        }
+        return __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7);
+    };
+
+    auto compute = [&](const uint8_t* buf) {
+        if constexpr (C::ELT == kEltBf16) {
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                bf16x8 xf[C::FM], wf[C::FN];
+#pragma unroll
+                for (int f = 0; f < C::FN; ++f) {
+                    if constexpr (C::WT) wf[f] = read_t(buf + C::XBYTES, C::BN * 2, (wn * C::FN + f) * 16, s);
+                    else wf[f] = __builtin_bit_cast(bf16x8, read_w(buf, f, 4 * s + g));
+                }
+#pragma unroll
+                for (int f = 0; f < C::FM; ++f) {
+                    if constexpr (C::XT) xf[f] = read_t(buf, C::BM * 2, xr0 + f * 16, s);
+                    else xf[f] = __builtin_bit_cast(bf16x8, read_x(buf, f, 4 * s + g));
+                }
+#pragma unroll
+                for (int j = 0; j < C::FM; ++j)
+#pragma unroll
+                    for (int i = 0; i < C::FN; ++i) acc[i][j] = mfma16x16x32(wf[i], xf[j], acc[i][j]);
+            }
+        } else {
+            // A lane's 32 elements are pieces g and 4 + g; its scale operand
+            // is that of block g of the step.
+            const uint8_t* sc = buf + C::XBYTES + C::WBYTES;
+            i32x8 wf[C::FN];
+            int wsc[C::FN];
+#pragma unroll
+            for (int f = 0; f < C::FN; ++f) {
+                const i32x4 lo = __builtin_bit_cast(i32x4, read_w(buf, f, g)), hi = __builtin_bit_cast(i32x4, read_w(buf, f, 4 + g));
+                wf[f] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+                wsc[f] = sc[(C::BM + wrow(f, l16)) * 4 + g];
+            }
+#pragma unroll
+            for (int j = 0; j < C::FM; ++j) {
+                const i32x4 lo = __builtin_bit_cast(i32x4, read_x(buf, j, g)), hi = __builtin_bit_cast(i32x4, read_x(buf, j, 4 + g));
+                const i32x8 xf = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+                const int xsc = sc[(xr0 + j * 16 + l16) * 4 + g];
+#pragma unroll
+                for (int i = 0; i < C::FN; ++i)
+                    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf[i], xf, acc[i][j], 0, 0, 0, wsc[i], 0, xsc);
+            }
+        }
+    };
+
+    if (kt0 < kt1) {
+        issue(s0, kt0);
+        load_scales(kt0);
+        store_scales(s0);
+        __syncthreads();
+        for (int kt = kt0; kt < kt1; kt += 2) {
+            if (kt + 1 < kt1) {
+                issue(s1, kt + 1);
+                load_scales(kt + 1);
+            }
+            compute(s0);
+            if (kt + 1 < kt1) store_scales(s1);
+            __syncthreads();
+            if (kt + 1 >= kt1) break;
+            if (kt + 2 < kt1) {
+                issue(s0, kt + 2);
+                load_scales(kt + 2);
+            }
+            compute(s1);
+            if (kt + 2 < kt1) store_scales(s0);
+            __syncthreads();
+        }
+    }
+
+    // Column of fragment f's lane results (the first of four), and the token.
+    auto m_of = [&](int fm) { return m0 + xr0 + fm * 16 + l16; };
+    auto n_of = [&](int f) {
+        if constexpr (C::WT) return n0 + (wn * C::FN + f) * 16 + 4 * g;
+        else return n0 + wn * 16 * C::F + g * 4 * C::F + (f % C::F) * 4;
+    };
+    if constexpr (C::LORA) {
+        if (a.lora.n > 0 && (!C::SPLIT || blockIdx.y == 0)) {
+            // As MFMA rows: row i = l16 of fragment f.
+            auto nrow = [&](int f) {
+                const int n = n0 + wn * 16 * C::F + (l16 >> 2) * 4 * C::F + (f % C::F) * 4 + (l16 & 3);
+                return n < a.N ? n + (C::GATED && f >= C::F ? a.N : 0) : -1;
+            };
+            auto mrow = [&](int fm) {
+                const int m = m_of(fm);
+                return m < a.M ? m : -1;
+            };
+            lora_accumulate<C::FN, C::FM>(a.lora, C::GATED ? 2 * (int64_t)a.N : a.N, acc, nrow, mrow, 0, 1);
+        }
+    }
+
+    if constexpr (C::SPLIT) {
+        const int64_t cols = C::GATED ? 2 * (int64_t)a.N : a.N;
+        float* pz = a.partial + (int64_t)blockIdx.y * a.M * cols;
+#pragma unroll
+        for (int j = 0; j < C::FM; ++j) {
+            const int m = m_of(j);
+            if (m >= a.M) continue;
+#pragma unroll
+            for (int f = 0; f < C::FN; ++f) {
+                const int n = n_of(f);
+                if (n < a.N) *(f32x4*)(pz + m * cols + n + (C::GATED && f >= C::F ? a.N : 0)) = acc[f][j];
+            }
+        }
+        return;
+    }
+
+#pragma unroll
+    for (int j = 0; j < C::FM; ++j) {
+        const int m = m_of(j);
+        const bool mok = m < a.M;
+        if constexpr (C::EPI == kEpiOut) {
+            if (!mok) continue;
+#pragma unroll
+            for (int f = 0; f < C::FN; ++f) {
+                const int n = n_of(f);
+                if (n >= a.N) continue;
+                f32x4 v = acc[f][j];
+                if (a.addend) {
+                    const u32x2 d = *(const u32x2*)(a.addend + m * a.ldadd + n);
+                    v[0] += __uint_as_float(d[0] << 16);
+                    v[1] += __uint_as_float(d[0] & 0xffff0000u);
+                    v[2] += __uint_as_float(d[1] << 16);
+                    v[3] += __uint_as_float(d[1] & 0xffff0000u);
+                }
+                if (a.out_f32) {
+                    *(f32x4*)((float*)a.out + m * a.ldo + n) = v;
+                } else {
+                    *(u32x2*)((uint16_t*)a.out + m * a.ldo + n) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+                }
+            }
+        } else if constexpr (C::GATED) {
+            float h[C::F][4], big = 0.0f;
+#pragma unroll
+            for (int f = 0; f < C::F; ++f)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    h[f][r] = swiglu(acc[f][j][r], acc[f + C::F][j][r]);
+                    big = fmaxf(big, mx8_finite_abs(h[f][r]));
+                }
+            if constexpr (C::EPI == kEpiGatedMx) {
+                // F == 2: the 32 columns of a block are the 8 of each of the
+                // four lanes l16, l16 + 16, ...; N % 32 == 0, so a block is
+                // inside the row as a whole.
+                static_assert(C::F == 2, "a wave's columns are one block");
+                big = fmaxf(big, __shfl_xor(big, 16));
+                big = fmaxf(big, __shfl_xor(big, 32));
+                const uint32_t sb = mx8_scale_byte(big);
+                const float inv = mx8_inv_scale(sb);
+                const int n = n_of(0);
+                if (mok && n < a.N) {
+                    u32x2 o;
+                    o[0] = mx8_pack4(h[0][0], h[0][1], h[0][2], h[0][3], inv);
+                    o[1] = mx8_pack4(h[1][0], h[1][1], h[1][2], h[1][3], inv);
+                    *(u32x2*)((uint8_t*)a.out + m * a.ldo + n) = o;
+                    if (g == 0) a.hs[m * (int64_t)(a.N / 32) + (n >> 5)] = (uint8_t)sb;
+                }
+            } else {
+                if (!mok) continue;
+#pragma unroll
+                for (int f = 0; f < C::F; ++f) {
+                    const int n = n_of(f);
+                    if (n >= a.N) continue;
+                    *(u32x2*)((uint16_t*)a.out + m * a.ldo + n) = u32x2{pack_bf16x2(h[f][0], h[f][1]), pack_bf16x2(h[f][2], h[f][3])};
+                    if (a.gate_up) {
+                        uint16_t* gu = a.gate_up + m * 2 * (int64_t)a.N + n;
+                        const f32x4 gv = acc[f][j], uv = acc[f + C::F][j];
+                        *(u32x2*)gu = u32x2{pack_bf16x2(gv[0], gv[1]), pack_bf16x2(gv[2], gv[3])};
+                        *(u32x2*)(gu + a.N) = u32x2{pack_bf16x2(uv[0], uv[1]), pack_bf16x2(uv[2], uv[3])};
+                    }
+                }
+            }
+        } else {  // kEpiGatedBwd
+            if (!mok) continue;
+#pragma unroll
+            for (int f = 0; f < C::FN; ++f) {
+                const int n = n_of(f);
+                if (n >= a.N) continue;
+                const uint16_t* gu = a.gate_up + m * 2 * (int64_t)a.N + n;
+                const u32x2 gb = *(const u32x2*)gu, ub = *(const u32x2*)(gu + a.N);
+                float dg[4], du[4], h[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const uint32_t gw = gb[r >> 1], uw = ub[r >> 1];
+                    const float gv = __uint_as_float(r & 1 ? gw & 0xffff0000u : gw << 16);
+                    const float uv = __uint_as_float(r & 1 ? uw & 0xffff0000u : uw << 16);
+                    const float dh = acc[f][j][r], sg = sigmoid(gv), silu = gv * sg;
+                    dg[r] = dh * uv * sg * (1.0f + gv * (1.0f - sg));
+                    du[r] = dh * silu;
+                    h[r] = silu * uv;
+                }
+                uint16_t* o = (uint16_t*)a.out + m * a.ldo + n;
+                *(u32x2*)o = u32x2{pack_bf16x2(dg[0], dg[1]), pack_bf16x2(dg[2], dg[3])};
+                *(u32x2*)(o + a.N) = u32x2{pack_bf16x2(du[0], du[1]), pack_bf16x2(du[2], du[3])};
+                if (a.h) *(u32x2*)(a.h + m * (int64_t)a.N + n) = u32x2{pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3])};
+            }
+        }
+    }
+}
+
+template <class C>
+inline hipError_t launch_tile(const DenseArgs& a, hipStream_t s) {
+    const int64_t tm = (a.M + C::BM - 1) / C::BM, tn = (a.N + C::BNC - 1) / C::BNC;
+    const dim3 grid((unsigned)(tm * tn), C::SPLIT ? (unsigned)a.splits : 1u), block(C::THREADS);
+    hipLaunchKernelGGL((dense_kernel<C>), grid, block, 0, s, a);
+    return hipGetLastError();
+}
+
+}  // namespace dense
+}  // namespace moe

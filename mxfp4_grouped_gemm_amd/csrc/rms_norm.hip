@@ -1,0 +1,213 @@
+// Residual addition and RMS norm of token rows, with a bf16 output and an
+// optional MXFP8 output:
+//   s = x + residual;  v = s / sqrt(mean(s^2) + eps) * (offset + weight);
+//   residual_out = s, y = bf16(v), (q, qs) = MXFP8(v).
+// s, the sum of squares and v are fp32; each output is rounded once, from the
+// fp32 value (y and q do not pass through each other).
+//
+// Bound by memory: 8 bytes an element with bf16 streams, about 9 with the
+// MXFP8 output. A row is read once and stays in registers between the sum and
+// the outputs. Every element is read and written by one lane, so outputs may
+// be the inputs' own buffers.
+#include "common.hpp"
+#include "dense.hpp"
+#include "mx8.hpp"
+
+namespace moe {
+
+namespace {
+
+typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
+}
+
+// Sum over the wave, the same in every lane: xor by 1 and 2 inside quads, then
+// mirrored halves of a row, then the rows.
+__device__ __forceinline__ float wave_sum(float v) {
+    v += dpp<0xB1>(v);   // quad_perm [1, 0, 3, 2]
+    v += dpp<0x4E>(v);   // quad_perm [2, 3, 0, 1]
+    v += dpp<0x141>(v);  // row_half_mirror
+    v += dpp<0x140>(v);  // row_mirror
+    const uint32_t u = __float_as_uint(v);
+    auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+    const uint32_t t = __float_as_uint(v);
+    auto b = __builtin_amdgcn_permlane32_swap(t, t, false, false);
+    return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
+// Eight elements i..i+7 of a row (VEC), or elements i, i + step, ... (the
+// layout of rows whose start or stride is not 16-byte aligned).
+template <bool VEC>
+__device__ __forceinline__ f32x8 load8(const void* row, bool f32, int i, int step, int H) {
+    f32x8 r;
+    if constexpr (VEC) {
+        if (f32) {
+            const f32x4 a = *(const f32x4*)((const float*)row + i), b = *(const f32x4*)((const float*)row + i + 4);
+            r = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+        } else {
+            const u16x8 u = *(const u16x8*)((const uint16_t*)row + i);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) r[e] = bf16_bits_to_f32(u[e]);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int k = i + e * step;
+            r[e] = k >= H ? 0.0f : f32 ? ((const float*)row)[k] : bf16_bits_to_f32(((const uint16_t*)row)[k]);
+        }
+    }
+    return r;
+}
+
+template <bool VEC>
+__device__ __forceinline__ void store8(void* row, bool f32, int i, int step, int H, f32x8 v) {
+    if constexpr (VEC) {
+        if (f32) {
+            *(f32x4*)((float*)row + i) = __builtin_shufflevector(v, v, 0, 1, 2, 3);
+            *(f32x4*)((float*)row + i + 4) = __builtin_shufflevector(v, v, 4, 5, 6, 7);
+        } else {
+            u32x4 o;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
+            *(u32x4*)((uint16_t*)row + i) = o;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int k = i + e * step;
+            if (k >= H) continue;
+            if (f32) ((float*)row)[k] = v[e];
+            else ((uint16_t*)row)[k] = f32_to_bf16_bits(v[e]);
+        }
+    }
+}
+
+}  // namespace
+
+// WAVES waves hold a row of at most WAVES * 512 * NC elements. WAVES == 1:
+// four rows a workgroup.
+template <int WAVES, int NC, bool VEC>
+__global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void rms_norm_kernel(NormArgs a) {
+    constexpr int kLanes = WAVES * 64;
+    const int tid = WAVES == 1 ? (int)threadIdx.x & 63 : (int)threadIdx.x;
+    const int t = WAVES == 1 ? (int)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6)
+                             : (int)blockIdx.x;
+    if (WAVES == 1 && t >= a.T) return;  // whole waves; no barrier below when WAVES == 1
+    const uint16_t* xr = a.x + t * a.ldx;
+    const char* rr = (const char*)a.residual + t * a.ldr * (a.res_f32 ? 4 : 2);
+    char* ro = (char*)a.residual_out + t * a.ldro * (a.res_f32 ? 4 : 2);
+    const int H = a.H;
+    // Chunk c of this lane: VEC elements [(c * kLanes + tid) * 8, +8); else
+    // elements c * 8 * kLanes + tid + e * kLanes.
+    auto first = [&](int c) { return VEC ? (c * kLanes + tid) * 8 : c * 8 * kLanes + tid; };
+    f32x8 s[NC];
+    float sum = 0.0f;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        const int i = first(c);
+        if (i < H) {
+            s[c] = load8<VEC>(xr, false, i, kLanes, H);
+            if (a.residual) s[c] += load8<VEC>(rr, a.res_f32, i, kLanes, H);
+        } else {
+            s[c] = f32x8{0, 0, 0, 0, 0, 0, 0, 0};
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        const int i = first(c);
+        if (a.residual_out && i < H) store8<VEC>(ro, a.res_f32, i, kLanes, H, s[c]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum = fmaf(s[c][e], s[c][e], sum);
+    }
+    sum = wave_sum(sum);
+    if constexpr (WAVES > 1) {
+        __shared__ float part[WAVES];
+        if ((tid & 63) == 0) part[tid >> 6] = sum;
+        __syncthreads();
+        sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) sum += part[w];
+    }
+    const float r = 1.0f / sqrtf(sum / (float)H + a.eps);
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        const int i = first(c);
+        if (i >= H) continue;
+        f32x8 v = load8<VEC>(a.weight, a.weight_f32, i, kLanes, H);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = s[c][e] * r * (a.offset + v[e]);
+        if (a.y) store8<VEC>(a.y + t * a.ldy, false, i, kLanes, H, v);
+        if (a.q) {
+            uint8_t* qr = a.q + t * a.ldq;
+            uint8_t* sr = a.qs + t * a.ldqs;
+            if constexpr (VEC) {
+                // A block of 32 is four lanes' chunks.
+                float m = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) m = fmaxf(m, mx8_finite_abs(v[e]));
+                m = fmaxf(m, dpp<0xB1>(m));
+                m = fmaxf(m, dpp<0x4E>(m));
+                const uint32_t b = mx8_scale_byte(m);
+                const float inv = mx8_inv_scale(b);
+                u32x2 o;
+                o[0] = mx8_pack4(v[0], v[1], v[2], v[3], inv);
+                o[1] = mx8_pack4(v[4], v[5], v[6], v[7], inv);
+                *(u32x2*)(qr + i) = o;
+                if ((tid & 3) == 0) sr[i >> 5] = (uint8_t)b;
+            } else {
+                // A block of 32 is 32 lanes' e-th elements; H % 32 == 0, so a
+                // block is inside the row for all of its lanes or none.
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int k = i + e * kLanes;
+                    float m = mx8_finite_abs(v[e]);
+#pragma unroll
+                    for (int d = 1; d < 32; d *= 2) m = fmaxf(m, __shfl_xor(m, d));
+                    const uint32_t b = mx8_scale_byte(m);
+                    if (k < H) {
+                        qr[k] = (uint8_t)mx8_pack<false>(v[e], v[e], mx8_inv_scale(b), 0u);
+                        if ((tid & 31) == 0) sr[k >> 5] = (uint8_t)b;
+                    }
+                }
+            }
+        }
+    }
+}
+
+template <int WAVES, int NC>
+static void launch(const NormArgs& a, bool vec, hipStream_t s) {
+    const dim3 grid(WAVES == 1 ? (unsigned)((a.T + 3) / 4) : (unsigned)a.T), block(WAVES == 1 ? 256 : WAVES * 64);
+    if (vec) hipLaunchKernelGGL((rms_norm_kernel<WAVES, NC, true>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((rms_norm_kernel<WAVES, NC, false>), grid, block, 0, s, a);
+}
+
+hipError_t launch_rms_norm(const NormArgs& a, hipStream_t s) {
+    auto ok = [](const void* p, int64_t ld, int bytes) {
+        return p == nullptr || ((uintptr_t)p % 16 == 0 && (ld * bytes) % 16 == 0);
+    };
+    const int rb = a.res_f32 ? 4 : 2;
+    const bool vec = a.H % 8 == 0 && ok(a.x, a.ldx, 2) && ok(a.residual, a.ldr, rb) &&
+                     ok(a.residual_out, a.ldro, rb) && ok(a.y, a.ldy, 2) && ok(a.weight, 0, 4) &&
+                     (a.q == nullptr || ((uintptr_t)a.q % 8 == 0 && a.ldq % 8 == 0));
+    // A wave a row when there are rows enough to fill the chip with them, else
+    // four waves a row (a row's latency is what counts then).
+    if (a.H <= 512) launch<1, 1>(a, vec, s);
+    else if (a.T >= 2048 && a.H <= 4096) {
+        if (a.H <= 1024) launch<1, 2>(a, vec, s);
+        else if (a.H <= 2048) launch<1, 4>(a, vec, s);
+        else launch<1, 8>(a, vec, s);
+    } else if (a.H <= 2048) launch<4, 1>(a, vec, s);
+    else if (a.H <= 4096) launch<4, 2>(a, vec, s);
+    else if (a.H <= 8192) launch<4, 4>(a, vec, s);
+    else if (a.H <= 16384) launch<4, 8>(a, vec, s);
+    else if (a.H <= 32768) launch<16, 4>(a, vec, s);
+    else launch<16, 8>(a, vec, s);
+    return hipGetLastError();
+}
+
+}  // namespace moe

@@ -1,0 +1,518 @@
+"""The dense operators around the routed experts against plain fp64 forms
+(MI355X). Tolerances: tests/dense_ref.py."""
+import math
+
+import pytest
+import torch
+
+from tests import dense_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+B8 = 2.0 ** -8   # half a bf16 step, relative
+F24 = 2.0 ** -24
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def moe():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import mxfp4_grouped_gemm_amd as m
+    return m
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def rnd(g, *shape, scale=1.0, dtype=BF):
+    return (torch.randn(*shape, generator=g) * scale).to(dtype)
+
+
+def weight(g, n, k):
+    return rnd(g, n, k, scale=1 / math.sqrt(k))
+
+
+def adapters(g, T, K, N, n, rank, ranks=True, scale=True, runs=False):
+    a = rnd(g, n, rank, K, scale=1 / math.sqrt(K))
+    b = rnd(g, n, N, rank, scale=0.5 / math.sqrt(rank))
+    index = torch.randint(-1, n, (T,), generator=g, dtype=torch.int32)
+    if runs:
+        index = index.sort().values
+    r = torch.randint(0, rank + 1, (n,), generator=g, dtype=torch.int32) if ranks else None
+    s = torch.rand(n, generator=g) + 0.5 if scale else None
+    return a, b, index, r, s
+
+
+def cuda(v):
+    if v is None:
+        return None
+    if isinstance(v, tuple):
+        return tuple(cuda(t) for t in v)
+    return v.cuda()
+
+
+def sum_tol(x, w):
+    """Bound of the fp32 sums of x @ w.T, per element."""
+    return (x.shape[1] / 8 + 64) * F24 * (x.abs() @ w.abs().t())
+
+
+# ------------------------------------------------------------------ norm
+@pytest.mark.parametrize("T,H", [(1, 1), (3, 7), (1, 3584), (5, 33), (2, 64), (4, 1000), (7, 2784), (2050, 520),
+                                 (2049, 1032), (2051, 3584), (3, 4104), (2, 8192), (3, 16384), (2, 20000),
+                                 (1, 65536)])
+@pytest.mark.parametrize("res", [None, BF, F32])
+def test_norm(moe, T, H, res):
+    g = gen(T * 131 + H)
+    x = rnd(g, T, H)
+    r = None if res is None else rnd(g, T, H, scale=3, dtype=res)
+    w = rnd(g, H, dtype=F32 if res == F32 else BF)
+    mx = H % 32 == 0
+    y, ro, q, qs = moe.moe_rms_norm(cuda(x), cuda(w), residual=cuda(r), eps=1e-5, weight_offset=1.0, mxfp8=mx)
+    s, v = ref.norm(x.double(), None if r is None else r.double(), w.double(), 1e-5, 1.0)
+    # fp32: the sum, its root, the quotient and two products, each 2^-24, and
+    # the squares' sum of at most 64 + 10 terms in a row
+    f = 90 * F24
+    # offset + weight cancels where weight is near -1: 2^-24 of the offset
+    k = f * (s / torch.sqrt((s * s).mean(-1, keepdim=True) + 1e-5)).abs()
+    ref.check(y, v, B8 * (1 + 2 ** -7) + f, absolute=float(k.max()), what="y")
+    if r is None:
+        assert ro is None
+    else:
+        ref.check(ro, s, B8 if res == BF else F24, what="residual_out")
+    if mx:
+        qf, sf = q.double().cpu(), qs.double().cpu()
+        want = ref.mx_scale(v)
+        # equal, but where the block's maximum is at the border of two scales
+        amax = v.unflatten(-1, (-1, 32)).abs().amax(-1)
+        border = (ref.mx_scale(v * (1 + 1e-4)) != ref.mx_scale(v * (1 - 1e-4)))
+        assert bool(((sf == want) | border).all()) and float(amax.min()) > 0
+        got = ref.mx_wide(qf, sf)
+        tol = torch.maximum(2.0 ** -4 * v.abs(), 2.0 ** -10 * sf.repeat_interleave(32, -1)) + k + 1e-5 * v.abs()
+        assert bool(((got - v).abs() <= tol).all())
+
+
+def test_norm_in_place_strides_and_rows_behind(moe):
+    g = gen(3)
+    T, H = 5, 96
+    big = rnd(g, 8, H + 40).cuda()
+    res = rnd(g, 8, H + 8, dtype=F32).cuda()
+    keep, keep_r = big.clone(), res.clone()
+    w = rnd(g, H).cuda()
+    x, r = big[1:1 + T, 3:3 + H], res[2:2 + T, :H]  # rows that are not 16-byte aligned
+    s, v = ref.norm(x.double().cpu(), r.double().cpu(), w.double().cpu(), 1e-6, 0.0)
+    q = torch.full((8, H + 5), 77, dtype=torch.uint8, device="cuda")
+    y, ro, _, qs = moe.moe_rms_norm(x, w, residual=r, y=x, residual_out=r, q=q[:T, 1:1 + H], mxfp8=True)
+    assert y.data_ptr() == x.data_ptr() and ro.data_ptr() == r.data_ptr()
+    ref.check(y, v, B8 * 1.01, what="y")
+    ref.check(ro, s, F24, what="residual")
+    got = ref.mx_wide(q[:T, 1:1 + H].view(torch.float8_e4m3fn).double().cpu(), qs.double().cpu())
+    tol = torch.maximum(2.0 ** -4 * v.abs(), 2.0 ** -10 * qs.double().cpu().repeat_interleave(32, -1))
+    assert bool(((got - v).abs() <= tol * 1.001).all())
+    keep[1:1 + T, 3:3 + H] = big[1:1 + T, 3:3 + H]
+    keep_r[2:2 + T, :H] = res[2:2 + T, :H]
+    assert torch.equal(keep, big) and torch.equal(keep_r, res)
+    assert bool((q[T:] == 77).all()) and bool((q[:, 0] == 77).all()) and bool((q[:, 1 + H:] == 77).all())
+
+
+def test_norm_special_values(moe):
+    H = 64
+    x = torch.zeros(6, H)
+    x[1] = 1e-30        # squares vanish next to eps
+    x[2, 5] = math.nan  # the row, and only the row
+    x[3, 40] = math.inf
+    x[4] = 3e38
+    x[5] = 2.0
+    w = torch.ones(H)
+    w[33] = math.nan    # one element of every row, not its block
+    y, _, q, qs = moe.moe_rms_norm(x.bfloat16().cuda(), w.cuda(), eps=1e-6, mxfp8=True)
+    y, q, qs = y.float().cpu(), q.float().cpu(), qs.float().cpu()
+    other = torch.arange(H) != 33
+    assert bool(y[:, 33].isnan().all()) and bool(q[:, 33].isnan().all())
+    assert bool((y[0][other] == 0).all()) and bool((q[0][other] == 0).all())
+    assert float(qs[0, 0]) == 2.0 ** -127
+    assert bool(y[2].isnan().all()) and bool(q[2].isnan().all())
+    assert bool(y[3][other & (torch.arange(H) != 40)].eq(0).all()) and bool(y[3, 40].isnan())
+    assert bool(y[4][other].eq(0).all())  # the squares overflow: s / inf
+    assert bool((y[5][other] == 1).all())
+    assert bool((q[5][other] * qs[5].repeat_interleave(32)[other] == 1).all())
+
+
+# ---------------------------------------------------------------- linear
+LINEAR = [(1, 8, 8), (1, 3584, 112), (3, 72, 40), (16, 520, 1000), (17, 136, 24), (33, 3584, 384), (64, 64, 72),
+          (65, 72, 136), (130, 1000, 520), (300, 3584, 896), (777, 264, 1032), (2100, 192, 4104)]
+
+
+@pytest.mark.parametrize("T,K,N", LINEAR)
+def test_linear(moe, T, K, N):
+    g = gen(T + K + N)
+    x, w = rnd(g, T, K), weight(g, N, K)
+    want = x.double() @ w.double().t()
+    tol = sum_tol(x.double(), w.double())
+    got = moe.moe_lora_linear(cuda(x), cuda(w), out_dtype=F32)
+    assert got.dtype == F32
+    assert bool(((got.double().cpu() - want).abs() <= tol).all())
+    got = moe.moe_lora_linear(cuda(x), cuda(w))
+    assert bool(((got.double().cpu() - want).abs() <= tol * 1.01 + B8 * want.abs()).all())
+
+
+@pytest.mark.parametrize("T,K,N", LINEAR)
+@pytest.mark.parametrize("n,rank,runs", [(1, 8, False), (5, 40, True), (40, 16, False)])
+def test_linear_adapters(moe, T, K, N, n, rank, runs):
+    g = gen(T + K + N + n)
+    x, w = rnd(g, T, K), weight(g, N, K)
+    lo = adapters(g, T, K, N, n, rank, runs=runs)
+    # what lies beyond an adapter's rank is never read as numbers
+    for i in range(n):
+        lo[0][i, int(lo[3][i]):] = math.nan
+        lo[1][i, :, int(lo[3][i]):] = math.inf
+    xd = x.double()
+    want = xd @ w.double().t() + ref.lora(xd, lo)
+    # the narrow product's sum, and two bf16 halves of v: 2^-16 of |B| |v|
+    wide = tuple(t if t is None or not t.is_floating_point() else torch.nan_to_num(t.double(), 0, 0, 0).abs() for t in lo)
+    extra = ref.lora(xd.abs(), wide)
+    tol = sum_tol(xd, w.double()) + extra * (2.0 ** -16 + (K / 8 + 128) * F24)
+    got = moe.moe_lora_linear(cuda(x), cuda(w), lora=cuda(lo), out_dtype=F32)
+    assert bool(((got.double().cpu() - want).abs() <= tol).all())
+    got = moe.moe_lora_linear(cuda(x), cuda(w), lora=moe.LoraAdapters(*cuda(lo)))
+    assert bool(((got.double().cpu() - want).abs() <= tol * 1.01 + B8 * want.abs()).all())
+
+
+@pytest.mark.parametrize("T", [9, 200])
+def test_linear_tokens_do_not_meet(moe, T):
+    """A NaN in one token, or in one adapter, stays with its tokens."""
+    g = gen(T)
+    K, N, n = 136, 72, 3
+    x, w = rnd(g, T, K), weight(g, N, K)
+    lo = adapters(g, T, K, N, n, 16, ranks=False, scale=False)
+    clean = moe.moe_lora_linear(cuda(x), cuda(w), lora=cuda(lo))
+    x[4, 7] = math.nan
+    lo[0][1, 3, 5] = math.inf
+    lo[1][1, 2, 3] = math.nan
+    got = moe.moe_lora_linear(cuda(x), cuda(w), lora=cuda(lo))
+    hit = (lo[2] == 1) | (torch.arange(T) == 4)
+    assert torch.equal(got[~hit.cuda()], clean[~hit.cuda()])
+    assert bool(got[4].isnan().all())
+
+
+@pytest.mark.parametrize("T", [5, 70, 300])
+def test_linear_index_outside_and_defaults(moe, T):
+    g = gen(T)
+    K, N, n = 64, 96, 4
+    x, w = rnd(g, T, K), weight(g, N, K)
+    lo = list(adapters(g, T, K, N, n, 8, ranks=False, scale=False))
+    plain = moe.moe_lora_linear(cuda(x), cuda(w))
+    for bad in (-1, n, 2 ** 31 - 1, -2 ** 31):
+        lo[2] = torch.full((T,), bad, dtype=torch.int32)
+        assert torch.equal(moe.moe_lora_linear(cuda(x), cuda(w), lora=cuda(tuple(lo))), plain)
+    lo[2] = torch.full((T,), 2, dtype=torch.int32)
+    lo[3] = torch.tensor([8, 8, 1000, 8], dtype=torch.int32)  # clamped to the stack's rank
+    a = moe.moe_lora_linear(cuda(x), cuda(w), lora=cuda(tuple(lo)))
+    lo[3] = None
+    assert torch.equal(a, moe.moe_lora_linear(cuda(x), cuda(w), lora=cuda(tuple(lo))))
+
+
+@pytest.mark.parametrize("T", [6, 90, 260])
+def test_linear_strides_and_rows_behind(moe, T):
+    g = gen(T)
+    K, N = 72, 40
+    xb, w = rnd(g, T + 2, K + 24), weight(g, N, K)
+    out = torch.full((T + 3, N + 16), 5.0, dtype=F32, device="cuda")
+    x = cuda(xb)[1:1 + T, 8:8 + K]
+    moe.moe_lora_linear(x, cuda(w), out=out[:T, 8:8 + N])
+    want = xb[1:1 + T, 8:8 + K].double() @ w.double().t()
+    tol = sum_tol(xb[1:1 + T, 8:8 + K].double(), w.double())
+    assert bool(((out[:T, 8:8 + N].double().cpu() - want).abs() <= tol).all())
+    assert bool((out[T:] == 5).all()) and bool((out[:, :8] == 5).all()) and bool((out[:, 8 + N:] == 5).all())
+
+
+# ------------------------------------------------------------------- ffn
+FFN = [(1, 8, 8), (1, 3584, 384), (2, 40, 72), (16, 520, 136), (17, 264, 1000), (37, 3584, 128), (64, 96, 64),
+       (65, 136, 72), (129, 520, 264), (300, 1032, 1000), (1030, 264, 392), (2200, 136, 2056)]
+
+
+@pytest.mark.parametrize("T,H,I", FFN)
+@pytest.mark.parametrize("lora", [False, True])
+def test_ffn_forward(moe, T, H, I, lora):
+    g = gen(T + H + I)
+    x, w13, w2, add = rnd(g, T, H), weight(g, 2 * I, H), weight(g, H, I), rnd(g, T, H)
+    l13 = adapters(g, T, H, 2 * I, 6, 24) if lora else None
+    l2 = adapters(g, T, I, H, 6, 16) if lora else None
+    want, gu, h = ref.ffn(x.double(), w13.double(), w2.double(), add.double(), l13, l2)
+    step = ref.step_tol(h, w2.double())
+    got, saved = moe.moe_ffn_forward(cuda(x), cuda(w13), cuda(w2), addend=cuda(add), lora13=cuda(l13),
+                                     lora2=cuda(l2), save_gate_up=True)
+    ref.check(saved, gu, B8, rms=1e-4, what="gate_up")
+    ref.check(got, want, B8, rms=ref.FLIPS, absolute=step, what="out", norm=ref.NORM)
+    assert torch.equal(moe.moe_ffn_forward(cuda(x), cuda(w13), cuda(w2), addend=cuda(add), lora13=cuda(l13),
+                                           lora2=cuda(l2)), got)
+    if not lora:
+        want, _, _ = ref.ffn(x.double(), w13.double(), w2.double())
+        ref.check(moe.moe_ffn_forward(cuda(x), cuda(w13), cuda(w2)), want, B8, rms=ref.FLIPS, absolute=step,
+                  what="no addend", norm=ref.NORM)
+
+
+@pytest.mark.parametrize("T,H,I", [(1, 32, 32), (1, 3584, 384), (5, 96, 160), (16, 544, 128), (20, 128, 1024),
+                                   (40, 256, 96), (64, 1056, 64), (65, 96, 160), (130, 544, 288), (300, 1024, 1056),
+                                   (1030, 288, 384), (2200, 160, 2080)])
+def test_ffn_forward_mxfp8(moe, T, H, I):
+    g = gen(T + H + I)
+    mats = []
+    for n, k, s in ((T, H, 1.0), (2 * I, H, 1 / math.sqrt(H)), (H, I, 1 / math.sqrt(I))):
+        q, sc = ref.mx_quant(rnd(g, n, k, scale=s).double())
+        mats += [q.float().to(torch.float8_e4m3fn), sc.float().to(torch.float8_e8m0fnu)]
+    add = rnd(g, T, H)
+    x, w13, w2 = (ref.mx_wide(mats[i].float(), mats[i + 1].float()) for i in (0, 2, 4))
+    gu = x @ w13.t()
+    h = ref.mx_wide(*ref.mx_quant(ref.silu(gu[:, :I]) * gu[:, I:]))
+    want = h @ w2.t()
+    dev = [cuda(m) for m in mats]
+    got = moe.moe_ffn_forward_mxfp8(*dev, addend=cuda(add))
+    step = ref.step_tol(h, w2, 2.0 ** -3)
+    ref.check(got, want + add.double(), B8, rms=ref.MXFLIPS, absolute=step, what="out", norm=ref.MXNORM)
+    as_bytes = [m.view(torch.uint8) for m in dev]
+    ref.check(moe.moe_ffn_forward_mxfp8(*as_bytes), want, B8, rms=ref.MXFLIPS, absolute=step, what="no addend",
+              norm=ref.MXNORM)
+
+
+def test_ffn_addend_in_place_and_strides(moe):
+    g = gen(11)
+    for T in (3, 100, 280):
+        H, I = 136, 72
+        x, w13, w2 = rnd(g, T, H + 8), weight(g, 2 * I, H), weight(g, H, I)
+        buf = rnd(g, T + 2, H + 32)
+        want, _, h = ref.ffn(x[:, 8:].double(), w13.double(), w2.double(), buf[:T, 16:16 + H].double())
+        b = cuda(buf)
+        moe.moe_ffn_forward(cuda(x)[:, 8:], cuda(w13), cuda(w2), addend=b[:T, 16:16 + H], out=b[:T, 16:16 + H])
+        ref.check(b[:T, 16:16 + H], want, B8, rms=ref.FLIPS, absolute=ref.step_tol(h, w2.double()), what="out")
+        after = b.cpu()
+        after[:T, 16:16 + H] = buf[:T, 16:16 + H]
+        assert torch.equal(after, buf)
+
+
+@pytest.mark.parametrize("T", [3, 200])
+def test_ffn_tokens_do_not_meet(moe, T):
+    g = gen(T)
+    H, I = 72, 264
+    x, w13, w2 = rnd(g, T, H), weight(g, 2 * I, H), weight(g, H, I)
+    clean = moe.moe_ffn_forward(cuda(x), cuda(w13), cuda(w2))
+    x[1, 9] = math.inf
+    got = moe.moe_ffn_forward(cuda(x), cuda(w13), cuda(w2))
+    rows = torch.arange(T, device="cuda") != 1
+    assert torch.equal(got[rows], clean[rows]) and not bool(torch.isfinite(got[1]).any())
+
+
+# -------------------------------------------------------------- backward
+@pytest.mark.parametrize("T,H,I", [(1, 8, 8), (2, 40, 72), (16, 520, 136), (63, 264, 1000), (64, 96, 64), (65, 136, 72),
+                                   (129, 520, 264), (300, 1032, 520), (777, 264, 392), (2200, 1032, 2056)])
+def test_ffn_backward(moe, T, H, I):
+    g = gen(T + H + I)
+    dout, x, gu = rnd(g, T, H), rnd(g, T, H), rnd(g, T, 2 * I)
+    w13, w2 = weight(g, 2 * I, H), weight(g, H, I)
+    want, steps = ref.ffn_backward(*(t.double() for t in (dout, x, gu, w13, w2)))
+    got = moe.moe_ffn_backward(*(cuda(t) for t in (dout, x, gu, w13, w2)))
+    for name, a, b, st in zip(("dx", "dw13", "dw2"), got, want, steps):
+        ref.check(a, b, B8, rms=ref.FLIPS, absolute=st, what=name, norm=ref.NORM)
+    again = moe.moe_ffn_backward(*(cuda(t) for t in (dout, x, gu, w13, w2)))
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+    # each gradient alone is the same
+    for k in range(3):
+        need = [i == k for i in range(3)]
+        one = moe.moe_ffn_backward(*(cuda(t) for t in (dout, x, gu, w13, w2)), *need)
+        assert [t is not None for t in one] == need and torch.equal(one[k], got[k])
+
+
+def test_ffn_backward_of_no_tokens(moe):
+    H, I = 64, 96
+    e = torch.empty(0, H, dtype=BF, device="cuda")
+    w13, w2 = torch.ones(2 * I, H, dtype=BF, device="cuda"), torch.ones(H, I, dtype=BF, device="cuda")
+    d13, d2 = torch.full_like(w13, math.nan), torch.full_like(w2, math.nan)
+    dx, _, _ = moe.moe_ffn_backward(e, e, torch.empty(0, 2 * I, dtype=BF, device="cuda"), w13, w2, dw13=d13, dw2=d2)
+    assert dx.shape == (0, H) and not bool(d13.any()) and not bool(d2.any())
+
+
+@pytest.mark.parametrize("T", [4, 150])
+def test_moe_ffn_gradients(moe, T):
+    """The differentiable form against the formula and against differences of
+    the fp64 forward."""
+    g = gen(T)
+    H, I = 136, 200
+    x, w13, w2, add = rnd(g, T, H), weight(g, 2 * I, H), weight(g, H, I), rnd(g, T, H)
+    leaves = [cuda(t).requires_grad_() for t in (x, w13, w2, add)]
+    out = moe.moe_ffn(*leaves)
+    probe = rnd(g, T, H)
+    out.backward(cuda(probe))
+    d = [t.double() for t in (x, w13, w2, add)]
+    gu = moe.moe_ffn_forward(*(t.detach() for t in leaves[:3]), save_gate_up=True)[1].double().cpu()
+    want, steps = ref.ffn_backward(probe.double(), d[0], gu, d[1], d[2])
+    for name, leaf, b, st in zip(("dx", "dw13", "dw2"), leaves, want, steps):
+        ref.check(leaf.grad, b, B8, rms=ref.FLIPS, absolute=st, what=name, norm=ref.NORM)
+    assert torch.equal(leaves[3].grad.cpu(), probe)
+
+    def loss(x, w13, w2, add):
+        gu = x @ w13.t()
+        return float((((ref.silu(gu[:, :I]) * gu[:, I:]) @ w2.t() + add) * probe.double()).sum())
+
+    for k, leaf in enumerate(leaves):
+        step = rnd(g, *leaf.shape, dtype=torch.float64)
+        e = 1e-5
+        plus, minus = list(d), list(d)
+        plus[k], minus[k] = d[k] + e * step, d[k] - e * step
+        slope = (loss(*plus) - loss(*minus)) / (2 * e)
+        grad = leaf.grad.double().cpu()
+        # Each element of the gradient is off by at most about three bf16
+        # roundings (saved gate_up, operand, result); over a random direction
+        # they add like independent errors of 3 * 2^-8: six of their sums.
+        tol = 6 * 3 * B8 * float((grad * step).square().sum().sqrt())
+        assert abs(float((grad * step).sum()) - slope) <= tol, (k, slope)
+
+
+def test_moe_ffn_partial_and_expanded_gradients(moe):
+    g = gen(8)
+    T, H, I = 20, 64, 96
+    x, w13, w2 = cuda(rnd(g, T, H)), cuda(weight(g, 2 * I, H)), cuda(weight(g, H, I))
+    xr = x.clone().requires_grad_()
+    moe.moe_ffn(xr, w13, w2).sum().backward()  # the gradient is one expanded value
+    _, gu = moe.moe_ffn_forward(x, w13, w2, save_gate_up=True)
+    dx, _, _ = moe.moe_ffn_backward(torch.ones(T, H, dtype=BF, device="cuda"), x, gu, w13, w2)
+    assert torch.equal(xr.grad, dx)
+    assert not moe.moe_ffn(x, w13, w2).requires_grad
+    a = torch.zeros(T, H, dtype=BF, device="cuda", requires_grad=True)
+    moe.moe_ffn(x, w13, w2, a).sum().backward()
+    assert bool((a.grad == 1).all())
+    # a leaf used twice
+    w = w2.clone().requires_grad_()
+    (moe.moe_ffn(x, w13, w) + moe.moe_ffn(x, w13, w)).sum().backward()
+    v = w2.clone().requires_grad_()
+    moe.moe_ffn(x, w13, v).sum().backward()
+    assert torch.equal(w.grad, v.grad + v.grad)
+
+
+# ------------------------------------------------------------- a block
+def _experts(moe, H, I, E, seed):
+    g = gen(seed)
+    def u8(*s, lo=0, hi=256):
+        return torch.randint(lo, hi, s, generator=g, dtype=torch.int32).to(torch.uint8).cuda()
+    return (u8(E, 2 * I, H // 2), u8(E, 2 * I, H // 32, lo=118, hi=124), u8(E, H, I // 2),
+            u8(E, H, I // 32, lo=118, hi=124))
+
+
+@pytest.mark.parametrize("T", [1, 5, 70])
+@pytest.mark.parametrize("shared", ["none", "bf16", "lora", "mxfp8"])
+def test_block(moe, T, shared):
+    """norm -> router -> routed experts + shared expert, against the steps."""
+    H, I, E, k = 256, 128, 8, 2
+    g = gen(T)
+    x, res, nw = cuda(rnd(g, T, H)), cuda(rnd(g, T, H, dtype=F32)), cuda(rnd(g, H))
+    rw = cuda(weight(g, E, H))
+    ex = _experts(moe, H, I, E, T)
+    w13, w2 = weight(g, 2 * I, H), weight(g, H, I)
+    kw = {}
+    if shared in ("bf16", "lora"):
+        kw["shared"] = (cuda(w13), cuda(w2))
+    if shared == "lora":
+        kw["lora13"], kw["lora2"] = cuda(adapters(g, T, H, 2 * I, 3, 16)), cuda(adapters(g, T, I, H, 3, 8))
+    if shared == "mxfp8":
+        mx = []
+        for m in (w13, w2):
+            q, s = ref.mx_quant(m.double())
+            mx += [cuda(q.float().to(torch.float8_e4m3fn)), cuda(s.float().to(torch.float8_e8m0fnu))]
+        kw["shared_mxfp8"] = tuple(mx)
+    out, new_res = moe.moe_a16w4_block(x, nw, rw, *ex, k, residual=res, eps=1e-5, **kw)
+    y, ro, q, qs = moe.moe_rms_norm(x, nw, residual=res, eps=1e-5, mxfp8=True)
+    s, v = ref.norm(x.double().cpu(), res.double().cpu(), nw.double().cpu(), 1e-5, 0.0)
+    ref.check(y, v, B8 * 1.01, what="y")
+    assert torch.equal(new_res, ro)
+    logits = moe.moe_lora_linear(y, rw, out_dtype=F32)
+    routed = moe.moe_a16w4_layer(y, logits, *ex, k)
+    if shared == "none":
+        assert torch.equal(out, routed)
+        return
+    yd, rd = y.double().cpu(), routed.double().cpu()
+    if shared == "mxfp8":
+        gu = ref.mx_wide(q.double().cpu(), qs.double().cpu()) @ ref.mx_wide(mx[0].double().cpu(), mx[1].double().cpu()).t()
+        h = ref.mx_wide(*ref.mx_quant(ref.silu(gu[:, :I]) * gu[:, I:]))
+        wide2 = ref.mx_wide(mx[2].double().cpu(), mx[3].double().cpu())
+        ref.check(out, h @ wide2.t() + rd, B8, rms=ref.MXFLIPS, absolute=ref.step_tol(h, wide2, 2.0 ** -3), what="out")
+    else:
+        want, _, h = ref.ffn(yd, w13.double(), w2.double(), rd, kw.get("lora13"), kw.get("lora2"))
+        ref.check(out, want, B8, rms=ref.FLIPS, absolute=ref.step_tol(h, w2.double()), what="out")
+
+
+# ---------------------------------------------- streams, graphs, two at once
+def test_block_in_a_graph(moe):
+    """Captured once and replayed, with new inputs and eager work between the
+    replays; a second graph has its own workspaces."""
+    H, I, E, k, T = 256, 128, 8, 2, 70
+    g = gen(1)
+    nw, rw, ex = cuda(rnd(g, H)), cuda(weight(g, E, H)), _experts(moe, H, I, E, 1)
+    sh = (cuda(weight(g, 2 * I, H)), cuda(weight(g, H, I)))
+    lo = cuda(adapters(g, T, H, 2 * I, 3, 16))
+
+    def step(x, res):
+        return moe.moe_a16w4_block(x, nw, rw, *ex, k, residual=res, shared=sh, lora13=lo)
+
+    xs = [cuda(rnd(g, T, H)) for _ in range(4)]
+    rs = [cuda(rnd(g, T, H, dtype=F32)) for _ in range(4)]
+    want = [step(x, r) for x, r in zip(xs, rs)]
+    graphs = []
+    for _ in range(2):
+        x, r = xs[0].clone(), rs[0].clone()
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            step(x, r)
+        torch.cuda.current_stream().wait_stream(side)
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            o = step(x, r)
+        graphs.append((gr, x, r, o))
+    for i in (1, 2, 3, 0):
+        for gr, x, r, o in graphs:
+            x.copy_(xs[i])
+            r.copy_(rs[i])
+            gr.replay()
+        again = step(xs[i], rs[i])
+        torch.cuda.synchronize()
+        for _, _, _, o in graphs:
+            assert torch.equal(o[0], want[i][0]) and torch.equal(o[1], want[i][1])
+        assert torch.equal(again[0], want[i][0])
+
+
+def test_backward_in_a_graph(moe):
+    g = gen(2)
+    T, H, I = 130, 136, 264
+    dout, x, gu = cuda(rnd(g, T, H)), cuda(rnd(g, T, H)), cuda(rnd(g, T, 2 * I))
+    w13, w2 = cuda(weight(g, 2 * I, H)), cuda(weight(g, H, I))
+    ws = torch.empty(moe.moe_ffn_backward_workspace_size(T, H, I), dtype=torch.uint8, device="cuda")
+    moe.moe_ffn_backward(dout, x, gu, w13, w2, workspace=ws)
+    torch.cuda.synchronize()
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        o = moe.moe_ffn_backward(dout, x, gu, w13, w2, workspace=ws)
+    for k in range(3):
+        dout.copy_(cuda(rnd(g, T, H)))
+        ws.fill_(k * 85)
+        gr.replay()
+        torch.cuda.synchronize()
+        want = moe.moe_ffn_backward(dout, x, gu, w13, w2)
+        assert all(torch.equal(a, b) for a, b in zip(o, want))
+
+
+def test_two_streams_at_once(moe):
+    g = gen(5)
+    T, H, I = 300, 264, 392
+    x = [cuda(rnd(g, T, H)) for _ in range(2)]
+    w13, w2 = cuda(weight(g, 2 * I, H)), cuda(weight(g, H, I))
+    lo = [cuda(adapters(g, T, H, 2 * I, 4, 16)) for _ in range(2)]
+    want = [moe.moe_ffn_forward(x[i], w13, w2, lora13=lo[i]) for i in range(2)]
+    torch.cuda.synchronize()
+    st = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(8):
+        for i in range(2):
+            got[i].append(moe.moe_ffn_forward(x[i], w13, w2, lora13=lo[i], stream=st[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(t, want[i]) for t in got[i])
