@@ -48,6 +48,20 @@ __device__ __forceinline__ void load_lds16(rsrc_t r, uint8_t* dst, uint32_t voff
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)dst, 16, voff, soff, 0, 0);
 }
 
+// Asks the scheduler to spread READS LDS reads and LOADS loads evenly over
+// MFMAS matrix instructions.
+template <int READS, int LOADS, int MFMAS, int I = 0>
+__device__ __forceinline__ void spread() {
+    if constexpr (I < READS) {
+        constexpr int loads = LOADS * (I + 1) / READS - LOADS * I / READS;
+        constexpr int mfmas = MFMAS * (I + 1) / READS - MFMAS * I / READS;
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        if constexpr (loads > 0) __builtin_amdgcn_sched_group_barrier(0x20, loads, 0);
+        if constexpr (mfmas > 0) __builtin_amdgcn_sched_group_barrier(0x8, mfmas, 0);
+        spread<READS, LOADS, MFMAS, I + 1>();
+    }
+}
+
 // e^x / (1 + e^x) and friends with the accurate expf: the epilogue runs once
 // per output.
 __device__ __forceinline__ float sigmoid(float g) { return 1.0f / (1.0f + expf(-g)); }
@@ -75,7 +89,7 @@ struct Tile {
 __device__ __forceinline__ int key_x(int r) { return (r >> 1) & 7; }
 template <int F>
 __device__ __forceinline__ int key_w(int r) {
-    constexpr int s = F == 4 ? 4 : F == 2 ? 3 : 2;
+    constexpr int s = F == 8 ? 5 : F == 4 ? 4 : F == 2 ? 3 : 2;
     return ((r >> 1) & 1) | (((r >> s) & 3) << 1);
 }
 __device__ __forceinline__ int key_t(int k) { return 2 * ((k & 3) | (((k >> 3) & 1) << 2)); }
@@ -173,7 +187,7 @@ __device__ __forceinline__ void lora_accumulate(const LoraArgs& l, int64_t brows
 }
 
 template <class C>
-__global__ __launch_bounds__(C::THREADS, C::THREADS == 256 ? 1 : 2) void dense_kernel(DenseArgs a) {
+__global__ __launch_bounds__(C::THREADS, 2) void dense_kernel(DenseArgs a) {
     __shared__ __align__(1024) uint8_t s0[C::BUF];
     __shared__ __align__(1024) uint8_t s1[C::BUF];
     const int tid = (int)threadIdx.x, lane = tid & 63;
@@ -207,18 +221,26 @@ __global__ __launch_bounds__(C::THREADS, C::THREADS == 256 ? 1 : 2) void dense_k
     const char* xb = (const char*)a.x + (C::XT ? (int64_t)m0 : (int64_t)m0 * a.ldx) * C::ESZ;
     const char* wb = (const char*)a.w + (C::WT ? (int64_t)n0 : (int64_t)n0 * a.ldw) * C::ESZ;
     uint32_t xo[C::XL], wo[C::WL];
-    int xk[C::XL], wk[C::WL];  // K of the piece in its step (elements)
+    // K of a piece in its step (elements).
+    auto xk = [&](int i) {
+        const int p = (w * C::XL + i) * 64 + lane;
+        if constexpr (C::XT) return (w * C::XL * 64 + lane) / (C::BM / 8) + i * 64 / (C::BM / 8);
+        else return ((p & 7) ^ key_x(p >> 3)) * (16 / C::ESZ);
+    };
+    auto wk = [&](int i) {
+        const int p = (w * C::WL + i) * 64 + lane;
+        if constexpr (C::WT) return (w * C::WL * 64 + lane) / (C::BN / 8) + i * 64 / (C::BN / 8);
+        else return ((p & 7) ^ key_w<C::F>(p >> 3)) * (16 / C::ESZ);
+    };
 #pragma unroll
     for (int i = 0; i < C::XL; ++i) {
         const int p = (w * C::XL + i) * 64 + lane;  // piece of the tile
         if constexpr (C::XT) {
             constexpr int PR = C::BM / 8;  // pieces a row
             const int k = p / PR, c = (p % PR) ^ key_t(k);
-            xk[i] = k;
             xo[i] = m0 + c * 8 < a.M ? (uint32_t)(k * a.ldx * 2 + c * 16) : kOob;
         } else {
             const int r = p >> 3, c = (p & 7) ^ key_x(r);
-            xk[i] = c * (16 / C::ESZ);
             xo[i] = m0 + r < a.M ? (uint32_t)(r * a.ldx * C::ESZ + c * 16) : kOob;
         }
     }
@@ -228,11 +250,9 @@ __global__ __launch_bounds__(C::THREADS, C::THREADS == 256 ? 1 : 2) void dense_k
         if constexpr (C::WT) {
             constexpr int PR = C::BN / 8;
             const int k = p / PR, c = (p % PR) ^ key_t(k);
-            wk[i] = k;
             wo[i] = n0 + c * 8 < a.N ? (uint32_t)(k * a.ldw * 2 + c * 16) : kOob;
         } else {
             const int r = p >> 3, c = (p & 7) ^ key_w<C::F>(r);
-            wk[i] = c * (16 / C::ESZ);
             if constexpr (C::GATED) {
                 // Rows [0, BNC) of the tile are gate rows, the others the up
                 // rows, N rows further on: their own base (wo is 32 bits).
@@ -245,62 +265,66 @@ __global__ __launch_bounds__(C::THREADS, C::THREADS == 256 ? 1 : 2) void dense_k
     }
     const int64_t up = C::GATED ? (int64_t)a.N * a.ldw * C::ESZ : 0;
 
+    const int kend = C::SPLIT && kt1 < steps ? kt1 * C::BK : a.K;
+    // Loads of step kt into a buffer. Pieces past the end of K (all of them
+    // for a step past the end) get out-of-range offsets: zeros, no traffic.
     auto issue = [&](uint8_t* buf, int kt) {
-        const bool tail = (kt + 1) * C::BK > a.K;
         const rsrc_t rx = make_rsrc(xb + (C::XT ? (int64_t)kt * C::BK * a.ldx * 2 : (int64_t)kt * kRowBytes), kRecord);
         const int64_t wadv = C::WT ? (int64_t)kt * C::BK * a.ldw * 2 : (int64_t)kt * kRowBytes;
         const rsrc_t rw = make_rsrc(wb + wadv, kRecord);
         const rsrc_t ru = make_rsrc(wb + wadv + up, kRecord);
-        const int left = a.K - kt * C::BK;
+        const int left = kend - kt * C::BK;
 #pragma unroll
         for (int i = 0; i < C::XL; ++i)
-            load_lds16(rx, buf + (w * C::XL + i) * 1024, tail && xk[i] >= left ? kOob : xo[i], 0);
+            load_lds16(rx, buf + (w * C::XL + i) * 1024, xk(i) < left ? xo[i] : kOob, 0);
 #pragma unroll
         for (int i = 0; i < C::WL; ++i) {
             const bool second = C::GATED && (w * C::WL + i) * 8 >= C::BNC;  // 8 rows a load: uniform
-            load_lds16(second ? ru : rw, buf + C::XBYTES + (w * C::WL + i) * 1024,
-                       tail && wk[i] >= left ? kOob : wo[i], 0);
+            load_lds16(second ? ru : rw, buf + C::XBYTES + (w * C::WL + i) * 1024, wk(i) < left ? wo[i] : kOob, 0);
         }
     };
 
-    // MXFP8 scales: thread t carries row t's four bytes of a step (and row
-    // t + THREADS's), in registers until its buffer is free.
-    constexpr int SR = C::ELT == kEltMx8 ? (C::BM + C::BN + C::THREADS - 1) / C::THREADS : 0;
-    uint32_t sv[SR > 0 ? SR : 1];
+    // MXFP8 scales: a thread carries the four bytes of one row's step, rows of
+    // X and then of W, through a register (a wave's rows share their base).
+    static_assert(C::ELT != kEltMx8 || C::BM + C::BN == C::THREADS, "one row of scales a thread");
+    // Rows of K / 32 bytes need not be aligned: the bytes of a step come from
+    // the one or two aligned words that hold them.
+    uint32_t slo = 0, shi = 0, so = 0;
+    bool srow = false;
     const int kb = a.K / 32;
+    const uint8_t* sbase = nullptr;
+    if constexpr (C::ELT == kEltMx8) {
+        const int r = w * 64;
+        int64_t first;
+        if (r < C::BM) {
+            first = (int64_t)(m0 + r) * kb;
+            sbase = a.xs;
+            srow = m0 + r + lane < a.M;
+        } else {
+            const int rw = r - C::BM, col = n0 + (C::GATED ? rw % C::BNC : rw);
+            first = (int64_t)(col + (C::GATED && rw >= C::BNC ? a.N : 0)) * kb;
+            sbase = a.ws;
+            srow = col + lane < a.N;
+        }
+        sbase += first & ~(int64_t)3;
+        so = (uint32_t)(first & 3) + (uint32_t)(lane * kb);
+    }
     auto load_scales = [&](int kt) {
         if constexpr (C::ELT == kEltMx8) {
-#pragma unroll
-            for (int i = 0; i < SR; ++i) {
-                const int r = tid + i * C::THREADS;
-                const uint8_t* p = nullptr;
-                if (r < C::BM) {
-                    if (m0 + r < a.M) p = a.xs + (int64_t)(m0 + r) * kb;
-                } else if (r < C::BM + C::BN) {
-                    const int rw = r - C::BM, col = C::GATED ? rw % C::BNC : rw;
-                    if (n0 + col < a.N) p = a.ws + (int64_t)(n0 + col + (C::GATED && rw >= C::BNC ? a.N : 0)) * kb;
-                }
-                uint32_t v = 0;
-                if (p) {
-                    if (kb % 4 == 0) {
-                        v = *(const uint32_t*)(p + kt * 4);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (kt * 4 + e < kb) v |= (uint32_t)p[kt * 4 + e] << (8 * e);
-                    }
-                }
-                sv[i] = v;
-            }
+            const rsrc_t rs = make_rsrc(sbase + (int64_t)kt * 4, kRecord);
+            const int left = kb - kt * 4;  // bytes of the row from this step on
+            const int in_word = (int)(so & 3);
+            slo = __builtin_amdgcn_raw_buffer_load_b32(rs, srow && left > 0 ? so & ~3u : kOob, 0, 0);
+            shi = __builtin_amdgcn_raw_buffer_load_b32(rs, srow && in_word > 0 && left + in_word > 4 ? (so & ~3u) + 4 : kOob, 0, 0);
         }
     };
-    auto store_scales = [&](uint8_t* buf) {
+    // Bytes past K get scale 2^-127 (their codes are zeros; a byte of the next
+    // row could be the NaN scale).
+    auto store_scales = [&](uint8_t* buf, int kt) {
         if constexpr (C::ELT == kEltMx8) {
-#pragma unroll
-            for (int i = 0; i < SR; ++i) {
-                const int r = tid + i * C::THREADS;
-                if (r < C::BM + C::BN) *(uint32_t*)(buf + C::XBYTES + C::WBYTES + r * 4) = sv[i];
-            }
+            const int left = kb - kt * 4;
+            const uint32_t keep = left >= 4 ? 0xffffffffu : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
+            *(uint32_t*)(buf + C::XBYTES + C::WBYTES + tid * 4) = __builtin_amdgcn_alignbyte(shi, slo, so & 3) & keep;
         }
     };
 
@@ -338,71 +362,128 @@ __global__ __launch_bounds__(C::THREADS, C::THREADS == 256 ? 1 : 2) void dense_k
         return __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7);
     };
 
-    auto compute = [&](const uint8_t* buf) {
-        if constexpr (C::ELT == kEltBf16) {
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                bf16x8 xf[C::FM], wf[C::FN];
-#pragma unroll
-                for (int f = 0; f < C::FN; ++f) {
-                    if constexpr (C::WT) wf[f] = read_t(buf + C::XBYTES, C::BN * 2, (wn * C::FN + f) * 16, s);
-                    else wf[f] = __builtin_bit_cast(bf16x8, read_w(buf, f, 4 * s + g));
-                }
-#pragma unroll
-                for (int f = 0; f < C::FM; ++f) {
-                    if constexpr (C::XT) xf[f] = read_t(buf, C::BM * 2, xr0 + f * 16, s);
-                    else xf[f] = __builtin_bit_cast(bf16x8, read_x(buf, f, 4 * s + g));
-                }
-#pragma unroll
-                for (int j = 0; j < C::FM; ++j)
-#pragma unroll
-                    for (int i = 0; i < C::FN; ++i) acc[i][j] = mfma16x16x32(wf[i], xf[j], acc[i][j]);
-            }
-        } else {
-            // A lane's 32 elements are pieces g and 4 + g; its scale operand
-            // is that of block g of the step.
-            const uint8_t* sc = buf + C::XBYTES + C::WBYTES;
-            i32x8 wf[C::FN];
-            int wsc[C::FN];
+    if constexpr (C::ELT == kEltBf16) {
+        // A step is four phases, (K half s, half h of the wave's rows of X),
+        // and while the MFMAs of one run, the operands of the next are read.
+        // The step's one barrier sits before its last phase: there the reads
+        // of this step's buffer are done and the next step's loads have
+        // landed, so the buffer takes the loads of the step after the next.
+        constexpr int FH = C::FM / 2;
+        bf16x8 xf[2][FH], wf[2][C::FN];
+        auto read_ws = [&](const uint8_t* buf, int s) {
 #pragma unroll
             for (int f = 0; f < C::FN; ++f) {
-                const i32x4 lo = __builtin_bit_cast(i32x4, read_w(buf, f, g)), hi = __builtin_bit_cast(i32x4, read_w(buf, f, 4 + g));
-                wf[f] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-                wsc[f] = sc[(C::BM + wrow(f, l16)) * 4 + g];
+                if constexpr (C::WT) wf[s][f] = read_t(buf + C::XBYTES, C::BN * 2, (wn * C::FN + f) * 16, s);
+                else wf[s][f] = __builtin_bit_cast(bf16x8, read_w(buf, f, 4 * s + g));
             }
+        };
+        auto read_xs = [&](const uint8_t* buf, int s, int h) {
 #pragma unroll
-            for (int j = 0; j < C::FM; ++j) {
-                const i32x4 lo = __builtin_bit_cast(i32x4, read_x(buf, j, g)), hi = __builtin_bit_cast(i32x4, read_x(buf, j, 4 + g));
-                const i32x8 xf = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-                const int xsc = sc[(xr0 + j * 16 + l16) * 4 + g];
+            for (int f = 0; f < FH; ++f) {
+                if constexpr (C::XT) xf[h][f] = read_t(buf, C::BM * 2, xr0 + (h * FH + f) * 16, s);
+                else xf[h][f] = __builtin_bit_cast(bf16x8, read_x(buf, h * FH + f, 4 * s + g));
+            }
+        };
+        auto multiply = [&](int s, int h) {
+#pragma unroll
+            for (int j = 0; j < FH; ++j)
 #pragma unroll
                 for (int i = 0; i < C::FN; ++i)
-                    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf[i], xf, acc[i][j], 0, 0, 0, wsc[i], 0, xsc);
+                    acc[i][h * FH + j] = mfma16x16x32(wf[s][i], xf[h][j], acc[i][h * FH + j]);
+        };
+        constexpr int kXR = FH * (C::XT ? 2 : 1), kWR = C::FN * (C::WT ? 2 : 1), kMfma = C::FN * FH;
+        auto step = [&](uint8_t* cur, uint8_t* nxt, int kt) {
+            read_xs(cur, 0, 1);
+            multiply(0, 0);
+            spread<kXR, 0, kMfma>();
+            __builtin_amdgcn_sched_barrier(0);
+            read_ws(cur, 1);
+            read_xs(cur, 1, 0);
+            multiply(0, 1);
+            spread<kXR + kWR, 0, kMfma>();
+            __builtin_amdgcn_sched_barrier(0);
+            read_xs(cur, 1, 1);
+            multiply(1, 0);
+            spread<kXR, 0, kMfma>();
+            __syncthreads();
+            issue(cur, kt + 2);
+            read_ws(nxt, 0);
+            read_xs(nxt, 0, 0);
+            multiply(1, 1);
+            spread<kXR + kWR, C::XL + C::WL, kMfma>();
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        if (kt0 < kt1) {
+            issue(s0, kt0);
+            __syncthreads();
+            issue(s1, kt0 + 1);
+            read_ws(s0, 0);
+            read_xs(s0, 0, 0);
+            // Two steps a turn, one for each buffer; a step past the end
+            // multiplies zeros.
+            for (int kt = kt0; kt < kt1; kt += 2) {
+                step(s0, s1, kt);
+                step(s1, s0, kt + 1);
             }
         }
-    };
-
-    if (kt0 < kt1) {
-        issue(s0, kt0);
-        load_scales(kt0);
-        store_scales(s0);
-        __syncthreads();
-        for (int kt = kt0; kt < kt1; kt += 2) {
-            if (kt + 1 < kt1) {
-                issue(s1, kt + 1);
-                load_scales(kt + 1);
+    } else {
+        // A lane's 32 elements are pieces g and 4 + g; its scale operand is
+        // that of block g of the step. A step is one phase a fragment of X,
+        // with the next fragment read meanwhile; the barrier sits before the
+        // last phase, which reads the next step's operands of W.
+        i32x8 xf[2], wf[2][C::FN];
+        int xsc[2], wsc[2][C::FN];
+        auto join8 = [](u32x4 lo, u32x4 hi) {
+            return __builtin_bit_cast(i32x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        };
+        auto read_ws = [&](const uint8_t* buf, int s) {
+            const uint8_t* sc = buf + C::XBYTES + C::WBYTES + C::BM * 4 + g;
+#pragma unroll
+            for (int f = 0; f < C::FN; ++f) {
+                wf[s][f] = join8(read_w(buf, f, g), read_w(buf, f, 4 + g));
+                wsc[s][f] = sc[wrow(f, l16) * 4];
             }
-            compute(s0);
-            if (kt + 1 < kt1) store_scales(s1);
-            __syncthreads();
-            if (kt + 1 >= kt1) break;
-            if (kt + 2 < kt1) {
-                issue(s0, kt + 2);
-                load_scales(kt + 2);
+        };
+        auto read_x1 = [&](const uint8_t* buf, int j) {
+            xf[j & 1] = join8(read_x(buf, j, g), read_x(buf, j, 4 + g));
+            xsc[j & 1] = buf[C::XBYTES + C::WBYTES + (xr0 + j * 16 + l16) * 4 + g];
+        };
+        auto multiply = [&](int s, int j) {
+#pragma unroll
+            for (int i = 0; i < C::FN; ++i)
+                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf[s][i], xf[j & 1], acc[i][j], 0, 0, 0,
+                                                                             wsc[s][i], 0, xsc[j & 1]);
+        };
+        static_assert(C::FM % 2 == 0, "the next step's first fragment goes to the free operand");
+        auto step = [&](uint8_t* cur, uint8_t* nxt, int s, int kt) {
+#pragma unroll
+            for (int j = 0; j < C::FM - 1; ++j) {
+                read_x1(cur, j + 1);
+                multiply(s, j);
+                __builtin_amdgcn_sched_barrier(0);
             }
-            compute(s1);
-            if (kt + 2 < kt1) store_scales(s0);
+            store_scales(nxt, kt + 1);
             __syncthreads();
+            issue(cur, kt + 2);
+            load_scales(kt + 2);
+            read_ws(nxt, s ^ 1);
+            read_x1(nxt, 0);
+            multiply(s, C::FM - 1);
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        if (kt0 < kt1) {
+            issue(s0, kt0);
+            load_scales(kt0);
+            store_scales(s0, kt0);
+            __syncthreads();
+            issue(s1, kt0 + 1);
+            load_scales(kt0 + 1);
+            read_ws(s0, 0);
+            read_x1(s0, 0);
+            for (int kt = kt0; kt < kt1; kt += 2) {
+                step(s0, s1, 0, kt);
+                step(s1, s0, 1, kt + 1);
+            }
         }
     }
 

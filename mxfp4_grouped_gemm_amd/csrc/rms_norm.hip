@@ -2,7 +2,9 @@
 // optional MXFP8 output:
 //   s = x + residual;  v = s / sqrt(mean(s^2) + eps) * (offset + weight);
 //   residual_out = s, y = bf16(v), (q, qs) = MXFP8(v).
-// s, the sum of squares and v are fp32; each output is rounded once, from the
+// s and v are fp32, the squares are summed by eights in fp32 and then in fp64
+// (an e4m3 code changes where v crosses a tie, so 1e-7 of the root counts
+// there); each output is rounded once, from the
 // fp32 value (y and q do not pass through each other).
 //
 // Bound by memory: 8 bytes an element with bf16 streams, about 9 with the
@@ -25,19 +27,34 @@ __device__ __forceinline__ float dpp(float v) {
     return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
 }
 
+template <int CTRL>
+__device__ __forceinline__ double dpp(double v) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_mov_dpp((int)b, CTRL, 0xf, 0xf, true);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_mov_dpp((int)(b >> 32), CTRL, 0xf, 0xf, true);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+__device__ __forceinline__ double join(uint32_t lo, uint32_t hi) {
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
 // Sum over the wave, the same in every lane: xor by 1 and 2 inside quads, then
-// mirrored halves of a row, then the rows.
-__device__ __forceinline__ float wave_sum(float v) {
+// mirrored halves of a row, then the rows. In fp64, as the last few additions
+// are what a long fp32 sum loses most in (and they are few).
+__device__ __forceinline__ double wave_sum(double v) {
     v += dpp<0xB1>(v);   // quad_perm [1, 0, 3, 2]
     v += dpp<0x4E>(v);   // quad_perm [2, 3, 0, 1]
     v += dpp<0x141>(v);  // row_half_mirror
     v += dpp<0x140>(v);  // row_mirror
-    const uint32_t u = __float_as_uint(v);
-    auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
-    v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
-    const uint32_t t = __float_as_uint(v);
-    auto b = __builtin_amdgcn_permlane32_swap(t, t, false, false);
-    return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+    uint64_t b = __builtin_bit_cast(uint64_t, v);
+    auto lo = __builtin_amdgcn_permlane16_swap((uint32_t)b, (uint32_t)b, false, false);
+    auto hi = __builtin_amdgcn_permlane16_swap((uint32_t)(b >> 32), (uint32_t)(b >> 32), false, false);
+    v = join(lo[0], hi[0]) + join(lo[1], hi[1]);
+    b = __builtin_bit_cast(uint64_t, v);
+    auto lo2 = __builtin_amdgcn_permlane32_swap((uint32_t)b, (uint32_t)b, false, false);
+    auto hi2 = __builtin_amdgcn_permlane32_swap((uint32_t)(b >> 32), (uint32_t)(b >> 32), false, false);
+    return join(lo2[0], hi2[0]) + join(lo2[1], hi2[1]);
 }
 
 // Eight elements i..i+7 of a row (VEC), or elements i, i + step, ... (the
@@ -106,7 +123,7 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void rms_norm_kernel
     // elements c * 8 * kLanes + tid + e * kLanes.
     auto first = [&](int c) { return VEC ? (c * kLanes + tid) * 8 : c * 8 * kLanes + tid; };
     f32x8 s[NC];
-    float sum = 0.0f;
+    double sum = 0.0;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
         const int i = first(c);
@@ -121,19 +138,21 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void rms_norm_kernel
     for (int c = 0; c < NC; ++c) {
         const int i = first(c);
         if (a.residual_out && i < H) store8<VEC>(ro, a.res_f32, i, kLanes, H, s[c]);
+        float q = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum = fmaf(s[c][e], s[c][e], sum);
+        for (int e = 0; e < 8; ++e) q = fmaf(s[c][e], s[c][e], q);
+        sum += (double)q;
     }
     sum = wave_sum(sum);
     if constexpr (WAVES > 1) {
-        __shared__ float part[WAVES];
+        __shared__ double part[WAVES];
         if ((tid & 63) == 0) part[tid >> 6] = sum;
         __syncthreads();
-        sum = 0.0f;
+        sum = 0.0;
 #pragma unroll
         for (int w = 0; w < WAVES; ++w) sum += part[w];
     }
-    const float r = 1.0f / sqrtf(sum / (float)H + a.eps);
+    const float r = (float)(1.0 / sqrt(sum / (double)H + (double)a.eps));
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
         const int i = first(c);
