@@ -483,24 +483,35 @@ def _fail_tensor(t, name, dtype, shape, device):
     raise ValueError(f"{name} must be contiguous")
 
 
+# A decode step calls these functions back to back, so what they do on the
+# host counts: one pass of cheap checks a tensor, and the messages only where
+# one fails. `device` is the device of a tensor that is known to be on a GPU.
 def _full(t, name, dtype, shape, device):
-    """A contiguous tensor of this type, shape and device."""
-    if (not isinstance(t, torch.Tensor) or t.device != device or not t.is_cuda or t.shape != shape
-            or not (t.dtype in dtype if isinstance(dtype, tuple) else t.dtype == dtype)
-            or not t.is_contiguous()):
-        _fail_tensor(t, name, dtype, shape, device)
-    return t.data_ptr()
+    """The address of a contiguous tensor of this type (or one of these),
+    shape and device."""
+    try:
+        if t.shape == shape and t.device == device and t.is_contiguous() and (
+                t.dtype in dtype if type(dtype) is tuple else t.dtype is dtype):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _fail_tensor(t, name, dtype, shape, device)
 
 
 def _rows(t, name, dtype, shape, device):
-    """A matrix whose rows are contiguous -> (pointer, row stride)."""
-    if (not isinstance(t, torch.Tensor) or t.device != device or not t.is_cuda or t.shape != shape
-            or not (t.dtype in dtype if isinstance(dtype, tuple) else t.dtype == dtype)):
-        _fail_tensor(t, name, dtype, shape, device)
-    T, cols = shape
-    if cols > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name} must have contiguous rows, got strides {t.stride()}")
-    return t.data_ptr(), t.stride(0) if T > 1 else cols
+    """A matrix whose rows are contiguous -> (address, row stride)."""
+    try:
+        if t.shape == shape and t.device == device and (
+                t.dtype in dtype if type(dtype) is tuple else t.dtype is dtype):
+            if t.is_contiguous():
+                return t.data_ptr(), shape[1]
+            T, cols = shape
+            if cols > 1 and t.stride(1) != 1:
+                raise ValueError(f"{name} must have contiguous rows, got strides {t.stride()}")
+            return t.data_ptr(), t.stride(0) if T > 1 else cols
+    except AttributeError:
+        pass
+    _fail_tensor(t, name, dtype, shape, device)
 
 
 def _matrix(t, name):
@@ -513,15 +524,21 @@ def _matrix(t, name):
     return t.shape
 
 
-def _run(device, stream, call):
-    """call(stream pointer) with `device` current, on `stream` or that
+def _run(device, stream, fn, *args):
+    """fn(*args, stream address) with `device` current, on `stream` or that
     device's current stream."""
-    if stream is not None and stream.device != device:
-        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
     if torch.cuda.current_device() != device.index:
         with torch.cuda.device(device):
-            return _run(device, stream, call)
-    _check(call((torch.cuda.current_stream() if stream is None else stream).cuda_stream))
+            return _run(device, stream, fn, *args)
+    if stream is None:
+        at = torch._C._cuda_getCurrentRawStream(device.index)
+    elif stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    else:
+        at = stream.cuda_stream
+    status = fn(*args, at)
+    if status != MOE_OK:
+        _check(status)
 
 
 def _empty(shape, dtype, device, stream):
@@ -532,31 +549,32 @@ def _empty(shape, dtype, device, stream):
 
 
 def _workspace(given, need, device, stream):
+    """-> (address, bytes, the tensor that holds them)."""
     if need < 0:
         raise MoeError(MOE_ERR_INVALID_ARG, "invalid sizes")
     if given is None:
-        return _empty(max(need, 256), torch.uint8, device, stream) if need else None
-    if given.dtype != torch.uint8 or not given.is_contiguous() or given.device != device:
+        if need == 0:
+            return None, 0, None
+        given = _empty(need, torch.uint8, device, stream)
+    elif given.dtype != torch.uint8 or not given.is_contiguous() or given.device != device:
         raise ValueError("workspace must be a contiguous uint8 tensor on the inputs' device")
-    return given
+    return given.data_ptr(), given.numel(), given
 
 
 def _lora(lora, name, T, K, N, device):
     """-> (ctypes struct or None, rank)."""
     if lora is None:
         return None, 0
-    lora = LoraAdapters(*lora)
-    a = lora.a
+    a, b, index, ranks, scale = lora if len(lora) == 5 else LoraAdapters(*lora)
     if not isinstance(a, torch.Tensor) or a.dim() != 3:
         raise ValueError(f"{name}.a must be a tensor [n, rank, {K}]")
     n, rank, _ = a.shape
-    s = _CLora(_full(a, name + ".a", torch.bfloat16, (n, rank, K), device),
-               _full(lora.b, name + ".b", torch.bfloat16, (n, N, rank), device),
-               _full(lora.index, name + ".index", torch.int32, (T,), device),
-               None if lora.ranks is None else _full(lora.ranks, name + ".ranks", torch.int32, (n,), device),
-               None if lora.scale is None else _full(lora.scale, name + ".scale", torch.float32, (n,), device),
-               n, rank)
-    return s, rank
+    return _CLora(_full(a, name + ".a", torch.bfloat16, (n, rank, K), device),
+                  _full(b, name + ".b", torch.bfloat16, (n, N, rank), device),
+                  _full(index, name + ".index", torch.int32, (T,), device),
+                  None if ranks is None else _full(ranks, name + ".ranks", torch.int32, (n,), device),
+                  None if scale is None else _full(scale, name + ".scale", torch.float32, (n,), device),
+                  n, rank), rank
 
 
 def moe_rms_norm(x, weight, residual=None, eps=1e-6, weight_offset=0.0, mxfp8=False, y=None,
@@ -578,11 +596,14 @@ def moe_rms_norm(x, weight, residual=None, eps=1e-6, weight_offset=0.0, mxfp8=Fa
     pw = _full(weight, "weight", (torch.bfloat16, torch.float32), (H,), device)
     if y is None:
         y = _empty((T, H), torch.bfloat16, device, stream)
+        py, ldy = y.data_ptr(), H
+    else:
+        py, ldy = _rows(y, "y", torch.bfloat16, (T, H), device)
+    po, ldo = None, H
     if residual_out is None and residual is not None:
         residual_out = _empty((T, H), rdt, device, stream)
-    py, ldy = _rows(y, "y", torch.bfloat16, (T, H), device)
-    po, ldo = None, H
-    if residual_out is not None:
+        po = residual_out.data_ptr()
+    elif residual_out is not None:
         po, ldo = _rows(residual_out, "residual_out", rdt or (torch.bfloat16, torch.float32), (T, H), device)
         rdt = residual_out.dtype
     pq, ldq, ps, lds = None, H, None, max(H // 32, 1)
@@ -595,10 +616,10 @@ def moe_rms_norm(x, weight, residual=None, eps=1e-6, weight_offset=0.0, mxfp8=Fa
             q_scale = _empty((T, H // 32), torch.float8_e8m0fnu, device, stream)
         pq, ldq = _rows(q, "q", _CODES, (T, H), device)
         ps, lds = _rows(q_scale, "q_scale", _SCALES, (T, H // 32), device)
-    _run(device, stream, lambda s: lib.moe_rms_norm(
-        px, ldx, pr, ldr, MOE_DT_F32 if rdt == torch.float32 else MOE_DT_BF16, pw,
-        MOE_DT_F32 if weight.dtype == torch.float32 else MOE_DT_BF16, eps, weight_offset, T, H, po, ldo,
-        py, ldy, pq, ldq, ps, lds, s))
+    _run(device, stream, lib.moe_rms_norm,
+         px, ldx, pr, ldr, MOE_DT_F32 if rdt is torch.float32 else MOE_DT_BF16, pw,
+         MOE_DT_F32 if weight.dtype is torch.float32 else MOE_DT_BF16, eps, weight_offset, T, H, po, ldo,
+         py, ldy, pq, ldq, ps, lds)
     return y, residual_out, q, q_scale
 
 
@@ -621,10 +642,10 @@ def moe_lora_linear(x, w, lora=None, out_dtype=torch.bfloat16, out=None, workspa
             raise ValueError(f"out_dtype must be bfloat16 or float32, got {out_dtype}")
         out = _empty((T, N), out_dtype, device, stream)
     po, ldo = _rows(out, "out", (torch.bfloat16, torch.float32), (T, N), device)
-    ws = _workspace(workspace, lib.moe_lora_linear_workspace_size(T, K, N, rank), device, stream)
-    _run(device, stream, lambda s: lib.moe_lora_linear(
-        px, ldx, pw, cl, T, K, N, po, ldo, MOE_DT_F32 if out.dtype == torch.float32 else MOE_DT_BF16,
-        ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0, s))
+    pws, nws, _ws = _workspace(workspace, lib.moe_lora_linear_workspace_size(T, K, N, rank), device, stream)
+    _run(device, stream, lib.moe_lora_linear,
+         px, ldx, pw, cl, T, K, N, po, ldo, MOE_DT_F32 if out.dtype is torch.float32 else MOE_DT_BF16,
+         pws, nws)
     return out
 
 
@@ -661,10 +682,10 @@ def moe_ffn_forward(x, w13, w2, addend=None, lora13=None, lora2=None, save_gate_
     if gate_up is None and save_gate_up:
         gate_up = _empty((T, 2 * I), torch.bfloat16, device, stream)
     pg = None if gate_up is None else _full(gate_up, "gate_up", torch.bfloat16, (T, 2 * I), device)
-    ws = _workspace(workspace, lib.moe_ffn_workspace_size(T, H, I, r13, r2), device, stream)
-    _run(device, stream, lambda s: lib.moe_ffn_forward(
-        px, ldx, p13, p2, act, pa, lda, c13, c2, T, H, I, po, ldo, pg,
-        ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0, s))
+    pws, nws, _ws = _workspace(workspace, lib.moe_ffn_workspace_size(T, H, I, r13, r2), device, stream)
+    _run(device, stream, lib.moe_ffn_forward,
+         px, ldx, p13, p2, act, pa, lda, c13, c2, T, H, I, po, ldo, pg,
+         pws, nws)
     return out if gate_up is None else (out, gate_up)
 
 
@@ -691,10 +712,10 @@ def moe_ffn_forward_mxfp8(x, x_scale, w13, w13_scale, w2, w2_scale, addend=None,
     if out is None:
         out = _empty((T, H), torch.bfloat16, device, stream)
     po, ldo = _rows(out, "out", torch.bfloat16, (T, H), device)
-    ws = _workspace(workspace, lib.moe_ffn_mxfp8_workspace_size(T, H, I), device, stream)
-    _run(device, stream, lambda s: lib.moe_ffn_forward_mxfp8(
-        px, pxs, p13, p13s, p2, p2s, act, pa, lda, T, H, I, po, ldo,
-        ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0, s))
+    pws, nws, _ws = _workspace(workspace, lib.moe_ffn_mxfp8_workspace_size(T, H, I), device, stream)
+    _run(device, stream, lib.moe_ffn_forward_mxfp8,
+         px, pxs, p13, p13s, p2, p2s, act, pa, lda, T, H, I, po, ldo,
+         pws, nws)
     return out
 
 
@@ -725,10 +746,10 @@ def moe_ffn_backward(dout, x, gate_up, w13, w2, need_dx=True, need_dw13=True, ne
     pdx, lddx = (None, H) if not need_dx else _rows(dx, "dx", torch.bfloat16, (T, H), device)
     pd13 = None if not need_dw13 else _full(dw13, "dw13", torch.bfloat16, (2 * I, H), device)
     pd2 = None if not need_dw2 else _full(dw2, "dw2", torch.bfloat16, (H, I), device)
-    ws = _workspace(workspace, lib.moe_ffn_backward_workspace_size(T, H, I), device, stream)
-    _run(device, stream, lambda s: lib.moe_ffn_backward(
-        pd, ldd, px, ldx, pg, p13, p2, act, T, H, I, pdx, lddx, pd13, pd2,
-        ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0, s))
+    pws, nws, _ws = _workspace(workspace, lib.moe_ffn_backward_workspace_size(T, H, I), device, stream)
+    _run(device, stream, lib.moe_ffn_backward,
+         pd, ldd, px, ldx, pg, p13, p2, act, T, H, I, pdx, lddx, pd13, pd2,
+         pws, nws)
     return dx if need_dx else None, dw13 if need_dw13 else None, dw2 if need_dw2 else None
 
 
