@@ -60,6 +60,7 @@ inline int64_t dense_partial_bytes(const DenseArgs& a, int splits, int epi) {
     return splits <= 1 ? 0 : (int64_t)splits * a.M * a.N * (epi == kEpiOut || epi == kEpiGatedBwd ? 1 : 2) * 4;
 }
 bool dense_big_tiles(const DenseArgs& a, int epi);
+bool dense_one_round(const DenseArgs& a, int epi);
 hipError_t launch_join(const DenseArgs& a, int epi, hipStream_t s);
 hipError_t launch_dense(const DenseArgs& a, int order, int elt, int epi, hipStream_t s);
 hipError_t launch_dense_nt(const DenseArgs& a, int epi, hipStream_t s);

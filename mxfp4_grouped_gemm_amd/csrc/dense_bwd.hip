@@ -11,7 +11,11 @@ template <bool XT, int EPI>
 static hipError_t launch_epi(const DenseArgs& a, hipStream_t s) {
     if (dense_big_tiles(a, EPI))
         return launch_tile<Tile<256, 256, 2, 4, XT, true, kEltBf16, EPI, false, false>>(a, s);
-    return launch_tile<Tile<128, 128, 2, 2, XT, true, kEltBf16, EPI, false, false>>(a, s);
+    if (!dense_one_round(a, EPI)) return launch_tile<Tile<128, 128, 2, 2, XT, true, kEltBf16, EPI, false, false>>(a, s);
+    // Too few 128 x 128 tiles for half of the compute units: 64 x 64 ones.
+    const int64_t tiles = (int64_t)((a.M + 127) / 128) * ((a.N + 127) / 128);
+    if (tiles < 128) return launch_tile<Tile<64, 64, 2, 2, XT, true, kEltBf16, EPI, false, false, 4>>(a, s);
+    return launch_tile<Tile<128, 128, 2, 2, XT, true, kEltBf16, EPI, false, false, 4>>(a, s);
 }
 
 hipError_t launch_dense_bwd(const DenseArgs& a, int order, int epi, hipStream_t s) {

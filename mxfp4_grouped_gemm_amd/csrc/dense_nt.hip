@@ -62,9 +62,12 @@ template <int EPI, bool LORA>
 hipError_t launch_epi(const DenseArgs& a, hipStream_t s) {
     if (dense_big_tiles(a, EPI))
         return launch_tile<Tile<256, 256, 2, 4, false, false, kEltBf16, EPI, false, LORA>>(a, s);
-    if (a.splits <= 1) return launch_tile<Tile<128, 128, 2, 2, false, false, kEltBf16, EPI, false, LORA>>(a, s);
-    const hipError_t e = launch_tile<Tile<128, 128, 2, 2, false, false, kEltBf16, EPI, true, LORA>>(a, s);
-    return e != hipSuccess ? e : launch_join(a, EPI, s);
+    if (a.splits > 1) {
+        const hipError_t e = launch_tile<Tile<128, 128, 2, 2, false, false, kEltBf16, EPI, true, LORA, 4>>(a, s);
+        return e != hipSuccess ? e : launch_join(a, EPI, s);
+    }
+    if (dense_one_round(a, EPI)) return launch_tile<Tile<128, 128, 2, 2, false, false, kEltBf16, EPI, false, LORA, 4>>(a, s);
+    return launch_tile<Tile<128, 128, 2, 2, false, false, kEltBf16, EPI, false, LORA>>(a, s);
 }
 
 }  // namespace
@@ -77,6 +80,13 @@ bool dense_big_tiles(const DenseArgs& a, int epi) {
     return (int64_t)((a.M + 255) / 256) * ((cols + 255) / 256) >= 160;
 }
 
+// 128 x 128 tiles with at most one workgroup a compute unit.
+bool dense_one_round(const DenseArgs& a, int epi) {
+    const bool gated = epi == kEpiGated || epi == kEpiGatedMx;
+    const int64_t cols = gated ? 2 * (int64_t)a.N : a.N;
+    return (int64_t)((a.M + 127) / 128) * ((cols + 127) / 128) <= 256;
+}
+
 int dense_splits(const DenseArgs& a, int order, int elt, int epi) {
     if (order != kNT || dense_big_tiles(a, epi)) return 1;
     const bool gated = epi == kEpiGated || epi == kEpiGatedMx;
@@ -84,7 +94,7 @@ int dense_splits(const DenseArgs& a, int order, int elt, int epi) {
     const int64_t tiles = (int64_t)((a.M + 127) / 128) * ((cols + 127) / 128);
     const int bk = elt == kEltBf16 ? 64 : 128;
     const int steps = (a.K + bk - 1) / bk;
-    int64_t s = 384 / tiles;
+    int64_t s = 256 / tiles;
     if (s > steps / 4) s = steps / 4;
     if (s > 16) s = 16;
     return s < 1 ? 1 : (int)s;

@@ -5,8 +5,13 @@
 // rows and their 8 up rows) and all of K: wave w takes the 128-byte K chunks
 // w, w + 8, ... of every row straight into the MFMA operand registers (lane
 // (i, g) holds pieces g and 4 + g of row i), with the tokens' chunks, which
-// all workgroups read, coming from L2. The waves' sums meet in LDS, always in
-// the same order.
+// all workgroups read, coming from L2. A batch of chunks is loaded before the
+// first of them is multiplied, so most of a wave's bytes are one round trip.
+// The waves' sums meet in LDS, always in the same order.
+//
+// The low-rank term of an output is a dot product of at most a few hundred
+// elements that depends on the output's token: the thread that finishes the
+// output computes it, while the first batch of weights is on its way.
 #include "dense_tile.hpp"
 
 namespace moe {
@@ -17,6 +22,38 @@ namespace {
 
 constexpr int kWaves = 8;
 
+// scale * B[a] (A[a] x) of one token for rows col..col+3 (and N + col.. of the
+// gated block), from v = scale * A[a] x.
+template <bool GATED>
+__device__ __forceinline__ void lora_dot(const LoraArgs& l, int N, int token, int col, f32x4 (&low)[2]) {
+    const int ad = l.index[token];
+    if ((unsigned)ad >= (unsigned)l.n) return;
+    int rank = l.ranks ? l.ranks[ad] : l.rank;
+    rank = rank < l.rank ? rank : l.rank;
+    const uint16_t* b = l.b + ((int64_t)ad * (GATED ? 2 * (int64_t)N : N) + col) * l.rank;
+    const float* v = l.v + (int64_t)token * l.vld;
+    for (int k = 0; k < rank; k += 8) {
+        const f32x4 v0 = *(const f32x4*)(v + k), v1 = *(const f32x4*)(v + k + 4);
+        u32x4 w[GATED ? 2 : 1][4];
+#pragma unroll
+        for (int s = 0; s < (GATED ? 2 : 1); ++s)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) w[s][r] = *(const u32x4*)(b + ((int64_t)s * N + r) * l.rank + k);
+#pragma unroll
+        for (int s = 0; s < (GATED ? 2 : 1); ++s)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    // Columns beyond the adapter's rank are not read as numbers.
+                    const uint32_t d = w[s][r][e / 2];
+                    const float f = __uint_as_float(e & 1 ? d & 0xffff0000u : d << 16);
+                    const float t = (e < 4 ? v0[e & 3] : v1[e & 3]);
+                    if (k + e < rank) low[s][r] = fmaf(f, t, low[s][r]);
+                }
+    }
+}
+
 // ELT: see dense_tile.hpp. NJ: 16-token column blocks. XF32: X is fp32 and is
 // quantised to MXFP8 as it is read (the second product of the MXFP8 block).
 template <int ELT, int NJ, bool GATED, bool XF32, bool LORA>
@@ -25,7 +62,7 @@ __global__ __launch_bounds__(kWaves * 64) void skinny_kernel(DenseArgs a, const 
     constexpr int ESZ = ELT == kEltBf16 ? 2 : 1;
     // Chunks in flight per wave: as many as the registers of two waves a SIMD
     // allow next to the tokens' operands.
-    constexpr int U = XF32 ? (NJ == 1 ? 2 : 1) : NJ == 1 ? 7 : NJ == 2 ? 4 : 2;
+    constexpr int U = XF32 ? (NJ <= 2 ? 2 : 1) : ELT == kEltMx8 ? (NJ <= 2 ? 4 : 2) : NJ <= 2 ? 7 : 4;
     __shared__ f32x4 red[kWaves][NJ][64];
     const int tid = (int)threadIdx.x, lane = tid & 63;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -51,9 +88,10 @@ __global__ __launch_bounds__(kWaves * 64) void skinny_kernel(DenseArgs a, const 
     for (int j = 0; j < NJ; ++j) acc[0][j] = f32x4{0, 0, 0, 0};
 
     const int nch = (a.K + BK - 1) / BK;
-    for (int c0 = w; c0 < nch; c0 += kWaves * U) {
-        u32x4 wv[U][2], xv[U][NJ][XF32 ? 8 : 2];
-        uint32_t ws[U], xs[U][NJ];
+    const rsrc_t rws = make_rsrc(a.ws, kRecord), rxs = make_rsrc(a.xs, kRecord);
+    u32x4 wv[U][2], xv[U][NJ][XF32 ? 8 : 2];
+    uint32_t ws[U], xs[U][NJ];
+    auto load = [&](int c0) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int c = c0 + kWaves * u;
@@ -77,13 +115,30 @@ __global__ __launch_bounds__(kWaves * 64) void skinny_kernel(DenseArgs a, const 
             if constexpr (ELT == kEltMx8) {
                 // Byte of block g of the chunk; blocks past the end have zero codes.
                 const int b = 4 * c + g;
-                ws[u] = wrow >= 0 && b < kb ? a.ws[wrow * kb + b] : 0;
+                ws[u] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(
+                    rws, wrow >= 0 && b < kb ? (uint32_t)(wrow * kb) + (uint32_t)b : kOob, 0, 0);
                 if constexpr (!XF32) {
 #pragma unroll
-                    for (int j = 0; j < NJ; ++j) xs[u][j] = m[j] < a.M && b < kb ? a.xs[(int64_t)m[j] * kb + b] : 0;
+                    for (int j = 0; j < NJ; ++j)
+                        xs[u][j] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(
+                            rxs, m[j] < a.M && b < kb ? (uint32_t)(m[j] * kb + b) : kOob, 0, 0);
                 }
             }
         }
+        __builtin_amdgcn_sched_barrier(0);  // all of the batch in flight
+    };
+    load(w);
+    // Thread (j, token, q) finishes rows 4q..4q+3 of the tile (gated: pairs,
+    // with the up rows in q + 2).
+    constexpr int Q = GATED ? 2 : 4;
+    const int fj = tid / (16 * Q), fq = (tid / 16) % Q, token = 16 * fj + i;
+    const int col = n0 + 4 * fq;
+    const bool finish = tid < NJ * 16 * Q && token < a.M && col < a.N;
+    f32x4 low[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+    if constexpr (LORA) {
+        if (finish) lora_dot<GATED>(a.lora, a.N, token, col, low);
+    }
+    for (int c0 = w;;) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
 #pragma unroll
@@ -132,30 +187,21 @@ __global__ __launch_bounds__(kWaves * 64) void skinny_kernel(DenseArgs a, const 
                 }
             }
         }
-    }
-    if constexpr (LORA) {
-        // The batch's adapters are dealt to the waves.
-        lora_accumulate<1, NJ>(
-            a.lora, GATED ? 2 * (int64_t)a.N : a.N, acc, [&](int) { return (int)wrow; },
-            [&](int j) { return m[j] < a.M ? m[j] : -1; }, w, kWaves);
+        c0 += kWaves * U;
+        if (c0 >= nch) break;
+        load(c0);
     }
 #pragma unroll
     for (int j = 0; j < NJ; ++j) red[w][j][lane] = acc[0][j];
     __syncthreads();
-    // Thread (j, token i, q): rows 4q..4q+3 of the tile (gated: pairs, with
-    // the up rows in q + 2).
-    constexpr int Q = GATED ? 2 : 4;
-    if (tid >= NJ * 16 * Q) return;
-    const int j = tid / (16 * Q), q = (tid / 16) % Q, token = 16 * j + i;
-    const int col = n0 + 4 * q;
-    if (token >= a.M || col >= a.N) return;
-    f32x4 v = red[0][j][16 * q + i];
+    if (!finish) return;
+    f32x4 v = low[0];
 #pragma unroll
-    for (int k = 1; k < kWaves; ++k) v += red[k][j][16 * q + i];
+    for (int k = 0; k < kWaves; ++k) v += red[k][fj][16 * fq + i];
     if constexpr (GATED) {
-        f32x4 up = red[0][j][16 * (q + 2) + i];
+        f32x4 up = low[1];
 #pragma unroll
-        for (int k = 1; k < kWaves; ++k) up += red[k][j][16 * (q + 2) + i];
+        for (int k = 0; k < kWaves; ++k) up += red[k][fj][16 * (fq + 2) + i];
         if (a.gate_up) {
             uint16_t* gu = a.gate_up + token * 2 * (int64_t)a.N + col;
             *(u32x2*)gu = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};

@@ -7,7 +7,9 @@
 // elements) with loads straight into LDS, one buffer ahead of the one that is
 // multiplied (two buffers, one barrier a step; the buffers are separate
 // __shared__ objects, so that the compiler sees that reads of one need not
-// wait for loads into the other).
+// wait for loads into the other). Tiles that leave compute units idle have no
+// second workgroup to hide a load behind: they run with four buffers, three
+// steps of loads in flight.
 //
 // W is the MFMA's first operand, so a lane's four results are four
 // consecutive n of one m. The rows of W are dealt to the fragments such that
@@ -24,6 +26,8 @@
 //    read (four rows of 16 elements -> each lane four elements of one column).
 //    Piece c of row k sits at c ^ (2 ((k & 3) | (k >> 3 & 1) << 2)).
 #pragma once
+
+#include <type_traits>
 
 #include "common.hpp"
 #include "dense.hpp"
@@ -62,12 +66,26 @@ __device__ __forceinline__ void spread() {
     }
 }
 
+// Waits until at most LOADS of this wave's loads are in flight and its LDS
+// reads are done, then for the workgroup. Loads complete in order, so what is
+// left in flight are the latest steps'.
+template <int LOADS>
+__device__ __forceinline__ void sync_step() {
+    if constexpr (LOADS == 0) {
+        __syncthreads();
+    } else {
+        static_assert(LOADS < 64, "six bits");
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LOADS) : "memory");
+    }
+}
+
 // e^x / (1 + e^x) and friends with the accurate expf: the epilogue runs once
 // per output.
 __device__ __forceinline__ float sigmoid(float g) { return 1.0f / (1.0f + expf(-g)); }
 
-template <int BM_, int BN_, int WM_, int WN_, bool XT_, bool WT_, int ELT_, int EPI_, bool SPLIT_, bool LORA_>
+template <int BM_, int BN_, int WM_, int WN_, bool XT_, bool WT_, int ELT_, int EPI_, bool SPLIT_, bool LORA_, int NB_ = 2>
 struct Tile {
+    static constexpr int NB = NB_;  // LDS buffers
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, ELT = ELT_, EPI = EPI_;
     static constexpr bool XT = XT_, WT = WT_, SPLIT = SPLIT_, LORA = LORA_;
     static constexpr bool GATED = EPI == kEpiGated || EPI == kEpiGatedMx;
@@ -92,7 +110,10 @@ __device__ __forceinline__ int key_w(int r) {
     constexpr int s = F == 8 ? 5 : F == 4 ? 4 : F == 2 ? 3 : 2;
     return ((r >> 1) & 1) | (((r >> s) & 3) << 1);
 }
-__device__ __forceinline__ int key_t(int k) { return 2 * ((k & 3) | (((k >> 3) & 1) << 2)); }
+template <int PIECES>
+__device__ __forceinline__ int key_t(int k) {
+    return (2 * ((k & 3) | (((k >> 3) & 1) << 2))) & (PIECES - 1);
+}
 
 // The low-rank term of a wave's accumulators: for each adapter that one of
 // the wave's rows uses, acc += B[a] v over its rank, with v (fp32) split into
@@ -190,6 +211,8 @@ template <class C>
 __global__ __launch_bounds__(C::THREADS, 2) void dense_kernel(DenseArgs a) {
     __shared__ __align__(1024) uint8_t s0[C::BUF];
     __shared__ __align__(1024) uint8_t s1[C::BUF];
+    __shared__ __align__(1024) uint8_t s2[C::NB > 2 ? C::BUF : 16];
+    __shared__ __align__(1024) uint8_t s3[C::NB > 2 ? C::BUF : 16];
     const int tid = (int)threadIdx.x, lane = tid & 63;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = w / C::WN, wn = w % C::WN;
@@ -237,7 +260,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void dense_kernel(DenseArgs a) {
         const int p = (w * C::XL + i) * 64 + lane;  // piece of the tile
         if constexpr (C::XT) {
             constexpr int PR = C::BM / 8;  // pieces a row
-            const int k = p / PR, c = (p % PR) ^ key_t(k);
+            const int k = p / PR, c = (p % PR) ^ key_t<PR>(k);
             xo[i] = m0 + c * 8 < a.M ? (uint32_t)(k * a.ldx * 2 + c * 16) : kOob;
         } else {
             const int r = p >> 3, c = (p & 7) ^ key_x(r);
@@ -249,7 +272,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void dense_kernel(DenseArgs a) {
         const int p = (w * C::WL + i) * 64 + lane;
         if constexpr (C::WT) {
             constexpr int PR = C::BN / 8;
-            const int k = p / PR, c = (p % PR) ^ key_t(k);
+            const int k = p / PR, c = (p % PR) ^ key_t<PR>(k);
             wo[i] = n0 + c * 8 < a.N ? (uint32_t)(k * a.ldw * 2 + c * 16) : kOob;
         } else {
             const int r = p >> 3, c = (p & 7) ^ key_w<C::F>(r);
@@ -349,13 +372,14 @@ __global__ __launch_bounds__(C::THREADS, 2) void dense_kernel(DenseArgs a) {
         return *(const u32x4*)(buf + C::XBYTES + r * kRowBytes + ((piece ^ key_w<C::F>(r)) << 4));
     };
     // Transposed operand: columns c0 + 0..15 of K rows 32 s + 8 g + 0..7.
-    auto read_t = [&](const uint8_t* base, int pitch, int c0, int s) -> bf16x8 {
+    auto read_t = [&](const uint8_t* base, auto pieces, int c0, int s) -> bf16x8 {
+        constexpr int PR = decltype(pieces)::value, pitch = PR * 16;
         bf16x4 v[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int k = 32 * s + 8 * g + 4 * h + (l16 >> 2);
             const int col = c0 + (l16 & 3) * 4;
-            const uint8_t* p = base + k * pitch + ((((col >> 3) ^ key_t(k)) << 4) | ((col & 4) << 1));
+            const uint8_t* p = base + k * pitch + ((((col >> 3) ^ key_t<PR>(k)) << 4) | ((col & 4) << 1));
             typedef __attribute__((address_space(3))) bf16x4* tp;
             v[h] = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((tp)p);
         }
@@ -373,14 +397,14 @@ __global__ __launch_bounds__(C::THREADS, 2) void dense_kernel(DenseArgs a) {
         auto read_ws = [&](const uint8_t* buf, int s) {
 #pragma unroll
             for (int f = 0; f < C::FN; ++f) {
-                if constexpr (C::WT) wf[s][f] = read_t(buf + C::XBYTES, C::BN * 2, (wn * C::FN + f) * 16, s);
+                if constexpr (C::WT) wf[s][f] = read_t(buf + C::XBYTES, std::integral_constant<int, C::BN / 8>(), (wn * C::FN + f) * 16, s);
                 else wf[s][f] = __builtin_bit_cast(bf16x8, read_w(buf, f, 4 * s + g));
             }
         };
         auto read_xs = [&](const uint8_t* buf, int s, int h) {
 #pragma unroll
             for (int f = 0; f < FH; ++f) {
-                if constexpr (C::XT) xf[h][f] = read_t(buf, C::BM * 2, xr0 + (h * FH + f) * 16, s);
+                if constexpr (C::XT) xf[h][f] = read_t(buf, std::integral_constant<int, C::BM / 8>(), xr0 + (h * FH + f) * 16, s);
                 else xf[h][f] = __builtin_bit_cast(bf16x8, read_x(buf, h * FH + f, 4 * s + g));
             }
         };
@@ -405,25 +429,37 @@ __global__ __launch_bounds__(C::THREADS, 2) void dense_kernel(DenseArgs a) {
             read_xs(cur, 1, 1);
             multiply(1, 0);
             spread<kXR, 0, kMfma>();
-            __syncthreads();
-            issue(cur, kt + 2);
+            sync_step<(C::NB - 2) * (C::XL + C::WL)>();
+            issue(cur, kt + C::NB);
             read_ws(nxt, 0);
             read_xs(nxt, 0, 0);
             multiply(1, 1);
             spread<kXR + kWR, C::XL + C::WL, kMfma>();
             __builtin_amdgcn_sched_barrier(0);
         };
+        static_assert(C::NB == 2 || C::NB == 4, "two or four buffers");
         if (kt0 < kt1) {
             issue(s0, kt0);
-            __syncthreads();
             issue(s1, kt0 + 1);
+            if constexpr (C::NB == 4) {
+                issue(s2, kt0 + 2);
+                issue(s3, kt0 + 3);
+            }
+            sync_step<(C::NB - 1) * (C::XL + C::WL)>();
             read_ws(s0, 0);
             read_xs(s0, 0, 0);
-            // Two steps a turn, one for each buffer; a step past the end
-            // multiplies zeros.
-            for (int kt = kt0; kt < kt1; kt += 2) {
-                step(s0, s1, kt);
-                step(s1, s0, kt + 1);
+            // A step for each buffer a turn; a step past the end multiplies
+            // zeros.
+            for (int kt = kt0; kt < kt1; kt += C::NB) {
+                if constexpr (C::NB == 2) {
+                    step(s0, s1, kt);
+                    step(s1, s0, kt + 1);
+                } else {
+                    step(s0, s1, kt);
+                    step(s1, s2, kt + 1);
+                    step(s2, s3, kt + 2);
+                    step(s3, s0, kt + 3);
+                }
             }
         }
     } else {

@@ -2,11 +2,17 @@
 // a = index[t], in fp32. The second factor, B[a] v, is added inside the
 // projection's own kernels.
 //
-// A workgroup takes 16 or 32 tokens in their own order and the s-th distinct
-// adapter among them (grid.y counts s; most of the grid of a batch whose
-// tokens share adapters leaves at once). Its eight waves split K and meet in
-// LDS in a fixed order. Tokens of other adapters run through the products too
-// and are not stored.
+// Few tokens (decode): a workgroup a token and 16 rows of its adapter's A, so
+// nothing has to be sorted or searched; rows that tokens share come from L2.
+//
+// Many tokens (prompts): a workgroup takes 32 tokens in their own order and
+// the s-th distinct adapter among them (grid.y counts s; most of the grid of
+// a batch whose tokens share adapters leaves at once), so A is read once per
+// 32 tokens. Tokens of other adapters run through the products too and are
+// not stored.
+//
+// In both, eight waves split K, hold a batch of 128-byte K chunks in flight
+// and meet in LDS in a fixed order.
 #include "dense_tile.hpp"
 
 namespace moe {
@@ -17,6 +23,55 @@ namespace {
 
 constexpr int kWaves = 8;
 constexpr int FR = 4;  // 16-row rank fragments a pass
+// Up to this many tokens a workgroup takes one token.
+constexpr int kTokenWise = 128;
+
+__global__ __launch_bounds__(kWaves * 64) void lora_shrink_token_kernel(const uint16_t* __restrict__ x, int64_t ldx,
+                                                                        int K, LoraArgs l) {
+    constexpr int U = 7;
+    __shared__ f32x4 red[kWaves][4];
+    const int tid = (int)threadIdx.x, lane = tid & 63;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int i = lane & 15, g = lane >> 4;
+    const int t = (int)blockIdx.x, r0 = (int)blockIdx.y * 16;
+    const int ad = l.index[t];
+    if ((unsigned)ad >= (unsigned)l.n) return;
+    int rank = l.ranks ? l.ranks[ad] : l.rank;
+    rank = rank < l.rank ? rank : l.rank;
+    const rsrc_t ra = make_rsrc(l.a + (int64_t)ad * l.rank * K, kRecord);
+    const rsrc_t rx = make_rsrc(x + t * ldx, kRecord);
+    const uint32_t ao = r0 + i < rank ? (uint32_t)((r0 + i) * K * 2) + 16u * g : kOob;
+    const int nch = (K + 63) / 64;
+    f32x4 acc = {0, 0, 0, 0};
+    for (int c0 = w; c0 < nch; c0 += kWaves * U) {
+        u32x4 av[U][2], xv[U][2];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int c = c0 + kWaves * u;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const bool ok = (4 * h + g) * 8 < K - c * 64;
+                av[u][h] = bld16(ra, ok && ao != kOob ? ao + c * 128 + 64 * h : kOob);
+                // The token is the MFMA's column 0; the other columns are zeros.
+                xv[u][h] = bld16(rx, ok && i == 0 ? (uint32_t)(c * 128 + 64 * h + 16 * g) : kOob);
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                acc = mfma16x16x32(__builtin_bit_cast(bf16x8, av[u][h]), __builtin_bit_cast(bf16x8, xv[u][h]), acc);
+    }
+    if (i == 0) red[w][g] = acc;
+    __syncthreads();
+    if (tid < 4) {
+        f32x4 v = red[0][tid];
+#pragma unroll
+        for (int k = 1; k < kWaves; ++k) v += red[k][tid];
+        *(f32x4*)(l.v + (int64_t)t * l.vld + r0 + 4 * tid) = v * (l.scale ? l.scale[ad] : 1.0f);
+    }
+}
 
 template <int FM>
 __global__ __launch_bounds__(kWaves * 64) void lora_shrink_kernel(const uint16_t* __restrict__ x, int64_t ldx, int T,
@@ -68,29 +123,34 @@ __global__ __launch_bounds__(kWaves * 64) void lora_shrink_kernel(const uint16_t
 #pragma unroll
             for (int f = 0; f < FM; ++f) acc[r][f] = f32x4{0, 0, 0, 0};
         }
-        const int nfr = rank - r0 > 48 ? 4 : rank - r0 > 32 ? 3 : rank - r0 > 16 ? 2 : rank - r0 > 0 ? 1 : 0;
-        if (nfr > 0) {
-            for (int c = w; c < nch; c += kWaves) {
-                bf16x8 xv[FM][2];
+        constexpr int U = 3;
+        for (int c0 = w; c0 < nch; c0 += kWaves * U) {
+            u32x4 xv[U][2][FM], av[U][2][FR];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int c = c0 + kWaves * u;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const bool ok = c * 64 + (4 * h + g) * 8 < K;
+                    const bool ok = (4 * h + g) * 8 < K - c * 64;
 #pragma unroll
                     for (int f = 0; f < FM; ++f)
-                        xv[f][h] = __builtin_bit_cast(bf16x8, bld16(rx, ok && xo[f] != kOob ? xo[f] + c * 128 + 64 * h : kOob));
-                }
+                        xv[u][h][f] = bld16(rx, ok && xo[f] != kOob ? xo[f] + c * 128 + 64 * h : kOob);
 #pragma unroll
-                for (int r = 0; r < FR; ++r) {
-                    if (r >= nfr) break;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const bool ok = c * 64 + (4 * h + g) * 8 < K;
-                        const bf16x8 av = __builtin_bit_cast(bf16x8, bld16(ra, ok && ao[r] != kOob ? ao[r] + c * 128 + 64 * h : kOob));
-#pragma unroll
-                        for (int f = 0; f < FM; ++f) acc[r][f] = mfma16x16x32(av, xv[f][h], acc[r][f]);
-                    }
+                    for (int r = 0; r < FR; ++r)
+                        av[u][h][r] = bld16(ra, ok && ao[r] != kOob ? ao[r] + c * 128 + 64 * h : kOob);
                 }
             }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int r = 0; r < FR; ++r)
+#pragma unroll
+                        for (int f = 0; f < FM; ++f)
+                            acc[r][f] = mfma16x16x32(__builtin_bit_cast(bf16x8, av[u][h][r]),
+                                                     __builtin_bit_cast(bf16x8, xv[u][h][f]), acc[r][f]);
         }
         if (r0 > 0) __syncthreads();  // the previous pass has been read
 #pragma unroll
@@ -117,12 +177,13 @@ __global__ __launch_bounds__(kWaves * 64) void lora_shrink_kernel(const uint16_t
 }  // namespace
 
 hipError_t launch_lora_shrink(const uint16_t* x, int64_t ldx, int T, int K, const LoraArgs& l, hipStream_t s) {
-    const int block_tokens = T <= 512 ? 16 : 32;
-    const dim3 grid((unsigned)((T + block_tokens - 1) / block_tokens), (unsigned)(l.n < block_tokens ? l.n : block_tokens));
-    if (block_tokens == 16)
-        hipLaunchKernelGGL(lora_shrink_kernel<1>, grid, dim3(kWaves * 64), 0, s, x, ldx, T, K, l);
-    else
+    if (T <= kTokenWise) {
+        hipLaunchKernelGGL(lora_shrink_token_kernel, dim3((unsigned)T, (unsigned)(l.vld / 16)), dim3(kWaves * 64), 0, s,
+                           x, ldx, K, l);
+    } else {
+        const dim3 grid((unsigned)((T + 31) / 32), (unsigned)(l.n < 32 ? l.n : 32));
         hipLaunchKernelGGL(lora_shrink_kernel<2>, grid, dim3(kWaves * 64), 0, s, x, ldx, T, K, l);
+    }
     return hipGetLastError();
 }
 
