@@ -9,8 +9,13 @@ using namespace dense;
 
 template <bool XT, int EPI>
 static hipError_t launch_epi(const DenseArgs& a, hipStream_t s) {
-    if (dense_big_tiles(a, EPI))
-        return launch_tile<Tile<256, 256, 2, 4, XT, true, kEltBf16, EPI, false, false>>(a, s);
+    if (dense_big_tiles(a, EPI)) {
+        // With both operands transposed the 128-byte steps need more address
+        // registers than there are; half steps in four buffers fit (4096 x
+        // 3584 over 8192 tokens: 202 -> 181 us). With one they lose 3 %.
+        if constexpr (XT) return launch_tile<Tile<256, 256, 2, 4, XT, true, kEltBf16, EPI, false, false, 4, 64>>(a, s);
+        else return launch_tile<Tile<256, 256, 2, 4, XT, true, kEltBf16, EPI, false, false>>(a, s);
+    }
     if (!dense_one_round(a, EPI)) return launch_tile<Tile<128, 128, 2, 2, XT, true, kEltBf16, EPI, false, false>>(a, s);
     // Too few 128 x 128 tiles for half of the compute units: 64 x 64 ones.
     const int64_t tiles = (int64_t)((a.M + 127) / 128) * ((a.N + 127) / 128);

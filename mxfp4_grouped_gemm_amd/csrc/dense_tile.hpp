@@ -40,7 +40,6 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kEltBf16 = 0, kEltMx8 = 1;
-constexpr int kRowBytes = 128;  // bytes of K a step
 constexpr int kGroupM = 4;      // tiles of M that share a column of W tiles
 // Every load's record: masked lanes carry kOob, the others stay inside the
 // tensor by construction (the tile's base is a 64-bit address).
@@ -66,6 +65,26 @@ __device__ __forceinline__ void spread() {
     }
 }
 
+template <int W>
+__device__ __forceinline__ void load_words(uint32_t (&d)[W], const void* p) {
+    if constexpr (W == 4) {
+        const u32x4 u = *(const u32x4*)p;
+        d[0] = u[0], d[1] = u[1], d[2] = u[2], d[3] = u[3];
+    } else {
+        const u32x2 u = *(const u32x2*)p;
+        d[0] = u[0], d[1] = u[1];
+    }
+}
+
+// Four or eight consecutive outputs, rounded.
+template <int V>
+__device__ __forceinline__ void store_bf16(uint16_t* p, const float* v) {
+    if constexpr (V == 8)
+        *(u32x4*)p = u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+    else
+        *(u32x2*)p = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+}
+
 // Waits until at most LOADS of this wave's loads are in flight and its LDS
 // reads are done, then for the workgroup. Loads complete in order, so what is
 // left in flight are the latest steps'.
@@ -83,8 +102,10 @@ __device__ __forceinline__ void sync_step() {
 // per output.
 __device__ __forceinline__ float sigmoid(float g) { return 1.0f / (1.0f + expf(-g)); }
 
-template <int BM_, int BN_, int WM_, int WN_, bool XT_, bool WT_, int ELT_, int EPI_, bool SPLIT_, bool LORA_, int NB_ = 2>
+template <int BM_, int BN_, int WM_, int WN_, bool XT_, bool WT_, int ELT_, int EPI_, bool SPLIT_, bool LORA_, int NB_ = 2,
+          int KB_ = 128>
 struct Tile {
+    static constexpr int KB = KB_;  // bytes of K a step
     static constexpr int NB = NB_;  // LDS buffers
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, ELT = ELT_, EPI = EPI_;
     static constexpr bool XT = XT_, WT = WT_, SPLIT = SPLIT_, LORA = LORA_;
@@ -93,9 +114,9 @@ struct Tile {
     static constexpr int FM = BM / WM / 16, FN = BN / WN / 16;
     static constexpr int F = GATED ? FN / 2 : FN;      // fragments of one column set
     static constexpr int BNC = GATED ? BN / 2 : BN;    // output columns (pairs) of a tile
-    static constexpr int BK = ELT == kEltBf16 ? 64 : 128;
     static constexpr int ESZ = ELT == kEltBf16 ? 2 : 1;
-    static constexpr int XBYTES = BM * kRowBytes, WBYTES = BN * kRowBytes;
+    static constexpr int BK = KB / ESZ;
+    static constexpr int XBYTES = BM * KB, WBYTES = BN * KB;
     static constexpr int SBYTES = ELT == kEltMx8 ? (BM + BN) * 4 : 0;  // scales of a step
     static constexpr int BUF = XBYTES + WBYTES + SBYTES;
     static constexpr int XL = XBYTES / 1024 / NW, WL = WBYTES / 1024 / NW;  // loads a wave issues per step
@@ -104,11 +125,14 @@ struct Tile {
 };
 
 // Swizzle keys (see the top).
-__device__ __forceinline__ int key_x(int r) { return (r >> 1) & 7; }
-template <int F>
+template <int KB>
+__device__ __forceinline__ int key_x(int r) {
+    return KB == 128 ? (r >> 1) & 7 : (r >> 2) & 3;
+}
+template <int KB, int F>
 __device__ __forceinline__ int key_w(int r) {
-    constexpr int s = F == 8 ? 5 : F == 4 ? 4 : F == 2 ? 3 : 2;
-    return ((r >> 1) & 1) | (((r >> s) & 3) << 1);
+    constexpr int s = F == 4 ? 4 : F == 2 ? 3 : 2;
+    return KB == 128 ? ((r >> 1) & 1) | (((r >> s) & 3) << 1) : (r >> s) & 3;
 }
 template <int PIECES>
 __device__ __forceinline__ int key_t(int k) {
@@ -244,16 +268,17 @@ __global__ __launch_bounds__(C::THREADS, 2) void dense_kernel(DenseArgs a) {
     const char* xb = (const char*)a.x + (C::XT ? (int64_t)m0 : (int64_t)m0 * a.ldx) * C::ESZ;
     const char* wb = (const char*)a.w + (C::WT ? (int64_t)n0 : (int64_t)n0 * a.ldw) * C::ESZ;
     uint32_t xo[C::XL], wo[C::WL];
+    constexpr int kPieces = C::KB / 16;  // of a K-major row
     // K of a piece in its step (elements).
     auto xk = [&](int i) {
         const int p = (w * C::XL + i) * 64 + lane;
         if constexpr (C::XT) return (w * C::XL * 64 + lane) / (C::BM / 8) + i * 64 / (C::BM / 8);
-        else return ((p & 7) ^ key_x(p >> 3)) * (16 / C::ESZ);
+        else return ((p % kPieces) ^ key_x<C::KB>(p / kPieces)) * (16 / C::ESZ);
     };
     auto wk = [&](int i) {
         const int p = (w * C::WL + i) * 64 + lane;
         if constexpr (C::WT) return (w * C::WL * 64 + lane) / (C::BN / 8) + i * 64 / (C::BN / 8);
-        else return ((p & 7) ^ key_w<C::F>(p >> 3)) * (16 / C::ESZ);
+        else return ((p % kPieces) ^ key_w<C::KB, C::F>(p / kPieces)) * (16 / C::ESZ);
     };
 #pragma unroll
     for (int i = 0; i < C::XL; ++i) {
@@ -263,7 +288,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void dense_kernel(DenseArgs a) {
             const int k = p / PR, c = (p % PR) ^ key_t<PR>(k);
             xo[i] = m0 + c * 8 < a.M ? (uint32_t)(k * a.ldx * 2 + c * 16) : kOob;
         } else {
-            const int r = p >> 3, c = (p & 7) ^ key_x(r);
+            const int r = p / kPieces, c = (p % kPieces) ^ key_x<C::KB>(r);
             xo[i] = m0 + r < a.M ? (uint32_t)(r * a.ldx * C::ESZ + c * 16) : kOob;
         }
     }
@@ -275,7 +300,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void dense_kernel(DenseArgs a) {
             const int k = p / PR, c = (p % PR) ^ key_t<PR>(k);
             wo[i] = n0 + c * 8 < a.N ? (uint32_t)(k * a.ldw * 2 + c * 16) : kOob;
         } else {
-            const int r = p >> 3, c = (p & 7) ^ key_w<C::F>(r);
+            const int r = p / kPieces, c = (p % kPieces) ^ key_w<C::KB, C::F>(r);
             if constexpr (C::GATED) {
                 // Rows [0, BNC) of the tile are gate rows, the others the up
                 // rows, N rows further on: their own base (wo is 32 bits).
@@ -292,8 +317,8 @@ __global__ __launch_bounds__(C::THREADS, 2) void dense_kernel(DenseArgs a) {
     // Loads of step kt into a buffer. Pieces past the end of K (all of them
     // for a step past the end) get out-of-range offsets: zeros, no traffic.
     auto issue = [&](uint8_t* buf, int kt) {
-        const rsrc_t rx = make_rsrc(xb + (C::XT ? (int64_t)kt * C::BK * a.ldx * 2 : (int64_t)kt * kRowBytes), kRecord);
-        const int64_t wadv = C::WT ? (int64_t)kt * C::BK * a.ldw * 2 : (int64_t)kt * kRowBytes;
+        const rsrc_t rx = make_rsrc(xb + (C::XT ? (int64_t)kt * C::BK * a.ldx * 2 : (int64_t)kt * C::KB), kRecord);
+        const int64_t wadv = C::WT ? (int64_t)kt * C::BK * a.ldw * 2 : (int64_t)kt * C::KB;
         const rsrc_t rw = make_rsrc(wb + wadv, kRecord);
         const rsrc_t ru = make_rsrc(wb + wadv + up, kRecord);
         const int left = kend - kt * C::BK;
@@ -302,7 +327,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void dense_kernel(DenseArgs a) {
             load_lds16(rx, buf + (w * C::XL + i) * 1024, xk(i) < left ? xo[i] : kOob, 0);
 #pragma unroll
         for (int i = 0; i < C::WL; ++i) {
-            const bool second = C::GATED && (w * C::WL + i) * 8 >= C::BNC;  // 8 rows a load: uniform
+            const bool second = C::GATED && (w * C::WL + i) * (64 / kPieces) >= C::BNC;  // whole loads: uniform
             load_lds16(second ? ru : rw, buf + C::XBYTES + (w * C::WL + i) * 1024, wk(i) < left ? wo[i] : kOob, 0);
         }
     };
@@ -365,11 +390,11 @@ __global__ __launch_bounds__(C::THREADS, 2) void dense_kernel(DenseArgs a) {
     const int xr0 = wm * C::FM * 16;
     auto read_x = [&](const uint8_t* buf, int fm, int piece) -> u32x4 {
         const int r = xr0 + fm * 16 + l16;
-        return *(const u32x4*)(buf + r * kRowBytes + ((piece ^ key_x(r)) << 4));
+        return *(const u32x4*)(buf + r * C::KB + ((piece ^ key_x<C::KB>(r)) << 4));
     };
     auto read_w = [&](const uint8_t* buf, int f, int piece) -> u32x4 {
         const int r = wrow(f, l16);
-        return *(const u32x4*)(buf + C::XBYTES + r * kRowBytes + ((piece ^ key_w<C::F>(r)) << 4));
+        return *(const u32x4*)(buf + C::XBYTES + r * C::KB + ((piece ^ key_w<C::KB, C::F>(r)) << 4));
     };
     // Transposed operand: columns c0 + 0..15 of K rows 32 s + 8 g + 0..7.
     auto read_t = [&](const uint8_t* base, auto pieces, int c0, int s) -> bf16x8 {
@@ -394,11 +419,11 @@ __global__ __launch_bounds__(C::THREADS, 2) void dense_kernel(DenseArgs a) {
         // landed, so the buffer takes the loads of the step after the next.
         constexpr int FH = C::FM / 2;
         bf16x8 xf[2][FH], wf[2][C::FN];
-        auto read_ws = [&](const uint8_t* buf, int s) {
+        auto read_ws = [&](const uint8_t* buf, int s, int set) {
 #pragma unroll
             for (int f = 0; f < C::FN; ++f) {
-                if constexpr (C::WT) wf[s][f] = read_t(buf + C::XBYTES, std::integral_constant<int, C::BN / 8>(), (wn * C::FN + f) * 16, s);
-                else wf[s][f] = __builtin_bit_cast(bf16x8, read_w(buf, f, 4 * s + g));
+                if constexpr (C::WT) wf[set][f] = read_t(buf + C::XBYTES, std::integral_constant<int, C::BN / 8>(), (wn * C::FN + f) * 16, s);
+                else wf[set][f] = __builtin_bit_cast(bf16x8, read_w(buf, f, 4 * s + g));
             }
         };
         auto read_xs = [&](const uint8_t* buf, int s, int h) {
@@ -416,24 +441,27 @@ __global__ __launch_bounds__(C::THREADS, 2) void dense_kernel(DenseArgs a) {
                     acc[i][h * FH + j] = mfma16x16x32(wf[s][i], xf[h][j], acc[i][h * FH + j]);
         };
         constexpr int kXR = FH * (C::XT ? 2 : 1), kWR = C::FN * (C::WT ? 2 : 1), kMfma = C::FN * FH;
-        auto step = [&](uint8_t* cur, uint8_t* nxt, int kt) {
+        auto step = [&](uint8_t* cur, uint8_t* nxt, int ws, int kt) {
             read_xs(cur, 0, 1);
-            multiply(0, 0);
+            multiply(ws, 0);
             spread<kXR, 0, kMfma>();
-            __builtin_amdgcn_sched_barrier(0);
-            read_ws(cur, 1);
-            read_xs(cur, 1, 0);
-            multiply(0, 1);
-            spread<kXR + kWR, 0, kMfma>();
-            __builtin_amdgcn_sched_barrier(0);
-            read_xs(cur, 1, 1);
-            multiply(1, 0);
-            spread<kXR, 0, kMfma>();
+            if constexpr (C::KB == 128) {
+                __builtin_amdgcn_sched_barrier(0);
+                read_ws(cur, 1, 1);
+                read_xs(cur, 1, 0);
+                multiply(0, 1);
+                spread<kXR + kWR, 0, kMfma>();
+                __builtin_amdgcn_sched_barrier(0);
+                read_xs(cur, 1, 1);
+                multiply(1, 0);
+                spread<kXR, 0, kMfma>();
+            }
             sync_step<(C::NB - 2) * (C::XL + C::WL)>();
             issue(cur, kt + C::NB);
-            read_ws(nxt, 0);
+            if constexpr (C::KB == 128) read_ws(nxt, 0, 0);
+            else read_ws(nxt, 0, ws ^ 1);
             read_xs(nxt, 0, 0);
-            multiply(1, 1);
+            multiply(C::KB == 128 ? 1 : ws, 1);
             spread<kXR + kWR, C::XL + C::WL, kMfma>();
             __builtin_amdgcn_sched_barrier(0);
         };
@@ -446,19 +474,19 @@ __global__ __launch_bounds__(C::THREADS, 2) void dense_kernel(DenseArgs a) {
                 issue(s3, kt0 + 3);
             }
             sync_step<(C::NB - 1) * (C::XL + C::WL)>();
-            read_ws(s0, 0);
+            read_ws(s0, 0, 0);
             read_xs(s0, 0, 0);
             // A step for each buffer a turn; a step past the end multiplies
             // zeros.
             for (int kt = kt0; kt < kt1; kt += C::NB) {
                 if constexpr (C::NB == 2) {
-                    step(s0, s1, kt);
-                    step(s1, s0, kt + 1);
+                    step(s0, s1, 0, kt);
+                    step(s1, s0, C::KB == 128 ? 0 : 1, kt + 1);
                 } else {
-                    step(s0, s1, kt);
-                    step(s1, s2, kt + 1);
-                    step(s2, s3, kt + 2);
-                    step(s3, s0, kt + 3);
+                    step(s0, s1, 0, kt);
+                    step(s1, s2, C::KB == 128 ? 0 : 1, kt + 1);
+                    step(s2, s3, 0, kt + 2);
+                    step(s3, s0, C::KB == 128 ? 0 : 1, kt + 3);
                 }
             }
         }
@@ -566,22 +594,27 @@ __global__ __launch_bounds__(C::THREADS, 2) void dense_kernel(DenseArgs a) {
         const bool mok = m < a.M;
         if constexpr (C::EPI == kEpiOut) {
             if (!mok) continue;
+            // W fragments: groups of V consecutive outputs of the lane.
+            constexpr int V = C::WT || C::FN % 2 ? 4 : 8;
 #pragma unroll
-            for (int f = 0; f < C::FN; ++f) {
+            for (int f = 0; f < C::FN; f += V / 4) {
                 const int n = n_of(f);
                 if (n >= a.N) continue;
-                f32x4 v = acc[f][j];
+                float v[V];
+#pragma unroll
+                for (int e = 0; e < V; ++e) v[e] = acc[f + e / 4][j][e % 4];
                 if (a.addend) {
-                    const u32x2 d = *(const u32x2*)(a.addend + m * a.ldadd + n);
-                    v[0] += __uint_as_float(d[0] << 16);
-                    v[1] += __uint_as_float(d[0] & 0xffff0000u);
-                    v[2] += __uint_as_float(d[1] << 16);
-                    v[3] += __uint_as_float(d[1] & 0xffff0000u);
+                    uint32_t d[V / 2];
+                    load_words<V / 2>(d, a.addend + m * a.ldadd + n);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) v[e] += __uint_as_float(e & 1 ? d[e / 2] & 0xffff0000u : d[e / 2] << 16);
                 }
                 if (a.out_f32) {
-                    *(f32x4*)((float*)a.out + m * a.ldo + n) = v;
+#pragma unroll
+                    for (int e = 0; e < V; e += 4)
+                        *(f32x4*)((float*)a.out + m * a.ldo + n + e) = f32x4{v[e], v[e + 1], v[e + 2], v[e + 3]};
                 } else {
-                    *(u32x2*)((uint16_t*)a.out + m * a.ldo + n) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+                    store_bf16<V>((uint16_t*)a.out + m * a.ldo + n, v);
                 }
             }
         } else if constexpr (C::GATED) {
@@ -612,16 +645,22 @@ __global__ __launch_bounds__(C::THREADS, 2) void dense_kernel(DenseArgs a) {
                 }
             } else {
                 if (!mok) continue;
+                constexpr int V = C::F % 2 ? 4 : 8;
 #pragma unroll
-                for (int f = 0; f < C::F; ++f) {
+                for (int f = 0; f < C::F; f += V / 4) {
                     const int n = n_of(f);
                     if (n >= a.N) continue;
-                    *(u32x2*)((uint16_t*)a.out + m * a.ldo + n) = u32x2{pack_bf16x2(h[f][0], h[f][1]), pack_bf16x2(h[f][2], h[f][3])};
+                    store_bf16<V>((uint16_t*)a.out + m * a.ldo + n, &h[f][0]);
                     if (a.gate_up) {
                         uint16_t* gu = a.gate_up + m * 2 * (int64_t)a.N + n;
-                        const f32x4 gv = acc[f][j], uv = acc[f + C::F][j];
-                        *(u32x2*)gu = u32x2{pack_bf16x2(gv[0], gv[1]), pack_bf16x2(gv[2], gv[3])};
-                        *(u32x2*)(gu + a.N) = u32x2{pack_bf16x2(uv[0], uv[1]), pack_bf16x2(uv[2], uv[3])};
+                        float gv[V], uv[V];
+#pragma unroll
+                        for (int e = 0; e < V; ++e) {
+                            gv[e] = acc[f + e / 4][j][e % 4];
+                            uv[e] = acc[f + C::F + e / 4][j][e % 4];
+                        }
+                        store_bf16<V>(gu, gv);
+                        store_bf16<V>(gu + a.N, uv);
                     }
                 }
             }
