@@ -548,6 +548,13 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _like(t, stride, cols, stream):
+    """A contiguous tensor of t's shape and type."""
+    if stream is None and stride == cols:
+        return torch.empty_like(t)
+    return _empty(t.shape, t.dtype, t.device, stream)
+
+
 def _workspace(given, need, device, stream):
     """-> (address, bytes, the tensor that holds them)."""
     if need < 0:
@@ -595,13 +602,13 @@ def moe_rms_norm(x, weight, residual=None, eps=1e-6, weight_offset=0.0, mxfp8=Fa
         rdt = residual.dtype
     pw = _full(weight, "weight", (torch.bfloat16, torch.float32), (H,), device)
     if y is None:
-        y = _empty((T, H), torch.bfloat16, device, stream)
+        y = _like(x, ldx, H, stream)
         py, ldy = y.data_ptr(), H
     else:
         py, ldy = _rows(y, "y", torch.bfloat16, (T, H), device)
     po, ldo = None, H
     if residual_out is None and residual is not None:
-        residual_out = _empty((T, H), rdt, device, stream)
+        residual_out = _like(residual, ldr, H, stream)
         po = residual_out.data_ptr()
     elif residual_out is not None:
         po, ldo = _rows(residual_out, "residual_out", rdt or (torch.bfloat16, torch.float32), (T, H), device)
@@ -677,8 +684,10 @@ def moe_ffn_forward(x, w13, w2, addend=None, lora13=None, lora2=None, save_gate_
     c13, r13 = _lora(lora13, "lora13", T, H, 2 * I, device)
     c2, r2 = _lora(lora2, "lora2", T, I, H, device)
     if out is None:
-        out = _empty((T, H), torch.bfloat16, device, stream)
-    po, ldo = _rows(out, "out", torch.bfloat16, (T, H), device)
+        out = _like(x, ldx, H, stream)
+        po, ldo = out.data_ptr(), H
+    else:
+        po, ldo = _rows(out, "out", torch.bfloat16, (T, H), device)
     if gate_up is None and save_gate_up:
         gate_up = _empty((T, 2 * I), torch.bfloat16, device, stream)
     pg = None if gate_up is None else _full(gate_up, "gate_up", torch.bfloat16, (T, 2 * I), device)
@@ -711,7 +720,9 @@ def moe_ffn_forward_mxfp8(x, x_scale, w13, w13_scale, w2, w2_scale, addend=None,
     pa, lda = (None, H) if addend is None else _rows(addend, "addend", torch.bfloat16, (T, H), device)
     if out is None:
         out = _empty((T, H), torch.bfloat16, device, stream)
-    po, ldo = _rows(out, "out", torch.bfloat16, (T, H), device)
+        po, ldo = out.data_ptr(), H
+    else:
+        po, ldo = _rows(out, "out", torch.bfloat16, (T, H), device)
     pws, nws, _ws = _workspace(workspace, lib.moe_ffn_mxfp8_workspace_size(T, H, I), device, stream)
     _run(device, stream, lib.moe_ffn_forward_mxfp8,
          px, pxs, p13, p13s, p2, p2s, act, pa, lda, T, H, I, po, ldo,

@@ -128,20 +128,24 @@ bool skinny(int T, int64_t rows, int K, int elt) {
     return T <= moe::kSkinnyMaxTokens && rows * K * (elt == 0 ? 2 : 1) <= kMaxSkinnyBytes;
 }
 
-// Bytes of split-K partials of a forward product.
-int64_t partial_bytes(int T, int N, int K, int elt, int epi) {
-    if (skinny(T, epi == moe::kEpiOut ? N : 2 * (int64_t)N, K, elt)) return 0;
-    const moe::DenseArgs a = product(nullptr, K, nullptr, K, T, N, K, nullptr, N);
-    return align_up(moe::dense_partial_bytes(a, moe::dense_splits(a, moe::kNT, elt, epi), epi), 256);
+int splits_of(const moe::DenseArgs& a, int elt, int epi, bool few) {
+    return few ? moe::skinny_splits(a, elt, epi) : moe::dense_splits(a, moe::kNT, elt, epi);
 }
 
-// A forward product in the kernels its size takes.
-hipError_t run_product(moe::DenseArgs& a, int elt, int epi, float* partial, hipStream_t s) {
-    if (skinny(a.M, epi == moe::kEpiOut ? a.N : 2 * (int64_t)a.N, a.K, elt))
-        return moe::launch_skinny(a, elt, epi, nullptr, s);
-    a.splits = moe::dense_splits(a, moe::kNT, elt, epi);
+// Bytes of split-K partials of a forward product; few: in the few-token
+// kernels, which join the products of adapters (rank > 0) in any case.
+int64_t partial_bytes(int T, int N, int K, int elt, int epi, bool few, int rank) {
+    moe::DenseArgs a = product(nullptr, K, nullptr, K, T, N, K, nullptr, N);
+    a.lora.n = rank > 0;
+    a.lora.rank = rank;
+    return align_up(moe::dense_partial_bytes(a, splits_of(a, elt, epi, few), epi, few && rank > 0), 256);
+}
+
+// A forward product. h_f32: see launch_skinny.
+hipError_t run_product(moe::DenseArgs& a, int elt, int epi, bool few, float* partial, const float* h_f32, hipStream_t s) {
+    a.splits = splits_of(a, elt, epi, few);
     a.partial = partial;
-    return moe::launch_dense(a, moe::kNT, elt, epi, s);
+    return few ? moe::launch_skinny(a, elt, epi, h_f32, s) : moe::launch_dense(a, moe::kNT, elt, epi, s);
 }
 
 struct FfnLayout {
@@ -151,7 +155,8 @@ struct FfnLayout {
 FfnLayout ffn_layout(int T, int H, int I, int rank13, int rank2) {
     FfnLayout L;
     const int vld = vld_of(rank13 > rank2 ? rank13 : rank2);
-    const int64_t p1 = partial_bytes(T, I, H, 0, moe::kEpiGated), p2 = partial_bytes(T, H, I, 0, moe::kEpiOut);
+    const int64_t p1 = partial_bytes(T, I, H, 0, moe::kEpiGated, skinny(T, 2 * (int64_t)I, H, 0), rank13);
+    const int64_t p2 = partial_bytes(T, H, I, 0, moe::kEpiOut, skinny(T, H, I, 0), rank2);
     L.h = 0;
     L.hs = 0;
     L.v = align_up((int64_t)T * I * 2, 256);
@@ -164,19 +169,14 @@ bool mx_skinny(int T, int H, int I) { return skinny(T, 2 * (int64_t)I, H, 1) && 
 
 FfnLayout ffn_mx_layout(int T, int H, int I) {
     FfnLayout L;
+    const bool few = mx_skinny(T, H, I);
+    const int64_t p1 = partial_bytes(T, I, H, 1, moe::kEpiGatedMx, few, 0), p2 = partial_bytes(T, H, I, 1, moe::kEpiOut, few, 0);
     L.h = 0;
     L.v = 0;
-    if (mx_skinny(T, H, I)) {
-        L.hs = L.partial = L.total = align_up((int64_t)T * I * 4, 256);  // h in fp32
-        return L;
-    }
-    const moe::DenseArgs a1 = product(nullptr, H, nullptr, H, T, I, H, nullptr, I);
-    const moe::DenseArgs a2 = product(nullptr, I, nullptr, I, T, H, I, nullptr, H);
-    const int64_t p1 = moe::dense_partial_bytes(a1, moe::dense_splits(a1, moe::kNT, 1, moe::kEpiGatedMx), moe::kEpiGatedMx);
-    const int64_t p2 = moe::dense_partial_bytes(a2, moe::dense_splits(a2, moe::kNT, 1, moe::kEpiOut), moe::kEpiOut);
-    L.hs = align_up((int64_t)T * I, 256);
-    L.partial = L.hs + align_up((int64_t)T * (I / 32), 256);
-    L.total = L.partial + align_up(p1 > p2 ? p1 : p2, 256);
+    // h: fp32 for the few-token kernels, else codes and scales.
+    L.hs = align_up((int64_t)T * I * (few ? 4 : 1), 256);
+    L.partial = L.hs + (few ? 0 : align_up((int64_t)T * (I / 32), 256));
+    L.total = L.partial + (p1 > p2 ? p1 : p2);
     return L;
 }
 
@@ -254,7 +254,7 @@ moe_status moe_rms_norm(const uint16_t* x, int64_t x_stride, const void* residua
 
 int64_t moe_lora_linear_workspace_size(int T, int K, int N, int rank) {
     if (!valid_sizes(T, K, N, 8) || !valid_rank(rank)) return -1;
-    return align_up((int64_t)T * vld_of(rank) * 4, 256) + partial_bytes(T, N, K, 0, moe::kEpiOut);
+    return align_up((int64_t)T * vld_of(rank) * 4, 256) + partial_bytes(T, N, K, 0, moe::kEpiOut, skinny(T, N, K, 0), rank);
 }
 
 moe_status moe_lora_linear(const uint16_t* x, int64_t x_stride, const uint16_t* w, const moe_lora* lora, int T, int K,
@@ -278,8 +278,8 @@ moe_status moe_lora_linear(const uint16_t* x, int64_t x_stride, const uint16_t* 
     a.out_f32 = out_type == MOE_DT_F32;
     a.lora = lora_args(lora, workspace);
     float* partial = (float*)((char*)workspace + align_up((int64_t)T * a.lora.vld * 4, 256));
-    if (lora) LAUNCH(moe::launch_lora_shrink(x, x_stride, T, K, a.lora, s), "moe_lora_linear (shrink)");
-    return hip_status(run_product(a, 0, moe::kEpiOut, partial, s), fn);
+    if (lora && !skinny(T, N, K, 0)) LAUNCH(moe::launch_lora_shrink(x, x_stride, T, K, a.lora, s), "moe_lora_linear (shrink)");
+    return hip_status(run_product(a, 0, moe::kEpiOut, skinny(T, N, K, 0), partial, nullptr, s), fn);
 }
 
 int64_t moe_ffn_workspace_size(int T, int H, int I, int rank13, int rank2) {
@@ -314,14 +314,16 @@ moe_status moe_ffn_forward(const uint16_t* x, int64_t x_stride, const uint16_t* 
     moe::DenseArgs a = product(x, x_stride, w13, H, T, I, H, h, I);
     a.gate_up = gate_up;
     a.lora = lora_args(lora13, ws + L.v);
-    if (lora13) LAUNCH(moe::launch_lora_shrink(x, x_stride, T, H, a.lora, s), "moe_ffn_forward (gate_up shrink)");
-    LAUNCH(run_product(a, 0, moe::kEpiGated, (float*)(ws + L.partial), s), "moe_ffn_forward (gate_up)");
+    if (lora13 && !skinny(T, 2 * (int64_t)I, H, 0))
+        LAUNCH(moe::launch_lora_shrink(x, x_stride, T, H, a.lora, s), "moe_ffn_forward (gate_up shrink)");
+    LAUNCH(run_product(a, 0, moe::kEpiGated, skinny(T, 2 * (int64_t)I, H, 0), (float*)(ws + L.partial), nullptr, s), "moe_ffn_forward (gate_up)");
     a = product(h, I, w2, I, T, H, I, out, out_stride);
     a.addend = addend;
     a.ldadd = addend_stride;
     a.lora = lora_args(lora2, ws + L.v);
-    if (lora2) LAUNCH(moe::launch_lora_shrink(h, I, T, I, a.lora, s), "moe_ffn_forward (down shrink)");
-    return hip_status(run_product(a, 0, moe::kEpiOut, (float*)(ws + L.partial), s), "moe_ffn_forward (down)");
+    if (lora2 && !skinny(T, H, I, 0))
+        LAUNCH(moe::launch_lora_shrink(h, I, T, I, a.lora, s), "moe_ffn_forward (down shrink)");
+    return hip_status(run_product(a, 0, moe::kEpiOut, skinny(T, H, I, 0), (float*)(ws + L.partial), nullptr, s), "moe_ffn_forward (down)");
 }
 
 int64_t moe_ffn_mxfp8_workspace_size(int T, int H, int I) {
@@ -355,18 +357,17 @@ moe_status moe_ffn_forward_mxfp8(const uint8_t* x, const uint8_t* x_scale, const
     a2.ws = w2_scale;
     a2.addend = addend;
     a2.ldadd = addend_stride;
-    if (mx_skinny(T, H, I)) {
+    float* partial = (float*)(ws + L.partial);
+    const bool few = mx_skinny(T, H, I);
+    if (few) {
         a1.out_f32 = 1;
-        LAUNCH(moe::launch_skinny(a1, 1, moe::kEpiGated, nullptr, s), "moe_ffn_forward_mxfp8 (gate_up)");
-        return hip_status(moe::launch_skinny(a2, 1, moe::kEpiOut, (const float*)(ws + L.h), s), "moe_ffn_forward_mxfp8 (down)");
+    } else {
+        a1.hs = (uint8_t*)(ws + L.hs);
+        a2.xs = (const uint8_t*)(ws + L.hs);
     }
-    a1.hs = (uint8_t*)(ws + L.hs);
-    a1.partial = a2.partial = (float*)(ws + L.partial);
-    a1.splits = moe::dense_splits(a1, moe::kNT, 1, moe::kEpiGatedMx);
-    LAUNCH(moe::launch_dense(a1, moe::kNT, 1, moe::kEpiGatedMx, s), "moe_ffn_forward_mxfp8 (gate_up)");
-    a2.xs = (const uint8_t*)(ws + L.hs);
-    a2.splits = moe::dense_splits(a2, moe::kNT, 1, moe::kEpiOut);
-    return hip_status(moe::launch_dense(a2, moe::kNT, 1, moe::kEpiOut, s), "moe_ffn_forward_mxfp8 (down)");
+    LAUNCH(run_product(a1, 1, few ? moe::kEpiGated : moe::kEpiGatedMx, few, partial, nullptr, s), "moe_ffn_forward_mxfp8 (gate_up)");
+    return hip_status(run_product(a2, 1, moe::kEpiOut, few, partial, few ? (const float*)(ws + L.h) : nullptr, s),
+                      "moe_ffn_forward_mxfp8 (down)");
 }
 
 int64_t moe_ffn_backward_workspace_size(int T, int H, int I) {

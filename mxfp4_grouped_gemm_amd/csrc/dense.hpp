@@ -56,8 +56,9 @@ enum DenseOrder { kNT = 0, kNN = 1, kTN = 2 };  // (X K-major, W K-major), (X K-
 // splits the launcher would take for this product, and the bytes of `partial`
 // that they need.
 int dense_splits(const DenseArgs& a, int order, int elt, int epi);
-inline int64_t dense_partial_bytes(const DenseArgs& a, int splits, int epi) {
-    return splits <= 1 ? 0 : (int64_t)splits * a.M * a.N * (epi == kEpiOut || epi == kEpiGatedBwd ? 1 : 2) * 4;
+// (join: the product is joined by a second kernel even if splits == 1).
+inline int64_t dense_partial_bytes(const DenseArgs& a, int splits, int epi, bool join) {
+    return splits <= 1 && !join ? 0 : (int64_t)splits * a.M * a.N * (epi == kEpiOut || epi == kEpiGatedBwd ? 1 : 2) * 4;
 }
 bool dense_big_tiles(const DenseArgs& a, int epi);
 bool dense_one_round(const DenseArgs& a, int epi);
@@ -72,6 +73,10 @@ constexpr int kSkinnyMaxTokens = 64;
 // elt 0: bf16; 1: MXFP8 activations and weights. h_f32: the fp32 h of the
 // MXFP8 block between its two products (written by kEpiGated, and read and
 // quantised by the second product).
+// Parts of K that launch_skinny takes for this product (a.splits).
+int skinny_splits(const DenseArgs& a, int elt, int epi);
+bool skinny_wide(const DenseArgs& a, bool gated);
+int skinny_narrow(const DenseArgs& a);  // workgroups of the adapters' narrow product
 hipError_t launch_skinny(const DenseArgs& a, int elt, int epi, const float* h_f32, hipStream_t s);
 
 // v[t] = scale * A[index[t]] x[t].

@@ -1,0 +1,83 @@
+// The end of a dense product for four consecutive outputs of one token: used
+// by the few-token kernels and by the kernel that joins a split K.
+#pragma once
+
+#include "common.hpp"
+#include "dense.hpp"
+
+namespace moe {
+namespace dense {
+
+// scale * B[a] (A[a] x) of one token for rows col..col+3 (and N + col.. of the
+// gated block), from v = scale * A[a] x: a dot product of at most a few
+// hundred elements.
+template <bool GATED>
+__device__ __forceinline__ void lora_dot(const LoraArgs& l, int N, int64_t token, int col, f32x4 (&low)[2]) {
+    const int ad = l.index[token];
+    if ((unsigned)ad >= (unsigned)l.n) return;
+    int rank = l.ranks ? l.ranks[ad] : l.rank;
+    rank = rank < l.rank ? rank : l.rank;
+    const uint16_t* b = l.b + ((int64_t)ad * (GATED ? 2 * (int64_t)N : N) + col) * l.rank;
+    const float* v = l.v + token * l.vld;
+    // Sixteen columns at a time; the first batch is loaded before the rank is
+    // known (v holds zeros from the rank to vld, and B has l.rank columns).
+    for (int k0 = 0;;) {
+        f32x4 vv[4];
+        u32x4 w[GATED ? 2 : 1][4][2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int k = k0 + 8 * h < l.rank ? k0 + 8 * h : k0;  // rank is a multiple of 8
+            vv[2 * h] = *(const f32x4*)(v + k);
+            vv[2 * h + 1] = *(const f32x4*)(v + k + 4);
+#pragma unroll
+            for (int s = 0; s < (GATED ? 2 : 1); ++s)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) w[s][r][h] = *(const u32x4*)(b + ((int64_t)s * N + r) * l.rank + k);
+        }
+#pragma unroll
+        for (int s = 0; s < (GATED ? 2 : 1); ++s)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    // Columns beyond the adapter's rank are not read as numbers.
+                    const uint32_t d = w[s][r][e / 8][e % 8 / 2];
+                    const float f = __uint_as_float(e & 1 ? d & 0xffff0000u : d << 16);
+                    if (k0 + e < rank) low[s][r] = fmaf(f, vv[e / 4][e % 4], low[s][r]);
+                }
+        k0 += 16;
+        if (k0 >= rank) break;
+    }
+}
+
+__device__ __forceinline__ u32x2 pack4(f32x4 v) { return u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])}; }
+
+// GATED: v gate, up up (saved to a.gate_up if asked for) -> silu(gate) * up;
+// else v + addend.
+template <bool GATED>
+__device__ __forceinline__ f32x4 finish4(const DenseArgs& a, int64_t token, int col, f32x4 v, f32x4 up) {
+    if constexpr (GATED) {
+        if (a.gate_up) {
+            uint16_t* gu = a.gate_up + token * 2 * (int64_t)a.N + col;
+            *(u32x2*)gu = pack4(v);
+            *(u32x2*)(gu + a.N) = pack4(up);
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[r] = swiglu(v[r], up[r]);
+    } else if (a.addend) {
+        const u32x2 d = *(const u32x2*)(a.addend + token * a.ldadd + col);
+        v[0] += __uint_as_float(d[0] << 16);
+        v[1] += __uint_as_float(d[0] & 0xffff0000u);
+        v[2] += __uint_as_float(d[1] << 16);
+        v[3] += __uint_as_float(d[1] & 0xffff0000u);
+    }
+    return v;
+}
+
+__device__ __forceinline__ void store4(const DenseArgs& a, int64_t token, int col, f32x4 v) {
+    if (a.out_f32) *(f32x4*)((float*)a.out + token * a.ldo + col) = v;
+    else *(u32x2*)((uint16_t*)a.out + token * a.ldo + col) = pack4(v);
+}
+
+}  // namespace dense
+}  // namespace moe

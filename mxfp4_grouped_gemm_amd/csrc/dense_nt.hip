@@ -1,5 +1,6 @@
 // Instances of the LDS-tiled product for the forward in bf16 (both operands
 // K-major), the choice of tile and K split, and the kernel that joins a split.
+#include "dense_epilogue.hpp"
 #include "dense_tile.hpp"
 
 namespace moe {
@@ -8,39 +9,27 @@ using namespace dense;
 
 namespace {
 
-// Sums the splits of a product in order and applies the epilogue. A thread
-// owns four columns (gated: four pairs).
+// Sums the parts of a split K in order, adds the low-rank term and applies
+// the epilogue. A thread owns four columns (gated: four pairs).
 template <int EPI>
-__global__ __launch_bounds__(256) void join_kernel(DenseArgs a) {
+__global__ __launch_bounds__(256) void join_kernel(DenseArgs a) {  // 64 or 256 threads
     constexpr bool kGated = EPI != kEpiOut;
-    const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t idx = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     const int per = a.N / 4;
     const int64_t m = idx / per;
     const int n = (int)(idx % per) * 4;
     const bool ok = m < a.M;  // N % 32 == 0 for MXFP8: eight threads a block, all of one row
     const int64_t cols = kGated ? 2 * (int64_t)a.N : a.N;
-    f32x4 v = {0, 0, 0, 0}, up = {0, 0, 0, 0};
+    f32x4 low[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+    if (ok && a.lora.n > 0) lora_dot<kGated>(a.lora, a.N, m, n, low);
+    f32x4 v = low[0], up = low[1];
     if (ok)
         for (int z = 0; z < a.splits; ++z) {
             const float* p = a.partial + ((int64_t)z * a.M + m) * cols + n;
             v += *(const f32x4*)p;
             if constexpr (kGated) up += *(const f32x4*)(p + a.N);
         }
-    if constexpr (kGated) {
-        if (ok && a.gate_up) {
-            uint16_t* gu = a.gate_up + m * 2 * (int64_t)a.N + n;
-            *(u32x2*)gu = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-            *(u32x2*)(gu + a.N) = u32x2{pack_bf16x2(up[0], up[1]), pack_bf16x2(up[2], up[3])};
-        }
-#pragma unroll
-        for (int r = 0; r < 4; ++r) v[r] = swiglu(v[r], up[r]);
-    } else if (ok && a.addend) {
-        const u32x2 d = *(const u32x2*)(a.addend + m * a.ldadd + n);
-        v[0] += __uint_as_float(d[0] << 16);
-        v[1] += __uint_as_float(d[0] & 0xffff0000u);
-        v[2] += __uint_as_float(d[1] << 16);
-        v[3] += __uint_as_float(d[1] & 0xffff0000u);
-    }
+    if (ok) v = finish4<kGated>(a, m, n, v, up);
     if constexpr (EPI == kEpiGatedMx) {
         float big = 0.0f;
 #pragma unroll
@@ -51,10 +40,8 @@ __global__ __launch_bounds__(256) void join_kernel(DenseArgs a) {
         if (!ok) return;
         *(uint32_t*)((uint8_t*)a.out + m * a.ldo + n) = mx8_pack4(v[0], v[1], v[2], v[3], mx8_inv_scale(sb));
         if ((n & 31) == 0) a.hs[m * (a.N / 32) + (n >> 5)] = (uint8_t)sb;
-    } else {
-        if (!ok) return;
-        if (a.out_f32) *(f32x4*)((float*)a.out + m * a.ldo + n) = v;
-        else *(u32x2*)((uint16_t*)a.out + m * a.ldo + n) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+    } else if (ok) {
+        store4(a, m, n, v);
     }
 }
 
@@ -63,7 +50,7 @@ hipError_t launch_epi(const DenseArgs& a, hipStream_t s) {
     if (dense_big_tiles(a, EPI))
         return launch_tile<Tile<256, 256, 2, 4, false, false, kEltBf16, EPI, false, LORA>>(a, s);
     if (a.splits > 1) {
-        const hipError_t e = launch_tile<Tile<128, 128, 2, 2, false, false, kEltBf16, EPI, true, LORA, 4>>(a, s);
+        const hipError_t e = launch_tile<Tile<128, 128, 2, 2, false, false, kEltBf16, EPI, true, false, 4>>(a, s);
         return e != hipSuccess ? e : launch_join(a, EPI, s);
     }
     if (dense_one_round(a, EPI)) return launch_tile<Tile<128, 128, 2, 2, false, false, kEltBf16, EPI, false, LORA, 4>>(a, s);
@@ -102,7 +89,9 @@ int dense_splits(const DenseArgs& a, int order, int elt, int epi) {
 
 hipError_t launch_join(const DenseArgs& a, int epi, hipStream_t s) {
     const int64_t threads = (int64_t)a.M * (a.N / 4);
-    const dim3 grid((unsigned)((threads + 255) / 256)), block(256);
+    // Small ones are latency: spread them over the compute units.
+    const int size = threads < 256 * 256 ? 64 : 256;
+    const dim3 grid((unsigned)((threads + size - 1) / size)), block(size);
     if (epi == kEpiOut) hipLaunchKernelGGL(join_kernel<kEpiOut>, grid, block, 0, s, a);
     else if (epi == kEpiGated) hipLaunchKernelGGL(join_kernel<kEpiGated>, grid, block, 0, s, a);
     else hipLaunchKernelGGL(join_kernel<kEpiGatedMx>, grid, block, 0, s, a);

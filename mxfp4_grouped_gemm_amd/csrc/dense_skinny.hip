@@ -7,12 +7,21 @@
 // (i, g) holds pieces g and 4 + g of row i), with the tokens' chunks, which
 // all workgroups read, coming from L2. A batch of chunks is loaded before the
 // first of them is multiplied, so most of a wave's bytes are one round trip.
-// The waves' sums meet in LDS, always in the same order.
+// The waves' sums meet in LDS, always in the same order. W is read with plain
+// loads (2048 pairs over K = 3584, one token: 6.8 us, 8.0 with streaming
+// ones).
 //
-// The low-rank term of an output is a dot product of at most a few hundred
-// elements that depends on the output's token: the thread that finishes the
-// output computes it, while the first batch of weights is on its way.
+// With more than 16 tokens the tokens' bytes count: every workgroup reads
+// T x K of them next to its 16 x K of W. There the workgroup takes 64 rows
+// and a part of K (or 16 rows, where W has few) and a second kernel joins the
+// parts.
+//
+// With adapters the narrow product v = scale * A x runs in workgroups of the
+// same launch (it is as short as a part of the product and does not depend on
+// it), and the joining kernel adds B v.
+#include "dense_epilogue.hpp"
 #include "dense_tile.hpp"
+#include "lora_shrink.hpp"
 
 namespace moe {
 
@@ -22,59 +31,53 @@ namespace {
 
 constexpr int kWaves = 8;
 
-// scale * B[a] (A[a] x) of one token for rows col..col+3 (and N + col.. of the
-// gated block), from v = scale * A[a] x.
-template <bool GATED>
-__device__ __forceinline__ void lora_dot(const LoraArgs& l, int N, int token, int col, f32x4 (&low)[2]) {
-    const int ad = l.index[token];
-    if ((unsigned)ad >= (unsigned)l.n) return;
-    int rank = l.ranks ? l.ranks[ad] : l.rank;
-    rank = rank < l.rank ? rank : l.rank;
-    const uint16_t* b = l.b + ((int64_t)ad * (GATED ? 2 * (int64_t)N : N) + col) * l.rank;
-    const float* v = l.v + (int64_t)token * l.vld;
-    for (int k = 0; k < rank; k += 8) {
-        const f32x4 v0 = *(const f32x4*)(v + k), v1 = *(const f32x4*)(v + k + 4);
-        u32x4 w[GATED ? 2 : 1][4];
-#pragma unroll
-        for (int s = 0; s < (GATED ? 2 : 1); ++s)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) w[s][r] = *(const u32x4*)(b + ((int64_t)s * N + r) * l.rank + k);
-#pragma unroll
-        for (int s = 0; s < (GATED ? 2 : 1); ++s)
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    // Columns beyond the adapter's rank are not read as numbers.
-                    const uint32_t d = w[s][r][e / 2];
-                    const float f = __uint_as_float(e & 1 ? d & 0xffff0000u : d << 16);
-                    const float t = (e < 4 ? v0[e & 3] : v1[e & 3]);
-                    if (k + e < rank) low[s][r] = fmaf(f, t, low[s][r]);
-                }
-    }
-}
-
 // ELT: see dense_tile.hpp. NJ: 16-token column blocks. XF32: X is fp32 and is
 // quantised to MXFP8 as it is read (the second product of the MXFP8 block).
-template <int ELT, int NJ, bool GATED, bool XF32, bool LORA>
+// NW: 16-row fragments of W. SPLIT: the workgroups take parts of K, into
+// a.partial; those past the last part take the narrow product of the adapters
+// (a token and 16 rows of its adapter each).
+template <int ELT, int NJ, int NW, bool GATED, bool XF32, bool SPLIT>
 __global__ __launch_bounds__(kWaves * 64) void skinny_kernel(DenseArgs a, const float* __restrict__ xf) {
     constexpr int BK = ELT == kEltBf16 ? 64 : 128;
     constexpr int ESZ = ELT == kEltBf16 ? 2 : 1;
     // Chunks in flight per wave: as many as the registers of two waves a SIMD
     // allow next to the tokens' operands.
-    constexpr int U = XF32 ? (NJ <= 2 ? 2 : 1) : ELT == kEltMx8 ? (NJ <= 2 ? 4 : 2) : NJ <= 2 ? 7 : 4;
-    __shared__ f32x4 red[kWaves][NJ][64];
+    constexpr int kRegs = NW * 8 + NJ * (XF32 ? 32 : 8);
+    constexpr int kFit = (NW * NJ > 8 ? 128 : 168) / kRegs;
+    constexpr int kMost = XF32 ? 2 : ELT == kEltMx8 ? 4 : 7;
+    constexpr int U = kFit < 1 ? 1 : kFit > kMost ? kMost : kFit;
+    __shared__ f32x4 red[kWaves][NW * NJ][64];
     const int tid = (int)threadIdx.x, lane = tid & 63;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int i = lane & 15, g = lane >> 4;
-    const int n0 = (int)blockIdx.x * (GATED ? 8 : 16);
+    constexpr int kRows = NW * (GATED ? 8 : 16);
+    int group = (int)blockIdx.x, part = 0;
+    if constexpr (SPLIT) {
+        const int groups = (a.N + kRows - 1) / kRows;
+        part = group / groups;
+        group %= groups;
+        if constexpr (ELT == kEltBf16) {
+            if (part >= a.splits) {
+                const int e = (int)blockIdx.x - groups * a.splits, per = (a.lora.rank + 15) / 16;
+                __shared__ f32x4 narrow[kShrinkWaves][4];
+                shrink_token((const uint16_t*)a.x, a.ldx, a.K, a.lora, e / per, e % per * 16, narrow);
+                return;
+            }
+        }
+    }
+    const int n0 = group * kRows;
     const int kb = a.K / 32;
 
-    const int n = GATED ? n0 + (i & 7) : n0 + i;
-    const int64_t wrow = n < a.N ? (int64_t)(GATED && i >= 8 ? a.N + n : n) : -1;
     // Weights of at most 2^31 bytes (checked by the caller of the launcher).
     const rsrc_t rw = make_rsrc(a.w, kRecord);
-    const uint32_t wo = wrow >= 0 ? (uint32_t)(wrow * a.ldw * ESZ) + 16u * g : kOob;
+    int64_t wrow[NW];
+    uint32_t wo[NW];
+#pragma unroll
+    for (int f = 0; f < NW; ++f) {
+        const int n = n0 + (GATED ? 8 * f + (i & 7) : 16 * f + i);
+        wrow[f] = n < a.N ? (int64_t)(GATED && i >= 8 ? a.N + n : n) : -1;
+        wo[f] = wrow[f] >= 0 ? (uint32_t)(wrow[f] * a.ldw * ESZ) + 16u * g : kOob;
+    }
     const rsrc_t rx = make_rsrc(XF32 ? (const void*)xf : a.x, kRecord);
     uint32_t xo[NJ];
     int m[NJ];
@@ -83,24 +86,29 @@ __global__ __launch_bounds__(kWaves * 64) void skinny_kernel(DenseArgs a, const 
         m[j] = 16 * j + i;
         xo[j] = m[j] < a.M ? (uint32_t)(m[j] * a.ldx * (XF32 ? 4 : ESZ)) + (XF32 ? 64u : 16u) * g : kOob;
     }
-    f32x4 acc[1][NJ];
+    f32x4 acc[NW][NJ];
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) acc[0][j] = f32x4{0, 0, 0, 0};
+    for (int f = 0; f < NW; ++f)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) acc[f][j] = f32x4{0, 0, 0, 0};
 
     const int nch = (a.K + BK - 1) / BK;
+    const int cbeg = SPLIT ? (int)((int64_t)nch * part / a.splits) : 0;
+    const int cend = SPLIT ? (int)((int64_t)nch * (part + 1) / a.splits) : nch;
     const rsrc_t rws = make_rsrc(a.ws, kRecord), rxs = make_rsrc(a.xs, kRecord);
-    u32x4 wv[U][2], xv[U][NJ][XF32 ? 8 : 2];
-    uint32_t ws[U], xs[U][NJ];
+    u32x4 wv[U][NW][2], xv[U][NJ][XF32 ? 8 : 2];
+    uint32_t ws[U][NW], xs[U][NJ];
     auto load = [&](int c0) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int c = c0 + kWaves * u;
-            const int left = a.K - c * BK;  // <= 0 past the end: everything masked
+            const int left = c < cend ? a.K - c * BK : 0;  // <= 0 past the end: everything masked
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int k = (4 * h + g) * (16 / ESZ);
                 const bool ok = k < left;
-                wv[u][h] = bld16nt(rw, ok && wo != kOob ? wo + c * 128 + 64 * h : kOob);
+#pragma unroll
+                for (int f = 0; f < NW; ++f) wv[u][f][h] = bld16(rw, ok && wo[f] != kOob ? wo[f] + c * 128 + 64 * h : kOob);
 #pragma unroll
                 for (int j = 0; j < NJ; ++j) {
                     if constexpr (XF32) {
@@ -115,8 +123,10 @@ __global__ __launch_bounds__(kWaves * 64) void skinny_kernel(DenseArgs a, const 
             if constexpr (ELT == kEltMx8) {
                 // Byte of block g of the chunk; blocks past the end have zero codes.
                 const int b = 4 * c + g;
-                ws[u] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(
-                    rws, wrow >= 0 && b < kb ? (uint32_t)(wrow * kb) + (uint32_t)b : kOob, 0, 0);
+#pragma unroll
+                for (int f = 0; f < NW; ++f)
+                    ws[u][f] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(
+                        rws, wrow[f] >= 0 && b < kb ? (uint32_t)(wrow[f] * kb) + (uint32_t)b : kOob, 0, 0);
                 if constexpr (!XF32) {
 #pragma unroll
                     for (int j = 0; j < NJ; ++j)
@@ -127,18 +137,14 @@ __global__ __launch_bounds__(kWaves * 64) void skinny_kernel(DenseArgs a, const 
         }
         __builtin_amdgcn_sched_barrier(0);  // all of the batch in flight
     };
-    load(w);
-    // Thread (j, token, q) finishes rows 4q..4q+3 of the tile (gated: pairs,
-    // with the up rows in q + 2).
-    constexpr int Q = GATED ? 2 : 4;
-    const int fj = tid / (16 * Q), fq = (tid / 16) % Q, token = 16 * fj + i;
-    const int col = n0 + 4 * fq;
-    const bool finish = tid < NJ * 16 * Q && token < a.M && col < a.N;
-    f32x4 low[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-    if constexpr (LORA) {
-        if (finish) lora_dot<GATED>(a.lora, a.N, token, col, low);
-    }
-    for (int c0 = w;;) {
+    load(cbeg + w);
+    // Item (f, j, q, token): rows 4q..4q+3 of fragment f (gated: pairs, with
+    // the up rows in q + 2), token 16 j + i. A thread finishes items tid,
+    // tid + 512, ... (e % 16 == i for all of them).
+    constexpr int Q = GATED ? 2 : 4, kItems = NW * NJ * 16 * Q;
+    auto col_of = [&](int e) { return n0 + e / (NJ * 16 * Q) * (GATED ? 8 : 16) + 4 * (e / 16 % Q); };
+    auto token_of = [&](int e) { return 16 * (e / (16 * Q) % NJ) + i; };
+    for (int c0 = cbeg + w;;) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
 #pragma unroll
@@ -146,7 +152,10 @@ __global__ __launch_bounds__(kWaves * 64) void skinny_kernel(DenseArgs a, const 
                 if constexpr (ELT == kEltBf16) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
-                        acc[0][j] = mfma16x16x32(__builtin_bit_cast(bf16x8, wv[u][h]), __builtin_bit_cast(bf16x8, xv[u][j][h]), acc[0][j]);
+#pragma unroll
+                        for (int f = 0; f < NW; ++f)
+                            acc[f][j] = mfma16x16x32(__builtin_bit_cast(bf16x8, wv[u][f][h]),
+                                                     __builtin_bit_cast(bf16x8, xv[u][j][h]), acc[f][j]);
                 } else {
                     i32x8 xq;
                     uint32_t sx;
@@ -181,77 +190,99 @@ __global__ __launch_bounds__(kWaves * 64) void skinny_kernel(DenseArgs a, const 
                         xq = __builtin_bit_cast(i32x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
                         sx = xs[u][j];
                     }
-                    const u32x4 lo = wv[u][0], hi = wv[u][1];
-                    const i32x8 wq = __builtin_bit_cast(i32x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-                    acc[0][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wq, xq, acc[0][j], 0, 0, 0, (int)ws[u], 0, (int)sx);
+#pragma unroll
+                    for (int f = 0; f < NW; ++f) {
+                        const u32x4 lo = wv[u][f][0], hi = wv[u][f][1];
+                        const i32x8 wq = __builtin_bit_cast(i32x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+                        acc[f][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wq, xq, acc[f][j], 0, 0, 0,
+                                                                                     (int)ws[u][f], 0, (int)sx);
+                    }
                 }
             }
         }
         c0 += kWaves * U;
-        if (c0 >= nch) break;
+        if (c0 >= cend) break;
         load(c0);
     }
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) red[w][j][lane] = acc[0][j];
+    for (int f = 0; f < NW; ++f)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) red[w][f * NJ + j][lane] = acc[f][j];
     __syncthreads();
-    if (!finish) return;
-    f32x4 v = low[0];
 #pragma unroll
-    for (int k = 0; k < kWaves; ++k) v += red[k][fj][16 * fq + i];
-    if constexpr (GATED) {
-        f32x4 up = low[1];
+    for (int e = tid; e < kItems; e += kWaves * 64) {
+        const int token = token_of(e), col = col_of(e), q = e / 16 % Q, at = e / (16 * Q);
+        if (token >= a.M || col >= a.N) continue;
+        f32x4 v = {0, 0, 0, 0}, up = {0, 0, 0, 0};
 #pragma unroll
-        for (int k = 0; k < kWaves; ++k) up += red[k][fj][16 * (fq + 2) + i];
-        if (a.gate_up) {
-            uint16_t* gu = a.gate_up + token * 2 * (int64_t)a.N + col;
-            *(u32x2*)gu = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-            *(u32x2*)(gu + a.N) = u32x2{pack_bf16x2(up[0], up[1]), pack_bf16x2(up[2], up[3])};
+        for (int k = 0; k < kWaves; ++k) {
+            v += red[k][at][16 * q + i];
+            if constexpr (GATED) up += red[k][at][16 * (q + 2) + i];
         }
-#pragma unroll
-        for (int r = 0; r < 4; ++r) v[r] = swiglu(v[r], up[r]);
-    } else if (a.addend) {
-        const u32x2 d = *(const u32x2*)(a.addend + token * a.ldadd + col);
-        v[0] += __uint_as_float(d[0] << 16);
-        v[1] += __uint_as_float(d[0] & 0xffff0000u);
-        v[2] += __uint_as_float(d[1] << 16);
-        v[3] += __uint_as_float(d[1] & 0xffff0000u);
+        if constexpr (SPLIT) {
+            const int64_t cols = GATED ? 2 * (int64_t)a.N : a.N;
+            float* p = a.partial + ((int64_t)part * a.M + token) * cols + col;
+            *(f32x4*)p = v;
+            if constexpr (GATED) *(f32x4*)(p + a.N) = up;
+        } else {
+            store4(a, token, col, finish4<GATED>(a, token, col, v, up));
+        }
     }
-    if (a.out_f32) *(f32x4*)((float*)a.out + token * a.ldo + col) = v;
-    else *(u32x2*)((uint16_t*)a.out + token * a.ldo + col) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
 }
 
-template <int ELT, int NJ, bool GATED, bool XF32>
-void launch_one(const DenseArgs& a, const float* xf, hipStream_t s) {
-    const dim3 grid((unsigned)((a.N + (GATED ? 7 : 15)) / (GATED ? 8 : 16))), block(kWaves * 64);
-    if constexpr (ELT == kEltBf16) {
-        if (a.lora.n > 0) {
-            hipLaunchKernelGGL((skinny_kernel<ELT, NJ, GATED, XF32, true>), grid, block, 0, s, a, xf);
-            return;
+template <int ELT, int NJ, int NW, bool GATED, bool XF32>
+hipError_t launch_one(const DenseArgs& a, const float* xf, hipStream_t s) {
+    constexpr int kRows = NW * (GATED ? 8 : 16);
+    const unsigned groups = (unsigned)((a.N + kRows - 1) / kRows);
+    const dim3 block(kWaves * 64);
+    if constexpr (NJ > 1 || ELT == kEltBf16) {
+        if (a.splits > 1 || a.lora.n > 0) {
+            const unsigned narrow = (unsigned)skinny_narrow(a);
+            hipLaunchKernelGGL((skinny_kernel<ELT, NJ, NW, GATED, XF32, true>), dim3(groups * (unsigned)a.splits + narrow),
+                               block, 0, s, a, xf);
+            const hipError_t e = hipGetLastError();
+            return e != hipSuccess ? e : launch_join(a, GATED ? kEpiGated : kEpiOut, s);
         }
     }
-    hipLaunchKernelGGL((skinny_kernel<ELT, NJ, GATED, XF32, false>), grid, block, 0, s, a, xf);
+    if constexpr (NW == 1)
+        hipLaunchKernelGGL((skinny_kernel<ELT, NJ, 1, GATED, XF32, false>), dim3(groups), block, 0, s, a, xf);
+    return hipGetLastError();
 }
 
 template <int ELT, bool GATED, bool XF32>
-void launch_nj(const DenseArgs& a, const float* xf, hipStream_t s) {
-    if (a.M <= 16) launch_one<ELT, 1, GATED, XF32>(a, xf, s);
-    else if (a.M <= 32) launch_one<ELT, 2, GATED, XF32>(a, xf, s);
-    else launch_one<ELT, 4, GATED, XF32>(a, xf, s);
+hipError_t launch_nj(const DenseArgs& a, const float* xf, hipStream_t s) {
+    if (a.M <= 16) return launch_one<ELT, 1, 1, GATED, XF32>(a, xf, s);
+    const bool wide = a.splits > 1 && skinny_wide(a, GATED);
+    if (a.M <= 32)
+        return wide ? launch_one<ELT, 2, 4, GATED, XF32>(a, xf, s) : launch_one<ELT, 2, 1, GATED, XF32>(a, xf, s);
+    return wide ? launch_one<ELT, 4, 4, GATED, XF32>(a, xf, s) : launch_one<ELT, 4, 1, GATED, XF32>(a, xf, s);
 }
 
 }  // namespace
 
+// Whether W has rows enough for 64 of them a workgroup.
+bool skinny_wide(const DenseArgs& a, bool gated) { return (gated ? 2 * (int64_t)a.N : a.N) >= 2048; }
+
+int skinny_narrow(const DenseArgs& a) { return a.lora.n > 0 ? a.M * ((a.lora.rank + 15) / 16) : 0; }
+
+int skinny_splits(const DenseArgs& a, int elt, int epi) {
+    if (a.M <= 16) return 1;
+    const bool gated = epi != kEpiOut;
+    const int64_t rows = gated ? 2 * (int64_t)a.N : a.N;
+    const int64_t groups = skinny_wide(a, gated) ? (rows + 63) / 64 : (rows + 15) / 16;
+    const int bk = elt == kEltBf16 ? 64 : 128;
+    // A part of K has a chunk for each wave; a workgroup a compute unit, those
+    // of the narrow product counted.
+    const int64_t most = (a.K + bk - 1) / bk / kWaves, room = (256 - skinny_narrow(a)) / groups;
+    const int64_t s = room < most ? room : most;
+    return s < 2 ? 1 : (int)s;
+}
+
 hipError_t launch_skinny(const DenseArgs& a, int elt, int epi, const float* h_f32, hipStream_t s) {
     const bool gated = epi != kEpiOut;
-    if (elt == kEltBf16) {
-        if (gated) launch_nj<kEltBf16, true, false>(a, nullptr, s);
-        else launch_nj<kEltBf16, false, false>(a, nullptr, s);
-    } else if (gated) {
-        launch_nj<kEltMx8, true, false>(a, nullptr, s);
-    } else {
-        launch_nj<kEltMx8, false, true>(a, h_f32, s);
-    }
-    return hipGetLastError();
+    if (elt == kEltBf16)
+        return gated ? launch_nj<kEltBf16, true, false>(a, nullptr, s) : launch_nj<kEltBf16, false, false>(a, nullptr, s);
+    return gated ? launch_nj<kEltMx8, true, false>(a, nullptr, s) : launch_nj<kEltMx8, false, true>(a, h_f32, s);
 }
 
 }  // namespace moe

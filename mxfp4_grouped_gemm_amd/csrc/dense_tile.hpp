@@ -142,25 +142,23 @@ __device__ __forceinline__ int key_t(int k) {
 // The low-rank term of a wave's accumulators: for each adapter that one of
 // the wave's rows uses, acc += B[a] v over its rank, with v (fp32) split into
 // two bf16 (hi + lo: 16 bits of it) and zero in the other adapters' rows.
-// n_of(f, lane) gives the W row (of the stack's N rows) of fragment f's MFMA
-// row lane % 16, or -1; m_of(fm) the token of this lane's column, or -1.
-// Adapters whose turn is not `turn` of `turns` are left to other waves.
+// n_of(f) gives the W row (of the stack's N rows) of fragment f's MFMA row
+// lane % 16, or -1; m_of(fm) the token of this lane's column counted from
+// `first`, or -1. All operands of 32 ranks are loaded before they are used.
 template <int FN, int FM, class NOF, class MOF>
-__device__ __forceinline__ void lora_accumulate(const LoraArgs& l, int64_t brows, f32x4 (&acc)[FN][FM], NOF n_of,
-                                                MOF m_of, int turn, int turns) {
+__device__ __forceinline__ void lora_accumulate(const LoraArgs& l, int64_t brows, int64_t first, f32x4 (&acc)[FN][FM],
+                                                NOF n_of, MOF m_of) {
     const int lane = (int)threadIdx.x & 63;
     const int g = lane >> 4;
+    const rsrc_t rv = make_rsrc(l.v + first * l.vld, kRecord);
     int idx[FM];
-    int64_t mrow[FM];
 #pragma unroll
     for (int fm = 0; fm < FM; ++fm) {
         const int m = m_of(fm);
-        mrow[fm] = m;
-        const int i = m >= 0 ? l.index[m] : -1;
+        const int i = m >= 0 ? l.index[first + m] : -1;
         idx[fm] = (unsigned)i < (unsigned)l.n ? i : 0x7fffffff;
     }
-    int last = -1;
-    for (int seen = 0;; ++seen) {
+    for (int last = -1;;) {
         // The smallest adapter above `last` among the wave's rows.
         int next = 0x7fffffff;
 #pragma unroll
@@ -173,60 +171,55 @@ __device__ __forceinline__ void lora_accumulate(const LoraArgs& l, int64_t brows
         next = __builtin_amdgcn_readfirstlane(next);
         if (next == 0x7fffffff) break;
         last = next;
-        if (seen % turns != turn) continue;
+        const rsrc_t rb = make_rsrc(l.b + (int64_t)next * brows * l.rank, kRecord);
         int rank = l.ranks ? l.ranks[next] : l.rank;
         rank = rank < l.rank ? rank : l.rank;
-        const uint16_t* bp = l.b + (int64_t)next * brows * l.rank;
-        for (int k0 = 0; k0 < rank; k0 += 32) {
+        for (int k0 = 0;;) {
             const int k = k0 + 8 * g;
-            bf16x8 bf[FN];
+            u32x4 bu[FN], vu[FM][2];
 #pragma unroll
             for (int f = 0; f < FN; ++f) {
                 const int n = n_of(f);
-                u32x4 u = {0, 0, 0, 0};
-                if (n >= 0 && k < rank) {
-                    u = *(const u32x4*)(bp + (int64_t)n * l.rank + k);
-                    if (k + 8 > rank) {  // columns beyond the adapter's rank are not read as numbers
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            if (k + 2 * e >= rank) u[e] = 0;
-                            else if (k + 2 * e + 1 >= rank) u[e] &= 0xffffu;
-                        }
-                    }
-                }
-                bf[f] = __builtin_bit_cast(bf16x8, u);
+                bu[f] = bld16(rb, n >= 0 && k < l.rank ? (uint32_t)(n * l.rank + k) * 2u : kOob);
             }
 #pragma unroll
             for (int fm = 0; fm < FM; ++fm) {
-                if (!__any(idx[fm] == next)) continue;
-                float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-                if (idx[fm] == next) {
-                    const float* vp = l.v + mrow[fm] * l.vld + k;
-                    const f32x4 a = *(const f32x4*)vp, b = *(const f32x4*)(vp + 4);
+                const uint32_t off = idx[fm] == next ? (uint32_t)(m_of(fm) * l.vld + k) * 4u : kOob;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        v[e] = a[e];
-                        v[4 + e] = b[e];
-                    }
+                for (int h = 0; h < 2; ++h) vu[fm][h] = bld16(rv, idx[fm] == next ? off + 16 * h : kOob);
+            }
+            // Columns beyond the adapter's rank are not read as numbers.
+#pragma unroll
+            for (int f = 0; f < FN; ++f)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (k + 2 * e >= rank) bu[f][e] = 0;
+                    else if (k + 2 * e + 1 >= rank) bu[f][e] &= 0xffffu;
                 }
+#pragma unroll
+            for (int fm = 0; fm < FM; ++fm) {
+                if (!__any(idx[fm] == next)) continue;
                 u32x4 hi, lo;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    hi[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
-                    lo[e] = pack_bf16x2(v[2 * e] - __uint_as_float(hi[e] << 16),
-                                        v[2 * e + 1] - __uint_as_float(hi[e] & 0xffff0000u));
+                    const float v0 = __uint_as_float(vu[fm][e / 2][2 * (e & 1)]);
+                    const float v1 = __uint_as_float(vu[fm][e / 2][2 * (e & 1) + 1]);
+                    hi[e] = pack_bf16x2(v0, v1);
+                    lo[e] = pack_bf16x2(v0 - __uint_as_float(hi[e] << 16), v1 - __uint_as_float(hi[e] & 0xffff0000u));
                 }
                 // A lane's results are one token's: only those of this adapter
                 // are kept (a NaN in its factors stays with its own tokens).
                 const bool mine = idx[fm] == next;
 #pragma unroll
                 for (int f = 0; f < FN; ++f) {
-                    f32x4 d = mfma16x16x32(bf[f], __builtin_bit_cast(bf16x8, hi), acc[f][fm]);
-                    d = mfma16x16x32(bf[f], __builtin_bit_cast(bf16x8, lo), d);
+                    f32x4 d = mfma16x16x32(__builtin_bit_cast(bf16x8, bu[f]), __builtin_bit_cast(bf16x8, hi), acc[f][fm]);
+                    d = mfma16x16x32(__builtin_bit_cast(bf16x8, bu[f]), __builtin_bit_cast(bf16x8, lo), d);
 #pragma unroll
                     for (int r = 0; r < 4; ++r) acc[f][fm][r] = mine ? d[r] : acc[f][fm][r];
                 }
             }
+            k0 += 32;
+            if (k0 >= rank) break;
         }
     }
 }
@@ -558,17 +551,15 @@ __global__ __launch_bounds__(C::THREADS, 2) void dense_kernel(DenseArgs a) {
         else return n0 + wn * 16 * C::F + g * 4 * C::F + (f % C::F) * 4;
     };
     if constexpr (C::LORA) {
-        if (a.lora.n > 0 && (!C::SPLIT || blockIdx.y == 0)) {
+        static_assert(!C::SPLIT, "the kernel that joins the parts adds the term");
+        if (a.lora.n > 0) {
             // As MFMA rows: row i = l16 of fragment f.
             auto nrow = [&](int f) {
                 const int n = n0 + wn * 16 * C::F + (l16 >> 2) * 4 * C::F + (f % C::F) * 4 + (l16 & 3);
                 return n < a.N ? n + (C::GATED && f >= C::F ? a.N : 0) : -1;
             };
-            auto mrow = [&](int fm) {
-                const int m = m_of(fm);
-                return m < a.M ? m : -1;
-            };
-            lora_accumulate<C::FN, C::FM>(a.lora, C::GATED ? 2 * (int64_t)a.N : a.N, acc, nrow, mrow, 0, 1);
+            auto mrow = [&](int fm) { return m_of(fm) < a.M ? m_of(fm) - m0 : -1; };
+            lora_accumulate<C::FN, C::FM>(a.lora, C::GATED ? 2 * (int64_t)a.N : a.N, m0, acc, nrow, mrow);
         }
     }
 
