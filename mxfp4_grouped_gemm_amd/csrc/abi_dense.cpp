@@ -129,7 +129,7 @@ bool skinny(int T, int64_t rows, int K, int elt) {
 }
 
 int splits_of(const moe::DenseArgs& a, int elt, int epi, bool few) {
-    return few ? moe::skinny_splits(a, elt, epi) : moe::dense_splits(a, moe::kNT, elt, epi);
+    return few ? moe::skinny_splits(a, elt, epi) : moe::dense_splits(a, elt, epi);
 }
 
 // Bytes of split-K partials of a forward product; few: in the few-token
@@ -145,7 +145,7 @@ int64_t partial_bytes(int T, int N, int K, int elt, int epi, bool few, int rank)
 hipError_t run_product(moe::DenseArgs& a, int elt, int epi, bool few, float* partial, const float* h_f32, hipStream_t s) {
     a.splits = splits_of(a, elt, epi, few);
     a.partial = partial;
-    return few ? moe::launch_skinny(a, elt, epi, h_f32, s) : moe::launch_dense(a, moe::kNT, elt, epi, s);
+    return few ? moe::launch_skinny(a, elt, epi, h_f32, s) : moe::launch_dense(a, elt, epi, s);
 }
 
 struct FfnLayout {
@@ -402,22 +402,13 @@ moe_status moe_ffn_backward(const uint16_t* dout, int64_t dout_stride, const uin
         moe::DenseArgs a = product(dout, dout_stride, w2, I, T, I, H, dgu, 2 * (int64_t)I);
         a.gate_up = const_cast<uint16_t*>(gate_up);
         a.h = dw2 ? h : nullptr;
-        LAUNCH(moe::launch_dense(a, moe::kNN, 0, moe::kEpiGatedBwd, s), "moe_ffn_backward (dh)");
-        if (dx) {
-            a = product(dgu, 2 * (int64_t)I, w13, H, T, H, 2 * I, dx, dx_stride);
-            LAUNCH(moe::launch_dense(a, moe::kNN, 0, moe::kEpiOut, s), "moe_ffn_backward (dx)");
-        }
+        LAUNCH(moe::launch_dense_dh(a, s), "moe_ffn_backward (dh)");
     }
-    // With T == 0 these sums are empty and write zeros.
-    if (dw13) {
-        const moe::DenseArgs a = product(dgu, 2 * (int64_t)I, x, x_stride, 2 * I, H, T, dw13, H);
-        LAUNCH(moe::launch_dense(a, moe::kTN, 0, moe::kEpiOut, s), "moe_ffn_backward (dw13)");
-    }
-    if (dw2) {
-        const moe::DenseArgs a = product(dout, dout_stride, h, I, H, I, T, dw2, I);
-        LAUNCH(moe::launch_dense(a, moe::kTN, 0, moe::kEpiOut, s), "moe_ffn_backward (dw2)");
-    }
-    return MOE_OK;
+    // With T == 0 the weights' sums are empty and write zeros.
+    const moe::DenseArgs g13 = product(dgu, 2 * (int64_t)I, x, x_stride, 2 * I, H, T, dw13, H);
+    const moe::DenseArgs g2 = product(dout, dout_stride, h, I, H, I, T, dw2, I);
+    const moe::DenseArgs gx = product(dgu, 2 * (int64_t)I, w13, H, T, H, 2 * I, dx, dx_stride);
+    return hip_status(moe::launch_dense_grads(g13, g2, gx, s), "moe_ffn_backward (gradients)");
 }
 
 }  // extern "C"

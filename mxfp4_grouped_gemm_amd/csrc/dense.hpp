@@ -50,12 +50,9 @@ struct DenseArgs {
     LoraArgs lora;          // lora.n == 0: none
 };
 
-// Operand orders: K-major rows, or K as the row index ("transposed").
-enum DenseOrder { kNT = 0, kNN = 1, kTN = 2 };  // (X K-major, W K-major), (X K-major, W transposed), (both transposed)
-
 // splits the launcher would take for this product, and the bytes of `partial`
 // that they need.
-int dense_splits(const DenseArgs& a, int order, int elt, int epi);
+int dense_splits(const DenseArgs& a, int elt, int epi);
 // (join: the product is joined by a second kernel even if splits == 1).
 inline int64_t dense_partial_bytes(const DenseArgs& a, int splits, int epi, bool join) {
     return splits <= 1 && !join ? 0 : (int64_t)splits * a.M * a.N * (epi == kEpiOut || epi == kEpiGatedBwd ? 1 : 2) * 4;
@@ -63,10 +60,15 @@ inline int64_t dense_partial_bytes(const DenseArgs& a, int splits, int epi, bool
 bool dense_big_tiles(const DenseArgs& a, int epi);
 bool dense_one_round(const DenseArgs& a, int epi);
 hipError_t launch_join(const DenseArgs& a, int epi, hipStream_t s);
-hipError_t launch_dense(const DenseArgs& a, int order, int elt, int epi, hipStream_t s);
+// A forward product (both operands K-major).
+hipError_t launch_dense(const DenseArgs& a, int elt, int epi, hipStream_t s);
 hipError_t launch_dense_nt(const DenseArgs& a, int epi, hipStream_t s);
 hipError_t launch_dense_mx(const DenseArgs& a, int epi, hipStream_t s);
-hipError_t launch_dense_bwd(const DenseArgs& a, int order, int epi, hipStream_t s);
+// Backward: dh (X K-major, W with K as its row index), then the gradients of
+// the weights (both operands with K as the row index) and of x (as dh). A
+// gradient whose `out` is null is not computed.
+hipError_t launch_dense_dh(const DenseArgs& a, hipStream_t s);
+hipError_t launch_dense_grads(const DenseArgs& dw13, const DenseArgs& dw2, const DenseArgs& dx, hipStream_t s);
 
 // Up to this many tokens the products stream the weights without LDS tiles.
 constexpr int kSkinnyMaxTokens = 64;

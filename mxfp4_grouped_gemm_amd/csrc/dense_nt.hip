@@ -74,8 +74,8 @@ bool dense_one_round(const DenseArgs& a, int epi) {
     return (int64_t)((a.M + 127) / 128) * ((cols + 127) / 128) <= 256;
 }
 
-int dense_splits(const DenseArgs& a, int order, int elt, int epi) {
-    if (order != kNT || dense_big_tiles(a, epi)) return 1;
+int dense_splits(const DenseArgs& a, int elt, int epi) {
+    if (dense_big_tiles(a, epi)) return 1;
     const bool gated = epi == kEpiGated || epi == kEpiGatedMx;
     const int64_t cols = gated ? 2 * (int64_t)a.N : a.N;
     const int64_t tiles = (int64_t)((a.M + 127) / 128) * ((cols + 127) / 128);
@@ -103,9 +103,8 @@ hipError_t launch_dense_nt(const DenseArgs& a, int epi, hipStream_t s) {
     return a.lora.n > 0 ? launch_epi<kEpiGated, true>(a, s) : launch_epi<kEpiGated, false>(a, s);
 }
 
-hipError_t launch_dense(const DenseArgs& a, int order, int elt, int epi, hipStream_t s) {
-    if (elt != kEltBf16) return launch_dense_mx(a, epi, s);
-    return order == kNT ? launch_dense_nt(a, epi, s) : launch_dense_bwd(a, order, epi, s);
+hipError_t launch_dense(const DenseArgs& a, int elt, int epi, hipStream_t s) {
+    return elt == kEltBf16 ? launch_dense_nt(a, epi, s) : launch_dense_mx(a, epi, s);
 }
 
 }  // namespace moe

@@ -224,12 +224,11 @@ __device__ __forceinline__ void lora_accumulate(const LoraArgs& l, int64_t brows
     }
 }
 
+// One tile: number `id` of the product's tiles, part `part` of a split K, with
+// buffers s0 and s1 (and s2, s3 of tiles with four of them).
 template <class C>
-__global__ __launch_bounds__(C::THREADS, 2) void dense_kernel(DenseArgs a) {
-    __shared__ __align__(1024) uint8_t s0[C::BUF];
-    __shared__ __align__(1024) uint8_t s1[C::BUF];
-    __shared__ __align__(1024) uint8_t s2[C::NB > 2 ? C::BUF : 16];
-    __shared__ __align__(1024) uint8_t s3[C::NB > 2 ? C::BUF : 16];
+__device__ __forceinline__ void dense_tile(const DenseArgs& a, int id, int part, uint8_t* s0, uint8_t* s1, uint8_t* s2,
+                                           uint8_t* s3) {
     const int tid = (int)threadIdx.x, lane = tid & 63;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = w / C::WN, wn = w % C::WN;
@@ -239,7 +238,6 @@ __global__ __launch_bounds__(C::THREADS, 2) void dense_kernel(DenseArgs a) {
     // XCDs; giving an XCD a contiguous run of tiles, in columns of kGroupM
     // tiles of M, keeps its W tiles in its own L2.
     const int tm = (a.M + C::BM - 1) / C::BM, tn = (a.N + C::BNC - 1) / C::BNC;
-    int id = (int)blockIdx.x;
     const int total = tm * tn;
     {
         const int q = total / 8, r = total % 8, xcd = id % 8, i = id / 8;
@@ -252,7 +250,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void dense_kernel(DenseArgs a) {
     const int steps = (a.K + C::BK - 1) / C::BK;
     int kt0 = 0, kt1 = steps;
     if constexpr (C::SPLIT) {
-        const int z = (int)blockIdx.y;
+        const int z = part;
         kt0 = (int)((int64_t)steps * z / a.splits);
         kt1 = (int)((int64_t)steps * (z + 1) / a.splits);
     }
@@ -389,14 +387,15 @@ __global__ __launch_bounds__(C::THREADS, 2) void dense_kernel(DenseArgs a) {
         const int r = wrow(f, l16);
         return *(const u32x4*)(buf + C::XBYTES + r * C::KB + ((piece ^ key_w<C::KB, C::F>(r)) << 4));
     };
-    // Transposed operand: columns c0 + 0..15 of K rows 32 s + 8 g + 0..7.
-    auto read_t = [&](const uint8_t* base, auto pieces, int c0, int s) -> bf16x8 {
+    // Transposed operand: four groups of four columns, c0 + q * stride, of K
+    // rows 32 s + 8 g + 0..7.
+    auto read_t = [&](const uint8_t* base, auto pieces, int c0, int stride, int s) -> bf16x8 {
         constexpr int PR = decltype(pieces)::value, pitch = PR * 16;
         bf16x4 v[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int k = 32 * s + 8 * g + 4 * h + (l16 >> 2);
-            const int col = c0 + (l16 & 3) * 4;
+            const int col = c0 + (l16 & 3) * stride;
             const uint8_t* p = base + k * pitch + ((((col >> 3) ^ key_t<PR>(k)) << 4) | ((col & 4) << 1));
             typedef __attribute__((address_space(3))) bf16x4* tp;
             v[h] = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((tp)p);
@@ -415,14 +414,14 @@ __global__ __launch_bounds__(C::THREADS, 2) void dense_kernel(DenseArgs a) {
         auto read_ws = [&](const uint8_t* buf, int s, int set) {
 #pragma unroll
             for (int f = 0; f < C::FN; ++f) {
-                if constexpr (C::WT) wf[set][f] = read_t(buf + C::XBYTES, std::integral_constant<int, C::BN / 8>(), (wn * C::FN + f) * 16, s);
+                if constexpr (C::WT) wf[set][f] = read_t(buf + C::XBYTES, std::integral_constant<int, C::BN / 8>(), wn * 16 * C::FN + f * 4, 4 * C::FN, s);
                 else wf[set][f] = __builtin_bit_cast(bf16x8, read_w(buf, f, 4 * s + g));
             }
         };
         auto read_xs = [&](const uint8_t* buf, int s, int h) {
 #pragma unroll
             for (int f = 0; f < FH; ++f) {
-                if constexpr (C::XT) xf[h][f] = read_t(buf, std::integral_constant<int, C::BM / 8>(), xr0 + (h * FH + f) * 16, s);
+                if constexpr (C::XT) xf[h][f] = read_t(buf, std::integral_constant<int, C::BM / 8>(), xr0 + (h * FH + f) * 16, 4, s);
                 else xf[h][f] = __builtin_bit_cast(bf16x8, read_x(buf, h * FH + f, 4 * s + g));
             }
         };
@@ -546,10 +545,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void dense_kernel(DenseArgs a) {
 
     // Column of fragment f's lane results (the first of four), and the token.
     auto m_of = [&](int fm) { return m0 + xr0 + fm * 16 + l16; };
-    auto n_of = [&](int f) {
-        if constexpr (C::WT) return n0 + (wn * C::FN + f) * 16 + 4 * g;
-        else return n0 + wn * 16 * C::F + g * 4 * C::F + (f % C::F) * 4;
-    };
+    auto n_of = [&](int f) { return n0 + wn * 16 * C::F + g * 4 * C::F + (f % C::F) * 4; };
     if constexpr (C::LORA) {
         static_assert(!C::SPLIT, "the kernel that joins the parts adds the term");
         if (a.lora.n > 0) {
@@ -565,7 +561,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void dense_kernel(DenseArgs a) {
 
     if constexpr (C::SPLIT) {
         const int64_t cols = C::GATED ? 2 * (int64_t)a.N : a.N;
-        float* pz = a.partial + (int64_t)blockIdx.y * a.M * cols;
+        float* pz = a.partial + (int64_t)part * a.M * cols;
 #pragma unroll
         for (int j = 0; j < C::FM; ++j) {
             const int m = m_of(j);
@@ -586,7 +582,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void dense_kernel(DenseArgs a) {
         if constexpr (C::EPI == kEpiOut) {
             if (!mok) continue;
             // W fragments: groups of V consecutive outputs of the lane.
-            constexpr int V = C::WT || C::FN % 2 ? 4 : 8;
+            constexpr int V = C::FN % 2 ? 4 : 8;
 #pragma unroll
             for (int f = 0; f < C::FN; f += V / 4) {
                 const int n = n_of(f);
@@ -657,36 +653,51 @@ __global__ __launch_bounds__(C::THREADS, 2) void dense_kernel(DenseArgs a) {
             }
         } else {  // kEpiGatedBwd
             if (!mok) continue;
+            constexpr int V = C::FN % 2 ? 4 : 8;
 #pragma unroll
-            for (int f = 0; f < C::FN; ++f) {
+            for (int f = 0; f < C::FN; f += V / 4) {
                 const int n = n_of(f);
                 if (n >= a.N) continue;
                 const uint16_t* gu = a.gate_up + m * 2 * (int64_t)a.N + n;
-                const u32x2 gb = *(const u32x2*)gu, ub = *(const u32x2*)(gu + a.N);
-                float dg[4], du[4], h[4];
+                uint32_t gb[V / 2], ub[V / 2];
+                load_words<V / 2>(gb, gu);
+                load_words<V / 2>(ub, gu + a.N);
+                float dg[V], du[V], h[V];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const uint32_t gw = gb[r >> 1], uw = ub[r >> 1];
-                    const float gv = __uint_as_float(r & 1 ? gw & 0xffff0000u : gw << 16);
-                    const float uv = __uint_as_float(r & 1 ? uw & 0xffff0000u : uw << 16);
-                    const float dh = acc[f][j][r], sg = sigmoid(gv), silu = gv * sg;
-                    dg[r] = dh * uv * sg * (1.0f + gv * (1.0f - sg));
-                    du[r] = dh * silu;
-                    h[r] = silu * uv;
+                for (int e = 0; e < V; ++e) {
+                    const float gv = __uint_as_float(e & 1 ? gb[e / 2] & 0xffff0000u : gb[e / 2] << 16);
+                    const float uv = __uint_as_float(e & 1 ? ub[e / 2] & 0xffff0000u : ub[e / 2] << 16);
+                    const float dh = acc[f + e / 4][j][e % 4], sg = sigmoid(gv), silu = gv * sg;
+                    dg[e] = dh * uv * sg * (1.0f + gv * (1.0f - sg));
+                    du[e] = dh * silu;
+                    h[e] = silu * uv;
                 }
                 uint16_t* o = (uint16_t*)a.out + m * a.ldo + n;
-                *(u32x2*)o = u32x2{pack_bf16x2(dg[0], dg[1]), pack_bf16x2(dg[2], dg[3])};
-                *(u32x2*)(o + a.N) = u32x2{pack_bf16x2(du[0], du[1]), pack_bf16x2(du[2], du[3])};
-                if (a.h) *(u32x2*)(a.h + m * (int64_t)a.N + n) = u32x2{pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3])};
+                store_bf16<V>(o, dg);
+                store_bf16<V>(o + a.N, du);
+                if (a.h) store_bf16<V>(a.h + m * (int64_t)a.N + n, h);
             }
         }
     }
 }
 
 template <class C>
+__global__ __launch_bounds__(C::THREADS, 2) void dense_kernel(DenseArgs a) {
+    __shared__ __align__(1024) uint8_t s0[C::BUF];
+    __shared__ __align__(1024) uint8_t s1[C::BUF];
+    __shared__ __align__(1024) uint8_t s2[C::NB > 2 ? C::BUF : 16];
+    __shared__ __align__(1024) uint8_t s3[C::NB > 2 ? C::BUF : 16];
+    dense_tile<C>(a, (int)blockIdx.x, (int)blockIdx.y, s0, s1, s2, s3);
+}
+
+template <class C>
+inline int64_t tiles_of(const DenseArgs& a) {
+    return (int64_t)((a.M + C::BM - 1) / C::BM) * ((a.N + C::BNC - 1) / C::BNC);
+}
+
+template <class C>
 inline hipError_t launch_tile(const DenseArgs& a, hipStream_t s) {
-    const int64_t tm = (a.M + C::BM - 1) / C::BM, tn = (a.N + C::BNC - 1) / C::BNC;
-    const dim3 grid((unsigned)(tm * tn), C::SPLIT ? (unsigned)a.splits : 1u), block(C::THREADS);
+    const dim3 grid((unsigned)tiles_of<C>(a), C::SPLIT ? (unsigned)a.splits : 1u), block(C::THREADS);
     hipLaunchKernelGGL((dense_kernel<C>), grid, block, 0, s, a);
     return hipGetLastError();
 }
