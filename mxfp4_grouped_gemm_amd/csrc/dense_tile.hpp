@@ -575,14 +575,38 @@ __device__ __forceinline__ void dense_tile(const DenseArgs& a, int id, int part,
         return;
     }
 
+    // What the epilogue reads from memory is loaded for several tokens before
+    // the first of them is stored (the compiler keeps loads behind stores that
+    // could be to the same place).
+    constexpr int V = C::F % 2 ? 4 : 8;          // consecutive outputs of a lane
+    constexpr int VN = C::F * 4 / V;             // groups of them
+    constexpr bool kBwd = C::EPI == kEpiGatedBwd, kReads = C::EPI == kEpiOut || kBwd;
+    constexpr int JB = kBwd && C::FM > 4 ? C::FM / 2 : C::FM;  // tokens a batch
+    uint32_t ra[kReads ? JB : 1][VN][V / 2], rb[kBwd ? JB : 1][VN][V / 2];
 #pragma unroll
     for (int j = 0; j < C::FM; ++j) {
         const int m = m_of(j);
         const bool mok = m < a.M;
+        if constexpr (kReads) {
+            if (j % JB == 0 && (kBwd || a.addend)) {
+#pragma unroll
+                for (int jj = 0; jj < JB; ++jj)
+#pragma unroll
+                    for (int v = 0; v < VN; ++v) {
+                        const int mm = m_of(j + jj), n = n_of(v * (V / 4));
+                        if (mm >= a.M || n >= a.N) continue;
+                        if constexpr (kBwd) {
+                            const uint16_t* gu = a.gate_up + mm * 2 * (int64_t)a.N + n;
+                            load_words<V / 2>(ra[jj][v], gu);
+                            load_words<V / 2>(rb[jj][v], gu + a.N);
+                        } else {
+                            load_words<V / 2>(ra[jj][v], a.addend + mm * a.ldadd + n);
+                        }
+                    }
+            }
+        }
         if constexpr (C::EPI == kEpiOut) {
             if (!mok) continue;
-            // W fragments: groups of V consecutive outputs of the lane.
-            constexpr int V = C::FN % 2 ? 4 : 8;
 #pragma unroll
             for (int f = 0; f < C::FN; f += V / 4) {
                 const int n = n_of(f);
@@ -591,8 +615,7 @@ __device__ __forceinline__ void dense_tile(const DenseArgs& a, int id, int part,
 #pragma unroll
                 for (int e = 0; e < V; ++e) v[e] = acc[f + e / 4][j][e % 4];
                 if (a.addend) {
-                    uint32_t d[V / 2];
-                    load_words<V / 2>(d, a.addend + m * a.ldadd + n);
+                    const auto& d = ra[j % JB][f / (V / 4)];
 #pragma unroll
                     for (int e = 0; e < V; ++e) v[e] += __uint_as_float(e & 1 ? d[e / 2] & 0xffff0000u : d[e / 2] << 16);
                 }
@@ -632,7 +655,6 @@ __device__ __forceinline__ void dense_tile(const DenseArgs& a, int id, int part,
                 }
             } else {
                 if (!mok) continue;
-                constexpr int V = C::F % 2 ? 4 : 8;
 #pragma unroll
                 for (int f = 0; f < C::F; f += V / 4) {
                     const int n = n_of(f);
@@ -653,15 +675,12 @@ __device__ __forceinline__ void dense_tile(const DenseArgs& a, int id, int part,
             }
         } else {  // kEpiGatedBwd
             if (!mok) continue;
-            constexpr int V = C::FN % 2 ? 4 : 8;
 #pragma unroll
             for (int f = 0; f < C::FN; f += V / 4) {
                 const int n = n_of(f);
                 if (n >= a.N) continue;
-                const uint16_t* gu = a.gate_up + m * 2 * (int64_t)a.N + n;
-                uint32_t gb[V / 2], ub[V / 2];
-                load_words<V / 2>(gb, gu);
-                load_words<V / 2>(ub, gu + a.N);
+                const auto& gb = ra[j % JB][f / (V / 4)];
+                const auto& ub = rb[j % JB][f / (V / 4)];
                 float dg[V], du[V], h[V];
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
