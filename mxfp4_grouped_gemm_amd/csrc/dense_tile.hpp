@@ -76,6 +76,18 @@ __device__ __forceinline__ void load_words(uint32_t (&d)[W], const void* p) {
     }
 }
 
+// The same with two matrix instructions a read and the rest behind the last
+// one, for the phase before a barrier, which waits for the reads.
+template <int READS, int MFMAS, int I = 0>
+__device__ __forceinline__ void spread_front() {
+    if constexpr (I < READS) {
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        constexpr int mfmas = 2 * READS <= MFMAS ? (I + 1 < READS ? 2 : MFMAS - 2 * (READS - 1)) : I + 1 < MFMAS ? 1 : 0;
+        if constexpr (mfmas > 0) __builtin_amdgcn_sched_group_barrier(0x8, mfmas, 0);
+        spread_front<READS, MFMAS, I + 1>();
+    }
+}
+
 // Four or eight consecutive outputs, rounded.
 template <int V>
 __device__ __forceinline__ void store_bf16(uint16_t* p, const float* v) {
@@ -446,7 +458,7 @@ __device__ __forceinline__ void dense_tile(const DenseArgs& a, int id, int part,
                 __builtin_amdgcn_sched_barrier(0);
                 read_xs(cur, 1, 1);
                 multiply(1, 0);
-                spread<kXR, 0, kMfma>();
+                spread_front<kXR, kMfma>();
             }
             sync_step<(C::NB - 2) * (C::XL + C::WL)>();
             issue(cur, kt + C::NB);
