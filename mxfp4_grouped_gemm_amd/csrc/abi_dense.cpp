@@ -91,7 +91,9 @@ moe_status check_lora(const char* fn, const char* name, const moe_lora* l, int T
 
 int vld_of(int rank) { return (int)align_up(rank, 32); }
 
-moe::LoraArgs lora_args(const moe_lora* l, void* v) {
+int64_t v_bytes(int T, int rank) { return align_up((int64_t)moe::lora_parts(T) * T * vld_of(rank) * 4, 256); }
+
+moe::LoraArgs lora_args(const moe_lora* l, void* v, int T) {
     moe::LoraArgs r;
     memset(&r, 0, sizeof r);
     if (!l) return r;
@@ -104,6 +106,8 @@ moe::LoraArgs lora_args(const moe_lora* l, void* v) {
     r.rank = l->rank;
     r.vld = vld_of(l->rank);
     r.v = (float*)v;
+    r.parts = moe::lora_parts(T);
+    r.part_stride = (int64_t)T * r.vld;
     return r;
 }
 
@@ -154,13 +158,12 @@ struct FfnLayout {
 
 FfnLayout ffn_layout(int T, int H, int I, int rank13, int rank2) {
     FfnLayout L;
-    const int vld = vld_of(rank13 > rank2 ? rank13 : rank2);
     const int64_t p1 = partial_bytes(T, I, H, 0, moe::kEpiGated, skinny(T, 2 * (int64_t)I, H, 0), rank13);
     const int64_t p2 = partial_bytes(T, H, I, 0, moe::kEpiOut, skinny(T, H, I, 0), rank2);
     L.h = 0;
     L.hs = 0;
     L.v = align_up((int64_t)T * I * 2, 256);
-    L.partial = L.v + align_up((int64_t)T * vld * 4, 256);
+    L.partial = L.v + v_bytes(T, rank13 > rank2 ? rank13 : rank2);
     L.total = L.partial + (p1 > p2 ? p1 : p2);
     return L;
 }
@@ -254,7 +257,7 @@ moe_status moe_rms_norm(const uint16_t* x, int64_t x_stride, const void* residua
 
 int64_t moe_lora_linear_workspace_size(int T, int K, int N, int rank) {
     if (!valid_sizes(T, K, N, 8) || !valid_rank(rank)) return -1;
-    return align_up((int64_t)T * vld_of(rank) * 4, 256) + partial_bytes(T, N, K, 0, moe::kEpiOut, skinny(T, N, K, 0), rank);
+    return v_bytes(T, rank) + partial_bytes(T, N, K, 0, moe::kEpiOut, skinny(T, N, K, 0), rank);
 }
 
 moe_status moe_lora_linear(const uint16_t* x, int64_t x_stride, const uint16_t* w, const moe_lora* lora, int T, int K,
@@ -276,8 +279,8 @@ moe_status moe_lora_linear(const uint16_t* x, int64_t x_stride, const uint16_t* 
     hipStream_t s = (hipStream_t)stream;
     moe::DenseArgs a = product(x, x_stride, w, K, T, N, K, out, out_stride);
     a.out_f32 = out_type == MOE_DT_F32;
-    a.lora = lora_args(lora, workspace);
-    float* partial = (float*)((char*)workspace + align_up((int64_t)T * a.lora.vld * 4, 256));
+    a.lora = lora_args(lora, workspace, T);
+    float* partial = (float*)((char*)workspace + v_bytes(T, lora ? lora->rank : 0));
     if (lora && !skinny(T, N, K, 0)) LAUNCH(moe::launch_lora_shrink(x, x_stride, T, K, a.lora, s), "moe_lora_linear (shrink)");
     return hip_status(run_product(a, 0, moe::kEpiOut, skinny(T, N, K, 0), partial, nullptr, s), fn);
 }
@@ -313,14 +316,14 @@ moe_status moe_ffn_forward(const uint16_t* x, int64_t x_stride, const uint16_t* 
     uint16_t* h = (uint16_t*)(ws + L.h);
     moe::DenseArgs a = product(x, x_stride, w13, H, T, I, H, h, I);
     a.gate_up = gate_up;
-    a.lora = lora_args(lora13, ws + L.v);
+    a.lora = lora_args(lora13, ws + L.v, T);
     if (lora13 && !skinny(T, 2 * (int64_t)I, H, 0))
         LAUNCH(moe::launch_lora_shrink(x, x_stride, T, H, a.lora, s), "moe_ffn_forward (gate_up shrink)");
     LAUNCH(run_product(a, 0, moe::kEpiGated, skinny(T, 2 * (int64_t)I, H, 0), (float*)(ws + L.partial), nullptr, s), "moe_ffn_forward (gate_up)");
     a = product(h, I, w2, I, T, H, I, out, out_stride);
     a.addend = addend;
     a.ldadd = addend_stride;
-    a.lora = lora_args(lora2, ws + L.v);
+    a.lora = lora_args(lora2, ws + L.v, T);
     if (lora2 && !skinny(T, H, I, 0))
         LAUNCH(moe::launch_lora_shrink(h, I, T, I, a.lora, s), "moe_ffn_forward (down shrink)");
     return hip_status(run_product(a, 0, moe::kEpiOut, skinny(T, H, I, 0), (float*)(ws + L.partial), nullptr, s), "moe_ffn_forward (down)");

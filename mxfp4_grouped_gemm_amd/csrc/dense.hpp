@@ -18,8 +18,9 @@ struct LoraArgs {
     const int32_t* index;    // [T]
     const int32_t* ranks;    // [n] or null (all `rank`)
     const float* scale;      // [n] or null (all 1)
-    float* v;                // fp32 [T, vld], vld = rank rounded up to 32
-    int n, rank, vld;
+    float* v;                // fp32 [parts, T, vld], vld = rank rounded up to 32
+    int64_t part_stride;     // T * vld
+    int n, rank, vld, parts; // v is the sum of the parts (of K)
 };
 
 // Epilogues of the dense products.
@@ -81,6 +82,8 @@ bool skinny_wide(const DenseArgs& a, bool gated);
 int skinny_narrow(const DenseArgs& a);  // workgroups of the adapters' narrow product
 hipError_t launch_skinny(const DenseArgs& a, int elt, int epi, const float* h_f32, hipStream_t s);
 
+// Parts of K that launch_lora_shrink takes (l.parts).
+int lora_parts(int T);
 // v[t] = scale * A[index[t]] x[t].
 hipError_t launch_lora_shrink(const uint16_t* x, int64_t ldx, int T, int K, const LoraArgs& l, hipStream_t s);
 

@@ -20,7 +20,7 @@ __device__ __forceinline__ void lora_dot(const LoraArgs& l, int N, int64_t token
     const uint16_t* b = l.b + ((int64_t)ad * (GATED ? 2 * (int64_t)N : N) + col) * l.rank;
     const float* v = l.v + token * l.vld;
     // Sixteen columns at a time; the first batch is loaded before the rank is
-    // known (v holds zeros from the rank to vld, and B has l.rank columns).
+    // known (what lies beyond it is memory of v and B, but not read as numbers).
     for (int k0 = 0;;) {
         f32x4 vv[4];
         u32x4 w[GATED ? 2 : 1][4][2];
@@ -29,6 +29,10 @@ __device__ __forceinline__ void lora_dot(const LoraArgs& l, int N, int64_t token
             const int k = k0 + 8 * h < l.rank ? k0 + 8 * h : k0;  // rank is a multiple of 8
             vv[2 * h] = *(const f32x4*)(v + k);
             vv[2 * h + 1] = *(const f32x4*)(v + k + 4);
+            for (int p = 1; p < l.parts; ++p) {
+                vv[2 * h] += *(const f32x4*)(v + p * l.part_stride + k);
+                vv[2 * h + 1] += *(const f32x4*)(v + p * l.part_stride + k + 4);
+            }
 #pragma unroll
             for (int s = 0; s < (GATED ? 2 : 1); ++s)
 #pragma unroll

@@ -151,6 +151,24 @@ __device__ __forceinline__ int key_t(int k) {
     return (2 * ((k & 3) | (((k >> 3) & 1) << 2))) & (PIECES - 1);
 }
 
+// Tokens without an adapter, in the searches over a tile's adapters.
+constexpr int kNoAdapter = 0x7fffffff;
+
+// Minimum over the 16 lanes of a row (rotations by 8, 4, 2 and 1).
+__device__ __forceinline__ int min16(int v) {
+#define MOE_MIN_ROR(N)                                                          \
+    {                                                                           \
+        const int o = __builtin_amdgcn_mov_dpp(v, 0x120 + N, 0xf, 0xf, true);   \
+        v = o < v ? o : v;                                                      \
+    }
+    MOE_MIN_ROR(8)
+    MOE_MIN_ROR(4)
+    MOE_MIN_ROR(2)
+    MOE_MIN_ROR(1)
+#undef MOE_MIN_ROR
+    return v;
+}
+
 // The low-rank term of a wave's accumulators: for each adapter that one of
 // the wave's rows uses, acc += B[a] v over its rank, with v (fp32) split into
 // two bf16 (hi + lo: 16 bits of it) and zero in the other adapters' rows.
@@ -168,39 +186,29 @@ __device__ __forceinline__ void lora_accumulate(const LoraArgs& l, int64_t brows
     for (int fm = 0; fm < FM; ++fm) {
         const int m = m_of(fm);
         const int i = m >= 0 ? l.index[first + m] : -1;
-        idx[fm] = (unsigned)i < (unsigned)l.n ? i : 0x7fffffff;
+        idx[fm] = (unsigned)i < (unsigned)l.n ? i : kNoAdapter;
     }
     for (int last = -1;;) {
         // The smallest adapter above `last` among the wave's rows.
-        int next = 0x7fffffff;
+        int next = kNoAdapter;
 #pragma unroll
         for (int fm = 0; fm < FM; ++fm) next = idx[fm] > last && idx[fm] < next ? idx[fm] : next;
-#pragma unroll
-        for (int d = 1; d < 16; d *= 2) {
-            const int o = __shfl_xor(next, d);
-            next = o < next ? o : next;
-        }
-        next = __builtin_amdgcn_readfirstlane(next);
-        if (next == 0x7fffffff) break;
+        next = __builtin_amdgcn_readfirstlane(min16(next));
+        if (next == kNoAdapter) break;
         last = next;
         const rsrc_t rb = make_rsrc(l.b + (int64_t)next * brows * l.rank, kRecord);
         int rank = l.ranks ? l.ranks[next] : l.rank;
         rank = rank < l.rank ? rank : l.rank;
         for (int k0 = 0;;) {
             const int k = k0 + 8 * g;
-            u32x4 bu[FN], vu[FM][2];
+            u32x4 bu[FN];
 #pragma unroll
             for (int f = 0; f < FN; ++f) {
                 const int n = n_of(f);
                 bu[f] = bld16(rb, n >= 0 && k < l.rank ? (uint32_t)(n * l.rank + k) * 2u : kOob);
             }
-#pragma unroll
-            for (int fm = 0; fm < FM; ++fm) {
-                const uint32_t off = idx[fm] == next ? (uint32_t)(m_of(fm) * l.vld + k) * 4u : kOob;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) vu[fm][h] = bld16(rv, idx[fm] == next ? off + 16 * h : kOob);
-            }
-            // Columns beyond the adapter's rank are not read as numbers.
+            // Columns beyond the adapter's rank are not read as numbers (nor
+            // are whole eights of v, which the narrow product leaves unwritten).
 #pragma unroll
             for (int f = 0; f < FN; ++f)
 #pragma unroll
@@ -208,26 +216,46 @@ __device__ __forceinline__ void lora_accumulate(const LoraArgs& l, int64_t brows
                     if (k + 2 * e >= rank) bu[f][e] = 0;
                     else if (k + 2 * e + 1 >= rank) bu[f][e] &= 0xffffu;
                 }
+            // The rows in two batches, as their operands' registers allow.
+            constexpr int FB = FM > 4 ? 4 : FM;
 #pragma unroll
-            for (int fm = 0; fm < FM; ++fm) {
-                if (!__any(idx[fm] == next)) continue;
-                u32x4 hi, lo;
+            for (int fb = 0; fb < FM; fb += FB) {
+                f32x4 vu[FB][2];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float v0 = __uint_as_float(vu[fm][e / 2][2 * (e & 1)]);
-                    const float v1 = __uint_as_float(vu[fm][e / 2][2 * (e & 1) + 1]);
-                    hi[e] = pack_bf16x2(v0, v1);
-                    lo[e] = pack_bf16x2(v0 - __uint_as_float(hi[e] << 16), v1 - __uint_as_float(hi[e] & 0xffff0000u));
+                for (int b = 0; b < FB; ++b)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        vu[b][h] = __builtin_bit_cast(f32x4, bld16(rv, idx[fb + b] == next && k < rank ? (uint32_t)(m_of(fb + b) * l.vld + k) * 4u + 16u * h : kOob));
+                for (int p = 1; p < l.parts; ++p) {
+                    const rsrc_t rp = make_rsrc(l.v + p * l.part_stride + first * l.vld, kRecord);
+#pragma unroll
+                    for (int b = 0; b < FB; ++b)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            vu[b][h] += __builtin_bit_cast(f32x4, bld16(rp, idx[fb + b] == next && k < rank ? (uint32_t)(m_of(fb + b) * l.vld + k) * 4u + 16u * h : kOob));
                 }
-                // A lane's results are one token's: only those of this adapter
-                // are kept (a NaN in its factors stays with its own tokens).
-                const bool mine = idx[fm] == next;
 #pragma unroll
-                for (int f = 0; f < FN; ++f) {
-                    f32x4 d = mfma16x16x32(__builtin_bit_cast(bf16x8, bu[f]), __builtin_bit_cast(bf16x8, hi), acc[f][fm]);
-                    d = mfma16x16x32(__builtin_bit_cast(bf16x8, bu[f]), __builtin_bit_cast(bf16x8, lo), d);
+                for (int b = 0; b < FB; ++b) {
+                    const int fm = fb + b;
+                    if (!__any(idx[fm] == next)) continue;
+                    u32x4 hi, lo;
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) acc[f][fm][r] = mine ? d[r] : acc[f][fm][r];
+                    for (int e = 0; e < 4; ++e) {
+                        const float v0 = vu[b][e / 2][2 * (e & 1)];
+                        const float v1 = vu[b][e / 2][2 * (e & 1) + 1];
+                        hi[e] = pack_bf16x2(v0, v1);
+                        lo[e] = pack_bf16x2(v0 - __uint_as_float(hi[e] << 16), v1 - __uint_as_float(hi[e] & 0xffff0000u));
+                    }
+                    // A lane's results are one token's: only those of this adapter
+                    // are kept (a NaN in its factors stays with its own tokens).
+                    const bool mine = idx[fm] == next;
+#pragma unroll
+                    for (int f = 0; f < FN; ++f) {
+                        f32x4 d = mfma16x16x32(__builtin_bit_cast(bf16x8, bu[f]), __builtin_bit_cast(bf16x8, hi), acc[f][fm]);
+                        d = mfma16x16x32(__builtin_bit_cast(bf16x8, bu[f]), __builtin_bit_cast(bf16x8, lo), d);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) acc[f][fm][r] = mine ? d[r] : acc[f][fm][r];
+                    }
                 }
             }
             k0 += 32;
