@@ -129,7 +129,7 @@ moe::DenseArgs product(const void* x, int64_t ldx, const void* w, int64_t ldw, i
 }
 
 bool skinny(int T, int64_t rows, int K, int elt) {
-    return T <= moe::kSkinnyMaxTokens && rows * K * (elt == 0 ? 2 : 1) <= kMaxSkinnyBytes;
+    return T <= (elt == 0 ? moe::kSkinnyMaxTokens : moe::kSkinnyMaxTokensMx) && rows * K * (elt == 0 ? 2 : 1) <= kMaxSkinnyBytes;
 }
 
 int splits_of(const moe::DenseArgs& a, int elt, int epi, bool few) {
@@ -180,6 +180,25 @@ FfnLayout ffn_mx_layout(int T, int H, int I) {
     L.hs = align_up((int64_t)T * I * (few ? 4 : 1), 256);
     L.partial = L.hs + (few ? 0 : align_up((int64_t)T * (I / 32), 256));
     L.total = L.partial + (p1 > p2 ? p1 : p2);
+    return L;
+}
+
+struct BwdLayout {
+    int64_t h, partial, total;  // dgate_up at 0
+    int splits_dh, splits_dx;
+};
+
+BwdLayout bwd_layout(int T, int H, int I) {
+    BwdLayout L;
+    const moe::DenseArgs dh = product(nullptr, H, nullptr, I, T, I, H, nullptr, I);
+    const moe::DenseArgs dx = product(nullptr, 2 * (int64_t)I, nullptr, H, T, H, 2 * I, nullptr, H);
+    L.splits_dh = moe::dense_bwd_splits(dh);
+    L.splits_dx = moe::dense_bwd_splits(dx);
+    const int64_t p1 = moe::dense_partial_bytes(dh, L.splits_dh, moe::kEpiGatedBwd, false);
+    const int64_t p2 = moe::dense_partial_bytes(dx, L.splits_dx, moe::kEpiOut, false);
+    L.h = align_up((int64_t)T * 2 * I * 2, 256);
+    L.partial = L.h + align_up((int64_t)T * I * 2, 256);
+    L.total = L.partial + align_up(p1 > p2 ? p1 : p2, 256);
     return L;
 }
 
@@ -375,7 +394,7 @@ moe_status moe_ffn_forward_mxfp8(const uint8_t* x, const uint8_t* x_scale, const
 
 int64_t moe_ffn_backward_workspace_size(int T, int H, int I) {
     if (!valid_sizes(T, H, I, 8)) return -1;
-    return align_up((int64_t)T * 2 * I * 2, 256) + align_up((int64_t)T * I * 2, 256);
+    return bwd_layout(T, H, I).total;
 }
 
 moe_status moe_ffn_backward(const uint16_t* dout, int64_t dout_stride, const uint16_t* x, int64_t x_stride,
@@ -396,21 +415,27 @@ moe_status moe_ffn_backward(const uint16_t* dout, int64_t dout_stride, const uin
     hipStream_t s = (hipStream_t)stream;
     uint16_t* dgu = nullptr;
     uint16_t* h = nullptr;
+    const BwdLayout L = bwd_layout(T, H, I);
+    float* partial = (float*)((char*)workspace + L.partial);
     if (T > 0) {
         const void* ptrs[] = {dout, x, gate_up, w13, w2};
         CHECK(check_pointers(fn, ptrs, 16));
-        CHECK(check_workspace(fn, workspace, workspace_bytes, moe_ffn_backward_workspace_size(T, H, I)));
+        CHECK(check_workspace(fn, workspace, workspace_bytes, L.total));
         dgu = (uint16_t*)workspace;
-        h = (uint16_t*)((char*)workspace + align_up((int64_t)T * 2 * I * 2, 256));
+        h = (uint16_t*)((char*)workspace + L.h);
         moe::DenseArgs a = product(dout, dout_stride, w2, I, T, I, H, dgu, 2 * (int64_t)I);
         a.gate_up = const_cast<uint16_t*>(gate_up);
         a.h = dw2 ? h : nullptr;
+        a.splits = L.splits_dh;
+        a.partial = partial;
         LAUNCH(moe::launch_dense_dh(a, s), "moe_ffn_backward (dh)");
     }
     // With T == 0 the weights' sums are empty and write zeros.
     const moe::DenseArgs g13 = product(dgu, 2 * (int64_t)I, x, x_stride, 2 * I, H, T, dw13, H);
     const moe::DenseArgs g2 = product(dout, dout_stride, h, I, H, I, T, dw2, I);
-    const moe::DenseArgs gx = product(dgu, 2 * (int64_t)I, w13, H, T, H, 2 * I, dx, dx_stride);
+    moe::DenseArgs gx = product(dgu, 2 * (int64_t)I, w13, H, T, H, 2 * I, dx, dx_stride);
+    gx.splits = L.splits_dx;
+    gx.partial = partial;
     return hip_status(moe::launch_dense_grads(g13, g2, gx, s), "moe_ffn_backward (gradients)");
 }
 

@@ -68,11 +68,16 @@ hipError_t launch_dense_mx(const DenseArgs& a, int epi, hipStream_t s);
 // Backward: dh (X K-major, W with K as its row index), then the gradients of
 // the weights (both operands with K as the row index) and of x (as dh). A
 // gradient whose `out` is null is not computed.
+// (Their a.splits: dense_bwd_splits, of dh and of dx.)
+int dense_bwd_splits(const DenseArgs& a);
 hipError_t launch_dense_dh(const DenseArgs& a, hipStream_t s);
 hipError_t launch_dense_grads(const DenseArgs& dw13, const DenseArgs& dw2, const DenseArgs& dx, hipStream_t s);
 
 // Up to this many tokens the products stream the weights without LDS tiles.
-constexpr int kSkinnyMaxTokens = 64;
+// (MXFP8 with H = 3584, I = 2048: 33 us at 64 tokens, 26 in tiles, where h is
+// quantised once and not by every workgroup of the second product; at 32 both
+// take 26.)
+constexpr int kSkinnyMaxTokens = 64, kSkinnyMaxTokensMx = 32;
 // elt 0: bf16; 1: MXFP8 activations and weights. h_f32: the fp32 h of the
 // MXFP8 block between its two products (written by kEpiGated, and read and
 // quantised by the second product).

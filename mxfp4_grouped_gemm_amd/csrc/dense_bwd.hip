@@ -21,11 +21,8 @@ struct GradArgs {
 // TN: tiles of the weight gradients; NN: of dx. Same buffers.
 template <class TN, class NN>
 __global__ __launch_bounds__(TN::THREADS, 2) void grad_kernel(GradArgs g) {
-    static_assert(TN::BUF == NN::BUF && TN::NB == 4 && NN::NB == 4 && TN::THREADS == NN::THREADS, "one launch");
-    __shared__ __align__(1024) uint8_t s0[TN::BUF];
-    __shared__ __align__(1024) uint8_t s1[TN::BUF];
-    __shared__ __align__(1024) uint8_t s2[TN::BUF];
-    __shared__ __align__(1024) uint8_t s3[TN::BUF];
+    static_assert(TN::BUF == NN::BUF && TN::NB == NN::NB && TN::THREADS == NN::THREADS, "one launch");
+    MOE_TILE_BUFFERS(s, TN::NB, TN::BUF);
     int id = (int)blockIdx.x;
     if (g.dx_first) {
         id = id < g.nx ? g.n13 + g.n2 + id : id - g.nx;
@@ -33,16 +30,16 @@ __global__ __launch_bounds__(TN::THREADS, 2) void grad_kernel(GradArgs g) {
     if (id < g.n13 + g.n2) {
         const bool second = id >= g.n13;
         const DenseArgs a = second ? g.dw2 : g.dw13;
-        dense_tile<TN>(a, second ? id - g.n13 : id, 0, s0, s1, s2, s3);
+        dense_tile<TN>(a, second ? id - g.n13 : id, 0, s);
     } else {
-        dense_tile<NN>(g.dx, id - g.n13 - g.n2, 0, s0, s1, s2, s3);
+        dense_tile<NN>(g.dx, id - g.n13 - g.n2, 0, s);
     }
 }
 
-template <int BM, int WM, int WN, int KB>
+template <int BM, int WM, int WN, int NB, int KB>
 hipError_t launch_grad(GradArgs& g, hipStream_t s) {
-    using TN = Tile<BM, BM, WM, WN, true, true, kEltBf16, kEpiOut, false, false, 4, KB>;
-    using NN = Tile<BM, BM, WM, WN, false, true, kEltBf16, kEpiOut, false, false, 4, KB>;
+    using TN = Tile<BM, BM, WM, WN, true, true, kEltBf16, kEpiOut, false, false, NB, KB>;
+    using NN = Tile<BM, BM, WM, WN, false, true, kEltBf16, kEpiOut, false, false, NB, KB>;
     g.n13 = g.dw13.out ? (int)tiles_of<TN>(g.dw13) : 0;
     g.n2 = g.dw2.out ? (int)tiles_of<TN>(g.dw2) : 0;
     g.nx = g.dx.out ? (int)tiles_of<NN>(g.dx) : 0;
@@ -59,25 +56,60 @@ int64_t square_tiles(const DenseArgs& a, int b) {
 
 }  // namespace
 
-hipError_t launch_dense_dh(const DenseArgs& a, hipStream_t s) {
-    constexpr int E = kEpiGatedBwd;
+// Few tokens give dh and dx few tiles of a long sum: 64 x 64 tiles that leave
+// three quarters of the compute units idle split K, eight steps a part at
+// least; those that leave half idle do so for sums of 64 steps and more. (One
+// token, H = 1024, I = 4096: the backward took 144 us without, 32 with.)
+int dense_bwd_splits(const DenseArgs& a) {
+    const int64_t tiles = (int64_t)((a.M + 63) / 64) * ((a.N + 63) / 64), steps = (a.K + 63) / 64;
+    if (tiles == 0 || tiles > 128 || (tiles > 64 && steps < 64)) return 1;
+    const int64_t most = steps / 8, room = 256 / tiles;
+    const int64_t s = room < most ? room : most;
+    return s < 2 ? 1 : s > 16 ? 16 : (int)s;
+}
+
+template <int EPI>
+static hipError_t launch_split(const DenseArgs& a, hipStream_t s) {
+    const hipError_t e = launch_tile<Tile<64, 64, 2, 2, false, true, kEltBf16, EPI, true, false, 8>>(a, s);
+    return e != hipSuccess ? e : launch_join(a, EPI, s);
+}
+
+template <int E>
+static hipError_t launch_nn(const DenseArgs& a, hipStream_t s) {
+    if (a.splits > 1) return launch_split<E>(a, s);
     if (dense_big_tiles(a, E)) return launch_tile<Tile<256, 256, 2, 4, false, true, kEltBf16, E, false, false>>(a, s);
     if (!dense_one_round(a, E)) return launch_tile<Tile<128, 128, 2, 2, false, true, kEltBf16, E, false, false>>(a, s);
     // Too few 128 x 128 tiles for half of the compute units: 64 x 64 ones.
     if (square_tiles(a, 128) < 128)
-        return launch_tile<Tile<64, 64, 2, 2, false, true, kEltBf16, E, false, false, 4>>(a, s);
+        return launch_tile<Tile<64, 64, 2, 2, false, true, kEltBf16, E, false, false, 8>>(a, s);
     return launch_tile<Tile<128, 128, 2, 2, false, true, kEltBf16, E, false, false, 4>>(a, s);
 }
+
+hipError_t launch_dense_dh(const DenseArgs& a, hipStream_t s) { return launch_nn<kEpiGatedBwd>(a, s); }
 
 hipError_t launch_dense_grads(const DenseArgs& dw13, const DenseArgs& dw2, const DenseArgs& dx, hipStream_t s) {
     GradArgs g;
     g.dw13 = dw13;
     g.dw2 = dw2;
     g.dx = dx;
-    auto tiles = [&](int b) { return square_tiles(dw13, b) + square_tiles(dw2, b) + square_tiles(dx, b); };
-    if (tiles(256) >= 160) return launch_grad<256, 2, 4, 64>(g, s);
-    if (tiles(128) >= 128) return launch_grad<128, 2, 2, 128>(g, s);
-    return launch_grad<64, 2, 2, 128>(g, s);
+    auto tiles = [&](int b) { return square_tiles(dw13, b) + square_tiles(dw2, b) + square_tiles(g.dx, b); };
+    // dx goes alone, in tiles of its own size, where the weights' many 256 x
+    // 256 tiles would leave it few of them, each a long sum: where that sum is
+    // over 2.5 times the compute units' mean share of all steps. (400 tokens,
+    // H = 1024, I = 4096: 8 tiles over K = 8192 took 150 us of the backward's
+    // 160, now 61; H = 3584, I = 2048, where the ratio is 3.7, 2.6 and 1.8 at
+    // 512, 700 and 1024 tokens: 95, 108 and 120 us together, 84, 110 and 130
+    // alone.)
+    const int64_t all = ((square_tiles(dw13, 256) + square_tiles(dw2, 256)) * (int64_t)dw13.K +
+                         square_tiles(dx, 256) * dx.K) / 256;
+    if (dx.out && (dx.splits > 1 || (tiles(256) >= 160 && 2 * (int64_t)dx.K > 5 * all))) {
+        const hipError_t e = launch_nn<kEpiOut>(dx, s);
+        if (e != hipSuccess) return e;
+        g.dx.out = nullptr;
+    }
+    if (tiles(256) >= 160) return launch_grad<256, 2, 4, 4, 64>(g, s);
+    if (tiles(128) >= 128) return launch_grad<128, 2, 2, 4, 128>(g, s);
+    return launch_grad<64, 2, 2, 8, 128>(g, s);
 }
 
 }  // namespace moe

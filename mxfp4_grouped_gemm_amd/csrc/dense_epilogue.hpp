@@ -1,5 +1,6 @@
-// The end of a dense product for four consecutive outputs of one token: used
-// by the few-token kernels and by the kernel that joins a split K.
+// The end of a dense product for four consecutive outputs of one token (the
+// few-token kernels and the kernel that joins a split K), and what the tiles'
+// epilogues share with it.
 #pragma once
 
 #include "common.hpp"
@@ -54,6 +55,9 @@ __device__ __forceinline__ void lora_dot(const LoraArgs& l, int N, int64_t token
     }
 }
 
+// With the accurate expf: an epilogue runs once per output.
+__device__ __forceinline__ float sigmoid(float g) { return 1.0f / (1.0f + expf(-g)); }
+
 __device__ __forceinline__ u32x2 pack4(f32x4 v) { return u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])}; }
 
 // GATED: v gate, up up (saved to a.gate_up if asked for) -> silu(gate) * up;
@@ -76,6 +80,27 @@ __device__ __forceinline__ f32x4 finish4(const DenseArgs& a, int64_t token, int 
         v[3] += __uint_as_float(d[1] & 0xffff0000u);
     }
     return v;
+}
+
+// dh of four columns -> dgate and dup (a.out, rows of [gate; up]) and h, from
+// the saved gate_up.
+__device__ __forceinline__ void backward4(const DenseArgs& a, int64_t token, int col, f32x4 dh) {
+    const uint16_t* gu = a.gate_up + token * 2 * (int64_t)a.N + col;
+    const u32x2 gb = *(const u32x2*)gu, ub = *(const u32x2*)(gu + a.N);
+    f32x4 dg, du, h;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float gv = __uint_as_float(e & 1 ? gb[e / 2] & 0xffff0000u : gb[e / 2] << 16);
+        const float uv = __uint_as_float(e & 1 ? ub[e / 2] & 0xffff0000u : ub[e / 2] << 16);
+        const float sg = sigmoid(gv), silu = gv * sg;
+        dg[e] = dh[e] * uv * sg * (1.0f + gv * (1.0f - sg));
+        du[e] = dh[e] * silu;
+        h[e] = silu * uv;
+    }
+    uint16_t* o = (uint16_t*)a.out + token * a.ldo + col;
+    *(u32x2*)o = pack4(dg);
+    *(u32x2*)(o + a.N) = pack4(du);
+    if (a.h) *(u32x2*)(a.h + token * (int64_t)a.N + col) = pack4(h);
 }
 
 __device__ __forceinline__ void store4(const DenseArgs& a, int64_t token, int col, f32x4 v) {

@@ -13,7 +13,7 @@ namespace {
 // the epilogue. A thread owns four columns (gated: four pairs).
 template <int EPI>
 __global__ __launch_bounds__(256) void join_kernel(DenseArgs a) {  // 64 or 256 threads
-    constexpr bool kGated = EPI != kEpiOut;
+    constexpr bool kGated = EPI == kEpiGated || EPI == kEpiGatedMx;
     const int64_t idx = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     const int per = a.N / 4;
     const int64_t m = idx / per;
@@ -29,6 +29,10 @@ __global__ __launch_bounds__(256) void join_kernel(DenseArgs a) {  // 64 or 256 
             v += *(const f32x4*)p;
             if constexpr (kGated) up += *(const f32x4*)(p + a.N);
         }
+    if constexpr (EPI == kEpiGatedBwd) {
+        if (ok) backward4(a, m, n, v);
+        return;
+    }
     if (ok) v = finish4<kGated>(a, m, n, v, up);
     if constexpr (EPI == kEpiGatedMx) {
         float big = 0.0f;
@@ -94,7 +98,8 @@ hipError_t launch_join(const DenseArgs& a, int epi, hipStream_t s) {
     const dim3 grid((unsigned)((threads + size - 1) / size)), block(size);
     if (epi == kEpiOut) hipLaunchKernelGGL(join_kernel<kEpiOut>, grid, block, 0, s, a);
     else if (epi == kEpiGated) hipLaunchKernelGGL(join_kernel<kEpiGated>, grid, block, 0, s, a);
-    else hipLaunchKernelGGL(join_kernel<kEpiGatedMx>, grid, block, 0, s, a);
+    else if (epi == kEpiGatedMx) hipLaunchKernelGGL(join_kernel<kEpiGatedMx>, grid, block, 0, s, a);
+    else hipLaunchKernelGGL(join_kernel<kEpiGatedBwd>, grid, block, 0, s, a);
     return hipGetLastError();
 }
 

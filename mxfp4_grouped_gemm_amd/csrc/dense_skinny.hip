@@ -235,7 +235,7 @@ hipError_t launch_one(const DenseArgs& a, const float* xf, hipStream_t s) {
     constexpr int kRows = NW * (GATED ? 8 : 16);
     const unsigned groups = (unsigned)((a.N + kRows - 1) / kRows);
     const dim3 block(kWaves * 64);
-    if constexpr (NJ > 1 || ELT == kEltBf16) {
+    if constexpr (ELT == kEltBf16) {
         if (a.splits > 1 || a.lora.n > 0) {
             const unsigned narrow = (unsigned)skinny_narrow(a);
             hipLaunchKernelGGL((skinny_kernel<ELT, NJ, NW, GATED, XF32, true>), dim3(groups * (unsigned)a.splits + narrow),
@@ -249,13 +249,21 @@ hipError_t launch_one(const DenseArgs& a, const float* xf, hipStream_t s) {
     return hipGetLastError();
 }
 
+template <int ELT, int NJ, bool GATED, bool XF32>
+hipError_t launch_width(const DenseArgs& a, bool wide, const float* xf, hipStream_t s) {
+    if constexpr (ELT == kEltBf16) {
+        if (wide) return launch_one<ELT, NJ, 4, GATED, XF32>(a, xf, s);
+    }
+    return launch_one<ELT, NJ, 1, GATED, XF32>(a, xf, s);
+}
+
 template <int ELT, bool GATED, bool XF32>
 hipError_t launch_nj(const DenseArgs& a, const float* xf, hipStream_t s) {
     if (a.M <= 16) return launch_one<ELT, 1, 1, GATED, XF32>(a, xf, s);
-    const bool wide = a.splits > 1 && skinny_wide(a, GATED);
-    if (a.M <= 32)
-        return wide ? launch_one<ELT, 2, 4, GATED, XF32>(a, xf, s) : launch_one<ELT, 2, 1, GATED, XF32>(a, xf, s);
-    return wide ? launch_one<ELT, 4, 4, GATED, XF32>(a, xf, s) : launch_one<ELT, 4, 1, GATED, XF32>(a, xf, s);
+    const bool wide = ELT == kEltBf16 && a.splits > 1 && skinny_wide(a, GATED);
+    if (a.M <= 32) return launch_width<ELT, 2, GATED, XF32>(a, wide, xf, s);
+    if constexpr (ELT == kEltMx8) return hipErrorInvalidValue;  // kSkinnyMaxTokensMx
+    else return launch_width<ELT, 4, GATED, XF32>(a, wide, xf, s);
 }
 
 }  // namespace
@@ -266,14 +274,16 @@ bool skinny_wide(const DenseArgs& a, bool gated) { return (gated ? 2 * (int64_t)
 int skinny_narrow(const DenseArgs& a) { return a.lora.n > 0 ? a.M * ((a.lora.rank + 15) / 16) : 0; }
 
 int skinny_splits(const DenseArgs& a, int elt, int epi) {
-    if (a.M <= 16) return 1;
+    // Up to 32 tokens the tokens' bytes do not pay for a second kernel, unless
+    // adapters need it anyway or W has few rows (2048 pairs, K = 3584, 32 tokens: 12.0 us, 13.5
+    // in parts; 64 tokens: 18.9 and 16.0).
     const bool gated = epi != kEpiOut;
     const int64_t rows = gated ? 2 * (int64_t)a.N : a.N;
+    if (elt != kEltBf16 || a.M <= 16 || (a.M <= 32 && a.lora.n == 0 && rows >= 2048)) return 1;
     const int64_t groups = skinny_wide(a, gated) ? (rows + 63) / 64 : (rows + 15) / 16;
-    const int bk = elt == kEltBf16 ? 64 : 128;
     // A part of K has a chunk for each wave; a workgroup a compute unit, those
     // of the narrow product counted.
-    const int64_t most = (a.K + bk - 1) / bk / kWaves, room = (256 - skinny_narrow(a)) / groups;
+    const int64_t most = (a.K + 63) / 64 / kWaves, room = (256 - skinny_narrow(a)) / groups;
     const int64_t s = room < most ? room : most;
     return s < 2 ? 1 : (int)s;
 }

@@ -8,8 +8,8 @@
 // multiplied (two buffers, one barrier a step; the buffers are separate
 // __shared__ objects, so that the compiler sees that reads of one need not
 // wait for loads into the other). Tiles that leave compute units idle have no
-// second workgroup to hide a load behind: they run with four buffers, three
-// steps of loads in flight.
+// second workgroup to hide a load behind: they run with four buffers (64 x 64
+// tiles with eight), three (seven) steps of loads in flight.
 //
 // W is the MFMA's first operand, so a lane's four results are four
 // consecutive n of one m. The rows of W are dealt to the fragments such that
@@ -31,6 +31,7 @@
 
 #include "common.hpp"
 #include "dense.hpp"
+#include "dense_epilogue.hpp"
 #include "mx8.hpp"
 
 namespace moe {
@@ -49,6 +50,15 @@ typedef __attribute__((address_space(3))) void* lds_ptr;
 
 __device__ __forceinline__ void load_lds16(rsrc_t r, uint8_t* dst, uint32_t voff, uint32_t soff) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)dst, 16, voff, soff, 0, 0);
+}
+
+// f(0), f(1), ... f(N - 1), each with its number as a constant.
+template <int I, int N, class F>
+__device__ __forceinline__ void each(F f) {
+    if constexpr (I < N) {
+        f(std::integral_constant<int, I>());
+        each<I + 1, N>(f);
+    }
 }
 
 // Asks the scheduler to spread READS LDS reads and LOADS loads evenly over
@@ -109,10 +119,6 @@ __device__ __forceinline__ void sync_step() {
         asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LOADS) : "memory");
     }
 }
-
-// e^x / (1 + e^x) and friends with the accurate expf: the epilogue runs once
-// per output.
-__device__ __forceinline__ float sigmoid(float g) { return 1.0f / (1.0f + expf(-g)); }
 
 template <int BM_, int BN_, int WM_, int WN_, bool XT_, bool WT_, int ELT_, int EPI_, bool SPLIT_, bool LORA_, int NB_ = 2,
           int KB_ = 128>
@@ -264,11 +270,22 @@ __device__ __forceinline__ void lora_accumulate(const LoraArgs& l, int64_t brows
     }
 }
 
-// One tile: number `id` of the product's tiles, part `part` of a split K, with
-// buffers s0 and s1 (and s2, s3 of tiles with four of them).
+// The LDS buffers of a kernel whose tiles need NB of BUF bytes: separate
+// objects (see the top), of which the unused ones vanish.
+#define MOE_TILE_BUFFERS(s, NB, BUF)                                      \
+    __shared__ __align__(1024) uint8_t s##0_[BUF];                        \
+    __shared__ __align__(1024) uint8_t s##1_[BUF];                        \
+    __shared__ __align__(1024) uint8_t s##2_[(NB) > 2 ? (BUF) : 16];      \
+    __shared__ __align__(1024) uint8_t s##3_[(NB) > 2 ? (BUF) : 16];      \
+    __shared__ __align__(1024) uint8_t s##4_[(NB) > 4 ? (BUF) : 16];      \
+    __shared__ __align__(1024) uint8_t s##5_[(NB) > 4 ? (BUF) : 16];      \
+    __shared__ __align__(1024) uint8_t s##6_[(NB) > 4 ? (BUF) : 16];      \
+    __shared__ __align__(1024) uint8_t s##7_[(NB) > 4 ? (BUF) : 16];      \
+    uint8_t* const s[8] = {s##0_, s##1_, s##2_, s##3_, s##4_, s##5_, s##6_, s##7_}
+
+// One tile: number `id` of the product's tiles, part `part` of a split K.
 template <class C>
-__device__ __forceinline__ void dense_tile(const DenseArgs& a, int id, int part, uint8_t* s0, uint8_t* s1, uint8_t* s2,
-                                           uint8_t* s3) {
+__device__ __forceinline__ void dense_tile(const DenseArgs& a, int id, int part, uint8_t* const (&s)[8]) {
     const int tid = (int)threadIdx.x, lane = tid & 63;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = w / C::WN, wn = w % C::WN;
@@ -497,30 +514,19 @@ __device__ __forceinline__ void dense_tile(const DenseArgs& a, int id, int part,
             spread<kXR + kWR, C::XL + C::WL, kMfma>();
             __builtin_amdgcn_sched_barrier(0);
         };
-        static_assert(C::NB == 2 || C::NB == 4, "two or four buffers");
+        static_assert(C::NB == 2 || C::NB == 4 || C::NB == 8, "the step's operand sets alternate");
         if (kt0 < kt1) {
-            issue(s0, kt0);
-            issue(s1, kt0 + 1);
-            if constexpr (C::NB == 4) {
-                issue(s2, kt0 + 2);
-                issue(s3, kt0 + 3);
-            }
+            each<0, C::NB>([&](auto i) { issue(s[i.value], kt0 + i.value); });
             sync_step<(C::NB - 1) * (C::XL + C::WL)>();
-            read_ws(s0, 0, 0);
-            read_xs(s0, 0, 0);
+            read_ws(s[0], 0, 0);
+            read_xs(s[0], 0, 0);
             // A step for each buffer a turn; a step past the end multiplies
             // zeros.
-            for (int kt = kt0; kt < kt1; kt += C::NB) {
-                if constexpr (C::NB == 2) {
-                    step(s0, s1, 0, kt);
-                    step(s1, s0, C::KB == 128 ? 0 : 1, kt + 1);
-                } else {
-                    step(s0, s1, 0, kt);
-                    step(s1, s2, C::KB == 128 ? 0 : 1, kt + 1);
-                    step(s2, s3, 0, kt + 2);
-                    step(s3, s0, C::KB == 128 ? 0 : 1, kt + 3);
-                }
-            }
+            for (int kt = kt0; kt < kt1; kt += C::NB)
+                each<0, C::NB>([&](auto i) {
+                    constexpr int b = i.value;
+                    step(s[b], s[(b + 1) % C::NB], C::KB == 128 ? 0 : b & 1, kt + b);
+                });
         }
     } else {
         // A lane's 32 elements are pieces g and 4 + g; its scale operand is
@@ -568,17 +574,17 @@ __device__ __forceinline__ void dense_tile(const DenseArgs& a, int id, int part,
             __builtin_amdgcn_sched_barrier(0);
         };
         if (kt0 < kt1) {
-            issue(s0, kt0);
+            issue(s[0], kt0);
             load_scales(kt0);
-            store_scales(s0, kt0);
+            store_scales(s[0], kt0);
             __syncthreads();
-            issue(s1, kt0 + 1);
+            issue(s[1], kt0 + 1);
             load_scales(kt0 + 1);
-            read_ws(s0, 0);
-            read_x1(s0, 0);
+            read_ws(s[0], 0);
+            read_x1(s[0], 0);
             for (int kt = kt0; kt < kt1; kt += 2) {
-                step(s0, s1, 0, kt);
-                step(s1, s0, 1, kt + 1);
+                step(s[0], s[1], 0, kt);
+                step(s[1], s[0], 1, kt + 1);
             }
         }
     }
@@ -742,11 +748,8 @@ __device__ __forceinline__ void dense_tile(const DenseArgs& a, int id, int part,
 
 template <class C>
 __global__ __launch_bounds__(C::THREADS, 2) void dense_kernel(DenseArgs a) {
-    __shared__ __align__(1024) uint8_t s0[C::BUF];
-    __shared__ __align__(1024) uint8_t s1[C::BUF];
-    __shared__ __align__(1024) uint8_t s2[C::NB > 2 ? C::BUF : 16];
-    __shared__ __align__(1024) uint8_t s3[C::NB > 2 ? C::BUF : 16];
-    dense_tile<C>(a, (int)blockIdx.x, (int)blockIdx.y, s0, s1, s2, s3);
+    MOE_TILE_BUFFERS(s, C::NB, C::BUF);
+    dense_tile<C>(a, (int)blockIdx.x, (int)blockIdx.y, s);
 }
 
 template <class C>

@@ -148,12 +148,15 @@ def test_binding_refuses_host_tensors():
         moe.moe_ffn_forward(x, torch.zeros(16, 64, dtype=torch.bfloat16), torch.zeros(64, 8, dtype=torch.bfloat16))
 
 
-def test_sizes_of_the_workspace_grow_with_the_batch():
-    last = 0
-    for T in (1, 16, 64, 65, 128, 1000, 8192):
-        for need in (moe.moe_ffn_workspace_size(T, 3584, 2048),):
-            assert need >= T * 2048 * 2 and need % 256 == 0
-        b = moe.moe_ffn_backward_workspace_size(T, 3584, 2048)
-        assert b > last
-        last = b
-    assert isinstance(moe._CLora().n, int) and ctypes.sizeof(moe._CLora) == 48
+def test_workspaces_hold_what_the_calls_keep():
+    """At least the intermediate tensors of the batch, in whole 256 bytes."""
+    H, I = 3584, 2048
+    for T in (1, 16, 17, 32, 33, 64, 65, 128, 1000, 8192):
+        for need, least in ((moe.moe_ffn_workspace_size(T, H, I), T * I * 2),
+                            (moe.moe_ffn_workspace_size(T, H, I, 16, 64), T * I * 2 + T * 64 * 4),
+                            (moe.moe_ffn_mxfp8_workspace_size(T, H, I), T * I + T * I // 32),
+                            (moe.moe_ffn_backward_workspace_size(T, H, I), T * I * 6),
+                            (moe.moe_lora_linear_workspace_size(T, H, I, 8), T * 8 * 4)):
+            assert need >= least and need % 256 == 0, (T, need, least)
+    assert moe.moe_lora_linear_workspace_size(16, H, I) == 0
+    assert ctypes.sizeof(moe._CLora) == 48
