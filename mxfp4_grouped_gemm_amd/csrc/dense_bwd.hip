@@ -93,22 +93,29 @@ hipError_t launch_dense_grads(const DenseArgs& dw13, const DenseArgs& dw2, const
     g.dw2 = dw2;
     g.dx = dx;
     auto tiles = [&](int b) { return square_tiles(dw13, b) + square_tiles(dw2, b) + square_tiles(g.dx, b); };
-    // dx goes alone, in tiles of its own size, where the weights' many 256 x
-    // 256 tiles would leave it few of them, each a long sum: where that sum is
-    // over 2.5 times the compute units' mean share of all steps. (400 tokens,
-    // H = 1024, I = 4096: 8 tiles over K = 8192 took 150 us of the backward's
-    // 160, now 61; H = 3584, I = 2048, where the ratio is 3.7, 2.6 and 1.8 at
-    // 512, 700 and 1024 tokens: 95, 108 and 120 us together, 84, 110 and 130
-    // alone.)
-    const int64_t all = ((square_tiles(dw13, 256) + square_tiles(dw2, 256)) * (int64_t)dw13.K +
-                         square_tiles(dx, 256) * dx.K) / 256;
-    if (dx.out && (dx.splits > 1 || (tiles(256) >= 160 && 2 * (int64_t)dx.K > 5 * all))) {
+    // 256 x 256 tiles from 192 of them on, or from 160 for long sums (H = 2048,
+    // I = 1408: at 700, 1024, 1500 and 2048 tokens, 160 to 200 tiles, the whole
+    // backward took 66, 83, 83 and 86 us in them, 49, 69, 85 and 112 in 128 x
+    // 128 ones; H = 1024, I = 4096, 192 tiles and more: 32 and 40 us at one
+    // token, 75 and 87 at 700), then 128 x 128.
+    const int64_t big = tiles(256);
+    const int edge = big >= 192 || (big >= 160 && dw13.K >= 1536) ? 256 : tiles(128) >= 128 ? 128 : 64;
+    // dx goes alone, in tiles of its own size, where the weights' many tiles
+    // would leave it few of them, each a long sum: where that sum is over 2.5
+    // times the compute units' mean share of all steps. (400 tokens, H = 1024,
+    // I = 4096: 8 tiles of 256 x 256 over K = 8192 took 150 us of the
+    // backward's 160, now 61; H = 3584, I = 2048, where the ratio is 3.7, 2.6
+    // and 1.8 at 512, 700 and 1024 tokens: 95, 108 and 120 us together, 84, 110
+    // and 130 alone.)
+    const int64_t share = ((square_tiles(dw13, edge) + square_tiles(dw2, edge)) * (int64_t)dw13.K +
+                           square_tiles(dx, edge) * dx.K) / 256;
+    if (dx.out && (dx.splits > 1 || (edge > 64 && 2 * (int64_t)dx.K > 5 * share))) {
         const hipError_t e = launch_nn<kEpiOut>(dx, s);
         if (e != hipSuccess) return e;
         g.dx.out = nullptr;
     }
-    if (tiles(256) >= 160) return launch_grad<256, 2, 4, 4, 64>(g, s);
-    if (tiles(128) >= 128) return launch_grad<128, 2, 2, 4, 128>(g, s);
+    if (edge == 256) return launch_grad<256, 2, 4, 4, 64>(g, s);
+    if (edge == 128) return launch_grad<128, 2, 2, 4, 128>(g, s);
     return launch_grad<64, 2, 2, 8, 128>(g, s);
 }
 

@@ -210,6 +210,26 @@ static void launch(const NormArgs& a, bool vec, hipStream_t s) {
 }
 
 hipError_t launch_rms_norm(const NormArgs& a, hipStream_t s) {
+    // A launch holds fewer than 2^32 threads (1024 a row at most).
+    constexpr int kMostRows = 1 << 21;
+    if (a.T > kMostRows) {
+        for (int t = 0; t < a.T; t += kMostRows) {
+            NormArgs b = a;
+            const int64_t rb = a.res_f32 ? 4 : 2;
+            b.T = a.T - t < kMostRows ? a.T - t : kMostRows;
+            b.x = a.x + t * a.ldx;
+            if (a.residual) b.residual = (const char*)a.residual + t * a.ldr * rb;
+            if (a.residual_out) b.residual_out = (char*)a.residual_out + t * a.ldro * rb;
+            if (a.y) b.y = a.y + t * a.ldy;
+            if (a.q) {
+                b.q = a.q + t * a.ldq;
+                b.qs = a.qs + t * a.ldqs;
+            }
+            const hipError_t e = launch_rms_norm(b, s);
+            if (e != hipSuccess) return e;
+        }
+        return hipSuccess;
+    }
     auto ok = [](const void* p, int64_t ld, int bytes) {
         return p == nullptr || ((uintptr_t)p % 16 == 0 && (ld * bytes) % 16 == 0);
     };

@@ -116,6 +116,15 @@ def test_norm_in_place_strides_and_rows_behind(moe):
     assert bool((q[T:] == 77).all()) and bool((q[:, 0] == 77).all()) and bool((q[:, 1 + H:] == 77).all())
 
 
+def test_norm_of_more_rows_than_a_launch(moe):
+    T, H = (1 << 21) + 3, 8
+    x = torch.ones(T, H, dtype=BF, device="cuda")
+    x[-4:] = 2.0
+    x[: 1 << 21] *= 3.0
+    y, _, _, _ = moe.moe_rms_norm(x, torch.ones(H, dtype=BF, device="cuda"), eps=0.0)
+    assert bool((y == 1).all())
+
+
 def test_norm_special_values(moe):
     H = 64
     x = torch.zeros(6, H)
@@ -141,7 +150,7 @@ def test_norm_special_values(moe):
 
 # ---------------------------------------------------------------- linear
 LINEAR = [(1, 8, 8), (1, 3584, 112), (3, 72, 40), (16, 520, 1000), (17, 136, 24), (33, 3584, 384), (64, 64, 72),
-          (65, 72, 136), (130, 1000, 520), (300, 3584, 896), (777, 264, 1032), (2100, 192, 4104)]
+          (65, 72, 136), (130, 1000, 520), (300, 3584, 896), (777, 264, 1032), (2100, 192, 4104), (4200, 200, 64)]
 
 
 @pytest.mark.parametrize("T,K,N", LINEAR)
@@ -305,7 +314,9 @@ def test_ffn_tokens_do_not_meet(moe, T):
 
 # -------------------------------------------------------------- backward
 @pytest.mark.parametrize("T,H,I", [(1, 8, 8), (2, 40, 72), (16, 520, 136), (63, 264, 1000), (64, 96, 64), (65, 136, 72),
-                                   (129, 520, 264), (300, 1032, 520), (777, 264, 392), (2200, 1032, 2056)])
+                                   (129, 520, 264), (300, 1032, 520), (777, 264, 392), (2200, 1032, 2056),
+                                   # parts of K for dh and dx, dx alone, 128 x 128 tiles
+                                   (1, 2056, 1032), (130, 264, 4104), (200, 2056, 2760), (520, 1032, 1032)])
 def test_ffn_backward(moe, T, H, I):
     g = gen(T + H + I)
     dout, x, gu = rnd(g, T, H), rnd(g, T, H), rnd(g, T, 2 * I)
