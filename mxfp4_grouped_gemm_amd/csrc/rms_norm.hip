@@ -2,18 +2,20 @@
 // optional MXFP8 output:
 //   s = x + residual;  v = s / sqrt(mean(s^2) + eps) * (offset + weight);
 //   residual_out = s, y = bf16(v), (q, qs) = MXFP8(v).
-// s and v are fp32, the squares are summed by eights in fp32 and then in fp64
-// (an e4m3 code changes where v crosses a tie, so 1e-7 of the root counts
-// there); each output is rounded once, from the
-// fp32 value (y and q do not pass through each other).
+// s is fp32 and its squares are summed in fp64. For the MXFP8 output v is the
+// fp32 number nearest to the exact product with what it was rounded off by,
+// and s carries what a sum with an fp32 residual was rounded off by: a code
+// changes where v crosses a tie, which an error of 1e-7 does for one element
+// in a million (eights of squares in fp32 were worth 0.7 us of 10.5 at 1531
+// rows, and changed single codes). y and q are each rounded once from v.
 //
 // Bound by memory: 8 bytes an element with bf16 streams, about 9 with the
 // MXFP8 output. A row is read once and stays in registers between the sum and
 // the outputs. Every element is read and written by one lane, so outputs may
 // be the inputs' own buffers. 16384 rows of 3584 with both outputs take 90 us,
-// 5.9 TB/s (a plain copy of 1 GiB: 5.1). Streaming stores count most in that
-// (ordinary ones: 95 us; at 1531 rows 9.7 against 8.1), then four waves a row
-// (a wave a row, with 56 elements a lane: 117 us with ordinary stores).
+// 5.9 TB/s (a plain copy of 1 GiB: 5.1). Streaming stores count in that
+// (ordinary ones: 95 us), and four waves a row (a wave a row, with 56 elements
+// a lane: 117 us with ordinary stores).
 #include "common.hpp"
 #include "dense.hpp"
 #include "mx8.hpp"
@@ -24,6 +26,33 @@ namespace {
 
 typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x8 __attribute__((ext_vector_type(8)));
+
+// (s + sl) * r * w as the nearest fp32 number and the rest, for r = rh + rl
+// and sl, rl at most half a step of s and rh: exact products by fma, to about
+// 2^-45. NaN and infinities come from the plain product.
+struct Product {
+    float v, rest;
+};
+__device__ __forceinline__ Product product3(float s, float sl, float rh, float rl, float w) {
+#pragma clang fp contract(off)  // p and v are the rounded products
+    const float p = s * rh;
+    const float ep = fmaf(sl, rh, fmaf(s, rl, fmaf(s, rh, -p)));
+    const float v = p * w;
+    const float ev = fmaf(ep, w, fmaf(p, w, -v));
+    const float n = v + ev;
+    const bool fine = fabsf(n) < __builtin_inff();
+    return {fine ? n : v, fine ? (v - n) + ev : 0.0f};
+}
+
+// Halfway between two e4m3 codes of the normal range.
+__device__ __forceinline__ bool tie(float z) { return (__float_as_uint(z) & 0xfffffu) == 0x80000u; }
+
+// z = v * inv for its e4m3 code: a tie goes by the rest that v was rounded
+// off by.
+__device__ __forceinline__ float settle(float z, float rest) {
+    const uint32_t step = (rest > 0.0f) == (z > 0.0f) ? 1u : 0xffffffffu;
+    return tie(z) && rest != 0.0f ? __uint_as_float(__float_as_uint(z) + step) : z;
+}
 
 template <int CTRL>
 __device__ __forceinline__ float dpp(float v) {
@@ -43,8 +72,7 @@ __device__ __forceinline__ double join(uint32_t lo, uint32_t hi) {
 }
 
 // Sum over the wave, the same in every lane: xor by 1 and 2 inside quads, then
-// mirrored halves of a row, then the rows. In fp64, as the last few additions
-// are what a long fp32 sum loses most in (and they are few).
+// mirrored halves of a row, then the rows.
 __device__ __forceinline__ double wave_sum(double v) {
     v += dpp<0xB1>(v);   // quad_perm [1, 0, 3, 2]
     v += dpp<0x4E>(v);   // quad_perm [2, 3, 0, 1]
@@ -126,26 +154,32 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void rms_norm_kernel
     // Chunk c of this lane: VEC elements [(c * kLanes + tid) * 8, +8); else
     // elements c * 8 * kLanes + tid + e * kLanes.
     auto first = [&](int c) { return VEC ? (c * kLanes + tid) * 8 : c * 8 * kLanes + tid; };
-    f32x8 s[NC];
+    f32x8 s[NC], sl[NC];  // sl: what an fp32 residual's sum was rounded off by
     double sum = 0.0;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
         const int i = first(c);
         if (i < H) {
             s[c] = load8<VEC>(xr, false, i, kLanes, H);
-            if (a.residual) s[c] += load8<VEC>(rr, a.res_f32, i, kLanes, H);
+            sl[c] = f32x8{0, 0, 0, 0, 0, 0, 0, 0};
+            if (a.residual) {
+                const f32x8 x = s[c], r = load8<VEC>(rr, a.res_f32, i, kLanes, H);
+                s[c] = x + r;
+                if (a.res_f32) {
+                    const f32x8 b = s[c] - x;
+                    sl[c] = (x - (s[c] - b)) + (r - b);
+                }
+            }
         } else {
-            s[c] = f32x8{0, 0, 0, 0, 0, 0, 0, 0};
+            s[c] = sl[c] = f32x8{0, 0, 0, 0, 0, 0, 0, 0};
         }
     }
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
         const int i = first(c);
         if (a.residual_out && i < H) store8<VEC>(ro, a.res_f32, i, kLanes, H, s[c]);
-        float q = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) q = fmaf(s[c][e], s[c][e], q);
-        sum += (double)q;
+        for (int e = 0; e < 8; ++e) sum = fma((double)s[c][e], (double)s[c][e], sum);
     }
     sum = wave_sum(sum);
     if constexpr (WAVES > 1) {
@@ -156,14 +190,21 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void rms_norm_kernel
 #pragma unroll
         for (int w = 0; w < WAVES; ++w) sum += part[w];
     }
-    const float r = (float)(1.0 / sqrt(sum / (double)H + (double)a.eps));
+    const double root = 1.0 / sqrt(sum / (double)H + (double)a.eps);
+    const float rh = (float)root;
+    const float rl = fabsf(rh) < __builtin_inff() ? (float)(root - (double)rh) : 0.0f;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
         const int i = first(c);
         if (i >= H) continue;
         f32x8 v = load8<VEC>(a.weight, a.weight_f32, i, kLanes, H);
+        Product p[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = s[c][e] * r * (a.offset + v[e]);
+        for (int e = 0; e < 8; ++e) {
+            if (a.q) p[e] = product3(s[c][e], sl[c][e], rh, rl, a.offset + v[e]);
+            else p[e] = {s[c][e] * rh * (a.offset + v[e]), 0.0f};  // bf16 needs no more
+            v[e] = p[e].v;
+        }
         if (a.y) store8<VEC>(a.y + t * a.ldy, false, i, kLanes, H, v);
         if (a.q) {
             uint8_t* qr = a.q + t * a.ldq;
@@ -178,8 +219,18 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void rms_norm_kernel
                 const uint32_t b = mx8_scale_byte(m);
                 const float inv = mx8_inv_scale(b);
                 u32x2 o;
-                o[0] = mx8_pack4(v[0], v[1], v[2], v[3], inv);
-                o[1] = mx8_pack4(v[4], v[5], v[6], v[7], inv);
+                bool ties = false;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    v[e] *= inv;
+                    ties |= tie(v[e]);
+                }
+                if (ties) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] = settle(v[e], p[e].rest);
+                }
+                o[0] = mx8_pack4(v[0], v[1], v[2], v[3], 1.0f);
+                o[1] = mx8_pack4(v[4], v[5], v[6], v[7], 1.0f);
                 __builtin_nontemporal_store(o, (u32x2*)(qr + i));
                 if ((tid & 3) == 0) sr[i >> 5] = (uint8_t)b;
             } else {
@@ -193,7 +244,8 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void rms_norm_kernel
                     for (int d = 1; d < 32; d *= 2) m = fmaxf(m, __shfl_xor(m, d));
                     const uint32_t b = mx8_scale_byte(m);
                     if (k < H) {
-                        qr[k] = (uint8_t)mx8_pack<false>(v[e], v[e], mx8_inv_scale(b), 0u);
+                        const float z = settle(v[e] * mx8_inv_scale(b), p[e].rest);
+                        qr[k] = (uint8_t)mx8_pack<false>(z, z, 1.0f, 0u);
                         if ((tid & 31) == 0) sr[k >> 5] = (uint8_t)b;
                     }
                 }
@@ -246,7 +298,7 @@ hipError_t launch_rms_norm(const NormArgs& a, hipStream_t s) {
     else if (a.H <= 8192) launch<4, 4>(a, vec, s);
     else if (a.H <= 16384) launch<4, 8>(a, vec, s);
     else if (a.H <= 32768) launch<16, 4>(a, vec, s);
-    else launch<16, 8>(a, vec, s);
+    else launch<16, 8>(a, vec, s);  // spills 172 bytes a lane
     return hipGetLastError();
 }
 

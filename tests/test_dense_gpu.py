@@ -125,6 +125,22 @@ def test_norm_of_more_rows_than_a_launch(moe):
     assert bool((y == 1).all())
 
 
+@pytest.mark.parametrize("H", [1536, 2784])
+@pytest.mark.parametrize("res", [None, BF, F32])
+def test_norm_codes_are_exact(moe, H, res):
+    """A code is the one of the exact value: the product is carried to 2^-45,
+    so of 2^22 elements none is expected within that of a tie."""
+    g = gen(H)
+    T = (1 << 22) // H
+    x, w = rnd(g, T, H), rnd(g, H)
+    r = None if res is None else rnd(g, T, H, scale=3, dtype=res)
+    _, _, q, qs = moe.moe_rms_norm(cuda(x), cuda(w), residual=cuda(r), mxfp8=True)
+    _, v = ref.norm(x.double(), None if r is None else r.double(), w.double(), 1e-6, 0.0)
+    want, scale = ref.mx_quant(v)
+    assert torch.equal(qs.double().cpu(), scale)
+    assert torch.equal(q.double().cpu(), want)
+
+
 def test_norm_special_values(moe):
     H = 64
     x = torch.zeros(6, H)
@@ -143,7 +159,7 @@ def test_norm_special_values(moe):
     assert float(qs[0, 0]) == 2.0 ** -127
     assert bool(y[2].isnan().all()) and bool(q[2].isnan().all())
     assert bool(y[3][other & (torch.arange(H) != 40)].eq(0).all()) and bool(y[3, 40].isnan())
-    assert bool(y[4][other].eq(0).all())  # the squares overflow: s / inf
+    assert bool(y[4][other].eq(1).all())  # fp32 squares would overflow: by the formula each is 1
     assert bool((y[5][other] == 1).all())
     assert bool((q[5][other] * qs[5].repeat_interleave(32)[other] == 1).all())
 
