@@ -55,8 +55,13 @@ __device__ __forceinline__ void lora_dot(const LoraArgs& l, int N, int64_t token
     }
 }
 
-// With the accurate expf: an epilogue runs once per output.
-__device__ __forceinline__ float sigmoid(float g) { return 1.0f / (1.0f + expf(-g)); }
+// With the hardware exp2 and reciprocal, about an ulp each (and |g| 2^-24 from
+// the exponent's product): every output of it is rounded to bf16 or e4m3. The
+// accurate expf and quotient are some 40 vector instructions for each of the
+// 64 outputs a lane has in a tile of the gated product (4096 pairs, K = 3584,
+// 8192 tokens: 353 us with them, 336 with these). Very negative g: exp
+// overflows, the reciprocal is 0.
+__device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }
 
 __device__ __forceinline__ u32x2 pack4(f32x4 v) { return u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])}; }
 
@@ -71,7 +76,7 @@ __device__ __forceinline__ f32x4 finish4(const DenseArgs& a, int64_t token, int 
             *(u32x2*)(gu + a.N) = pack4(up);
         }
 #pragma unroll
-        for (int r = 0; r < 4; ++r) v[r] = swiglu(v[r], up[r]);
+        for (int r = 0; r < 4; ++r) v[r] = v[r] * sigmoid(v[r]) * up[r];
     } else if (a.addend) {
         const u32x2 d = *(const u32x2*)(a.addend + token * a.ldadd + col);
         v[0] += __uint_as_float(d[0] << 16);

@@ -679,7 +679,7 @@ __device__ __forceinline__ void dense_tile(const DenseArgs& a, int id, int part,
             for (int f = 0; f < C::F; ++f)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    h[f][r] = swiglu(acc[f][j][r], acc[f + C::F][j][r]);
+                    h[f][r] = acc[f][j][r] * sigmoid(acc[f][j][r]) * acc[f + C::F][j][r];
                     big = fmaxf(big, mx8_finite_abs(h[f][r]));
                 }
             if constexpr (C::EPI == kEpiGatedMx) {
