@@ -15,7 +15,8 @@
 // be the inputs' own buffers. 16384 rows of 3584 with both outputs take 90 us,
 // 5.9 TB/s (a plain copy of 1 GiB: 5.1). Streaming stores count in that
 // (ordinary ones: 95 us), and four waves a row (a wave a row, with 56 elements
-// a lane: 117 us with ordinary stores).
+// a lane: 117 us with ordinary stores). Rows at any element address: 19248 of
+// 2794, bf16 residual and output, 109 us (element by element: 200).
 #include "common.hpp"
 #include "dense.hpp"
 #include "mx8.hpp"
@@ -88,24 +89,32 @@ __device__ __forceinline__ double wave_sum(double v) {
     return join(lo2[0], hi2[0]) + join(lo2[1], hi2[1]);
 }
 
-// Eight elements i..i+7 of a row (VEC), or elements i, i + step, ... (the
-// layout of rows whose start or stride is not 16-byte aligned).
+// Eight elements i..i+7 of a row. VEC: all of them are in the row and 16-byte
+// aligned (8 bytes in q); else they are at any element's address, which one
+// wide load or store takes as well, and the row's last eight may be fewer.
+typedef f32x4 __attribute__((aligned(4))) f32x4_any;
+typedef u16x8 __attribute__((aligned(2))) u16x8_any;
+typedef u32x4 __attribute__((aligned(2))) u32x4_any;
+typedef u32x2 __attribute__((aligned(1))) u32x2_any;
+
 template <bool VEC>
-__device__ __forceinline__ f32x8 load8(const void* row, bool f32, int i, int step, int H) {
+__device__ __forceinline__ f32x8 load8(const void* row, bool f32, int i, int H) {
     f32x8 r;
-    if constexpr (VEC) {
+    if (VEC || i + 8 <= H) {
         if (f32) {
-            const f32x4 a = *(const f32x4*)((const float*)row + i), b = *(const f32x4*)((const float*)row + i + 4);
+            const f32x4_any* p = (const f32x4_any*)((const float*)row + i);
+            const f32x4 a = VEC ? *(const f32x4*)p : p[0], b = VEC ? ((const f32x4*)p)[1] : p[1];
             r = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
         } else {
-            const u16x8 u = *(const u16x8*)((const uint16_t*)row + i);
+            const u16x8_any* p = (const u16x8_any*)((const uint16_t*)row + i);
+            const u16x8 u = VEC ? *(const u16x8*)p : *p;
 #pragma unroll
             for (int e = 0; e < 8; ++e) r[e] = bf16_bits_to_f32(u[e]);
         }
     } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const int k = i + e * step;
+            const int k = i + e;
             r[e] = k >= H ? 0.0f : f32 ? ((const float*)row)[k] : bf16_bits_to_f32(((const uint16_t*)row)[k]);
         }
     }
@@ -113,22 +122,30 @@ __device__ __forceinline__ f32x8 load8(const void* row, bool f32, int i, int ste
 }
 
 template <bool VEC>
-__device__ __forceinline__ void store8(void* row, bool f32, int i, int step, int H, f32x8 v) {
-    if constexpr (VEC) {
+__device__ __forceinline__ void store8(void* row, bool f32, int i, int H, f32x8 v) {
+    if (VEC || i + 8 <= H) {
         if (f32) {
             const f32x4 lo = __builtin_shufflevector(v, v, 0, 1, 2, 3), hi = __builtin_shufflevector(v, v, 4, 5, 6, 7);
-            __builtin_nontemporal_store(lo, (f32x4*)((float*)row + i));
-            __builtin_nontemporal_store(hi, (f32x4*)((float*)row + i + 4));
+            f32x4_any* p = (f32x4_any*)((float*)row + i);
+            if constexpr (VEC) {
+                __builtin_nontemporal_store(lo, (f32x4*)p);
+                __builtin_nontemporal_store(hi, (f32x4*)p + 1);
+            } else {
+                p[0] = lo;
+                p[1] = hi;
+            }
         } else {
             u32x4 o;
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
-            __builtin_nontemporal_store(o, (u32x4*)((uint16_t*)row + i));
+            u32x4_any* p = (u32x4_any*)((uint16_t*)row + i);
+            if constexpr (VEC) __builtin_nontemporal_store(o, (u32x4*)p);
+            else *p = o;
         }
     } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const int k = i + e * step;
+            const int k = i + e;
             if (k >= H) continue;
             if (f32) ((float*)row)[k] = v[e];
             else ((uint16_t*)row)[k] = f32_to_bf16_bits(v[e]);
@@ -151,19 +168,18 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void rms_norm_kernel
     const char* rr = (const char*)a.residual + t * a.ldr * (a.res_f32 ? 4 : 2);
     char* ro = (char*)a.residual_out + t * a.ldro * (a.res_f32 ? 4 : 2);
     const int H = a.H;
-    // Chunk c of this lane: VEC elements [(c * kLanes + tid) * 8, +8); else
-    // elements c * 8 * kLanes + tid + e * kLanes.
-    auto first = [&](int c) { return VEC ? (c * kLanes + tid) * 8 : c * 8 * kLanes + tid; };
+    // Chunk c of this lane: elements [first(c), +8).
+    auto first = [&](int c) { return (c * kLanes + tid) * 8; };
     f32x8 s[NC], sl[NC];  // sl: what an fp32 residual's sum was rounded off by
     double sum = 0.0;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
         const int i = first(c);
         if (i < H) {
-            s[c] = load8<VEC>(xr, false, i, kLanes, H);
+            s[c] = load8<VEC>(xr, false, i, H);
             sl[c] = f32x8{0, 0, 0, 0, 0, 0, 0, 0};
             if (a.residual) {
-                const f32x8 x = s[c], r = load8<VEC>(rr, a.res_f32, i, kLanes, H);
+                const f32x8 x = s[c], r = load8<VEC>(rr, a.res_f32, i, H);
                 s[c] = x + r;
                 if (a.res_f32) {
                     const f32x8 b = s[c] - x;
@@ -177,7 +193,7 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void rms_norm_kernel
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
         const int i = first(c);
-        if (a.residual_out && i < H) store8<VEC>(ro, a.res_f32, i, kLanes, H, s[c]);
+        if (a.residual_out && i < H) store8<VEC>(ro, a.res_f32, i, H, s[c]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum = fma((double)s[c][e], (double)s[c][e], sum);
     }
@@ -197,7 +213,7 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void rms_norm_kernel
     for (int c = 0; c < NC; ++c) {
         const int i = first(c);
         if (i >= H) continue;
-        f32x8 v = load8<VEC>(a.weight, a.weight_f32, i, kLanes, H);
+        f32x8 v = load8<VEC>(a.weight, a.weight_f32, i, H);
         Product p[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -205,51 +221,35 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void rms_norm_kernel
             else p[e] = {s[c][e] * rh * (a.offset + v[e]), 0.0f};  // bf16 needs no more
             v[e] = p[e].v;
         }
-        if (a.y) store8<VEC>(a.y + t * a.ldy, false, i, kLanes, H, v);
+        if (a.y) store8<VEC>(a.y + t * a.ldy, false, i, H, v);
         if (a.q) {
             uint8_t* qr = a.q + t * a.ldq;
             uint8_t* sr = a.qs + t * a.ldqs;
-            if constexpr (VEC) {
-                // A block of 32 is four lanes' chunks.
-                float m = 0.0f;
+            // A block of 32 is four lanes' chunks; H % 32 == 0, so a block is
+            // inside the row for all of its lanes or none.
+            float m = 0.0f;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) m = fmaxf(m, mx8_finite_abs(v[e]));
-                m = fmaxf(m, dpp<0xB1>(m));
-                m = fmaxf(m, dpp<0x4E>(m));
-                const uint32_t b = mx8_scale_byte(m);
-                const float inv = mx8_inv_scale(b);
-                u32x2 o;
-                bool ties = false;
+            for (int e = 0; e < 8; ++e) m = fmaxf(m, mx8_finite_abs(v[e]));
+            m = fmaxf(m, dpp<0xB1>(m));
+            m = fmaxf(m, dpp<0x4E>(m));
+            const uint32_t b = mx8_scale_byte(m);
+            const float inv = mx8_inv_scale(b);
+            u32x2 o;
+            bool ties = false;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    v[e] *= inv;
-                    ties |= tie(v[e]);
-                }
-                if (ties) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] = settle(v[e], p[e].rest);
-                }
-                o[0] = mx8_pack4(v[0], v[1], v[2], v[3], 1.0f);
-                o[1] = mx8_pack4(v[4], v[5], v[6], v[7], 1.0f);
-                __builtin_nontemporal_store(o, (u32x2*)(qr + i));
-                if ((tid & 3) == 0) sr[i >> 5] = (uint8_t)b;
-            } else {
-                // A block of 32 is 32 lanes' e-th elements; H % 32 == 0, so a
-                // block is inside the row for all of its lanes or none.
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int k = i + e * kLanes;
-                    float m = mx8_finite_abs(v[e]);
-#pragma unroll
-                    for (int d = 1; d < 32; d *= 2) m = fmaxf(m, __shfl_xor(m, d));
-                    const uint32_t b = mx8_scale_byte(m);
-                    if (k < H) {
-                        const float z = settle(v[e] * mx8_inv_scale(b), p[e].rest);
-                        qr[k] = (uint8_t)mx8_pack<false>(z, z, 1.0f, 0u);
-                        if ((tid & 31) == 0) sr[k >> 5] = (uint8_t)b;
-                    }
-                }
+            for (int e = 0; e < 8; ++e) {
+                v[e] *= inv;
+                ties |= tie(v[e]);
             }
+            if (ties) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = settle(v[e], p[e].rest);
+            }
+            o[0] = mx8_pack4(v[0], v[1], v[2], v[3], 1.0f);
+            o[1] = mx8_pack4(v[4], v[5], v[6], v[7], 1.0f);
+            if constexpr (VEC) __builtin_nontemporal_store(o, (u32x2*)(qr + i));
+            else *(u32x2_any*)(qr + i) = o;
+            if ((tid & 3) == 0) sr[i >> 5] = (uint8_t)b;
         }
     }
 }
