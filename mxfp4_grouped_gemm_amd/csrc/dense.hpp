@@ -12,6 +12,8 @@ namespace moe {
 // scale[a] * B[a] (A[a] x[t]) for a = index[t]; an index outside [0, n) adds
 // nothing. v [T, vld] (fp32) receives scale * A x from the narrow product and
 // is read by the projection's kernels.
+constexpr int kMaxLoraParts = 4;
+
 struct LoraArgs {
     const uint16_t* a;       // bf16 [n, rank, K]
     const uint16_t* b;       // bf16 [n, N, rank]

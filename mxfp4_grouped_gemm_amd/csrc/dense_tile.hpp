@@ -175,97 +175,176 @@ __device__ __forceinline__ int min16(int v) {
     return v;
 }
 
-// The low-rank term of a wave's accumulators: for each adapter that one of
-// the wave's rows uses, acc += B[a] v over its rank, with v (fp32) split into
-// two bf16 (hi + lo: 16 bits of it) and zero in the other adapters' rows.
-// n_of(f) gives the W row (of the stack's N rows) of fragment f's MFMA row
-// lane % 16, or -1; m_of(fm) the token of this lane's column counted from
-// `first`, or -1. All operands of 32 ranks are loaded before they are used.
-template <int FN, int FM, class NOF, class MOF>
-__device__ __forceinline__ void lora_accumulate(const LoraArgs& l, int64_t brows, int64_t first, f32x4 (&acc)[FN][FM],
-                                                NOF n_of, MOF m_of) {
+// The adapters of a lane's tokens (one a fragment of X) and their ranks, loaded
+// ahead of a tile's product.
+template <class C>
+struct LoraRows {
+    int idx[C::FM], rank[C::FM];
+};
+
+// row(r) is the token of the tile's row r counted from `first`, or -1.
+template <class C, class ROW>
+__device__ __forceinline__ void lora_rows(const LoraArgs& l, int64_t first, ROW row, LoraRows<C>& o) {
     const int lane = (int)threadIdx.x & 63;
-    const int g = lane >> 4;
-    const rsrc_t rv = make_rsrc(l.v + first * l.vld, kRecord);
-    int idx[FM];
+    const int r0 = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6) / C::WN * C::FM * 16 + (lane & 15);
+    const rsrc_t ri = make_rsrc(l.index + first, kRecord);
+    int t[C::FM];
+    uint32_t i[C::FM];
 #pragma unroll
-    for (int fm = 0; fm < FM; ++fm) {
-        const int m = m_of(fm);
-        const int i = m >= 0 ? l.index[first + m] : -1;
-        idx[fm] = (unsigned)i < (unsigned)l.n ? i : kNoAdapter;
+    for (int fm = 0; fm < C::FM; ++fm) {
+        t[fm] = row(r0 + fm * 16);
+        i[fm] = __builtin_amdgcn_raw_buffer_load_b32(ri, t[fm] >= 0 ? (uint32_t)t[fm] * 4u : kOob, 0, 0);
+        o.rank[fm] = l.rank;
     }
-    for (int last = -1;;) {
-        // The smallest adapter above `last` among the wave's rows.
-        int next = kNoAdapter;
 #pragma unroll
-        for (int fm = 0; fm < FM; ++fm) next = idx[fm] > last && idx[fm] < next ? idx[fm] : next;
+    for (int fm = 0; fm < C::FM; ++fm) o.idx[fm] = t[fm] >= 0 && i[fm] < (uint32_t)l.n ? (int)i[fm] : kNoAdapter;
+    if (!l.ranks) return;
+    const rsrc_t rr = make_rsrc(l.ranks, kRecord);
+#pragma unroll
+    for (int fm = 0; fm < C::FM; ++fm) {
+        const int r = __builtin_amdgcn_raw_buffer_load_b32(rr, o.idx[fm] != kNoAdapter ? (uint32_t)o.idx[fm] * 4u : kOob, 0, 0);
+        o.rank[fm] = r < l.rank ? r : l.rank;
+    }
+}
+
+// The low-rank term of a tile's accumulators: for each adapter that one of a
+// wave's rows uses, acc += B[a] v over its rank, with v (fp32) split into two
+// bf16 (hi + lo: 16 bits of it). The tile's rows of v, 64 ranks at a time, are
+// summed over the parts and split once for all waves, into the first two LDS
+// buffers (32 ranks each: 128-byte rows, hi in pieces 0..3, lo in 4..7,
+// permuted as rows of X are). An adapter's part is a memory latency and a few
+// matrix instructions, so the rows of B of the next three halves (of 32 ranks) are
+// on their way while those of one are multiplied. n_of(f) gives the W row (of
+// the stack's `brows` rows) of fragment f's MFMA row lane % 16, or -1.
+template <class C, class ROW, class NOF>
+__device__ __forceinline__ void lora_accumulate(const LoraArgs& l, int64_t brows, int64_t first, const LoraRows<C>& rows,
+                                                f32x4 (&acc)[C::FN][C::FM], ROW row, NOF n_of, uint8_t* s0, uint8_t* s1) {
+    const int tid = (int)threadIdx.x, lane = tid & 63;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int g = lane >> 4, l16 = lane & 15, r0 = w / C::WN * C::FM * 16;
+    struct Step {
+        int ad, h, rank;  // an adapter, the half of the 64 ranks, the adapter's rank
+    };
+    // The smallest adapter above `last` among the wave's rows.
+    auto above = [&](int last) -> Step {
+        int next = kNoAdapter, rank = 0;
+#pragma unroll
+        for (int fm = 0; fm < C::FM; ++fm) next = rows.idx[fm] > last && rows.idx[fm] < next ? rows.idx[fm] : next;
         next = __builtin_amdgcn_readfirstlane(min16(next));
-        if (next == kNoAdapter) break;
-        last = next;
-        const rsrc_t rb = make_rsrc(l.b + (int64_t)next * brows * l.rank, kRecord);
-        int rank = l.ranks ? l.ranks[next] : l.rank;
-        rank = rank < l.rank ? rank : l.rank;
-        for (int k0 = 0;;) {
-            const int k = k0 + 8 * g;
-            u32x4 bu[FN];
 #pragma unroll
-            for (int f = 0; f < FN; ++f) {
+        for (int fm = 0; fm < C::FM; ++fm) rank = rows.idx[fm] == next ? -rows.rank[fm] : rank;
+        return {next, 0, -__builtin_amdgcn_readfirstlane(min16(rank))};
+    };
+    static_assert(C::BUF >= C::BM * 128 && C::NB >= 2, "a buffer holds 32 ranks of the tile's rows");
+    constexpr int kAll = C::BM * 8 / C::THREADS;  // eights of ranks a thread stages
+    constexpr int P = 2;                          // at a time, as the registers allow
+    for (int k0 = 0; k0 < l.rank; k0 += 64) {
+        auto load_b = [&](u32x4 (&d)[C::FN], const Step& p) {
+            const bool some = p.ad != kNoAdapter;
+            const rsrc_t rb = make_rsrc(l.b + (int64_t)(some ? p.ad : 0) * brows * l.rank, kRecord);
+            const int k = k0 + 32 * p.h + 8 * g;
+#pragma unroll
+            for (int f = 0; f < C::FN; ++f) {
                 const int n = n_of(f);
-                bu[f] = bld16(rb, n >= 0 && k < l.rank ? (uint32_t)(n * l.rank + k) * 2u : kOob);
+                const uint32_t at = (uint32_t)(n * l.rank + k) * 2u;
+                d[f] = bld16(rb, some & (n >= 0) & (k < l.rank) ? at : kOob);
             }
-            // Columns beyond the adapter's rank are not read as numbers (nor
-            // are whole eights of v, which the narrow product leaves unwritten).
+        };
+        // The second half of an adapter whose rank reaches into it, else the
+        // next adapter.
+        auto after = [&](const Step& p) -> Step {
+            return p.h == 0 && k0 + 32 < p.rank ? Step{p.ad, 1, p.rank} : above(p.ad);
+        };
+        u32x4 bu[4][C::FN];
+        Step st[4];
+        st[0] = above(-1);
+        load_b(bu[0], st[0]);
+        // The last loads into the buffers and the reads of them are done.
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 #pragma unroll
-            for (int f = 0; f < FN; ++f)
+        for (int i0 = 0; i0 < kAll; i0 += P) {
+            f32x4 v[P][2], part[kMaxLoraParts - 1][P][2];
+            auto load_v = [&](f32x4 (&d)[P][2], int p) {
+                const rsrc_t rv = make_rsrc(l.v + p * l.part_stride + first * l.vld, kRecord);
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    const int q = tid + (i0 + i) * C::THREADS, k = k0 + q % 8 * 8, t = row(q / 8);
+                    const uint32_t at = (uint32_t)(t * l.vld + k) * 4u;
+                    const uint32_t o = (t >= 0) & (k < l.rank) & (p < l.parts) ? at : kOob;
+                    d[i][0] = __builtin_bit_cast(f32x4, bld16(rv, o));
+                    d[i][1] = __builtin_bit_cast(f32x4, bld16(rv, o == kOob ? o : o + 16));
+                }
+            };
+            load_v(v, 0);
+            if (l.parts > 1) {
+#pragma unroll
+                for (int p = 1; p < kMaxLoraParts; ++p) load_v(part[p - 1], p);
+#pragma unroll
+                for (int p = 1; p < kMaxLoraParts; ++p)
+#pragma unroll
+                    for (int i = 0; i < P; ++i)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) v[i][h] += part[p - 1][i][h];
+            }
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                const int q = tid + (i0 + i) * C::THREADS, r = q / 8, c = q % 4;
+                u32x4 hi, lo;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    if (k + 2 * e >= rank) bu[f][e] = 0;
-                    else if (k + 2 * e + 1 >= rank) bu[f][e] &= 0xffffu;
+                    const float x0 = v[i][e / 2][2 * (e & 1)], x1 = v[i][e / 2][2 * (e & 1) + 1];
+                    hi[e] = pack_bf16x2(x0, x1);
+                    lo[e] = pack_bf16x2(x0 - __uint_as_float(hi[e] << 16), x1 - __uint_as_float(hi[e] & 0xffff0000u));
                 }
-            // The rows in two batches, as their operands' registers allow.
-            constexpr int FB = FM > 4 ? 4 : FM;
+                uint8_t* dst = (q % 8 < 4 ? s0 : s1) + r * 128;
+                *(u32x4*)(dst + ((c ^ key_x<128>(r)) << 4)) = hi;
+                *(u32x4*)(dst + (((4 + c) ^ key_x<128>(r)) << 4)) = lo;
+            }
+        }
+        __syncthreads();
+        auto multiply = [&](u32x4 (&d)[C::FN], const Step& p) {
+            // Columns beyond the adapter's rank are not read as numbers.
+            const int left = p.rank - (k0 + 32 * p.h + 8 * g);
+            u32x4 keep;
 #pragma unroll
-            for (int fb = 0; fb < FM; fb += FB) {
-                f32x4 vu[FB][2];
+            for (int e = 0; e < 4; ++e) {
+                const int bits = (left - 2 * e) * 16;
+                keep[e] = (uint32_t)((1ull << (bits < 0 ? 0 : bits > 32 ? 32 : bits)) - 1);
+            }
 #pragma unroll
-                for (int b = 0; b < FB; ++b)
+            for (int f = 0; f < C::FN; ++f) d[f] &= keep;
+            const uint8_t* buf = p.h ? s1 : s0;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        vu[b][h] = __builtin_bit_cast(f32x4, bld16(rv, idx[fb + b] == next && k < rank ? (uint32_t)(m_of(fb + b) * l.vld + k) * 4u + 16u * h : kOob));
-                for (int p = 1; p < l.parts; ++p) {
-                    const rsrc_t rp = make_rsrc(l.v + p * l.part_stride + first * l.vld, kRecord);
+            for (int fm = 0; fm < C::FM; ++fm) {
+                // A lane's results are one token's: only those of this adapter
+                // are kept (a NaN in its factors stays with its own tokens).
+                const bool mine = rows.idx[fm] == p.ad;
+                if (!__any(mine)) continue;
+                const int r = r0 + fm * 16 + l16;
+                const u32x4 hi = *(const u32x4*)(buf + r * 128 + ((g ^ key_x<128>(r)) << 4));
+                const u32x4 lo = *(const u32x4*)(buf + r * 128 + (((4 + g) ^ key_x<128>(r)) << 4));
 #pragma unroll
-                    for (int b = 0; b < FB; ++b)
+                for (int f = 0; f < C::FN; ++f) {
+                    f32x4 o = mfma16x16x32(__builtin_bit_cast(bf16x8, d[f]), __builtin_bit_cast(bf16x8, hi), acc[f][fm]);
+                    o = mfma16x16x32(__builtin_bit_cast(bf16x8, d[f]), __builtin_bit_cast(bf16x8, lo), o);
 #pragma unroll
-                        for (int h = 0; h < 2; ++h)
-                            vu[b][h] += __builtin_bit_cast(f32x4, bld16(rp, idx[fb + b] == next && k < rank ? (uint32_t)(m_of(fb + b) * l.vld + k) * 4u + 16u * h : kOob));
-                }
-#pragma unroll
-                for (int b = 0; b < FB; ++b) {
-                    const int fm = fb + b;
-                    if (!__any(idx[fm] == next)) continue;
-                    u32x4 hi, lo;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float v0 = vu[b][e / 2][2 * (e & 1)];
-                        const float v1 = vu[b][e / 2][2 * (e & 1) + 1];
-                        hi[e] = pack_bf16x2(v0, v1);
-                        lo[e] = pack_bf16x2(v0 - __uint_as_float(hi[e] << 16), v1 - __uint_as_float(hi[e] & 0xffff0000u));
-                    }
-                    // A lane's results are one token's: only those of this adapter
-                    // are kept (a NaN in its factors stays with its own tokens).
-                    const bool mine = idx[fm] == next;
-#pragma unroll
-                    for (int f = 0; f < FN; ++f) {
-                        f32x4 d = mfma16x16x32(__builtin_bit_cast(bf16x8, bu[f]), __builtin_bit_cast(bf16x8, hi), acc[f][fm]);
-                        d = mfma16x16x32(__builtin_bit_cast(bf16x8, bu[f]), __builtin_bit_cast(bf16x8, lo), d);
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) acc[f][fm][r] = mine ? d[r] : acc[f][fm][r];
-                    }
+                    for (int e = 0; e < 4; ++e) acc[f][fm][e] = mine ? o[e] : acc[f][fm][e];
                 }
             }
-            k0 += 32;
-            if (k0 >= rank) break;
+        };
+        each<1, 4>([&](auto i) {
+            st[i.value] = after(st[i.value - 1]);
+            load_b(bu[i.value], st[i.value]);
+        });
+        auto use = [&](auto i) {
+            if (st[i.value].ad == kNoAdapter) return false;
+            multiply(bu[i.value], st[i.value]);
+            st[i.value] = after(st[(i.value + 3) % 4]);
+            load_b(bu[i.value], st[i.value]);
+            return true;
+        };
+        while (use(std::integral_constant<int, 0>()) && use(std::integral_constant<int, 1>()) &&
+               use(std::integral_constant<int, 2>()) && use(std::integral_constant<int, 3>())) {
         }
     }
 }
@@ -311,6 +390,10 @@ __device__ __forceinline__ void dense_tile(const DenseArgs& a, int id, int part,
         kt0 = (int)((int64_t)steps * z / a.splits);
         kt1 = (int)((int64_t)steps * (z + 1) / a.splits);
     }
+
+    auto row = [&](int r) { return m0 + r < a.M ? r : -1; };
+    LoraRows<C> lrows;
+    if constexpr (C::LORA) lora_rows<C>(a.lora, m0, row, lrows);
 
     // Loads: offsets of this lane's pieces from the tile's first element.
     const char* xb = (const char*)a.x + (C::XT ? (int64_t)m0 : (int64_t)m0 * a.ldx) * C::ESZ;
@@ -594,15 +677,12 @@ __device__ __forceinline__ void dense_tile(const DenseArgs& a, int id, int part,
     auto n_of = [&](int f) { return n0 + wn * 16 * C::F + g * 4 * C::F + (f % C::F) * 4; };
     if constexpr (C::LORA) {
         static_assert(!C::SPLIT, "the kernel that joins the parts adds the term");
-        if (a.lora.n > 0) {
-            // As MFMA rows: row i = l16 of fragment f.
-            auto nrow = [&](int f) {
-                const int n = n0 + wn * 16 * C::F + (l16 >> 2) * 4 * C::F + (f % C::F) * 4 + (l16 & 3);
-                return n < a.N ? n + (C::GATED && f >= C::F ? a.N : 0) : -1;
-            };
-            auto mrow = [&](int fm) { return m_of(fm) < a.M ? m_of(fm) - m0 : -1; };
-            lora_accumulate<C::FN, C::FM>(a.lora, C::GATED ? 2 * (int64_t)a.N : a.N, m0, acc, nrow, mrow);
-        }
+        // As MFMA rows: row i = l16 of fragment f.
+        auto nrow = [&](int f) {
+            const int n = n0 + wn * 16 * C::F + (l16 >> 2) * 4 * C::F + (f % C::F) * 4 + (l16 & 3);
+            return n < a.N ? n + (C::GATED && f >= C::F ? a.N : 0) : -1;
+        };
+        lora_accumulate<C>(a.lora, C::GATED ? 2 * (int64_t)a.N : a.N, m0, lrows, acc, row, nrow, s[0], s[1]);
     }
 
     if constexpr (C::SPLIT) {

@@ -153,7 +153,7 @@ __global__ __launch_bounds__(kWaves * 64) void lora_shrink_kernel(const uint16_t
 int lora_parts(int T) {
     if (T <= kTokenWise) return 1;
     const int groups = (T + 31) / 32;
-    return groups > 128 ? 1 : groups > 64 ? 2 : 4;
+    return groups > 128 ? 1 : groups > 64 ? 2 : kMaxLoraParts;
 }
 
 hipError_t launch_lora_shrink(const uint16_t* x, int64_t ldx, int T, int K, const LoraArgs& l, hipStream_t s) {
