@@ -91,12 +91,24 @@ moe_status check_lora(const char* fn, const char* name, const moe_lora* l, int T
 
 int vld_of(int rank) { return (int)align_up(rank, 32); }
 
-int64_t v_bytes(int T, int rank) { return align_up((int64_t)moe::lora_parts(T) * T * vld_of(rank) * 4, 256); }
+// What adapters keep in the workspace: the tokens' order with its adapters (for
+// any number of adapters), and v.
+int64_t order_bytes(int T) { return moe::lora_sorts(T, 3) ? 2 * align_up((int64_t)T * 4, 256) : 0; }
+int64_t lora_bytes(int T, int rank) {
+    return rank > 0 ? order_bytes(T) + align_up((int64_t)moe::lora_parts(T) * T * vld_of(rank) * 4, 256) : 0;
+}
 
-moe::LoraArgs lora_args(const moe_lora* l, void* v, int T) {
+// joined: the product's parts are joined token by token, else its tiles read v.
+moe::LoraArgs lora_args(const moe_lora* l, void* ws, int T, int64_t ldx, bool joined) {
     moe::LoraArgs r;
     memset(&r, 0, sizeof r);
     if (!l) return r;
+    // Rows in an order are loaded by 32-bit offsets from the first.
+    if (moe::lora_sorts(T, l->n) && T * ldx * 2 < (int64_t)1 << 30) {
+        r.order = (int32_t*)ws;
+        r.sorted = (int32_t*)((char*)ws + order_bytes(T) / 2);
+        r.v_sorted = !joined;
+    }
     r.a = l->a;
     r.b = l->b;
     r.index = l->index;
@@ -105,7 +117,7 @@ moe::LoraArgs lora_args(const moe_lora* l, void* v, int T) {
     r.n = l->n;
     r.rank = l->rank;
     r.vld = vld_of(l->rank);
-    r.v = (float*)v;
+    r.v = (float*)((char*)ws + order_bytes(T));
     r.parts = moe::lora_parts(T);
     r.part_stride = (int64_t)T * r.vld;
     return r;
@@ -145,6 +157,15 @@ int64_t partial_bytes(int T, int N, int K, int elt, int epi, bool few, int rank)
     return align_up(moe::dense_partial_bytes(a, splits_of(a, elt, epi, few), epi, few && rank > 0), 256);
 }
 
+// The narrow product; sorted: the order is there already (of the same index).
+hipError_t run_shrink(const uint16_t* x, int64_t ldx, int T, int K, const moe::LoraArgs& l, bool sorted, hipStream_t s) {
+    if (l.order && !sorted) {
+        const hipError_t e = moe::launch_lora_sort(l.index, T, l.n, (int32_t*)l.order, (int32_t*)l.sorted, s);
+        if (e != hipSuccess) return e;
+    }
+    return moe::launch_lora_shrink(x, ldx, T, K, l, s);
+}
+
 // A forward product. h_f32: see launch_skinny.
 hipError_t run_product(moe::DenseArgs& a, int elt, int epi, bool few, float* partial, const float* h_f32, hipStream_t s) {
     a.splits = splits_of(a, elt, epi, few);
@@ -163,7 +184,7 @@ FfnLayout ffn_layout(int T, int H, int I, int rank13, int rank2) {
     L.h = 0;
     L.hs = 0;
     L.v = align_up((int64_t)T * I * 2, 256);
-    L.partial = L.v + v_bytes(T, rank13 > rank2 ? rank13 : rank2);
+    L.partial = L.v + lora_bytes(T, rank13 > rank2 ? rank13 : rank2);
     L.total = L.partial + (p1 > p2 ? p1 : p2);
     return L;
 }
@@ -276,7 +297,7 @@ moe_status moe_rms_norm(const uint16_t* x, int64_t x_stride, const void* residua
 
 int64_t moe_lora_linear_workspace_size(int T, int K, int N, int rank) {
     if (!valid_sizes(T, K, N, 8) || !valid_rank(rank)) return -1;
-    return v_bytes(T, rank) + partial_bytes(T, N, K, 0, moe::kEpiOut, skinny(T, N, K, 0), rank);
+    return lora_bytes(T, rank) + partial_bytes(T, N, K, 0, moe::kEpiOut, skinny(T, N, K, 0), rank);
 }
 
 moe_status moe_lora_linear(const uint16_t* x, int64_t x_stride, const uint16_t* w, const moe_lora* lora, int T, int K,
@@ -298,10 +319,11 @@ moe_status moe_lora_linear(const uint16_t* x, int64_t x_stride, const uint16_t* 
     hipStream_t s = (hipStream_t)stream;
     moe::DenseArgs a = product(x, x_stride, w, K, T, N, K, out, out_stride);
     a.out_f32 = out_type == MOE_DT_F32;
-    a.lora = lora_args(lora, workspace, T);
-    float* partial = (float*)((char*)workspace + v_bytes(T, lora ? lora->rank : 0));
-    if (lora && !skinny(T, N, K, 0)) LAUNCH(moe::launch_lora_shrink(x, x_stride, T, K, a.lora, s), "moe_lora_linear (shrink)");
-    return hip_status(run_product(a, 0, moe::kEpiOut, skinny(T, N, K, 0), partial, nullptr, s), fn);
+    const bool few = skinny(T, N, K, 0);
+    a.lora = lora_args(lora, workspace, T, x_stride, splits_of(a, 0, moe::kEpiOut, few) > 1);
+    float* partial = (float*)((char*)workspace + lora_bytes(T, lora ? lora->rank : 0));
+    if (lora && !few) LAUNCH(run_shrink(x, x_stride, T, K, a.lora, false, s), "moe_lora_linear (shrink)");
+    return hip_status(run_product(a, 0, moe::kEpiOut, few, partial, nullptr, s), fn);
 }
 
 int64_t moe_ffn_workspace_size(int T, int H, int I, int rank13, int rank2) {
@@ -335,17 +357,17 @@ moe_status moe_ffn_forward(const uint16_t* x, int64_t x_stride, const uint16_t* 
     uint16_t* h = (uint16_t*)(ws + L.h);
     moe::DenseArgs a = product(x, x_stride, w13, H, T, I, H, h, I);
     a.gate_up = gate_up;
-    a.lora = lora_args(lora13, ws + L.v, T);
-    if (lora13 && !skinny(T, 2 * (int64_t)I, H, 0))
-        LAUNCH(moe::launch_lora_shrink(x, x_stride, T, H, a.lora, s), "moe_ffn_forward (gate_up shrink)");
-    LAUNCH(run_product(a, 0, moe::kEpiGated, skinny(T, 2 * (int64_t)I, H, 0), (float*)(ws + L.partial), nullptr, s), "moe_ffn_forward (gate_up)");
+    const bool few13 = skinny(T, 2 * (int64_t)I, H, 0), few2 = skinny(T, H, I, 0);
+    a.lora = lora_args(lora13, ws + L.v, T, x_stride, splits_of(a, 0, moe::kEpiGated, few13) > 1);
+    if (lora13 && !few13) LAUNCH(run_shrink(x, x_stride, T, H, a.lora, false, s), "moe_ffn_forward (gate_up shrink)");
+    const bool sorted = lora2 && !few13 && a.lora.order && lora2->index == lora13->index && lora2->n == lora13->n;
+    LAUNCH(run_product(a, 0, moe::kEpiGated, few13, (float*)(ws + L.partial), nullptr, s), "moe_ffn_forward (gate_up)");
     a = product(h, I, w2, I, T, H, I, out, out_stride);
     a.addend = addend;
     a.ldadd = addend_stride;
-    a.lora = lora_args(lora2, ws + L.v, T);
-    if (lora2 && !skinny(T, H, I, 0))
-        LAUNCH(moe::launch_lora_shrink(h, I, T, I, a.lora, s), "moe_ffn_forward (down shrink)");
-    return hip_status(run_product(a, 0, moe::kEpiOut, skinny(T, H, I, 0), (float*)(ws + L.partial), nullptr, s), "moe_ffn_forward (down)");
+    a.lora = lora_args(lora2, ws + L.v, T, I, splits_of(a, 0, moe::kEpiOut, few2) > 1);
+    if (lora2 && !few2) LAUNCH(run_shrink(h, I, T, I, a.lora, sorted, s), "moe_ffn_forward (down shrink)");
+    return hip_status(run_product(a, 0, moe::kEpiOut, few2, (float*)(ws + L.partial), nullptr, s), "moe_ffn_forward (down)");
 }
 
 int64_t moe_ffn_mxfp8_workspace_size(int T, int H, int I) {

@@ -18,11 +18,14 @@ struct LoraArgs {
     const uint16_t* a;       // bf16 [n, rank, K]
     const uint16_t* b;       // bf16 [n, N, rank]
     const int32_t* index;    // [T]
+    const int32_t* order;    // [T] tokens by adapter, or null: the tokens' own order
+    const int32_t* sorted;   // [T] their adapters (-1: none), with `order`
     const int32_t* ranks;    // [n] or null (all `rank`)
     const float* scale;      // [n] or null (all 1)
     float* v;                // fp32 [parts, T, vld], vld = rank rounded up to 32
     int64_t part_stride;     // T * vld
     int n, rank, vld, parts; // v is the sum of the parts (of K)
+    bool v_sorted;           // row p of v is token order[p]'s, else token p's
 };
 
 // Epilogues of the dense products.
@@ -89,6 +92,10 @@ bool skinny_wide(const DenseArgs& a, bool gated);
 int skinny_narrow(const DenseArgs& a);  // workgroups of the adapters' narrow product
 hipError_t launch_skinny(const DenseArgs& a, int elt, int epi, const float* h_f32, hipStream_t s);
 
+// Whether the tokens are taken adapter by adapter (l.order, l.sorted), and the
+// sort for it.
+bool lora_sorts(int T, int n);
+hipError_t launch_lora_sort(const int32_t* index, int T, int n, int32_t* order, int32_t* sorted, hipStream_t s);
 // Parts of K that launch_lora_shrink takes (l.parts).
 int lora_parts(int T);
 // v[t] = scale * A[index[t]] x[t].

@@ -179,25 +179,35 @@ __device__ __forceinline__ int min16(int v) {
 // ahead of a tile's product.
 template <class C>
 struct LoraRows {
-    int idx[C::FM], rank[C::FM];
+    int idx[C::FM], rank[C::FM], token[C::FM];  // token: M for rows past the end
 };
 
-// row(r) is the token of the tile's row r counted from `first`, or -1.
-template <class C, class ROW>
-__device__ __forceinline__ void lora_rows(const LoraArgs& l, int64_t first, ROW row, LoraRows<C>& o) {
+// The tile's rows are rows m0.. of l.order or, without it, tokens m0...
+template <class C>
+__device__ __forceinline__ void lora_rows(const LoraArgs& l, int m0, int M, LoraRows<C>& o) {
     const int lane = (int)threadIdx.x & 63;
     const int r0 = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6) / C::WN * C::FM * 16 + (lane & 15);
-    const rsrc_t ri = make_rsrc(l.index + first, kRecord);
-    int t[C::FM];
+    const rsrc_t ri = make_rsrc((l.order ? l.sorted : l.index) + m0, kRecord);
     uint32_t i[C::FM];
 #pragma unroll
     for (int fm = 0; fm < C::FM; ++fm) {
-        t[fm] = row(r0 + fm * 16);
-        i[fm] = __builtin_amdgcn_raw_buffer_load_b32(ri, t[fm] >= 0 ? (uint32_t)t[fm] * 4u : kOob, 0, 0);
+        const int r = r0 + fm * 16;
+        i[fm] = __builtin_amdgcn_raw_buffer_load_b32(ri, m0 + r < M ? (uint32_t)r * 4u : kOob, 0, 0);
+        o.token[fm] = m0 + r < M ? m0 + r : M;
         o.rank[fm] = l.rank;
     }
+    if (l.order) {
+        const rsrc_t ro = make_rsrc(l.order + m0, kRecord);
 #pragma unroll
-    for (int fm = 0; fm < C::FM; ++fm) o.idx[fm] = t[fm] >= 0 && i[fm] < (uint32_t)l.n ? (int)i[fm] : kNoAdapter;
+        for (int fm = 0; fm < C::FM; ++fm) {
+            const int r = r0 + fm * 16;
+            const int t = __builtin_amdgcn_raw_buffer_load_b32(ro, m0 + r < M ? (uint32_t)r * 4u : kOob, 0, 0);
+            o.token[fm] = m0 + r < M ? t : M;
+        }
+    }
+#pragma unroll
+    for (int fm = 0; fm < C::FM; ++fm)
+        o.idx[fm] = m0 + r0 + fm * 16 < M && i[fm] < (uint32_t)l.n ? (int)i[fm] : kNoAdapter;
     if (!l.ranks) return;
     const rsrc_t rr = make_rsrc(l.ranks, kRecord);
 #pragma unroll
@@ -216,9 +226,9 @@ __device__ __forceinline__ void lora_rows(const LoraArgs& l, int64_t first, ROW 
 // matrix instructions, so the rows of B of the next three halves (of 32 ranks) are
 // on their way while those of one are multiplied. n_of(f) gives the W row (of
 // the stack's `brows` rows) of fragment f's MFMA row lane % 16, or -1.
-template <class C, class ROW, class NOF>
-__device__ __forceinline__ void lora_accumulate(const LoraArgs& l, int64_t brows, int64_t first, const LoraRows<C>& rows,
-                                                f32x4 (&acc)[C::FN][C::FM], ROW row, NOF n_of, uint8_t* s0, uint8_t* s1) {
+template <class C, class NOF>
+__device__ __forceinline__ void lora_accumulate(const LoraArgs& l, int64_t brows, int m0, int M, const LoraRows<C>& rows,
+                                                f32x4 (&acc)[C::FN][C::FM], NOF n_of, uint8_t* s0, uint8_t* s1) {
     const int tid = (int)threadIdx.x, lane = tid & 63;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 4, l16 = lane & 15, r0 = w / C::WN * C::FM * 16;
@@ -237,7 +247,7 @@ __device__ __forceinline__ void lora_accumulate(const LoraArgs& l, int64_t brows
     };
     static_assert(C::BUF >= C::BM * 128 && C::NB >= 2, "a buffer holds 32 ranks of the tile's rows");
     constexpr int kAll = C::BM * 8 / C::THREADS;  // eights of ranks a thread stages
-    constexpr int P = 2;                          // at a time, as the registers allow
+    constexpr int P = C::FM > 4 ? 1 : 2;          // at a time, as the registers allow
     for (int k0 = 0; k0 < l.rank; k0 += 64) {
         auto load_b = [&](u32x4 (&d)[C::FN], const Step& p) {
             const bool some = p.ad != kNoAdapter;
@@ -265,12 +275,12 @@ __device__ __forceinline__ void lora_accumulate(const LoraArgs& l, int64_t brows
         for (int i0 = 0; i0 < kAll; i0 += P) {
             f32x4 v[P][2], part[kMaxLoraParts - 1][P][2];
             auto load_v = [&](f32x4 (&d)[P][2], int p) {
-                const rsrc_t rv = make_rsrc(l.v + p * l.part_stride + first * l.vld, kRecord);
+                const rsrc_t rv = make_rsrc(l.v + p * l.part_stride + (int64_t)m0 * l.vld, kRecord);
 #pragma unroll
                 for (int i = 0; i < P; ++i) {
-                    const int q = tid + (i0 + i) * C::THREADS, k = k0 + q % 8 * 8, t = row(q / 8);
+                    const int q = tid + (i0 + i) * C::THREADS, k = k0 + q % 8 * 8, t = q / 8;
                     const uint32_t at = (uint32_t)(t * l.vld + k) * 4u;
-                    const uint32_t o = (t >= 0) & (k < l.rank) & (p < l.parts) ? at : kOob;
+                    const uint32_t o = (m0 + t < M) & (k < l.rank) & (p < l.parts) ? at : kOob;
                     d[i][0] = __builtin_bit_cast(f32x4, bld16(rv, o));
                     d[i][1] = __builtin_bit_cast(f32x4, bld16(rv, o == kOob ? o : o + 16));
                 }
@@ -391,12 +401,14 @@ __device__ __forceinline__ void dense_tile(const DenseArgs& a, int id, int part,
         kt1 = (int)((int64_t)steps * (z + 1) / a.splits);
     }
 
-    auto row = [&](int r) { return m0 + r < a.M ? r : -1; };
+    // With an order of the tokens the tile's rows are gathered: their offsets
+    // are from the first token.
+    const bool gather = C::LORA && a.lora.order != nullptr;
     LoraRows<C> lrows;
-    if constexpr (C::LORA) lora_rows<C>(a.lora, m0, row, lrows);
+    if constexpr (C::LORA) lora_rows<C>(a.lora, m0, a.M, lrows);
 
     // Loads: offsets of this lane's pieces from the tile's first element.
-    const char* xb = (const char*)a.x + (C::XT ? (int64_t)m0 : (int64_t)m0 * a.ldx) * C::ESZ;
+    const char* xb = (const char*)a.x + (C::XT ? (int64_t)m0 : gather ? 0 : (int64_t)m0 * a.ldx) * C::ESZ;
     const char* wb = (const char*)a.w + (C::WT ? (int64_t)n0 : (int64_t)n0 * a.ldw) * C::ESZ;
     uint32_t xo[C::XL], wo[C::WL];
     constexpr int kPieces = C::KB / 16;  // of a K-major row
@@ -420,7 +432,8 @@ __device__ __forceinline__ void dense_tile(const DenseArgs& a, int id, int part,
             xo[i] = m0 + c * 8 < a.M ? (uint32_t)(k * a.ldx * 2 + c * 16) : kOob;
         } else {
             const int r = p / kPieces, c = (p % kPieces) ^ key_x<C::KB>(r);
-            xo[i] = m0 + r < a.M ? (uint32_t)(r * a.ldx * C::ESZ + c * 16) : kOob;
+            const int t = gather ? a.lora.order[m0 + r < a.M ? m0 + r : 0] : r;
+            xo[i] = m0 + r < a.M ? (uint32_t)(t * a.ldx * C::ESZ + c * 16) : kOob;
         }
     }
 #pragma unroll
@@ -673,7 +686,10 @@ __device__ __forceinline__ void dense_tile(const DenseArgs& a, int id, int part,
     }
 
     // Column of fragment f's lane results (the first of four), and the token.
-    auto m_of = [&](int fm) { return m0 + xr0 + fm * 16 + l16; };
+    auto m_of = [&](int fm) {
+        if constexpr (C::LORA) return lrows.token[fm];
+        else return m0 + xr0 + fm * 16 + l16;
+    };
     auto n_of = [&](int f) { return n0 + wn * 16 * C::F + g * 4 * C::F + (f % C::F) * 4; };
     if constexpr (C::LORA) {
         static_assert(!C::SPLIT, "the kernel that joins the parts adds the term");
@@ -682,7 +698,7 @@ __device__ __forceinline__ void dense_tile(const DenseArgs& a, int id, int part,
             const int n = n0 + wn * 16 * C::F + (l16 >> 2) * 4 * C::F + (f % C::F) * 4 + (l16 & 3);
             return n < a.N ? n + (C::GATED && f >= C::F ? a.N : 0) : -1;
         };
-        lora_accumulate<C>(a.lora, C::GATED ? 2 * (int64_t)a.N : a.N, m0, lrows, acc, row, nrow, s[0], s[1]);
+        lora_accumulate<C>(a.lora, C::GATED ? 2 * (int64_t)a.N : a.N, m0, a.M, lrows, acc, nrow, s[0], s[1]);
     }
 
     if constexpr (C::SPLIT) {

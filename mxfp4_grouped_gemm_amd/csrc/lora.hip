@@ -5,10 +5,12 @@
 // Few tokens (decode): a workgroup a token and 16 rows of its adapter's A, so
 // nothing has to be sorted or searched; rows that tokens share come from L2.
 //
-// Many tokens (prompts): a workgroup takes 32 tokens in their own order and
-// four 16-row pieces of the A of the distinct adapters among them, in the
-// order of the adapters, so A is read once per 32 tokens. Tokens of other adapters run through the products too and
-// are not stored.
+// Many tokens: a workgroup takes 32 tokens and four 16-row pieces of the A of
+// the distinct adapters among them, in the order of the adapters, so A is read
+// once per 32 tokens. Tokens of other adapters run through the products too and
+// are not stored. With three adapters or more the tokens are taken adapter by
+// adapter, here and in the projection's tiles, after a sort: tokens that come
+// mixed (a decode batch) would have each adapter among every 32.
 //
 // With few groups of tokens K is split over workgroups too, and what reads v
 // adds the parts. In both forms eight waves split K, hold a batch of 128-byte K chunks in flight
@@ -25,11 +27,78 @@ constexpr int kWaves = kShrinkWaves;
 constexpr int FR = 4;  // 16-row rank fragments a pass
 // Up to this many tokens a workgroup takes one token.
 constexpr int kTokenWise = 128;
+constexpr int kSortKeys = 1024;  // adapters of a sort, and none
 
 __global__ __launch_bounds__(kWaves * 64) void lora_shrink_token_kernel(const uint16_t* __restrict__ x, int64_t ldx,
                                                                         int K, LoraArgs l) {
     __shared__ f32x4 red[kWaves][4];
     shrink_token(x, ldx, K, l, (int)blockIdx.x, (int)blockIdx.y * 16, red);
+}
+
+// Counting sort of the tokens by adapter, those without one last, in one
+// workgroup: each wave counts its own run of tokens, a thread a key sums the
+// waves' counts, and the tokens take their places. Their order inside an adapter
+// changes no result: a token's column of a product does not see the others.
+constexpr int kSortWaves = 16, kSortKeep = 8;
+__global__ __launch_bounds__(kSortWaves * 64) void lora_sort_kernel(const int32_t* __restrict__ index, int T, int n,
+                                                                     int32_t* __restrict__ order,
+                                                                     int32_t* __restrict__ sorted) {
+    __shared__ int at[kSortWaves][kSortKeys];
+    __shared__ int total[kSortWaves];
+    static_assert(kSortKeys == kSortWaves * 64, "a thread a key");
+    const int tid = (int)threadIdx.x, lane = tid & 63, w = tid >> 6;
+#pragma unroll
+    for (int i = 0; i < kSortWaves; ++i) at[i][tid] = 0;
+    const int64_t per = ((int64_t)T + kSortWaves * 64 - 1) / (kSortWaves * 64) * 64;  // tokens a wave
+    const int64_t beg = w * per, end = beg + per < T ? beg + per : T;
+    int key[kSortKeep];
+    auto load = [&](int64_t t0) {
+#pragma unroll
+        for (int i = 0; i < kSortKeep; ++i) {
+            const int64_t t = t0 + i * 64 + lane;
+            const int a = t < end ? index[t] : 0;
+            key[i] = (unsigned)a < (unsigned)n ? a : n;
+        }
+    };
+    __syncthreads();
+    for (int64_t t0 = beg; t0 < end; t0 += kSortKeep * 64) {
+        load(t0);
+#pragma unroll
+        for (int i = 0; i < kSortKeep; ++i)
+            if (t0 + i * 64 + lane < end) atomicAdd(&at[w][key[i]], 1);
+    }
+    __syncthreads();
+    int count = 0;
+#pragma unroll
+    for (int i = 0; i < kSortWaves; ++i) count += at[i][tid];
+    int upto = count;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const int o = __shfl_up(upto, d);
+        if (lane >= d) upto += o;
+    }
+    if (lane == 63) total[w] = upto;
+    __syncthreads();
+    int base = upto - count;
+    for (int i = 0; i < w; ++i) base += total[i];
+#pragma unroll
+    for (int i = 0; i < kSortWaves; ++i) {
+        const int c = at[i][tid];
+        at[i][tid] = base;
+        base += c;
+    }
+    __syncthreads();
+    for (int64_t t0 = beg; t0 < end; t0 += kSortKeep * 64) {
+        if (per > kSortKeep * 64) load(t0);
+#pragma unroll
+        for (int i = 0; i < kSortKeep; ++i) {
+            const int64_t t = t0 + i * 64 + lane;
+            if (t >= end) continue;
+            const int p = atomicAdd(&at[w][key[i]], 1);
+            order[p] = (int32_t)t;
+            sorted[p] = key[i] < n ? key[i] : -1;
+        }
+    }
 }
 
 __global__ __launch_bounds__(kWaves * 64) void lora_shrink_kernel(const uint16_t* __restrict__ x, int64_t ldx, int T,
@@ -40,18 +109,18 @@ __global__ __launch_bounds__(kWaves * 64) void lora_shrink_kernel(const uint16_t
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int i = lane & 15, g = lane >> 4;
     const int t0 = (int)blockIdx.x * 16 * FM;
-    int idx[FM];
+    int idx[FM], row[FM];  // row: of x and v, counted from t0 or, with an order, from 0
 #pragma unroll
     for (int f = 0; f < FM; ++f) {
         const int t = t0 + 16 * f + i;
-        const int v = t < T ? l.index[t] : -1;
+        const int v = t < T ? (l.order ? l.sorted : l.index)[t] : -1;
         idx[f] = (unsigned)v < (unsigned)l.n ? v : kNoAdapter;
+        row[f] = l.order ? l.order[t < T ? t : 0] : 16 * f + i;
     }
-    const rsrc_t rx = make_rsrc(x + (int64_t)t0 * ldx, kRecord);
+    const rsrc_t rx = make_rsrc(l.order ? x : x + (int64_t)t0 * ldx, kRecord);
     uint32_t xo[FM];
 #pragma unroll
-    for (int f = 0; f < FM; ++f)
-        xo[f] = t0 + 16 * f + i < T ? (uint32_t)((16 * f + i) * ldx * 2) + 16u * g : kOob;
+    for (int f = 0; f < FM; ++f) xo[f] = t0 + 16 * f + i < T ? (uint32_t)(row[f] * ldx * 2) + 16u * g : kOob;
     const int nch = (K + 63) / 64;
     const int cbeg = (int)((int64_t)nch * blockIdx.z / l.parts), cend = (int)((int64_t)nch * (blockIdx.z + 1) / l.parts);
     // Piece q is rows 16 (q % per).. of distinct adapter q / per; a workgroup's
@@ -138,7 +207,8 @@ __global__ __launch_bounds__(kWaves * 64) void lora_shrink_kernel(const uint16_t
                 f32x4 v = red[0][r][f][lane];
 #pragma unroll
                 for (int k = 1; k < kWaves; ++k) v += red[k][r][f][lane];
-                *(f32x4*)(l.v + blockIdx.z * l.part_stride + (int64_t)(t0 + 16 * f + i) * l.vld + row0[r] + 4 * g) = v * scale[r];
+                const int64_t to = l.order && !l.v_sorted ? row[f] : t0 + 16 * f + i;
+                *(f32x4*)(l.v + blockIdx.z * l.part_stride + to * l.vld + row0[r] + 4 * g) = v * scale[r];
             }
     }
 }
@@ -154,6 +224,17 @@ int lora_parts(int T) {
     if (T <= kTokenWise) return 1;
     const int groups = (T + 31) / 32;
     return groups > 128 ? 1 : groups > 64 ? 2 : kMaxLoraParts;
+}
+
+// The sort is 4 us (30 adapters of rank 32, K = N = 3584, 1000 tokens: mixed 105
+// us in their own order, 57 by adapter; 4096 tokens, K = N = 2048, 32 of rank 64:
+// mixed 243 and 69, in runs 67 and 75). Up to 256 tokens neither way is ahead
+// by more than that: 205 tokens mixed 28 and 24, in runs 21 and 26.
+bool lora_sorts(int T, int n) { return T > 256 && n > 2 && n < kSortKeys; }
+
+hipError_t launch_lora_sort(const int32_t* index, int T, int n, int32_t* order, int32_t* sorted, hipStream_t s) {
+    hipLaunchKernelGGL(lora_sort_kernel, dim3(1), dim3(kSortWaves * 64), 0, s, index, T, n, order, sorted);
+    return hipGetLastError();
 }
 
 hipError_t launch_lora_shrink(const uint16_t* x, int64_t ldx, int T, int K, const LoraArgs& l, hipStream_t s) {

@@ -204,7 +204,61 @@ def test_linear_adapters(moe, T, K, N, n, rank, runs):
     assert bool(((got.double().cpu() - want).abs() <= tol * 1.01 + B8 * want.abs()).all())
 
 
-@pytest.mark.parametrize("T", [9, 200])
+@pytest.mark.parametrize("T,K,N,n,runs", [
+    (257, 72, 304, 3, False),      # a tile's own rows
+    (300, 1032, 264, 40, False),   # K in parts, joined token by token
+    (1500, 264, 2056, 30, False),  # tiles side by side
+    (1500, 264, 2056, 30, True),
+    (9000, 136, 1160, 5, False),   # a sort in more than one batch, large tiles
+    (400, 64, 128, 1023, False),   # the most adapters of a sort
+    (400, 64, 128, 1024, False),   # and one more
+])
+def test_linear_adapters_by_order(moe, T, K, N, n, runs):
+    """Many tokens are taken adapter by adapter; x and out have rows of their
+    own strides, and what lies behind them stays."""
+    g = gen(T + n)
+    rank = 72
+    xb, w = rnd(g, T, K + 8), weight(g, N, K)
+    lo = adapters(g, T, K, N, n, rank, runs=runs)
+    for i in range(n):
+        lo[0][i, int(lo[3][i]):] = math.nan
+        lo[1][i, :, int(lo[3][i]):] = math.inf
+    xd = xb[:, :K].double()
+    want = xd @ w.double().t() + ref.lora(xd, lo)
+    wide = tuple(t if t is None or not t.is_floating_point() else torch.nan_to_num(t.double(), 0, 0, 0).abs() for t in lo)
+    extra = ref.lora(xd.abs(), wide)
+    tol = sum_tol(xd, w.double()) + extra * (2.0 ** -16 + (K / 8 + 128) * F24)
+    out = torch.full((T + 2, N + 8), 5.0, dtype=F32, device="cuda")
+    moe.moe_lora_linear(cuda(xb)[:, :K], cuda(w), lora=cuda(lo), out=out[:T, :N])
+    assert bool(((out[:T, :N].double().cpu() - want).abs() <= tol).all())
+    assert bool((out[T:] == 5).all()) and bool((out[:, N:] == 5).all())
+    # a token's result does not depend on its place
+    p = torch.randperm(T, generator=g)
+    lo2 = (lo[0], lo[1], lo[2][p], lo[3], lo[4])
+    got = moe.moe_lora_linear(cuda(xb[p])[:, :K], cuda(w), lora=cuda(lo2), out_dtype=F32)
+    assert torch.equal(got, out[:T, :N][p.cuda()])
+
+
+@pytest.mark.parametrize("same", [True, False])
+@pytest.mark.parametrize("T,H,I", [(700, 264, 392), (3000, 136, 2056)])
+def test_ffn_adapters_by_order(moe, T, H, I, same):
+    g = gen(T + I)
+    x, w13, w2, add = rnd(g, T, H), weight(g, 2 * I, H), weight(g, H, I), rnd(g, T, H)
+    l13 = adapters(g, T, H, 2 * I, 7, 24)
+    l2 = adapters(g, T, I, H, 7, 16)
+    c13, c2 = cuda(l13), cuda(l2)
+    if same:  # one index tensor for both
+        l2 = (l2[0], l2[1], l13[2], l2[3], l2[4])
+        c2 = (c2[0], c2[1], c13[2], c2[3], c2[4])
+    want, gu, h = ref.ffn(x.double(), w13.double(), w2.double(), add.double(), l13, l2)
+    out = cuda(add)  # the addend's own buffer
+    _, saved = moe.moe_ffn_forward(cuda(x), cuda(w13), cuda(w2), addend=out, lora13=c13, lora2=c2, out=out,
+                                   save_gate_up=True)
+    ref.check(saved, gu, B8, rms=1e-4, what="gate_up")
+    ref.check(out, want, B8, rms=ref.FLIPS, absolute=ref.step_tol(h, w2.double()), what="out", norm=ref.NORM)
+
+
+@pytest.mark.parametrize("T", [9, 200, 500])
 def test_linear_tokens_do_not_meet(moe, T):
     """A NaN in one token, or in one adapter, stays with its tokens."""
     g = gen(T)
