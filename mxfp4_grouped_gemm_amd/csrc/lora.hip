@@ -60,12 +60,25 @@ __global__ __launch_bounds__(kSortWaves * 64) void lora_sort_kernel(const int32_
             key[i] = (unsigned)a < (unsigned)n ? a : n;
         }
     };
+    // Counts the i-th tokens and gives their places; those of one adapter (a
+    // run) at once, as 64 additions to one word take their turns (4099 tokens in
+    // eight runs: 11.6 us by additions alone, 7.5).
+    auto take = [&](int i, int64_t t0) -> int {
+        const int64_t left = end - (t0 + i * 64);
+        if (left <= 0) return 0;
+        const int k0 = __builtin_amdgcn_readfirstlane(key[i]);
+        if (left >= 64 && __all(key[i] == k0)) {
+            const int p = lane == 0 ? atomicAdd(&at[w][k0], 64) : 0;
+            return __builtin_amdgcn_readfirstlane(p) + lane;
+        }
+        return lane < left ? atomicAdd(&at[w][key[i]], 1) : 0;
+    };
     __syncthreads();
     for (int64_t t0 = beg; t0 < end; t0 += kSortKeep * 64) {
         load(t0);
 #pragma unroll
         for (int i = 0; i < kSortKeep; ++i)
-            if (t0 + i * 64 + lane < end) atomicAdd(&at[w][key[i]], 1);
+            take(i, t0);
     }
     __syncthreads();
     int count = 0;
@@ -93,8 +106,8 @@ __global__ __launch_bounds__(kSortWaves * 64) void lora_sort_kernel(const int32_
 #pragma unroll
         for (int i = 0; i < kSortKeep; ++i) {
             const int64_t t = t0 + i * 64 + lane;
+            const int p = take(i, t0);
             if (t >= end) continue;
-            const int p = atomicAdd(&at[w][key[i]], 1);
             order[p] = (int32_t)t;
             sorted[p] = key[i] < n ? key[i] : -1;
         }
