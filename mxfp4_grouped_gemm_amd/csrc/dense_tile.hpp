@@ -24,7 +24,8 @@
 //  * K as the row index (the other operand order of a backward product): rows
 //    of BM or BN elements; the operand is read through the transposing LDS
 //    read (four rows of 16 elements -> each lane four elements of one column).
-//    Piece c of row k sits at c ^ (2 ((k & 3) | (k >> 3 & 1) << 2)).
+//    Piece c of row k sits at c ^ key(k), such that the four rows of 16 lanes'
+//    read, whose columns are consecutive (X) or 16 apart (W), share no bank.
 #pragma once
 
 #include <type_traits>
@@ -155,6 +156,13 @@ __device__ __forceinline__ int key_w(int r) {
 template <int PIECES>
 __device__ __forceinline__ int key_t(int k) {
     return (2 * ((k & 3) | (((k >> 3) & 1) << 2))) & (PIECES - 1);
+}
+
+// For W, whose 16 columns of a read are groups of four at a stride of 16 (rows
+// of 128 columns or more) or 8.
+template <int PIECES>
+__device__ __forceinline__ int key_tw(int k) {
+    return PIECES >= 16 ? (k & 1) | ((k >> 3) & 1) << 1 | (k & 2) << 2 : key_t<PIECES>(k);
 }
 
 // Tokens without an adapter, in the searches over a tile's adapters.
@@ -441,7 +449,8 @@ __device__ __forceinline__ void dense_tile(const DenseArgs& a, int id, int part,
         const int p = (w * C::WL + i) * 64 + lane;
         if constexpr (C::WT) {
             constexpr int PR = C::BN / 8;
-            const int k = p / PR, c = (p % PR) ^ key_t<PR>(k);
+            static_assert(C::FN == (PR >= 16 ? 4 : 2), "the keys are for this stride of a read's columns");
+            const int k = p / PR, c = (p % PR) ^ key_tw<PR>(k);
             wo[i] = n0 + c * 8 < a.N ? (uint32_t)(k * a.ldw * 2 + c * 16) : kOob;
         } else {
             const int r = p / kPieces, c = (p % kPieces) ^ key_w<C::KB, C::F>(r);
@@ -549,7 +558,7 @@ __device__ __forceinline__ void dense_tile(const DenseArgs& a, int id, int part,
         for (int h = 0; h < 2; ++h) {
             const int k = 32 * s + 8 * g + 4 * h + (l16 >> 2);
             const int col = c0 + (l16 & 3) * stride;
-            const uint8_t* p = base + k * pitch + ((((col >> 3) ^ key_t<PR>(k)) << 4) | ((col & 4) << 1));
+            const uint8_t* p = base + k * pitch + ((((col >> 3) ^ (stride > 4 ? key_tw<PR>(k) : key_t<PR>(k))) << 4) | ((col & 4) << 1));
             typedef __attribute__((address_space(3))) bf16x4* tp;
             v[h] = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((tp)p);
         }
