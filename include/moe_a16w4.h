@@ -330,7 +330,7 @@ moe_status moe_rms_norm(const uint16_t* x, int64_t x_stride, const void* residua
  *           and columns of B[i] (what lies beyond is not read as numbers;
  *           values outside [0, rank] are clamped).
  *   scale   fp32 [n] or NULL (1).
- *   n >= 1, rank a multiple of 8 in [8, 256]. a and b 16-byte aligned. */
+ *   1 <= n <= 2^24, rank a multiple of 8 in [8, 256]. a and b 16-byte aligned. */
 typedef struct {
     const uint16_t* a;
     const uint16_t* b;

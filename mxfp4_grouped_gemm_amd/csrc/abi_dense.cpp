@@ -20,6 +20,7 @@ constexpr int64_t kMaxCols = 1 << 18;
 constexpr int64_t kMaxStride = 1 << 20;
 constexpr int kMaxTokens = 1 << 24;
 constexpr int kMaxRank = 256;
+constexpr int kMaxAdapters = 1 << 24;  // `ranks` has 32-bit offsets
 // Weights that the few-token kernels address with 32-bit offsets.
 constexpr int64_t kMaxSkinnyBytes = 0x7fff0000LL;
 
@@ -67,6 +68,7 @@ moe_status check_workspace(const char* fn, const void* ws, size_t have, int64_t 
 moe_status check_lora(const char* fn, const char* name, const moe_lora* l, int T) {
     if (!l) return MOE_OK;
     if (l->n < 1) return fail(MOE_ERR_INVALID_ARG, "%s: %s has n=%d < 1", fn, name, l->n);
+    if (l->n > kMaxAdapters) return fail(MOE_ERR_UNSUPPORTED, "%s: %s has n=%d > %d", fn, name, l->n, kMaxAdapters);
     if (l->rank < 8 || l->rank % 8 != 0)
         return fail(MOE_ERR_INVALID_ARG, "%s: %s has rank=%d, not a positive multiple of 8", fn, name, l->rank);
     if (l->rank > kMaxRank) return fail(MOE_ERR_UNSUPPORTED, "%s: %s has rank=%d > %d", fn, name, l->rank, kMaxRank);

@@ -24,7 +24,7 @@ struct LoraArgs {
     const float* scale;      // [n] or null (all 1)
     float* v;                // fp32 [parts, T, vld], vld = rank rounded up to 32
     int64_t part_stride;     // T * vld
-    int n, rank, vld, parts; // v is the sum of the parts (of K)
+    int n, rank, vld, parts; // v is the sum of the parts (of K), of A x without the scale if there are several
     bool v_sorted;           // row p of v is token order[p]'s, else token p's
 };
 

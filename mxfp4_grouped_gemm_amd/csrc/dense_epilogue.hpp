@@ -53,14 +53,19 @@ __device__ __forceinline__ void lora_dot(const LoraArgs& l, int N, int64_t token
         k0 += 16;
         if (k0 >= rank) break;
     }
+    if (l.parts > 1 && l.scale) {
+        const float scale = l.scale[ad];
+        low[0] *= scale;
+        if constexpr (GATED) low[1] *= scale;
+    }
 }
 
 // With the hardware exp2 and reciprocal, about an ulp each (and |g| 2^-24 from
 // the exponent's product): every output of it is rounded to bf16 or e4m3. The
 // accurate expf and quotient are some 40 vector instructions for each of the
 // 64 outputs a lane has in a tile of the gated product (4096 pairs, K = 3584,
-// 8192 tokens: 353 us with them, 336 with these). Very negative g: exp
-// overflows, the reciprocal is 0.
+// 8192 tokens: 353 us with them, 336 with these). Below -87 the value is under 2^-125 and
+// comes out as 0.
 __device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }
 
 __device__ __forceinline__ u32x2 pack4(f32x4 v) { return u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])}; }

@@ -64,7 +64,7 @@ hipError_t launch_epi(const DenseArgs& a, hipStream_t s) {
 }  // namespace
 
 // 256 x 256 tiles when they come close to filling the 256 compute units, else
-// 128 x 128 ones.
+// 128 x 128 ones, which read twice the LDS bytes for a product.
 bool dense_big_tiles(const DenseArgs& a, int epi) {
     const bool gated = epi == kEpiGated || epi == kEpiGatedMx;
     const int64_t cols = gated ? 2 * (int64_t)a.N : a.N;

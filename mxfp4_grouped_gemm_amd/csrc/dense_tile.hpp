@@ -11,6 +11,13 @@
 // second workgroup to hide a load behind: they run with four buffers (64 x 64
 // tiles with eight), three (seven) steps of loads in flight.
 //
+// Bound by the matrix cores, at the 1.9 GHz that their power leaves: in tiles of
+// 256 x 256 they are busy 50 to 78% of the time. 8192 tokens: gated, 4096 pairs
+// over K = 3584, 336 us in a long run of this call alone (1.43 PFLOP/s of
+// bf16); 3584 columns over K = 4096, 178 us (1.35); the library's plain
+// products of these sizes take 321 and 169 there. MFMAs of 32 x 32 were slower:
+// the same LDS bytes, and fewer, longer instructions to place reads between.
+//
 // W is the MFMA's first operand, so a lane's four results are four
 // consecutive n of one m. The rows of W are dealt to the fragments such that
 // a lane's fragments are consecutive too (`n = 4 F q + 4 f + p` for fragment f
@@ -303,6 +310,18 @@ __device__ __forceinline__ void lora_accumulate(const LoraArgs& l, int64_t brows
                     for (int i = 0; i < P; ++i)
 #pragma unroll
                         for (int h = 0; h < 2; ++h) v[i][h] += part[p - 1][i][h];
+                if (l.scale) {
+                    const rsrc_t ri = make_rsrc((l.order ? l.sorted : l.index) + m0, kRecord), rs = make_rsrc(l.scale, kRecord);
+#pragma unroll
+                    for (int i = 0; i < P; ++i) {
+                        const int t = (tid + (i0 + i) * C::THREADS) / 8;
+                        const uint32_t ad = __builtin_amdgcn_raw_buffer_load_b32(ri, m0 + t < M ? (uint32_t)t * 4u : kOob, 0, 0);
+                        const float scale = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, ad < (uint32_t)l.n ? ad * 4u : kOob, 0, 0));
+                        // (Zeros, as beyond the rank, for any scale.)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) v[i][e / 4][e % 4] = v[i][e / 4][e % 4] != 0.0f ? v[i][e / 4][e % 4] * scale : 0.0f;
+                    }
+                }
             }
 #pragma unroll
             for (int i = 0; i < P; ++i) {
@@ -312,7 +331,9 @@ __device__ __forceinline__ void lora_accumulate(const LoraArgs& l, int64_t brows
                 for (int e = 0; e < 4; ++e) {
                     const float x0 = v[i][e / 2][2 * (e & 1)], x1 = v[i][e / 2][2 * (e & 1) + 1];
                     hi[e] = pack_bf16x2(x0, x1);
-                    lo[e] = pack_bf16x2(x0 - __uint_as_float(hi[e] << 16), x1 - __uint_as_float(hi[e] & 0xffff0000u));
+                    // An infinite half has no rest.
+                    const float h0 = __uint_as_float(hi[e] << 16), h1 = __uint_as_float(hi[e] & 0xffff0000u);
+                    lo[e] = pack_bf16x2(fabsf(h0) < __builtin_inff() ? x0 - h0 : 0.0f, fabsf(h1) < __builtin_inff() ? x1 - h1 : 0.0f);
                 }
                 uint8_t* dst = (q % 8 < 4 ? s0 : s1) + r * 128;
                 *(u32x4*)(dst + ((c ^ key_x<128>(r)) << 4)) = hi;

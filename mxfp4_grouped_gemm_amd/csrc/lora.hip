@@ -13,7 +13,7 @@
 // mixed (a decode batch) would have each adapter among every 32.
 //
 // With few groups of tokens K is split over workgroups too, and what reads v
-// adds the parts. In both forms eight waves split K, hold a batch of 128-byte K chunks in flight
+// adds the parts and then scales. In both forms eight waves split K, hold a batch of 128-byte K chunks in flight
 // and meet in LDS in a fixed order.
 #include "lora_shrink.hpp"
 
@@ -162,13 +162,15 @@ __global__ __launch_bounds__(kWaves * 64) void lora_shrink_kernel(const uint16_t
         rsrc_t ra[FR];
         uint32_t ao[FR];
         float scale[FR];
+        int ranks[FR];
 #pragma unroll
         for (int r = 0; r < FR; ++r) {
             const bool some = ad[r] != kNoAdapter;
             const int at = some ? ad[r] : 0;
             int rank = l.ranks ? l.ranks[at] : l.rank;
             rank = rank < l.rank ? rank : l.rank;
-            scale[r] = l.scale ? l.scale[at] : 1.0f;
+            scale[r] = l.scale && l.parts == 1 ? l.scale[at] : 1.0f;
+            ranks[r] = rank;
             ra[r] = make_rsrc(l.a + ((int64_t)at * l.rank + row0[r]) * K, kRecord);
             ao[r] = some && row0[r] + i < rank ? (uint32_t)(i * K * 2) + 16u * g : kOob;
 #pragma unroll
@@ -221,7 +223,10 @@ __global__ __launch_bounds__(kWaves * 64) void lora_shrink_kernel(const uint16_t
 #pragma unroll
                 for (int k = 1; k < kWaves; ++k) v += red[k][r][f][lane];
                 const int64_t to = l.order && !l.v_sorted ? row[f] : t0 + 16 * f + i;
-                *(f32x4*)(l.v + blockIdx.z * l.part_stride + to * l.vld + row0[r] + 4 * g) = v * scale[r];
+                // Rows beyond the rank are zeros for any scale.
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = row0[r] + 4 * g + e < ranks[r] ? v[e] * scale[r] : 0.0f;
+                *(f32x4*)(l.v + blockIdx.z * l.part_stride + to * l.vld + row0[r] + 4 * g) = v;
             }
     }
 }

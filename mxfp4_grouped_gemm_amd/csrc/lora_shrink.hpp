@@ -54,7 +54,10 @@ __device__ __forceinline__ void shrink_token(const uint16_t* __restrict__ x, int
         f32x4 v = red[0][tid];
 #pragma unroll
         for (int k = 1; k < kWaves; ++k) v += red[k][tid];
-        *(f32x4*)(l.v + (int64_t)t * l.vld + r0 + 4 * tid) = v * (l.scale ? l.scale[ad] : 1.0f);
+        const float scale = l.scale ? l.scale[ad] : 1.0f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = r0 + 4 * tid + e < rank ? v[e] * scale : 0.0f;
+        *(f32x4*)(l.v + (int64_t)t * l.vld + r0 + 4 * tid) = v;
     }
 }
 

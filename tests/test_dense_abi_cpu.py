@@ -68,7 +68,7 @@ def test_linear_refusals():
     for bad in (dict(n=0), dict(rank=0), dict(rank=12), dict(a=None), dict(b=None), dict(index=None), dict(a=P + 8),
                 dict(index=P + 2), dict(ranks=P + 1), dict(scale=P + 2)):
         assert said(linear(lo=lora(**bad)), "lora") == BAD, bad
-    assert linear(lo=lora(rank=264)) == NOT
+    assert linear(lo=lora(rank=264)) == NOT and linear(lo=lora(n=(1 << 24) + 1)) == NOT
     need = moe.moe_lora_linear_workspace_size(100, 64, 32, 16)
     assert need >= 100 * 32 * 4 and need % 256 == 0
     assert said(linear(lo=lora(), wsb=need - 1), "workspace") == BAD

@@ -275,6 +275,20 @@ def test_linear_tokens_do_not_meet(moe, T):
     assert bool(got[4].isnan().all())
 
 
+@pytest.mark.parametrize("T", [5, 70, 200, 400])
+def test_linear_infinite_scale(moe, T):
+    """An infinite scale takes part in the adapter's own rank alone."""
+    g = gen(T)
+    K, N, n = 64, 96, 4
+    x, w = rnd(g, T, K).abs(), weight(g, N, K)
+    a, b, index, _, _ = adapters(g, T, K, N, n, 24, ranks=False, scale=False)
+    lo = (a.abs() + 0.01, b.abs() + 0.01, index, torch.tensor([8, 24, 0, 13], dtype=torch.int32),
+          torch.tensor([math.inf, 1.0, math.inf, math.inf]))
+    got = moe.moe_lora_linear(cuda(x), cuda(w), lora=cuda(lo)).cpu()
+    hit = (index == 0) | (index == 3)
+    assert bool(got[hit].isinf().all()) and bool(got[~hit].isfinite().all())
+
+
 @pytest.mark.parametrize("T", [5, 70, 300])
 def test_linear_index_outside_and_defaults(moe, T):
     g = gen(T)
