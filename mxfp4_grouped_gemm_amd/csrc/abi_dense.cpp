@@ -143,7 +143,9 @@ moe::DenseArgs product(const void* x, int64_t ldx, const void* w, int64_t ldw, i
 }
 
 bool skinny(int T, int64_t rows, int K, int elt) {
-    return T <= (elt == 0 ? moe::kSkinnyMaxTokens : moe::kSkinnyMaxTokensMx) && rows * K * (elt == 0 ? 2 : 1) <= kMaxSkinnyBytes;
+    const bool many = rows >= (elt == 0 ? moe::kSkinnyManyRows : moe::kSkinnyManyRowsMx);
+    const int most = many ? 16 : elt == 0 ? moe::kSkinnyMaxTokens : moe::kSkinnyMaxTokensMx;
+    return T <= most && rows * K * (elt == 0 ? 2 : 1) <= kMaxSkinnyBytes;
 }
 
 int splits_of(const moe::DenseArgs& a, int elt, int epi, bool few) {
@@ -151,12 +153,13 @@ int splits_of(const moe::DenseArgs& a, int elt, int epi, bool few) {
 }
 
 // Bytes of split-K partials of a forward product; few: in the few-token
-// kernels, which join the products of adapters (rank > 0) in any case.
+// kernels.
 int64_t partial_bytes(int T, int N, int K, int elt, int epi, bool few, int rank) {
     moe::DenseArgs a = product(nullptr, K, nullptr, K, T, N, K, nullptr, N);
     a.lora.n = rank > 0;
     a.lora.rank = rank;
-    return align_up(moe::dense_partial_bytes(a, splits_of(a, elt, epi, few), epi, few && rank > 0), 256);
+    const int splits = splits_of(a, elt, epi, few);
+    return align_up(moe::dense_partial_bytes(a, splits, epi, few && moe::skinny_joins(a, splits, elt, epi)), 256);
 }
 
 // The narrow product; sorted: the order is there already (of the same index).

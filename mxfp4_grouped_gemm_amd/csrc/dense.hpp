@@ -81,14 +81,22 @@ hipError_t launch_dense_grads(const DenseArgs& dw13, const DenseArgs& dw2, const
 // Up to this many tokens the products stream the weights without LDS tiles.
 // (MXFP8 with H = 3584, I = 2048: 33 us at 64 tokens, 26 in tiles, where h is
 // quantised once and not by every workgroup of the second product; at 32 both
-// take 26.)
+// take 26.) More than 16 tokens only with fewer rows of W than give tiles of
+// their own to half of the compute units with K in few parts (K = 3584, 64
+// tokens: 4096 rows 15.2 us, 16.1 in tiles; 8192 rows 22.8 and 19.4; 16384
+// rows 42 and 31, at 25 tokens 34 and 27); in MXFP8 with one round of
+// workgroups (H = 3584, I = 8192, 32 tokens: 69 us, 38 in tiles; H = 7168, I =
+// 2048: 39 and 28).
 constexpr int kSkinnyMaxTokens = 64, kSkinnyMaxTokensMx = 32;
+constexpr int kSkinnyManyRows = 8192, kSkinnyManyRowsMx = 4104;  // from here on 16 tokens at most
 // elt 0: bf16; 1: MXFP8 activations and weights. h_f32: the fp32 h of the
 // MXFP8 block between its two products (written by kEpiGated, and read and
 // quantised by the second product).
 // Parts of K that launch_skinny takes for this product (a.splits).
 int skinny_splits(const DenseArgs& a, int elt, int epi);
 bool skinny_wide(const DenseArgs& a, bool gated);
+// Whether its results are joined from a.partial (even of one part).
+bool skinny_joins(const DenseArgs& a, int splits, int elt, int epi);
 int skinny_narrow(const DenseArgs& a);  // workgroups of the adapters' narrow product
 hipError_t launch_skinny(const DenseArgs& a, int elt, int epi, const float* h_f32, hipStream_t s);
 

@@ -236,7 +236,7 @@ hipError_t launch_one(const DenseArgs& a, const float* xf, hipStream_t s) {
     const unsigned groups = (unsigned)((a.N + kRows - 1) / kRows);
     const dim3 block(kWaves * 64);
     if constexpr (ELT == kEltBf16) {
-        if (a.splits > 1 || a.lora.n > 0) {
+        if (NW > 1 || a.splits > 1 || a.lora.n > 0) {
             const unsigned narrow = (unsigned)skinny_narrow(a);
             hipLaunchKernelGGL((skinny_kernel<ELT, NJ, NW, GATED, XF32, true>), dim3(groups * (unsigned)a.splits + narrow),
                                block, 0, s, a, xf);
@@ -257,10 +257,21 @@ hipError_t launch_width(const DenseArgs& a, bool wide, const float* xf, hipStrea
     return launch_one<ELT, NJ, 1, GATED, XF32>(a, xf, s);
 }
 
+// Up to 32 tokens the tokens' bytes do not pay for a second kernel, unless
+// adapters need it anyway, W has few rows, or more of them than one round of
+// workgroups takes and more than a batch of K (2048 pairs, K = 3584, 32
+// tokens: 12.0 us, 13.5 in parts; 64 tokens: 18.9 and 16.0; 25 tokens: 4624
+// rows over K = 3904 23.6 and 14.5, 6000 rows over 1024 11.6 and 11.0, over
+// 512 9.1 and 10.8; 16384 rows over 3584 with 64 tokens 79 and 43).
+bool one_kernel(const DenseArgs& a, bool gated) {
+    const int64_t rows = gated ? 2 * (int64_t)a.N : a.N;
+    return a.M <= 16 || (a.M <= 32 && a.lora.n == 0 && rows >= 2048 && (rows <= 4096 || a.K <= 512));
+}
+
 template <int ELT, bool GATED, bool XF32>
 hipError_t launch_nj(const DenseArgs& a, const float* xf, hipStream_t s) {
     if (a.M <= 16) return launch_one<ELT, 1, 1, GATED, XF32>(a, xf, s);
-    const bool wide = ELT == kEltBf16 && a.splits > 1 && skinny_wide(a, GATED);
+    const bool wide = ELT == kEltBf16 && !one_kernel(a, GATED) && skinny_wide(a, GATED);
     if (a.M <= 32) return launch_width<ELT, 2, GATED, XF32>(a, wide, xf, s);
     if constexpr (ELT == kEltMx8) return hipErrorInvalidValue;  // kSkinnyMaxTokensMx
     else return launch_width<ELT, 4, GATED, XF32>(a, wide, xf, s);
@@ -274,18 +285,20 @@ bool skinny_wide(const DenseArgs& a, bool gated) { return (gated ? 2 * (int64_t)
 int skinny_narrow(const DenseArgs& a) { return a.lora.n > 0 ? a.M * ((a.lora.rank + 15) / 16) : 0; }
 
 int skinny_splits(const DenseArgs& a, int elt, int epi) {
-    // Up to 32 tokens the tokens' bytes do not pay for a second kernel, unless
-    // adapters need it anyway or W has few rows (2048 pairs, K = 3584, 32 tokens: 12.0 us, 13.5
-    // in parts; 64 tokens: 18.9 and 16.0).
     const bool gated = epi != kEpiOut;
     const int64_t rows = gated ? 2 * (int64_t)a.N : a.N;
-    if (elt != kEltBf16 || a.M <= 16 || (a.M <= 32 && a.lora.n == 0 && rows >= 2048)) return 1;
+    if (elt != kEltBf16 || one_kernel(a, gated)) return 1;
     const int64_t groups = skinny_wide(a, gated) ? (rows + 63) / 64 : (rows + 15) / 16;
     // A part of K has a chunk for each wave; a workgroup a compute unit, those
     // of the narrow product counted.
     const int64_t most = (a.K + 63) / 64 / kWaves, room = (256 - skinny_narrow(a)) / groups;
     const int64_t s = room < most ? room : most;
     return s < 2 ? 1 : (int)s;
+}
+
+bool skinny_joins(const DenseArgs& a, int splits, int elt, int epi) {
+    const bool gated = epi != kEpiOut;
+    return elt == kEltBf16 && (a.lora.n > 0 || splits > 1 || (!one_kernel(a, gated) && skinny_wide(a, gated)));
 }
 
 hipError_t launch_skinny(const DenseArgs& a, int elt, int epi, const float* h_f32, hipStream_t s) {

@@ -258,6 +258,25 @@ def test_ffn_adapters_by_order(moe, T, H, I, same):
     ref.check(out, want, B8, rms=ref.FLIPS, absolute=ref.step_tol(h, w2.double()), what="out", norm=ref.NORM)
 
 
+@pytest.mark.parametrize("T,K,N", [(17, 72, 4096), (25, 264, 4104), (25, 2056, 4624), (40, 136, 16400), (20, 72, 20000),
+                                   (64, 520, 8200), (33, 72, 2040), (33, 72, 2048)])
+@pytest.mark.parametrize("n", [0, 3])
+def test_linear_few_tokens_many_rows(moe, T, K, N, n):
+    g = gen(T + N + n)
+    x, w = rnd(g, T, K), weight(g, N, K)
+    xd, wd = x.double(), w.double()
+    want, tol = xd @ wd.t(), sum_tol(xd, wd)
+    lo = None
+    if n:
+        lo = adapters(g, T, K, N, n, 16, ranks=False)
+        want += ref.lora(xd, lo)
+        wide = tuple(t if t is None or not t.is_floating_point() else t.double().abs() for t in lo)
+        tol += ref.lora(xd.abs(), wide) * (2.0 ** -16 + (K / 8 + 128) * F24)
+    got = moe.moe_lora_linear(cuda(x), cuda(w), lora=cuda(lo), out_dtype=F32)
+    assert bool(((got.double().cpu() - want).abs() <= tol).all())
+    assert torch.equal(moe.moe_lora_linear(cuda(x), cuda(w), lora=cuda(lo)), got.bfloat16())
+
+
 @pytest.mark.parametrize("T", [9, 200, 500])
 def test_linear_tokens_do_not_meet(moe, T):
     """A NaN in one token, or in one adapter, stays with its tokens."""
@@ -321,7 +340,7 @@ def test_linear_strides_and_rows_behind(moe, T):
 
 
 # ------------------------------------------------------------------- ffn
-FFN = [(1, 8, 8), (1, 3584, 384), (2, 40, 72), (16, 520, 136), (17, 264, 1000), (37, 3584, 128), (64, 96, 64),
+FFN = [(20, 72, 4200), (50, 4200, 72), (1, 8, 8), (1, 3584, 384), (2, 40, 72), (16, 520, 136), (17, 264, 1000), (37, 3584, 128), (64, 96, 64),
        (65, 136, 72), (129, 520, 264), (300, 1032, 1000), (1030, 264, 392), (2200, 136, 2056)]
 
 
@@ -346,7 +365,7 @@ def test_ffn_forward(moe, T, H, I, lora):
                   what="no addend", norm=ref.NORM)
 
 
-@pytest.mark.parametrize("T,H,I", [(1, 32, 32), (1, 3584, 384), (5, 96, 160), (16, 544, 128), (20, 128, 1024),
+@pytest.mark.parametrize("T,H,I", [(1, 32, 32), (20, 64, 2080), (32, 4128, 64), (1, 3584, 384), (5, 96, 160), (16, 544, 128), (20, 128, 1024),
                                    (40, 256, 96), (64, 1056, 64), (65, 96, 160), (130, 544, 288), (300, 1024, 1056),
                                    (1030, 288, 384), (2200, 160, 2080)])
 def test_ffn_forward_mxfp8(moe, T, H, I):
