@@ -244,7 +244,7 @@ int lora_parts(int T) {
     return groups > 128 ? 1 : groups > 64 ? 2 : kMaxLoraParts;
 }
 
-// The sort is 4 us (30 adapters of rank 32, K = N = 3584, 1000 tokens: mixed 105
+// The sort is 4 to 8 us (30 adapters of rank 32, K = N = 3584, 1000 tokens: mixed 105
 // us in their own order, 57 by adapter; 4096 tokens, K = N = 2048, 32 of rank 64:
 // mixed 243 and 69, in runs 67 and 75). Up to 256 tokens neither way is ahead
 // by more than that: 205 tokens mixed 28 and 24, in runs 21 and 26.
