@@ -83,6 +83,7 @@ int dense_splits(const DenseArgs& a, int elt, int epi) {
     const bool gated = epi == kEpiGated || epi == kEpiGatedMx;
     const int64_t cols = gated ? 2 * (int64_t)a.N : a.N;
     const int64_t tiles = (int64_t)((a.M + 127) / 128) * ((cols + 127) / 128);
+    if (tiles == 0) return 1;  // no tokens
     const int bk = elt == kEltBf16 ? 64 : 128;
     const int steps = (a.K + bk - 1) / bk;
     int64_t s = 256 / tiles;

@@ -2,6 +2,9 @@
 test_abi_cpu.py, the calls pass null or made-up device pointers, so this file
 runs only where no GPU is visible."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -160,3 +163,16 @@ def test_workspaces_hold_what_the_calls_keep():
             assert need >= least and need % 256 == 0, (T, need, least)
     assert moe.moe_lora_linear_workspace_size(16, H, I) == 0
     assert ctypes.sizeof(moe._CLora) == 48
+
+
+@pytest.mark.parametrize("call", [
+    "moe_lora_linear_workspace_size(0, 8192, 152064)", "moe_lora_linear_workspace_size(0, 8192, 152064, 16)",
+    "moe_ffn_workspace_size(0, 16384, 32768)", "moe_ffn_workspace_size(0, 16384, 32768, 8, 8)",
+    "moe_ffn_mxfp8_workspace_size(0, 32768, 65536)", "moe_ffn_backward_workspace_size(0, 16384, 32768)"])
+def test_workspaces_of_no_tokens_beside_large_weights(call):
+    """Weights above 2 GiB are not for the few-token kernels: the tiles' rule
+    for parts of K has to take no tiles too (in a process of its own, since a
+    division by zero ends it)."""
+    r = subprocess.run([sys.executable, "-c", f"import mxfp4_grouped_gemm_amd as m; print(m.{call})"],
+                       capture_output=True, text=True, cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and r.stdout.split() == ["0"], (r.returncode, r.stdout, r.stderr[-500:])
