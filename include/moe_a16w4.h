@@ -398,8 +398,9 @@ moe_status moe_ffn_forward_mxfp8(const uint8_t* x, const uint8_t* x_scale, const
  * products); the gradient of addend is dout itself.
  *   dout, x  bf16 [T, H];  gate_up bf16 [T, 2I];  w13, w2 as above.
  *   dx       out bf16 [T, H], dw13 bf16 [2I, H], dw2 bf16 [H, I]; each may be
- *            NULL (not computed), at least one is required. dw13 and dw2 are
- *            overwritten, and no sum depends on the order of atomics. */
+ *            NULL (not computed), at least one is required unless T == 0 (an
+ *            empty dx may have no address). dw13 and dw2 are overwritten,
+ *            and no sum depends on the order of atomics. */
 int64_t moe_ffn_backward_workspace_size(int T, int H, int I);
 moe_status moe_ffn_backward(const uint16_t* dout, int64_t dout_stride, const uint16_t* x,
                             int64_t x_stride, const uint16_t* gate_up, const uint16_t* w13,

@@ -176,3 +176,11 @@ def test_workspaces_of_no_tokens_beside_large_weights(call):
     r = subprocess.run([sys.executable, "-c", f"import mxfp4_grouped_gemm_amd as m; print(m.{call})"],
                        capture_output=True, text=True, cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
     assert r.returncode == 0 and r.stdout.split() == ["0"], (r.returncode, r.stdout, r.stderr[-500:])
+
+
+def test_ffn_backward_of_no_tokens_with_only_an_empty_dx():
+    """An empty tensor's address is null: not a call without outputs."""
+    assert bwd(T=0, dout=None, x=None, gu=None, dx=None, d13=None, d2=None, ws=None, wsb=0) == moe.MOE_OK
+    assert said(bwd(T=1, dx=None, d13=None, d2=None), "no output") == BAD
+    assert bwd(T=0, lddx=8, d13=None, d2=None) == BAD  # what is given is checked as ever
+    assert bwd(T=0, dx=None, d13=None, d2=P + 2) == BAD

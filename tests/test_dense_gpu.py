@@ -446,6 +446,18 @@ def test_ffn_backward_of_no_tokens(moe):
     assert dx.shape == (0, H) and not bool(d13.any()) and not bool(d2.any())
 
 
+@pytest.mark.parametrize("frozen", [True, False])
+def test_moe_ffn_gradients_of_no_tokens(moe, frozen):
+    H, I = 64, 96
+    x = torch.empty(0, H, dtype=BF, device="cuda", requires_grad=True)
+    w13 = torch.ones(2 * I, H, dtype=BF, device="cuda", requires_grad=not frozen)
+    w2 = torch.ones(H, I, dtype=BF, device="cuda", requires_grad=not frozen)
+    moe.moe_ffn(x, w13, w2).sum().backward()
+    assert x.grad.shape == (0, H)
+    if not frozen:
+        assert not bool(w13.grad.any()) and not bool(w2.grad.any())
+
+
 @pytest.mark.parametrize("T", [4, 150])
 def test_moe_ffn_gradients(moe, T):
     """The differentiable form against the formula and against differences of
