@@ -94,6 +94,7 @@ hipError_t launch_dense_grads(const DenseArgs& dw13, const DenseArgs& dw2, const
     g.dw13 = dw13;
     g.dw2 = dw2;
     g.dx = dx;
+    if (dx.M == 0) g.dx.out = nullptr;  // no tokens: a grid of its own would be empty
     auto tiles = [&](int b) { return square_tiles(dw13, b) + square_tiles(dw2, b) + square_tiles(g.dx, b); };
     // 256 x 256 tiles from 192 of them on, or from 160 for long sums (H = 2048,
     // I = 1408: at 700, 1024, 1500 and 2048 tokens, 160 to 200 tiles, the whole
@@ -111,7 +112,7 @@ hipError_t launch_dense_grads(const DenseArgs& dw13, const DenseArgs& dw2, const
     // and 130 alone.)
     const int64_t share = ((square_tiles(dw13, edge) + square_tiles(dw2, edge)) * (int64_t)dw13.K +
                            square_tiles(dx, edge) * dx.K) / 256;
-    if (dx.out && (dx.splits > 1 || (edge > 64 && 2 * (int64_t)dx.K > 5 * share))) {
+    if (g.dx.out && (dx.splits > 1 || (edge > 64 && 2 * (int64_t)dx.K > 5 * share))) {
         const hipError_t e = launch_nn<kEpiOut>(dx, s);
         if (e != hipSuccess) return e;
         g.dx.out = nullptr;

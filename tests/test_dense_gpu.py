@@ -446,6 +446,23 @@ def test_ffn_backward_of_no_tokens(moe):
     assert dx.shape == (0, H) and not bool(d13.any()) and not bool(d2.any())
 
 
+@pytest.mark.parametrize("H,I", [(64, 96), (1024, 1024), (3584, 2048)])  # tiles of 64, 128 and 256
+@pytest.mark.parametrize("given", [(True, True, True), (True, True, False), (True, False, False)])
+def test_ffn_backward_of_no_tokens_with_addresses(moe, H, I, given):
+    """From C an empty dx may have an address: nothing is written there, and
+    the weights' gradients are zeros."""
+    w13, w2 = torch.ones(2 * I, H, dtype=BF, device="cuda"), torch.ones(H, I, dtype=BF, device="cuda")
+    grads = [torch.full_like(t, math.nan) if on else None
+             for t, on in zip((torch.empty(8, H, dtype=BF, device="cuda"), w13, w2), given)]
+    ptrs = [None if t is None else t.data_ptr() for t in grads]
+    p, s = w13.data_ptr(), torch.cuda.current_stream().cuda_stream
+    status = moe.lib.moe_ffn_backward(p, H, p, H, p, p, w2.data_ptr(), 0, 0, H, I, ptrs[0], H, ptrs[1], ptrs[2], None, 0, s)
+    assert status == moe.MOE_OK, moe.moe_last_error()
+    torch.cuda.synchronize()
+    assert bool(grads[0].isnan().all())
+    assert all(not bool(t.any()) for t in grads[1:] if t is not None)
+
+
 @pytest.mark.parametrize("frozen", [True, False])
 def test_moe_ffn_gradients_of_no_tokens(moe, frozen):
     H, I = 64, 96
