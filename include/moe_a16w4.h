@@ -322,8 +322,9 @@ moe_status moe_rms_norm(const uint16_t* x, int64_t x_stride, const void* residua
                         int64_t q_scale_stride, void* stream);
 
 /* Low-rank adapters of many requests beside one projection [N, K]: token t
- * adds scale[i] * B[i] (A[i] x[t]) for i = index[t]; an index outside [0, n)
- * adds nothing.
+ * adds B[i] (scale[i] * (A[i] x[t])) for i = index[t]; an index outside [0, n)
+ * adds nothing. The scale acts within the adapter's rank: an infinite one makes
+ * an element of A x that is 0 a NaN, and one beyond the rank adds nothing.
  *   a       bf16 [n, rank, K];  b bf16 [n, N, rank].
  *   index   int32 [T].
  *   ranks   int32 [n] or NULL: adapter i uses the first ranks[i] rows of A[i]

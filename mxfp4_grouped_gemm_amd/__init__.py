@@ -455,7 +455,7 @@ def requantize_mxfp4_experts(w, scale_e8m0, chunk=8, stream=None):
 
 class LoraAdapters(NamedTuple):
     """A stack of low-rank adapters beside one projection [N, K]: token t adds
-    scale[i] * B[i] (A[i] x[t]) for i = index[t] (outside [0, n): nothing).
+    B[i] (scale[i] * (A[i] x[t])) for i = index[t] (outside [0, n): nothing).
     a bf16 [n, rank, K]; b bf16 [n, N, rank]; index int32 [T]; ranks int32 [n]
     (adapter i uses its first ranks[i]) and scale fp32 [n], each optional."""
     a: torch.Tensor

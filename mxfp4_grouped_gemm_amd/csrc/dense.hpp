@@ -9,7 +9,7 @@
 namespace moe {
 
 // A stack of low-rank adapters beside one projection [N, K]: token t adds
-// scale[a] * B[a] (A[a] x[t]) for a = index[t]; an index outside [0, n) adds
+// B[a] (scale[a] * (A[a] x[t])) for a = index[t]; an index outside [0, n) adds
 // nothing. v [T, vld] (fp32) receives scale * A x from the narrow product and
 // is read by the projection's kernels.
 constexpr int kMaxLoraParts = 4;

@@ -9,7 +9,7 @@
 namespace moe {
 namespace dense {
 
-// scale * B[a] (A[a] x) of one token for rows col..col+3 (and N + col.. of the
+// B[a] (scale A[a] x) of one token for rows col..col+3 (and N + col.. of the
 // gated block), from v = scale * A[a] x: a dot product of at most a few
 // hundred elements.
 template <bool GATED>
@@ -20,6 +20,9 @@ __device__ __forceinline__ void lora_dot(const LoraArgs& l, int N, int64_t token
     rank = rank < l.rank ? rank : l.rank;
     const uint16_t* b = l.b + ((int64_t)ad * (GATED ? 2 * (int64_t)N : N) + col) * l.rank;
     const float* v = l.v + token * l.vld;
+    // Parts come without the scale, which multiplies their sum and so acts
+    // within the rank alone, as where there is one part.
+    const float scale = l.parts > 1 && l.scale ? l.scale[ad] : 1.0f;
     // Sixteen columns at a time; the first batch is loaded before the rank is
     // known (what lies beyond it is memory of v and B, but not read as numbers).
     for (int k0 = 0;;) {
@@ -34,6 +37,8 @@ __device__ __forceinline__ void lora_dot(const LoraArgs& l, int N, int64_t token
                 vv[2 * h] += *(const f32x4*)(v + p * l.part_stride + k);
                 vv[2 * h + 1] += *(const f32x4*)(v + p * l.part_stride + k + 4);
             }
+            vv[2 * h] *= scale;
+            vv[2 * h + 1] *= scale;
 #pragma unroll
             for (int s = 0; s < (GATED ? 2 : 1); ++s)
 #pragma unroll
@@ -52,11 +57,6 @@ __device__ __forceinline__ void lora_dot(const LoraArgs& l, int N, int64_t token
                 }
         k0 += 16;
         if (k0 >= rank) break;
-    }
-    if (l.parts > 1 && l.scale) {
-        const float scale = l.scale[ad];
-        low[0] *= scale;
-        if constexpr (GATED) low[1] *= scale;
     }
 }
 

@@ -312,14 +312,18 @@ __device__ __forceinline__ void lora_accumulate(const LoraArgs& l, int64_t brows
                         for (int h = 0; h < 2; ++h) v[i][h] += part[p - 1][i][h];
                 if (l.scale) {
                     const rsrc_t ri = make_rsrc((l.order ? l.sorted : l.index) + m0, kRecord), rs = make_rsrc(l.scale, kRecord);
+                    const rsrc_t rr = make_rsrc(l.ranks, kRecord);
 #pragma unroll
                     for (int i = 0; i < P; ++i) {
-                        const int t = (tid + (i0 + i) * C::THREADS) / 8;
+                        const int q = tid + (i0 + i) * C::THREADS, t = q / 8;
                         const uint32_t ad = __builtin_amdgcn_raw_buffer_load_b32(ri, m0 + t < M ? (uint32_t)t * 4u : kOob, 0, 0);
-                        const float scale = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, ad < (uint32_t)l.n ? ad * 4u : kOob, 0, 0));
-                        // (Zeros, as beyond the rank, for any scale.)
+                        const uint32_t at = m0 + t < M && ad < (uint32_t)l.n ? ad * 4u : kOob;
+                        const float scale = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, at, 0, 0));
+                        int rank = l.ranks ? (int)__builtin_amdgcn_raw_buffer_load_b32(rr, at, 0, 0) : l.rank;
+                        rank = (rank < 0 ? 0 : rank < l.rank ? rank : l.rank) - (k0 + q % 8 * 8);
+                        // Beyond the rank zeros stay zeros for any scale.
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) v[i][e / 4][e % 4] = v[i][e / 4][e % 4] != 0.0f ? v[i][e / 4][e % 4] * scale : 0.0f;
+                        for (int e = 0; e < 8; ++e) v[i][e / 4][e % 4] = e < rank ? v[i][e / 4][e % 4] * scale : 0.0f;
                     }
                 }
             }

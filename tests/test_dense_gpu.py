@@ -308,6 +308,31 @@ def test_linear_infinite_scale(moe, T):
     assert bool(got[hit].isinf().all()) and bool(got[~hit].isfinite().all())
 
 
+# One part of K; parts joined token by token (tokens in their own order, and by
+# adapter); parts that the tiles read (N of more rows than are split over).
+@pytest.mark.parametrize("T,K,N", [(5, 64, 96), (40, 1024, 96), (70, 64, 96), (70, 1024, 96), (200, 64, 96), (200, 1024, 96), (400, 1024, 96),
+                                   (200, 264, 2056), (400, 264, 2056), (2100, 264, 4104), (5000, 64, 96)])
+@pytest.mark.parametrize("ranks", [True, False])
+def test_linear_infinite_scale_over_parts(moe, T, K, N, ranks):
+    """An infinite scale acts within the rank alone, on every path: an adapter
+    of rank 0 adds nothing, A x of 0 within the rank becomes a NaN, other
+    values infinities."""
+    g = gen(T + K)
+    n, rank = 5, 24
+    x, w = rnd(g, T, K).abs(), weight(g, N, K)
+    a, b, index, _, _ = adapters(g, T, K, N, n, rank, ranks=False, scale=False)
+    a, b = a.abs() + 0.01, b.abs() + 0.01
+    a[4, 5] = 0
+    r = torch.tensor([8, 24, 0, 13, 8], dtype=torch.int32) if ranks else None
+    scale = torch.tensor([math.inf, 1.0, math.inf if ranks else 2.0, math.inf, math.inf])
+    plain = moe.moe_lora_linear(cuda(x), cuda(w)).cpu()
+    got = moe.moe_lora_linear(cuda(x), cuda(w), lora=cuda((a, b, index, r, scale))).cpu()
+    assert bool(got[(index == 0) | (index == 3)].isinf().all()) and bool(got[index == 4].isnan().all())
+    assert bool(got[(index < 0) | (index == 1) | (index == 2)].isfinite().all())
+    same = (index < 0) | (index == 2) if ranks else index < 0
+    assert torch.equal(got[same], plain[same])
+
+
 @pytest.mark.parametrize("T", [5, 70, 300])
 def test_linear_index_outside_and_defaults(moe, T):
     g = gen(T)
