@@ -228,7 +228,7 @@ __device__ __forceinline__ void lora_rows(const LoraArgs& l, int m0, int M, Lora
 #pragma unroll
     for (int fm = 0; fm < C::FM; ++fm) {
         const int r = __builtin_amdgcn_raw_buffer_load_b32(rr, o.idx[fm] != kNoAdapter ? (uint32_t)o.idx[fm] * 4u : kOob, 0, 0);
-        o.rank[fm] = r < l.rank ? r : l.rank;
+        o.rank[fm] = r < 0 ? 0 : r < l.rank ? r : l.rank;  // (negated and subtracted from below)
     }
 }
 

@@ -350,6 +350,21 @@ def test_linear_index_outside_and_defaults(moe, T):
     assert torch.equal(a, moe.moe_lora_linear(cuda(x), cuda(w), lora=cuda(tuple(lo))))
 
 
+@pytest.mark.parametrize("T,K,N", [(5, 64, 96), (40, 1024, 96), (70, 64, 96), (200, 1024, 96), (200, 264, 2056),
+                                   (400, 264, 2056), (5000, 64, 96)])
+def test_linear_ranks_outside_are_clamped(moe, T, K, N):
+    """Any int32 below 0 is rank 0, any above the stack's rank is the stack's."""
+    g = gen(T + N)
+    n, rank = 5, 40
+    x, w = rnd(g, T, K), weight(g, N, K)
+    a, b, index, _, scale = adapters(g, T, K, N, n, rank, ranks=False)
+    want = moe.moe_lora_linear(cuda(x), cuda(w), lora=cuda((a, b, index, torch.tensor([0, 40, 0, 0, 40], dtype=torch.int32), scale)))
+    r = torch.tensor([-2 ** 31, 2 ** 31 - 1, -2 ** 31 + 1, -1, 41], dtype=torch.int32)
+    b[0], b[2], b[3] = math.inf, math.nan, math.inf
+    got = moe.moe_lora_linear(cuda(x), cuda(w), lora=cuda((a, b, index, r, scale)))
+    assert torch.equal(got, want)
+
+
 @pytest.mark.parametrize("T", [6, 90, 260])
 def test_linear_strides_and_rows_behind(moe, T):
     g = gen(T)
