@@ -572,6 +572,89 @@ def test_moe_ffn_partial_and_expanded_gradients(moe):
     assert torch.equal(w.grad, v.grad + v.grad)
 
 
+@pytest.mark.parametrize("T,H,I", [(5, 72, 40), (200, 136, 264), (700, 264, 392), (2400, 136, 4104)])
+def test_ffn_backward_strides_and_rows_behind(moe, T, H, I):
+    """dout, x and dx with rows of their own strides; what lies between and
+    behind the rows of dx stays."""
+    g = gen(T + H)
+    dout, x, gu = rnd(g, T + 1, H + 24), rnd(g, T + 2, H + 8), rnd(g, T, 2 * I)
+    w13, w2 = weight(g, 2 * I, H), weight(g, H, I)
+    dx = torch.full((T + 3, H + 40), 5.0, dtype=BF, device="cuda")
+    got = moe.moe_ffn_backward(cuda(dout)[1:, 8:8 + H], cuda(x)[2:, :H], cuda(gu), cuda(w13), cuda(w2),
+                               dx=dx[1:1 + T, 16:16 + H])
+    plain = moe.moe_ffn_backward(cuda(dout[1:, 8:8 + H].contiguous()), cuda(x[2:, :H].contiguous()), cuda(gu),
+                                 cuda(w13), cuda(w2))
+    assert all(torch.equal(a, b) for a, b in zip(got, plain))
+    want, steps = ref.ffn_backward(*(t.double() for t in (dout[1:, 8:8 + H], x[2:, :H], gu, w13, w2)))
+    for name, a, b, st in zip(("dx", "dw13", "dw2"), got, want, steps):
+        ref.check(a, b, B8, rms=ref.FLIPS, absolute=st, what=name, norm=ref.NORM)
+    dx[1:1 + T, 16:16 + H] = 5.0
+    assert bool((dx == 5).all())
+
+
+# -------------------------------------------- tiles of 256 x 256 (160 of them)
+@pytest.mark.parametrize("T,K,N", [(2400, 192, 4104), (2561, 72, 4096)])
+def test_linear_large_tiles(moe, T, K, N):
+    g = gen(T + K + N)
+    xb, w = rnd(g, T, K + 8), weight(g, N, K)
+    x = xb[:, 8:]
+    want = x.double() @ w.double().t()
+    tol = sum_tol(x.double(), w.double())
+    out = torch.full((T + 1, N + 8), 5.0, dtype=F32, device="cuda")
+    moe.moe_lora_linear(cuda(xb)[:, 8:], cuda(w), out=out[:T, :N])
+    assert bool(((out[:T, :N].double().cpu() - want).abs() <= tol).all())
+    assert bool((out[T:] == 5).all()) and bool((out[:, N:] == 5).all())
+    assert torch.equal(moe.moe_lora_linear(cuda(x.contiguous()), cuda(w)), out[:T, :N].bfloat16())
+
+
+# gate_up, down, and both in large tiles
+@pytest.mark.parametrize("T,H,I", [(2400, 136, 2056), (2400, 4104, 72), (2561, 4096, 2048)])
+def test_ffn_forward_large_tiles(moe, T, H, I):
+    g = gen(T + H + I)
+    x, w13, w2, add = rnd(g, T, H), weight(g, 2 * I, H), weight(g, H, I), rnd(g, T, H)
+    want, gu, h = ref.ffn(x.double(), w13.double(), w2.double(), add.double())
+    got, saved = moe.moe_ffn_forward(cuda(x), cuda(w13), cuda(w2), addend=cuda(add), save_gate_up=True)
+    ref.check(saved, gu, B8, rms=1e-4, what="gate_up")
+    ref.check(got, want, B8, rms=ref.FLIPS, absolute=ref.step_tol(h, w2.double()), what="out", norm=ref.NORM)
+    assert torch.equal(moe.moe_ffn_forward(cuda(x), cuda(w13), cuda(w2), addend=cuda(add)), got)
+
+
+@pytest.mark.parametrize("T,H,I", [(2400, 160, 2080), (2400, 4128, 160), (2561, 4096, 2048), (3, 64, 96), (40, 96, 160),
+                                   (130, 544, 288)])
+def test_ffn_mxfp8_large_tiles_and_strides(moe, T, H, I):
+    g = gen(T + H + I)
+    mats = []
+    for n, k, s in ((T, H, 1.0), (2 * I, H, 1 / math.sqrt(H)), (H, I, 1 / math.sqrt(I))):
+        q, sc = ref.mx_quant(rnd(g, n, k, scale=s).double())
+        mats += [q.float().to(torch.float8_e4m3fn), sc.float().to(torch.float8_e8m0fnu)]
+    add = rnd(g, T + 1, H + 16)
+    x, w13, w2 = (ref.mx_wide(mats[i].float(), mats[i + 1].float()) for i in (0, 2, 4))
+    gu = x @ w13.t()
+    h = ref.mx_wide(*ref.mx_quant(ref.silu(gu[:, :I]) * gu[:, I:]))
+    want = h @ w2.t() + add[1:, 8:8 + H].double()
+    out = torch.full((T + 2, H + 24), 5.0, dtype=BF, device="cuda")
+    moe.moe_ffn_forward_mxfp8(*(cuda(m) for m in mats), addend=cuda(add)[1:, 8:8 + H], out=out[1:1 + T, 16:16 + H])
+    ref.check(out[1:1 + T, 16:16 + H], want, B8, rms=ref.MXFLIPS, absolute=ref.step_tol(h, w2, 2.0 ** -3), what="out",
+              norm=ref.MXNORM)
+    out[1:1 + T, 16:16 + H] = 5.0
+    assert bool((out == 5).all())
+
+
+# dh in large tiles; all of the backward; dx alone in more 128 x 128 tiles than compute units
+@pytest.mark.parametrize("T,H,I,need", [(2400, 136, 4104, (True, True, True)), (2561, 1032, 4096, (True, True, True)),
+                                        (129, 16512, 256, (True, True, False))])
+def test_ffn_backward_large_tiles(moe, T, H, I, need):
+    g = gen(T + H + I)
+    dout, x, gu = rnd(g, T, H), rnd(g, T, H), rnd(g, T, 2 * I)
+    w13, w2 = weight(g, 2 * I, H), weight(g, H, I)
+    want, steps = ref.ffn_backward(*(t.double() for t in (dout, x, gu, w13, w2)))
+    got = moe.moe_ffn_backward(*(cuda(t) for t in (dout, x, gu, w13, w2)), *need)
+    for name, a, b, st, on in zip(("dx", "dw13", "dw2"), got, want, steps, need):
+        assert (a is not None) == on
+        if on:
+            ref.check(a, b, B8, rms=ref.FLIPS, absolute=st, what=name, norm=ref.NORM)
+
+
 # ------------------------------------------------------------- a block
 def _experts(moe, H, I, E, seed):
     g = gen(seed)
