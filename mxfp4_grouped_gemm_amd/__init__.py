@@ -804,15 +804,25 @@ def moe_a16w4_block(x, norm_weight, router_w, w13, w13_scale, w2, w2_scale, topk
     shared expert added to their output: shared = (w13, w2) in bf16
     (moe_ffn_forward, with its adapters), or shared_mxfp8 = (w13, w13_scale,
     w2, w2_scale) (moe_ffn_forward_mxfp8 on the norm's MXFP8 output).
+    The projection computes logits in eights: where E is no multiple of 8,
+    router_w is padded in every call, or may be given with its rows padded to
+    the next multiple (what these hold does not matter).
     -> (out bf16 [T, H], the residual for the next layer)."""
     if shared is not None and shared_mxfp8 is not None:
         raise ValueError("shared and shared_mxfp8 exclude each other")
     if shared is None and (lora13 is not None or lora2 is not None):
         raise ValueError("lora13 and lora2 belong to the bf16 shared expert")
+    E, rows = w13.shape[0], _matrix(router_w, "router_w")[0]
+    if rows not in (E, -(-E // 8) * 8):
+        raise ValueError(f"router_w has {rows} rows for {E} experts")
     with torch.cuda.device(x.device), _on(stream):
         y, res, q, qs = moe_rms_norm(x, norm_weight, residual=residual, eps=eps, weight_offset=weight_offset,
                                      mxfp8=shared_mxfp8 is not None, stream=stream)
+        if rows % 8:
+            router_w = torch.nn.functional.pad(router_w, (0, 0, 0, -E % 8))
         logits = moe_lora_linear(y, router_w, out_dtype=torch.float32, stream=stream)
+        if logits.shape[1] != E:
+            logits = logits[:, :E].contiguous()
         out = moe_a16w4_layer(y, logits, w13, w13_scale, w2, w2_scale, topk, fmt=fmt, renormalize=renormalize,
                               block_m=block_m, stream=stream)
         if shared is not None:

@@ -706,6 +706,48 @@ def test_block(moe, T, shared):
         ref.check(out, want, B8, rms=ref.FLIPS, absolute=ref.step_tol(h, w2.double()), what="out")
 
 
+@pytest.mark.parametrize("T", [1, 5, 70])
+@pytest.mark.parametrize("E,k", [(1, 1), (4, 2), (130, 3), (300, 6)])
+def test_block_any_number_of_experts(moe, T, E, k):
+    """The router takes every E that the routed layer takes, with its weights
+    as they are or already padded to eights."""
+    H, I = 256, 128
+    g = gen(T + E)
+    x, res, nw = cuda(rnd(g, T, H)), cuda(rnd(g, T, H)), cuda(rnd(g, H))
+    rw, ex = weight(g, E, H), _experts(moe, H, I, E, T)
+    sh = (cuda(weight(g, 2 * I, H)), cuda(weight(g, H, I)))
+    out, new_res = moe.moe_a16w4_block(x, nw, cuda(rw), *ex, k, residual=res, shared=sh)
+    y, ro, _, _ = moe.moe_rms_norm(x, nw, residual=res)
+    padded = torch.full(((E + 7) // 8 * 8, H), math.nan, dtype=BF)
+    padded[:E] = rw
+    logits = moe.moe_lora_linear(y, cuda(padded), out_dtype=F32)[:, :E].contiguous()
+    yd, wd = y.double().cpu(), rw.double()
+    assert bool(((logits.double().cpu() - yd @ wd.t()).abs() <= sum_tol(yd, wd)).all())
+    want = moe.moe_ffn_forward(y, *sh, addend=moe.moe_a16w4_layer(y, logits, *ex, k))
+    assert torch.equal(out, want) and torch.equal(new_res, ro)
+    again, _ = moe.moe_a16w4_block(x, nw, cuda(padded), *ex, k, residual=res, shared=sh)
+    assert torch.equal(again, want)
+
+
+def test_block_refuses_a_router_of_other_experts(moe):
+    H, I, E, T = 256, 128, 12, 3
+    x, nw = cuda(rnd(gen(1), T, H)), cuda(rnd(gen(2), H))
+    ex = _experts(moe, H, I, E, T)
+    for rows in (8, 11, 13, 24):
+        with pytest.raises(ValueError, match="router_w"):
+            moe.moe_a16w4_block(x, nw, cuda(weight(gen(3), rows, H)), *ex, 2)
+
+
+def test_block_of_no_tokens(moe):
+    H, I, E = 256, 128, 5
+    x, res, nw = (torch.empty(0, H, dtype=BF, device="cuda") for _ in range(3))
+    nw = torch.ones(H, dtype=BF, device="cuda")
+    ex = _experts(moe, H, I, E, 1)
+    sh = tuple(torch.ones(s, dtype=BF, device="cuda") for s in ((2 * I, H), (H, I)))
+    out, new_res = moe.moe_a16w4_block(x, nw, torch.ones(E, H, dtype=BF, device="cuda"), *ex, 2, residual=res, shared=sh)
+    assert out.shape == (0, H) and new_res.shape == (0, H)
+
+
 # ---------------------------------------------- streams, graphs, two at once
 def test_block_in_a_graph(moe):
     """Captured once and replayed, with new inputs and eager work between the
