@@ -797,13 +797,15 @@ def moe_ffn(x, w13, w2, addend=None):
 
 def moe_a16w4_block(x, norm_weight, router_w, w13, w13_scale, w2, w2_scale, topk, residual=None, eps=1e-6,
                     weight_offset=0.0, shared=None, shared_mxfp8=None, lora13=None, lora2=None,
-                    renormalize=True, fmt=MOE_W_MXFP4, block_m=None, stream=None):
+                    renormalize=True, fmt=MOE_W_MXFP4, block_m=None, stream=None, w13_bias=None, w2_bias=None,
+                    swiglu_limit=0.0):
     """The feed-forward half of a decoder layer on one stream: residual
     addition and norm (moe_rms_norm), router logits (moe_lora_linear in fp32
-    with router_w bf16 [E, H]), the routed experts (moe_a16w4_layer) and the
-    shared expert added to their output: shared = (w13, w2) in bf16
-    (moe_ffn_forward, with its adapters), or shared_mxfp8 = (w13, w13_scale,
-    w2, w2_scale) (moe_ffn_forward_mxfp8 on the norm's MXFP8 output).
+    with router_w bf16 [E, H]), the routed experts (moe_a16w4_layer, with the
+    expert biases and the clamp if given) and the shared expert added to their
+    output: shared = (w13, w2) in bf16 (moe_ffn_forward, with its adapters), or
+    shared_mxfp8 = (w13, w13_scale, w2, w2_scale) (moe_ffn_forward_mxfp8 on the
+    norm's MXFP8 output).
     The projection computes logits in eights: where E is no multiple of 8,
     router_w is padded in every call, or may be given with its rows padded to
     the next multiple (what these hold does not matter).
@@ -824,7 +826,8 @@ def moe_a16w4_block(x, norm_weight, router_w, w13, w13_scale, w2, w2_scale, topk
         if logits.shape[1] != E:
             logits = logits[:, :E].contiguous()
         out = moe_a16w4_layer(y, logits, w13, w13_scale, w2, w2_scale, topk, fmt=fmt, renormalize=renormalize,
-                              block_m=block_m, stream=stream)
+                              block_m=block_m, stream=stream, w13_bias=w13_bias, w2_bias=w2_bias,
+                              swiglu_limit=swiglu_limit)
         if shared is not None:
             out = moe_ffn_forward(y, *shared, addend=out, out=out, lora13=lora13, lora2=lora2, stream=stream)
         elif shared_mxfp8 is not None:

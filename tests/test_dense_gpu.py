@@ -738,6 +738,22 @@ def test_block_refuses_a_router_of_other_experts(moe):
             moe.moe_a16w4_block(x, nw, cuda(weight(gen(3), rows, H)), *ex, 2)
 
 
+@pytest.mark.parametrize("T", [1, 5, 70])
+def test_block_biases_and_limit(moe, T):
+    H, I, E, k = 256, 128, 8, 2
+    g = gen(T)
+    x, nw, rw, ex = cuda(rnd(g, T, H)), cuda(rnd(g, H)), cuda(weight(g, E, H)), _experts(moe, H, I, E, T)
+    sh = (cuda(weight(g, 2 * I, H)), cuda(weight(g, H, I)))
+    kw = dict(w13_bias=cuda(rnd(g, E, 2 * I)), w2_bias=cuda(rnd(g, E, H)), swiglu_limit=1.5)
+    out, _ = moe.moe_a16w4_block(x, nw, rw, *ex, k, shared=sh, **kw)
+    y = moe.moe_rms_norm(x, nw)[0]
+    logits = moe.moe_lora_linear(y, rw, out_dtype=F32)
+    assert torch.equal(out, moe.moe_ffn_forward(y, *sh, addend=moe.moe_a16w4_layer(y, logits, *ex, k, **kw)))
+    for name in kw:  # each of them takes part
+        other, _ = moe.moe_a16w4_block(x, nw, rw, *ex, k, shared=sh, **{n: v for n, v in kw.items() if n != name})
+        assert not torch.equal(other, out)
+
+
 def test_block_of_no_tokens(moe):
     H, I, E = 256, 128, 5
     x, res, nw = (torch.empty(0, H, dtype=BF, device="cuda") for _ in range(3))
