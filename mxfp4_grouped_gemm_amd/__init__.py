@@ -452,6 +452,10 @@ def requantize_mxfp4_experts(w, scale_e8m0, chunk=8, stream=None):
 
 # ---------------------------------------------------------------------------
 # Dense operators around the routed experts.
+#
+# moe_ffn is the one that autograd sees. The others compute and record nothing,
+# as the routed layer does: what they return has no graph, also for inputs that
+# require gradients.
 
 class LoraAdapters(NamedTuple):
     """A stack of low-rank adapters beside one projection [N, K]: token t adds
@@ -591,7 +595,8 @@ def moe_rms_norm(x, weight, residual=None, eps=1e-6, weight_offset=0.0, mxfp8=Fa
     residual bf16 or fp32 [T, H] (None: s = x, and no residual_out unless a
     buffer is given); weight bf16 or fp32 [H]. mxfp8: also the MXFP8 output,
     for moe_ffn_forward_mxfp8. -> (y bf16, residual_out of residual's type or
-    None, q float8_e4m3fn or None, q_scale float8_e8m0fnu [T, H/32] or None).
+    None, q float8_e4m3fn or None, q_scale float8_e8m0fnu [T, H/32] or None),
+    without a graph for gradients.
     Buffers may be given; y=x and residual_out=residual work in place."""
     T, H = _matrix(x, "x")
     device = x.device
@@ -637,7 +642,8 @@ def moe_lora_linear_workspace_size(T, K, N, rank=0) -> int:
 def moe_lora_linear(x, w, lora=None, out_dtype=torch.bfloat16, out=None, workspace=None, stream=None):
     """x bf16 [T, K] times w bf16 [N, K] transposed, plus each token's low-rank
     adapter (LoraAdapters, or a tuple of its fields) -> out [T, N] in bf16 or
-    fp32 (without adapters and in fp32: a router's logits)."""
+    fp32 (without adapters and in fp32: a router's logits), without a graph for
+    gradients."""
     T, K = _matrix(x, "x")
     N = _matrix(w, "w")[0]
     device = x.device
@@ -674,7 +680,8 @@ def moe_ffn_forward(x, w13, w2, addend=None, lora13=None, lora2=None, save_gate_
     h = silu(gate) * up, out = w2 h (+ addend). x bf16 [T, H], w13 bf16
     [2I, H], w2 bf16 [H, I], addend bf16 [T, H]; lora13 / lora2: adapters of
     the two projections. save_gate_up (or a gate_up buffer): -> (out, gate_up
-    bf16 [T, 2I], what moe_ffn_backward needs), else out."""
+    bf16 [T, 2I], what moe_ffn_backward needs), else out. No graph is recorded
+    for gradients: moe_ffn does that (without adapters)."""
     T, H, I = _ffn_sizes(x, w13, w2)
     device = x.device
     px, ldx = _rows(x, "x", torch.bfloat16, (T, H), device)
@@ -706,7 +713,8 @@ def moe_ffn_forward_mxfp8(x, x_scale, w13, w13_scale, w2, w2_scale, addend=None,
                           out=None, workspace=None, stream=None):
     """moe_ffn_forward with MXFP8 activations and weights: codes e4m3 x [T, H],
     w13 [2I, H], w2 [H, I] (float8_e4m3fn or uint8) and e8m0 scales [rows,
-    columns / 32] (float8_e8m0fnu or uint8) -> out bf16 [T, H]."""
+    columns / 32] (float8_e8m0fnu or uint8) -> out bf16 [T, H], without a graph
+    for gradients."""
     T, H, I = _ffn_sizes(x, w13, w2)
     device = x.device
     if H % 32 or I % 32:
@@ -791,7 +799,8 @@ class _Ffn(torch.autograd.Function):
 def moe_ffn(x, w13, w2, addend=None):
     """The shared expert as a differentiable function of bf16 x [T, H], w13
     [2I, H], w2 [H, I] and addend [T, H]: moe_ffn_forward, with
-    moe_ffn_backward for the gradients that are asked for."""
+    moe_ffn_backward for the gradients that are asked for. There is no second
+    derivative, and there are no gradients of adapters."""
     return _Ffn.apply(x, w13, w2, addend)
 
 
@@ -809,7 +818,8 @@ def moe_a16w4_block(x, norm_weight, router_w, w13, w13_scale, w2, w2_scale, topk
     The projection computes logits in eights: where E is no multiple of 8,
     router_w is padded in every call, or may be given with its rows padded to
     the next multiple (what these hold does not matter).
-    -> (out bf16 [T, H], the residual for the next layer)."""
+    -> (out bf16 [T, H], the residual for the next layer), without a graph for
+    gradients (of its parts only the bf16 shared expert has one: moe_ffn)."""
     if shared is not None and shared_mxfp8 is not None:
         raise ValueError("shared and shared_mxfp8 exclude each other")
     if shared is None and (lora13 is not None or lora2 is not None):
