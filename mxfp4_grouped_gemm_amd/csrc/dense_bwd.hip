@@ -79,7 +79,10 @@ static hipError_t launch_split(const DenseArgs& a, hipStream_t s) {
 template <int E>
 static hipError_t launch_nn(const DenseArgs& a, hipStream_t s) {
     if (a.splits > 1) return launch_split<E>(a, s);
-    if (dense_big_tiles(a, E)) return launch_tile<Tile<256, 256, 2, 4, false, true, kEltBf16, E, false, false>>(a, s);
+    // (A dx of so many tiles shares a grid with the weights' gradients.)
+    if constexpr (E == kEpiGatedBwd) {
+        if (dense_big_tiles(a, E)) return launch_tile<Tile<256, 256, 2, 4, false, true, kEltBf16, E, false, false>>(a, s);
+    }
     if (!dense_one_round(a, E)) return launch_tile<Tile<128, 128, 2, 2, false, true, kEltBf16, E, false, false>>(a, s);
     // Too few 128 x 128 tiles for half of the compute units: 64 x 64 ones.
     if (square_tiles(a, 128) < 128)
