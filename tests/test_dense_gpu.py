@@ -764,6 +764,70 @@ def test_block_of_no_tokens(moe):
     assert out.shape == (0, H) and new_res.shape == (0, H)
 
 
+# --------------------------------------------------- the ends of the ranges
+@pytest.mark.parametrize("T", [0, 3, 70])
+def test_linear_weights_above_2_gib(moe, T):
+    """Rows that 32-bit byte offsets from the first do not reach."""
+    K, N = 8192, 152064
+    dev = torch.Generator(device="cuda").manual_seed(T)
+    w = torch.empty(N, K, dtype=BF, device="cuda").normal_(0, 1 / math.sqrt(K), generator=dev)
+    x = torch.randn(T, K, generator=dev, device="cuda").bfloat16()
+    got = moe.moe_lora_linear(x, w, out_dtype=F32)
+    assert got.shape == (T, N)
+    for rows in (slice(0, 40), slice(131040, 131110), slice(N - 40, N)):  # 131072 rows are 2 GiB
+        xd, wd = x.double().cpu(), w[rows].double().cpu()
+        assert bool(((got[:, rows].double().cpu() - xd @ wd.t()).abs() <= sum_tol(xd, wd)).all())
+
+
+@pytest.mark.parametrize("n", [0, 5])
+def test_linear_tokens_above_2_gib(moe, n):
+    T, K, N = 140001, 8192, 72
+    dev = torch.Generator(device="cuda").manual_seed(n)
+    x = torch.empty(T, K, dtype=BF, device="cuda").normal_(0, 1, generator=dev)
+    w = weight(gen(1), N, K)
+    lo = adapters(gen(2), T, K, N, n, 16, ranks=False) if n else None
+    got = moe.moe_lora_linear(x, cuda(w), lora=cuda(lo), out_dtype=F32)
+    for rows in (slice(0, 40), slice(131040, 131110), slice(T - 40, T)):
+        xd, wd = x[rows].double().cpu(), w.double()
+        want, tol = xd @ wd.t(), sum_tol(xd, wd)
+        if n:
+            part = (lo[0], lo[1], lo[2][rows], None, lo[4])
+            want += ref.lora(xd, part)
+            tol += ref.lora(xd.abs(), (lo[0].double().abs(), lo[1].double().abs(), *part[2:])) * (2.0 ** -16 + (K / 8 + 128) * F24)
+        assert bool(((got[rows].double().cpu() - want).abs() <= tol).all())
+
+
+def test_norm_above_4_gib(moe):
+    T, H = 530001, 4128
+    x = torch.empty(T, H, dtype=BF, device="cuda").normal_(0, 1, generator=torch.Generator(device="cuda").manual_seed(1))
+    w = rnd(gen(1), H)
+    y, _, q, qs = moe.moe_rms_norm(x, cuda(w), mxfp8=True)
+    for rows in (slice(0, 3), slice(260110, 260120), slice(520220, 520230), slice(T - 3, T)):  # of 2 and 4 GiB
+        _, v = ref.norm(x[rows].double().cpu(), None, w.double(), 1e-6, 0.0)
+        ref.check(y[rows], v, B8 * 1.01, what="y")
+        want, scale = ref.mx_quant(v)
+        assert torch.equal(qs[rows].double().cpu(), scale) and torch.equal(q[rows].double().cpu(), want)
+
+
+@pytest.mark.parametrize("T,K,N", [(1, 72, 40), (5, 1032, 264), (40, 1032, 264), (70, 72, 2056), (200, 1032, 264), (300, 264, 4104),
+                                   (700, 264, 520)])
+def test_linear_adapters_of_the_largest_rank(moe, T, K, N):
+    g = gen(T + K + N)
+    n, rank = 4, 256
+    x, w = rnd(g, T, K), weight(g, N, K)
+    lo = adapters(g, T, K, N, n, rank)
+    lo[3][0], lo[3][1] = 256, 255
+    for i in range(n):
+        lo[0][i, int(lo[3][i]):] = math.nan
+        lo[1][i, :, int(lo[3][i]):] = math.inf
+    xd = x.double()
+    want = xd @ w.double().t() + ref.lora(xd, lo)
+    wide = tuple(t if t is None or not t.is_floating_point() else torch.nan_to_num(t.double(), 0, 0, 0).abs() for t in lo)
+    tol = sum_tol(xd, w.double()) + ref.lora(xd.abs(), wide) * (2.0 ** -16 + (K / 8 + 256) * F24)
+    got = moe.moe_lora_linear(cuda(x), cuda(w), lora=cuda(lo), out_dtype=F32)
+    assert bool(((got.double().cpu() - want).abs() <= tol).all())
+
+
 # ---------------------------------------------- streams, graphs, two at once
 def test_block_in_a_graph(moe):
     """Captured once and replayed, with new inputs and eager work between the
@@ -821,6 +885,35 @@ def test_backward_in_a_graph(moe):
         gr.replay()
         torch.cuda.synchronize()
         want = moe.moe_ffn_backward(dout, x, gu, w13, w2)
+        assert all(torch.equal(a, b) for a, b in zip(o, want))
+
+
+def test_gradients_in_a_graph(moe):
+    """Forward and gradients of the differentiable form captured together."""
+    g = gen(4)
+    T, H, I = 130, 136, 264
+    x, probe = cuda(rnd(g, T, H)).requires_grad_(), cuda(rnd(g, T, H))
+    w13, w2 = cuda(weight(g, 2 * I, H)).requires_grad_(), cuda(weight(g, H, I)).requires_grad_()
+
+    def step():
+        out = moe.moe_ffn(x, w13, w2)
+        return (out.detach(), *torch.autograd.grad(out, (x, w13, w2), probe))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        o = step()
+    for _ in range(3):
+        with torch.no_grad():
+            x.copy_(cuda(rnd(g, T, H)))
+            probe.copy_(cuda(rnd(g, T, H)))
+        gr.replay()
+        torch.cuda.synchronize()
+        want = step()
         assert all(torch.equal(a, b) for a, b in zip(o, want))
 
 
