@@ -1,7 +1,8 @@
 // The backward of the gated block: dh = dout W2 with the activation's backward
 // as its epilogue, and then dx and the two weight gradients in one launch.
 // 8192 tokens, H = 3584, I = 2048: dh 118 to 130 us, the gradients 463 (1.30
-// PFLOP/s; matrix cores busy 78% of the time).
+// PFLOP/s; matrix cores busy 78% of the time). Called in a loop over three sets of inputs
+// the backward takes 577 us, the library's four plain products 720.
 #include "dense_tile.hpp"
 
 namespace moe {

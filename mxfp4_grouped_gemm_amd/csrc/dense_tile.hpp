@@ -11,11 +11,15 @@
 // second workgroup to hide a load behind: they run with four buffers (64 x 64
 // tiles with eight), three (seven) steps of loads in flight.
 //
-// Bound by the matrix cores, at the 1.9 GHz that their power leaves: in tiles of
-// 256 x 256 they are busy 50 to 78% of the time. 8192 tokens: gated, 4096 pairs
+// Tiles of 256 x 256 have the matrix cores busy for 60 and 55% of the time in the
+// two products of the forward, 53 and 41% in MXFP8, 49% in dh and 78% in the
+// gradients, at the clock that their power leaves (1.9 GHz in a long run); what
+// the rest waits for has not been parted. 8192 tokens: gated, 4096 pairs
 // over K = 3584, 336 us in a long run of this call alone (1.43 PFLOP/s of
 // bf16); 3584 columns over K = 4096, 178 us (1.35); the library's plain
-// products of these sizes take 321 and 169 there. MFMAs of 32 x 32 were slower:
+// products of these sizes take 321 and 169 there. One after the other, over
+// three sets of inputs, both take 607 to 620 us with their epilogues, the library's two
+// products alone 483. MFMAs of 32 x 32 were slower:
 // the same LDS bytes, and fewer, longer instructions to place reads between.
 //
 // W is the MFMA's first operand, so a lane's four results are four
