@@ -10,9 +10,12 @@ namespace moe {
 // exponent and mantissa bits of amax, so no rounding decides it. amax = m 2^e
 // with m in [1, 2): 448 = 1.75 * 2^8, so s = 2^(e-8) up to m = 1.75, else
 // 2^(e-7). Bytes are clamped at 0 (2^-127; an all-zero block has byte 0).
-__device__ __forceinline__ uint32_t mx8_scale_byte(float amax) {
+// above: the magnitude is above amax by what amax was rounded off by, which
+// counts where amax is at the border itself.
+__device__ __forceinline__ bool mx8_at_border(float amax) { return (__float_as_uint(amax) & 0x7fffffu) == 0x600000u; }
+__device__ __forceinline__ uint32_t mx8_scale_byte(float amax, bool above = false) {
     const uint32_t b = __float_as_uint(amax);
-    const int e = (int)(b >> 23) - 8 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);
+    const int e = (int)(b >> 23) - 8 + ((b & 0x7fffffu) > 0x600000u || (above && mx8_at_border(amax)) ? 1 : 0);
     return (uint32_t)(e < 0 ? 0 : e);
 }
 

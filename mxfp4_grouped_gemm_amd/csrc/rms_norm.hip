@@ -6,7 +6,7 @@
 // fp32 number nearest to the exact product with what it was rounded off by,
 // and s carries what a sum with an fp32 residual was rounded off by: a code
 // changes where v crosses a tie, which an error of 1e-7 does for one element
-// in a million (eights of squares in fp32 were worth 0.7 us at 1531 rows of
+// in a million, and a scale where the block's largest crosses the border of two (eights of squares in fp32 were worth 0.7 us at 1531 rows of
 // 2784, which take 12, and changed single codes). y and q are each rounded once from v.
 //
 // Bound by memory: 8 bytes an element with bf16 streams, about 9 with the
@@ -232,7 +232,17 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void rms_norm_kernel
             for (int e = 0; e < 8; ++e) m = fmaxf(m, mx8_finite_abs(v[e]));
             m = fmaxf(m, dpp<0xB1>(m));
             m = fmaxf(m, dpp<0x4E>(m));
-            const uint32_t b = mx8_scale_byte(m);
+            // A maximum that rounds to the border of two scales goes by its rest
+            // (the four lanes have the same m).
+            float above = 0.0f;
+            if (mx8_at_border(m)) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    above = fabsf(v[e]) == m && p[e].rest != 0.0f && (p[e].rest > 0.0f) == (v[e] > 0.0f) ? 1.0f : above;
+                above = fmaxf(above, dpp<0xB1>(above));
+                above = fmaxf(above, dpp<0x4E>(above));
+            }
+            const uint32_t b = mx8_scale_byte(m, above > 0.0f);
             const float inv = mx8_inv_scale(b);
             u32x2 o;
             bool ties = false;

@@ -141,6 +141,44 @@ def test_norm_codes_are_exact(moe, H, res):
     assert torch.equal(q.double().cpu(), want)
 
 
+def _just_above_448():
+    """(s, w, eps) with mean and eps such that r = 1/2 exactly and s w / 2 is
+    above 1.75 by less than half an fp32 step there, so that it rounds to it."""
+    for m in range(129, 256):
+        s = m / 128  # a bf16 number
+        w = torch.tensor(3.5 / s, dtype=torch.float64).float().double()
+        for w in (w, torch.nextafter(w.float(), torch.tensor(9.0)).double()):
+            if 0 < float(s * w / 2) - 1.75 < 2.0 ** -24:
+                yield s, float(w)
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("far", [0, 31])
+def test_norm_scale_of_a_value_that_rounds_to_the_border(moe, sign, far):
+    """The largest e4m3 is 448 = 1.75 * 2^8: a block whose exact maximum is
+    above 1.75 takes the next scale, though its fp32 number is 1.75."""
+    H, seen = 64, 0
+    for s, w in _just_above_448():
+        x, wt = torch.ones(1, H), torch.full((H,), 0.25)
+        x[0, 32 + far], wt[32 + far] = s * sign, w
+        eps = 4 - float(x.double().square().mean())
+        assert torch.tensor(eps).double() == eps
+        _, v = ref.norm(x.double(), None, wt.double(), eps, 0.0)
+        assert float(v.abs().max()) > 1.75 and float(v.abs().max().float()) == 1.75
+        want, scale = ref.mx_quant(v)
+        _, _, q, qs = moe.moe_rms_norm(cuda(x.bfloat16()), cuda(wt), eps=eps, mxfp8=True)
+        assert torch.equal(qs.double().cpu(), scale) and torch.equal(q.double().cpu(), want), (s, w)
+        # and not above: the smaller scale
+        wt[32 + far] = 1.75 / (s / 2)
+        _, v = ref.norm(x.double(), None, wt.double(), eps, 0.0)
+        if float(v.abs().max()) <= 1.75:
+            want, scale = ref.mx_quant(v)
+            _, _, q, qs = moe.moe_rms_norm(cuda(x.bfloat16()), cuda(wt), eps=eps, mxfp8=True)
+            assert torch.equal(qs.double().cpu(), scale) and torch.equal(q.double().cpu(), want), (s, w)
+        seen += 1
+    assert seen >= 5
+
+
 def test_norm_special_values(moe):
     H = 64
     x = torch.zeros(6, H)
