@@ -45,14 +45,16 @@ __device__ __forceinline__ Product product3(float s, float sl, float rh, float r
     return {fine ? n : v, fine ? (v - n) + ev : 0.0f};
 }
 
-// Halfway between two e4m3 codes of the normal range.
-__device__ __forceinline__ bool tie(float z) { return (__float_as_uint(z) & 0xfffffu) == 0x80000u; }
+// Whether z can be halfway between two e4m3 codes: ties have four mantissa bits
+// in the normal range and at most three below 2^-6.
+__device__ __forceinline__ bool may_tie(float z) { return (__float_as_uint(z) & 0x7ffffu) == 0u; }
 
-// z = v * inv for its e4m3 code: a tie goes by the rest that v was rounded
-// off by.
+// z = v * inv for its e4m3 code: a tie goes by the rest that v was rounded off
+// by, one step of z towards it. (A code, or a number between code and tie, is
+// rounded as before from there.)
 __device__ __forceinline__ float settle(float z, float rest) {
-    const uint32_t step = (rest > 0.0f) == (z > 0.0f) ? 1u : 0xffffffffu;
-    return tie(z) && rest != 0.0f ? __uint_as_float(__float_as_uint(z) + step) : z;
+    const int step = ((int)(__float_as_uint(z) ^ __float_as_uint(rest)) >> 31) | 1;
+    return may_tie(z) && rest != 0.0f && z != 0.0f ? __uint_as_float(__float_as_uint(z) + (uint32_t)step) : z;
 }
 
 template <int CTRL>
@@ -249,7 +251,7 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void rms_norm_kernel
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 v[e] *= inv;
-                ties |= tie(v[e]);
+                ties |= may_tie(v[e]);
             }
             if (ties) {
 #pragma unroll

@@ -142,8 +142,8 @@ def test_norm_codes_are_exact(moe, H, res):
 
 
 def _just_above_448():
-    """(s, w, eps) with mean and eps such that r = 1/2 exactly and s w / 2 is
-    above 1.75 by less than half an fp32 step there, so that it rounds to it."""
+    """(s, w) with s w / 2 above 1.75 by less than half an fp32 step there, so
+    that it rounds to it."""
     for m in range(129, 256):
         s = m / 128  # a bf16 number
         w = torch.tensor(3.5 / s, dtype=torch.float64).float().double()
@@ -177,6 +177,33 @@ def test_norm_scale_of_a_value_that_rounds_to_the_border(moe, sign, far):
             assert torch.equal(qs.double().cpu(), scale) and torch.equal(q.double().cpu(), want), (s, w)
         seen += 1
     assert seen >= 5
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("k", [-10, -9, -8, -7, -6, -5, 0, 4])
+def test_norm_codes_next_to_ties(moe, sign, k):
+    """Exact values next to a tie of two codes that round to it in fp32, in the
+    normal range of e4m3 (2^-6 and more) and below it (steps of 2^-9). r = 1/2
+    exactly, and the block's scale is 1."""
+    H, seen = 64, 0
+    x, wt = torch.ones(1, H), torch.full((H,), 1.0)
+    wt[32] = 2.0 * 448
+    step = 2.0 ** (max(k, -6) - 3)
+    for n in range(int(2.0 ** k / step), int(2.0 ** (k + 1) / step)) if k > -10 else [0]:
+        tie = (n + 0.5) * step  # its fp32 neighbours are 2^-24 of it or more apart
+        for m in range(129, 256, 2):
+            s = m / 128
+            w = float(torch.tensor(2 * tie / s, dtype=torch.float64).float())
+            v = s * w / 2  # 8 and 24 bits: exact in fp64
+            if v != tie and float(torch.tensor(v, dtype=torch.float64).float()) == tie:
+                x[0, 40], wt[40] = s * sign, w
+                eps = 4 - float(x.double().square().mean())
+                _, v = ref.norm(x.double(), None, wt.double(), eps, 0.0)
+                want, scale = ref.mx_quant(v)
+                _, _, q, qs = moe.moe_rms_norm(cuda(x.bfloat16()), cuda(wt), eps=eps, mxfp8=True)
+                assert torch.equal(qs.double().cpu(), scale) and torch.equal(q.double().cpu(), want), (n, s, w)
+                seen += 1
+    assert seen >= 3
 
 
 def test_norm_special_values(moe):
