@@ -12,8 +12,8 @@
 // Bound by memory: 8 bytes an element with bf16 streams, about 9 with the
 // MXFP8 output. A row is read once and stays in registers between the sum and
 // the outputs. Every element is read and written by one lane, so outputs may
-// be the inputs' own buffers. 16384 rows of 3584 with both outputs take 90 us,
-// 5.9 TB/s (a plain copy of 1 GiB: 5.1). Streaming stores count in that
+// be the inputs' own buffers. 16384 rows of 3584 with both outputs take 91 us,
+// 5.8 TB/s (a plain copy of 1 GiB: 5.1). Streaming stores count in that
 // (ordinary ones: 95 us), and four waves a row (a wave a row, with 56 elements
 // a lane: 117 us with ordinary stores). Rows at any element address: 19248 of
 // 2794, bf16 residual and output, 109 us (element by element: 200).
