@@ -6,8 +6,9 @@
 // fp32 number nearest to the exact product with what it was rounded off by,
 // and s carries what a sum with an fp32 residual was rounded off by: a code
 // changes where v crosses a tie, which an error of 1e-7 does for one element
-// in a million, and a scale where the block's largest crosses the border of two (eights of squares in fp32 were worth 0.7 us at 1531 rows of
-// 2784, which take 12, and changed single codes). y and q are each rounded once from v.
+// in a million, and a scale where the block's largest crosses the border of
+// two (eights of squares in fp32 were worth 0.7 us at 1531 rows of 2784, which
+// take 12, and changed single codes). y and q are each rounded once from v.
 //
 // Bound by memory: 8 bytes an element with bf16 streams, about 9 with the
 // MXFP8 output. A row is read once and stays in registers between the sum and
