@@ -295,7 +295,7 @@ moe_status mxfp4_to_int4g32_requant(const uint8_t* w, const uint8_t* scale_e8m0,
  * invalid sizes), 256-byte aligned; it is scratch for that call alone. Unless
  * stated otherwise, outputs must not overlap inputs or each other.
  * ------------------------------------------------------------------------ */
-typedef enum { MOE_DT_BF16 = 0, MOE_DT_F32 = 1 } moe_dtype;
+typedef enum { MOE_DT_BF16 = 0, MOE_DT_F32 = 1, MOE_DT_U8 = 2 /* bytes; moe_permute alone */ } moe_dtype;
 
 /* Residual addition and RMS norm of token rows:
  *   s = x + residual (s = x when residual is NULL)
@@ -408,6 +408,141 @@ moe_status moe_ffn_backward(const uint16_t* dout, int64_t dout_stride, const uin
                             const uint16_t* w2, moe_act act, int T, int H, int I, uint16_t* dx,
                             int64_t dx_stride, uint16_t* dw13, uint16_t* dw2, void* workspace,
                             size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Operators of a trainable expert block: layer norm, tokens sorted by expert
+ * and back, and the product with bias, activation and addend, each with its
+ * backward pass. The rules of the dense operators hold.
+ * ------------------------------------------------------------------------ */
+
+/* Residual addition and layer norm of token rows:
+ *   s = x + residual (s = x when residual is NULL)
+ *   n = (s - mean(s)) * r,  r = 1 / sqrt(mean((s - mean(s))^2) + eps)
+ *   residual_out = s;  y = n * weight + bias;  mean, rstd = mean(s), r.
+ *   x             bf16 [T, H]; residual [T, H] of residual_type, or NULL.
+ *   weight, bias  [H] of weight_type; bias may be NULL (0).
+ *   residual_out  out [T, H] of residual_type, or NULL.
+ *   y             out bf16 [T, H], or NULL.
+ *   mean, rstd    out fp32 [T], both or neither: for the backward pass.
+ * At least one output is required. 1 <= H <= 65536. Pointers need their
+ * element's alignment only (rows that are 16-byte aligned are faster). An output
+ * may be an input's own buffer with the same row stride and element size (y = x,
+ * residual_out = residual). eps must be >= 0 and finite. Sums are fp64. */
+moe_status moe_layer_norm_forward(const uint16_t* x, int64_t x_stride, const void* residual,
+                                  int64_t residual_stride, moe_dtype residual_type,
+                                  const void* weight, const void* bias, moe_dtype weight_type,
+                                  float eps, int T, int H, void* residual_out,
+                                  int64_t residual_out_stride, uint16_t* y, int64_t y_stride,
+                                  float* mean, float* rstd, void* stream);
+
+/* Its backward from s, mean and rstd, with n as above (of this s) and g = dy * weight:
+ *   ds = rstd * (g - mean(g) - n * mean(g * n)) + dresidual_out
+ *   dweight = sum over rows of dy * n;  dbias = sum over rows of dy.
+ * ds is the gradient of x and of the residual alike.
+ *   dy       bf16 [T, H];  s [T, H] of s_type (the forward's residual_out, or x).
+ *   dresidual_out  [T, H] of s_type: the gradient of residual_out, or NULL.
+ *   dx       out bf16 [T, H]: ds, or NULL;  dresidual  out [T, H] of s_type: ds, or NULL.
+ *   dweight, dbias  out [H] of weight_type, each may be NULL; overwritten, and
+ *            no sum depends on the order of atomics.
+ * At least one output is required unless T == 0 (dweight and dbias are then
+ * zeros). The workspace is needed for dweight or dbias. */
+int64_t moe_layer_norm_backward_workspace_size(int T, int H);
+moe_status moe_layer_norm_backward(const uint16_t* dy, int64_t dy_stride, const void* s,
+                                   int64_t s_stride, moe_dtype s_type, const float* mean,
+                                   const float* rstd, const void* weight, moe_dtype weight_type,
+                                   const void* dresidual_out, int64_t dresidual_out_stride, int T,
+                                   int H, uint16_t* dx, int64_t dx_stride, void* dresidual,
+                                   int64_t dresidual_stride, void* dweight, void* dbias,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+
+/* Token rows sorted by expert, without padding: pair p = t * topk + j of token t
+ * goes to the row that a stable sort of the pairs by expert gives it.
+ *   x               [T, H] of type (MOE_DT_U8: 8-bit codes or scales).
+ *   topk_ids        int32 [T, topk]; ids outside [0, E) are no expert's: their
+ *                   pairs come after all others. An expert may be chosen twice.
+ *   out             out [T * topk, H]: out[row(p)] = x[t]; rows of no expert
+ *                   (from expert_offsets[E] on) are zeros.
+ *   rows            out int32 [T, topk]: row(p), or -1 - row(p) for a pair of no
+ *                   expert.
+ *   expert_offsets  out int32 [E + 1]: first row of each expert, and their end.
+ * 1 <= E <= 1024, 1 <= topk <= 64, 1 <= H <= 2^18, T <= 2^22. T == 0 writes
+ * expert_offsets (zeros). Pointers need their element's alignment only. The
+ * gradient of x is moe_unpermute of the gradient of out, without weights; other
+ * rows by the same order: moe_unpermute_backward without weights and y. */
+int64_t moe_permute_workspace_size(int T, int topk, int E);
+moe_status moe_permute(const void* x, int64_t x_stride, moe_dtype type, const int32_t* topk_ids,
+                       int T, int topk, int E, int H, void* out, int64_t out_stride, int32_t* rows,
+                       int32_t* expert_offsets, void* workspace, size_t workspace_bytes,
+                       void* stream);
+
+/* Sorted rows back to their tokens: out[t] = residual[t] + the sum over j
+ * (ascending, fp32) of weights[t, j] * y[rows[t, j]].
+ *   y        [T * topk, H] of y_type (bf16 or fp32).
+ *   rows     int32 [T, topk] of moe_permute; a negative entry (or one past the
+ *            last row) adds nothing, whatever its weight.
+ *   weights  fp32 [T, topk], or NULL (1).
+ *   residual [T, H] of out_type, or NULL; may be out itself.
+ *   out      out [T, H] of out_type (bf16 or fp32).
+ * Sizes as moe_permute. */
+moe_status moe_unpermute(const void* y, int64_t y_stride, moe_dtype y_type, const int32_t* rows,
+                         const float* weights, const void* residual, int64_t residual_stride, int T,
+                         int topk, int H, void* out, int64_t out_stride, moe_dtype out_type,
+                         void* stream);
+
+/* Its gradients (that of residual is dout itself):
+ *   dy[rows[t, j]] = weights[t, j] * dout[t], zeros in the rows of no expert;
+ *   dweights[t, j] = <dout[t], y[rows[t, j]]>, 0 for pairs of no expert.
+ *   dout [T, H] of out_type;  dy out [T * topk, H] of y_type, or NULL;
+ *   dweights out fp32 [T, topk], or NULL (y is read for it alone).
+ * Entries of rows whose row (-1 - entry for a negative one) is not in
+ * [0, T * topk) are skipped. */
+moe_status moe_unpermute_backward(const void* dout, int64_t dout_stride, moe_dtype out_type,
+                                  const int32_t* rows, const float* weights, const void* y,
+                                  int64_t y_stride, moe_dtype y_type, int T, int topk, int H,
+                                  void* dy, int64_t dy_stride, float* dweights, void* stream);
+
+/* Activations of moe_linear_forward: z, max(z, 0), z / (1 + exp(-z)),
+ * z Phi(z) with the normal distribution Phi, and its tanh form
+ * z / (1 + exp(-2 sqrt(2 / pi) (z + 0.044715 z^3))). */
+typedef enum {
+    MOE_LINEAR_NONE = 0,
+    MOE_LINEAR_RELU = 1,
+    MOE_LINEAR_SILU = 2,
+    MOE_LINEAR_GELU = 3,
+    MOE_LINEAR_GELU_TANH = 4
+} moe_linear_act;
+
+/* Product with bias, activation and addend: z = W x + bias, out = act(z) + addend.
+ *   x       bf16 [T, K];  w bf16 [N, K];  bias [N] of bias_type, or NULL.
+ *   addend  [T, N] of out_type, or NULL, added before the one rounding of out;
+ *           may be out itself.
+ *   out     out [T, N] of out_type.
+ *   pre     out bf16 [T, N] or NULL: z, for moe_linear_backward.
+ * K and N multiples of 8, >= 8; strides multiples of 8; pointers 16-byte
+ * aligned. */
+int64_t moe_linear_workspace_size(int T, int K, int N);
+moe_status moe_linear_forward(const uint16_t* x, int64_t x_stride, const uint16_t* w,
+                              const void* bias, moe_dtype bias_type, moe_linear_act act,
+                              const void* addend, int64_t addend_stride, int T, int K, int N,
+                              void* out, int64_t out_stride, moe_dtype out_type, uint16_t* pre,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
+/* Its backward from the saved pre: dz = dout * act'(pre), dx = W^T dz,
+ * dw = dz^T x, dbias = sum over the tokens of dz; the gradient of addend is dout.
+ * dz is rounded to bf16 for the two products (they take bf16 operands); dbias
+ * sums it unrounded.
+ *   dout  [T, N] of dout_type;  pre bf16 [T, N] (not read for MOE_LINEAR_NONE).
+ *   dx    out bf16 [T, K], dw out bf16 [N, K], dbias out [N] of bias_type; each
+ *         may be NULL, at least one is required unless T == 0 (an empty dx may
+ *         have no address). x is read for dw, w for dx. dw and dbias are
+ *         overwritten, and no sum depends on the order of atomics. */
+int64_t moe_linear_backward_workspace_size(int T, int K, int N);
+moe_status moe_linear_backward(const void* dout, int64_t dout_stride, moe_dtype dout_type,
+                               const uint16_t* x, int64_t x_stride, const uint16_t* pre,
+                               const uint16_t* w, moe_linear_act act, int T, int K, int N,
+                               uint16_t* dx, int64_t dx_stride, uint16_t* dw, void* dbias,
+                               moe_dtype bias_type, void* workspace, size_t workspace_bytes,
+                               void* stream);
 
 #ifdef __cplusplus
 }

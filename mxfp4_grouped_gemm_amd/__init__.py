@@ -14,8 +14,12 @@ Functions mirror the C ABI names:
   moe_a16w4_forward_noalloc,
   mxfp4_to_int4g32_requant, moe_last_error,
   moe_rms_norm, moe_lora_linear, moe_ffn_forward, moe_ffn_forward_mxfp8,
-  moe_ffn_backward (the dense operators around the routed experts)
+  moe_ffn_backward (the dense operators around the routed experts),
+  moe_layer_norm_forward, moe_layer_norm_backward, moe_permute, moe_unpermute,
+  moe_unpermute_backward, moe_linear_forward, moe_linear_backward (the
+  operators of a trainable expert block)
 plus compositions: moe_ffn (the shared expert as a differentiable function),
+moe_layer_norm, moe_dispatch, moe_combine and moe_linear (differentiable),
 moe_a16w4_block (norm -> router -> routed experts + shared expert),
 moe_a16w4_layer (route -> sort -> forward, the
 in-kernel routing path of apply_monolithic on the vLLM mxfp4 API page) and
@@ -36,7 +40,8 @@ LIB_PATH = os.path.join(HERE, "libmoe_a16w4.so")
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_HIP = 0, 1, 2, 3
 MOE_W_MXFP4, MOE_W_INT4G32 = 0, 1
 MOE_ACT_SWIGLU = 0
-MOE_DT_BF16, MOE_DT_F32 = 0, 1
+MOE_DT_BF16, MOE_DT_F32, MOE_DT_U8 = 0, 1, 2
+MOE_LINEAR_NONE, MOE_LINEAR_RELU, MOE_LINEAR_SILU, MOE_LINEAR_GELU, MOE_LINEAR_GELU_TANH = 0, 1, 2, 3, 4
 MOE_STAGE_GATE_UP, MOE_STAGE_DOWN, MOE_STAGE_COMBINE, MOE_STAGE_ALL = 1, 2, 4, 7
 
 # Every symbol include/moe_a16w4.h declares.
@@ -49,6 +54,9 @@ EXPORTS = (
     "moe_rms_norm", "moe_lora_linear_workspace_size", "moe_lora_linear", "moe_ffn_workspace_size",
     "moe_ffn_forward", "moe_ffn_mxfp8_workspace_size", "moe_ffn_forward_mxfp8",
     "moe_ffn_backward_workspace_size", "moe_ffn_backward",
+    "moe_layer_norm_forward", "moe_layer_norm_backward_workspace_size", "moe_layer_norm_backward",
+    "moe_permute_workspace_size", "moe_permute", "moe_unpermute", "moe_unpermute_backward",
+    "moe_linear_workspace_size", "moe_linear_forward", "moe_linear_backward_workspace_size", "moe_linear_backward",
 )
 # Scratch of the allocation-free forward (MOE_NOALLOC_SCRATCH_BYTES).
 NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -121,6 +129,28 @@ def _load():
     L.moe_ffn_backward_workspace_size.argtypes = [i, i, i]
     L.moe_ffn_backward.restype = i
     L.moe_ffn_backward.argtypes = [p, i64, p, i64, p, p, p, i, i, i, i, p, i64, p, p, p, sz, p]
+    L.moe_layer_norm_forward.restype = i
+    L.moe_layer_norm_forward.argtypes = [p, i64, p, i64, i, p, p, i, f, i, i, p, i64, p, i64, p, p, p]
+    L.moe_layer_norm_backward_workspace_size.restype = i64
+    L.moe_layer_norm_backward_workspace_size.argtypes = [i, i]
+    L.moe_layer_norm_backward.restype = i
+    L.moe_layer_norm_backward.argtypes = [p, i64, p, i64, i, p, p, p, i, p, i64, i, i, p, i64, p, i64, p, p, p, sz, p]
+    L.moe_permute_workspace_size.restype = i64
+    L.moe_permute_workspace_size.argtypes = [i, i, i]
+    L.moe_permute.restype = i
+    L.moe_permute.argtypes = [p, i64, i, p, i, i, i, i, p, i64, p, p, p, sz, p]
+    L.moe_unpermute.restype = i
+    L.moe_unpermute.argtypes = [p, i64, i, p, p, p, i64, i, i, i, p, i64, i, p]
+    L.moe_unpermute_backward.restype = i
+    L.moe_unpermute_backward.argtypes = [p, i64, i, p, p, p, i64, i, i, i, i, p, i64, p, p]
+    L.moe_linear_workspace_size.restype = i64
+    L.moe_linear_workspace_size.argtypes = [i, i, i]
+    L.moe_linear_forward.restype = i
+    L.moe_linear_forward.argtypes = [p, i64, p, p, i, i, p, i64, i, i, i, p, i64, i, p, p, sz, p]
+    L.moe_linear_backward_workspace_size.restype = i64
+    L.moe_linear_backward_workspace_size.argtypes = [i, i, i]
+    L.moe_linear_backward.restype = i
+    L.moe_linear_backward.argtypes = [p, i64, i, p, i64, p, p, i, i, i, i, p, i64, p, p, i, p, sz, p]
     return L
 
 
@@ -804,10 +834,412 @@ def moe_ffn(x, w13, w2, addend=None):
     return _Ffn.apply(x, w13, w2, addend)
 
 
+# ---------------------------------------------------------------------------
+# Operators of a trainable expert block. moe_layer_norm, moe_dispatch,
+# moe_combine and moe_linear are what autograd sees; the others record nothing.
+
+_FLOATS = (torch.bfloat16, torch.float32)
+# What moe_permute moves: floats, and the codes and scales of 8-bit rows.
+_DT = {torch.bfloat16: MOE_DT_BF16, torch.float32: MOE_DT_F32, torch.uint8: MOE_DT_U8, torch.float8_e4m3fn: MOE_DT_U8,
+       torch.float8_e8m0fnu: MOE_DT_U8}
+
+
+def moe_layer_norm_forward(x, weight, bias=None, residual=None, eps=1e-5, save_stats=False, y=None, residual_out=None,
+                           mean=None, rstd=None, stream=None):
+    """Residual addition and layer norm of x bf16 [T, H]: s = x + residual,
+    y = (s - mean(s)) / sqrt(var(s) + eps) * weight + bias. residual bf16 or
+    fp32 [T, H] (None: s = x, and no residual_out unless a buffer is given);
+    weight bf16 or fp32 [H], bias of its type or None. save_stats: also each
+    row's mean and 1 / deviation, for moe_layer_norm_backward. -> (y bf16,
+    residual_out of residual's type or None, mean fp32 [T] or None, rstd fp32
+    [T] or None), without a graph for gradients: moe_layer_norm records one.
+    Buffers may be given; y=x and residual_out=residual work in place."""
+    T, H = _matrix(x, "x")
+    device = x.device
+    px, ldx = _rows(x, "x", torch.bfloat16, (T, H), device)
+    pr, ldr, rdt = None, H, None
+    if residual is not None:
+        pr, ldr = _rows(residual, "residual", _FLOATS, (T, H), device)
+        rdt = residual.dtype
+    pw = _full(weight, "weight", _FLOATS, (H,), device)
+    pb = None if bias is None else _full(bias, "bias", weight.dtype, (H,), device)
+    if y is None:
+        y = _like(x, ldx, H, stream)
+        py, ldy = y.data_ptr(), H
+    else:
+        py, ldy = _rows(y, "y", torch.bfloat16, (T, H), device)
+    po, ldo = None, H
+    if residual_out is None and residual is not None:
+        residual_out = _like(residual, ldr, H, stream)
+        po = residual_out.data_ptr()
+    elif residual_out is not None:
+        po, ldo = _rows(residual_out, "residual_out", rdt or _FLOATS, (T, H), device)
+        rdt = residual_out.dtype
+    pm = ps = None
+    if save_stats or mean is not None or rstd is not None:
+        if mean is None:
+            mean = _empty((T,), torch.float32, device, stream)
+        if rstd is None:
+            rstd = _empty((T,), torch.float32, device, stream)
+        pm = _full(mean, "mean", torch.float32, (T,), device)
+        ps = _full(rstd, "rstd", torch.float32, (T,), device)
+    _run(device, stream, lib.moe_layer_norm_forward,
+         px, ldx, pr, ldr, MOE_DT_F32 if rdt is torch.float32 else MOE_DT_BF16, pw, pb,
+         MOE_DT_F32 if weight.dtype is torch.float32 else MOE_DT_BF16, eps, T, H, po, ldo, py, ldy, pm, ps)
+    return y, residual_out, mean, rstd
+
+
+def moe_layer_norm_backward_workspace_size(T, H) -> int:
+    return int(lib.moe_layer_norm_backward_workspace_size(T, H))
+
+
+def moe_layer_norm_backward(dy, s, mean, rstd, weight, dresidual_out=None, need_dx=True, need_dresidual=False,
+                            need_dweight=True, need_dbias=True, dx=None, dresidual=None, dweight=None, dbias=None,
+                            workspace=None, stream=None):
+    """Backward of moe_layer_norm_forward from its s (residual_out, or x where
+    there was no residual; bf16 or fp32 [T, H]), mean and rstd: dy bf16 [T, H],
+    dresidual_out (of s's type) the gradient that residual_out has of its own
+    -> (dx bf16 [T, H], dresidual [T, H] of s's type, dweight, dbias [H] of
+    weight's type); what is not needed is None. dx and dresidual are the same
+    gradient in two types: of a bf16 residual it is dx."""
+    T, H = _matrix(dy, "dy")
+    device = dy.device
+    pd, ldd = _rows(dy, "dy", torch.bfloat16, (T, H), device)
+    ps, lds = _rows(s, "s", _FLOATS, (T, H), device)
+    pm = _full(mean, "mean", torch.float32, (T,), device)
+    pq = _full(rstd, "rstd", torch.float32, (T,), device)
+    pw = _full(weight, "weight", _FLOATS, (H,), device)
+    pr, ldr = (None, H) if dresidual_out is None else _rows(dresidual_out, "dresidual_out", s.dtype, (T, H), device)
+    if not (need_dx or need_dresidual or need_dweight or need_dbias):
+        return None, None, None, None
+    if need_dx and dx is None:
+        dx = _empty((T, H), torch.bfloat16, device, stream)
+    if need_dresidual and dresidual is None:
+        dresidual = _empty((T, H), s.dtype, device, stream)
+    if need_dweight and dweight is None:
+        dweight = _empty((H,), weight.dtype, device, stream)
+    if need_dbias and dbias is None:
+        dbias = _empty((H,), weight.dtype, device, stream)
+    px, lddx = (None, H) if not need_dx else _rows(dx, "dx", torch.bfloat16, (T, H), device)
+    po, lddo = (None, H) if not need_dresidual else _rows(dresidual, "dresidual", s.dtype, (T, H), device)
+    pdw = None if not need_dweight else _full(dweight, "dweight", weight.dtype, (H,), device)
+    pdb = None if not need_dbias else _full(dbias, "dbias", weight.dtype, (H,), device)
+    need = lib.moe_layer_norm_backward_workspace_size(T, H) if need_dweight or need_dbias else 0
+    pws, nws, _ws = _workspace(workspace, need, device, stream)
+    _run(device, stream, lib.moe_layer_norm_backward,
+         pd, ldd, ps, lds, MOE_DT_F32 if s.dtype is torch.float32 else MOE_DT_BF16, pm, pq, pw,
+         MOE_DT_F32 if weight.dtype is torch.float32 else MOE_DT_BF16, pr, ldr, T, H, px, lddx, po, lddo, pdw, pdb,
+         pws, nws)
+    return (dx if need_dx else None, dresidual if need_dresidual else None, dweight if need_dweight else None,
+            dbias if need_dbias else None)
+
+
+def _dense(t):
+    """A gradient, which may come expanded, transposed or as a view, as rows
+    that a call takes."""
+    if t is None:
+        return None
+    t = t.contiguous()
+    return t.clone() if t.data_ptr() % 16 else t
+
+
+class _LayerNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, residual, eps):
+        needs = any(ctx.needs_input_grad)
+        y, s, mean, rstd = moe_layer_norm_forward(x, weight, bias, residual=residual, eps=eps, save_stats=needs)
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(x if residual is None else s, weight, mean, rstd)
+        return y, s
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy, ds):
+        s, weight, mean, rstd = ctx.saved_tensors
+        nx, nw, nb, nr, _ = ctx.needs_input_grad
+        if dy is None:  # y was not used
+            if ds is None:
+                return None, None, None, None, None
+            return ds.to(torch.bfloat16) if nx else None, None, None, ds if nr else None, None
+        wide = s.dtype is torch.float32
+        dx, dres, dweight, dbias = moe_layer_norm_backward(
+            _dense(dy), s, mean, rstd, weight, dresidual_out=_dense(ds), need_dx=nx or (nr and not wide),
+            need_dresidual=nr and wide, need_dweight=nw, need_dbias=nb)
+        return dx if nx else None, dweight, dbias, None if not nr else dres if wide else dx, None
+
+
+def moe_layer_norm(x, weight, bias=None, residual=None, eps=1e-5):
+    """Residual addition and layer norm as a differentiable function
+    (moe_layer_norm_forward, with moe_layer_norm_backward for the gradients of
+    x, weight, bias and residual) -> (y, s): s = x + residual in residual's
+    type, None without a residual. There is no second derivative."""
+    return _LayerNorm.apply(x, weight, bias, residual, eps)
+
+
+def moe_permute_workspace_size(T, topk, E) -> int:
+    return int(lib.moe_permute_workspace_size(T, topk, E))
+
+
+def moe_permute(x, topk_ids, E, out=None, rows=None, expert_offsets=None, workspace=None, stream=None):
+    """Token rows sorted by expert: x [T, H] in bf16, fp32 or 8-bit codes (or
+    scales), topk_ids int32 [T, topk] (outside [0, E): no expert's) -> (out [T *
+    topk, H], rows int32 [T, topk]: each pair's row of out, -1 - row for a pair
+    of no expert, whose row is zeros behind all others, expert_offsets int32 [E
+    + 1]: each expert's first row). Pairs of one expert keep their order. Without
+    a graph for gradients: moe_dispatch records one."""
+    T, H = _matrix(x, "x")
+    topk = _matrix(topk_ids, "topk_ids")[1]
+    device = x.device
+    px, ldx = _rows(x, "x", tuple(_DT), (T, H), device)
+    pi = _full(topk_ids, "topk_ids", torch.int32, (T, topk), device)
+    if out is None:
+        out = _empty((T * topk, H), x.dtype, device, stream)
+        po, ldo = out.data_ptr(), H
+    else:
+        po, ldo = _rows(out, "out", x.dtype, (T * topk, H), device)
+    if rows is None:
+        rows = _empty((T, topk), torch.int32, device, stream)
+    if expert_offsets is None:
+        expert_offsets = _empty((max(E, 0) + 1,), torch.int32, device, stream)
+    pr = _full(rows, "rows", torch.int32, (T, topk), device)
+    pe = _full(expert_offsets, "expert_offsets", torch.int32, (E + 1,), device)
+    need = lib.moe_permute_workspace_size(T, topk, E)
+    pws, nws, _ws = _workspace(workspace, max(need, 0), device, stream)
+    _run(device, stream, lib.moe_permute, px, ldx, _DT[x.dtype], pi, T, topk, E, H, po, ldo, pr, pe, pws, nws)
+    return out, rows, expert_offsets
+
+
+def _plan(rows, device):
+    """rows of moe_permute -> (address, T, topk)."""
+    T, topk = _matrix(rows, "rows")
+    return _full(rows, "rows", torch.int32, (T, topk), device), T, topk
+
+
+def moe_unpermute(y, rows, weights=None, residual=None, out_dtype=None, out=None, stream=None):
+    """Sorted rows back to their tokens: out[t] = residual[t] + the sum over j of
+    weights[t, j] y[rows[t, j]], for y bf16 or fp32 [T * topk, H], rows of
+    moe_permute, weights fp32 [T, topk] (None: 1) and residual [T, H] of the
+    output's type, which is residual's or out_dtype or y's -> out [T, H], without
+    a graph for gradients: moe_combine records one. out=residual works in place."""
+    P, H = _matrix(y, "y")
+    device = y.device
+    pr, T, topk = _plan(rows, device)
+    py, ldy = _rows(y, "y", _FLOATS, (T * topk, H), device)
+    pw = None if weights is None else _full(weights, "weights", torch.float32, (T, topk), device)
+    if out is not None:
+        dtype = out.dtype
+    else:
+        dtype = out_dtype or (y if residual is None else residual).dtype
+        if dtype not in _FLOATS:
+            raise ValueError(f"out_dtype must be bfloat16 or float32, got {dtype}")
+    ps, lds = (None, H) if residual is None else _rows(residual, "residual", dtype, (T, H), device)
+    if out is None:
+        out = _empty((T, H), dtype, device, stream)
+        po, ldo = out.data_ptr(), H
+    else:
+        po, ldo = _rows(out, "out", _FLOATS, (T, H), device)
+    _run(device, stream, lib.moe_unpermute,
+         py, ldy, MOE_DT_F32 if y.dtype is torch.float32 else MOE_DT_BF16, pr, pw, ps, lds, T, topk, H, po, ldo,
+         MOE_DT_F32 if dtype is torch.float32 else MOE_DT_BF16)
+    return out
+
+
+def moe_unpermute_backward(dout, rows, y=None, weights=None, y_dtype=None, need_dy=True, need_dweights=True, dy=None,
+                           dweights=None, stream=None):
+    """Gradients of moe_unpermute: dout bf16 or fp32 [T, H] -> (dy [T * topk, H]
+    of y's type (or y_dtype, or dout's): weights[t, j] dout[t] in row rows[t, j],
+    zeros in the rows of no expert; dweights fp32 [T, topk]: <dout[t], y[rows[t,
+    j]]>, for which y is needed); what is not needed, or dweights without y, is
+    None. The gradient of residual is dout. Without weights and y it puts any
+    rows into the order of `rows`."""
+    T, H = _matrix(dout, "dout")
+    device = dout.device
+    pr, Tr, topk = _plan(rows, device)
+    if Tr != T:
+        raise ValueError(f"rows has {Tr} tokens, dout {T}")
+    pd, ldd = _rows(dout, "dout", _FLOATS, (T, H), device)
+    need_dweights = need_dweights and y is not None
+    py, ldy = (None, H) if y is None else _rows(y, "y", _FLOATS, (T * topk, H), device)
+    pw = None if weights is None else _full(weights, "weights", torch.float32, (T, topk), device)
+    dtype = y.dtype if y is not None else dy.dtype if dy is not None else y_dtype or dout.dtype
+    if dtype not in _FLOATS:
+        raise ValueError(f"y_dtype must be bfloat16 or float32, got {dtype}")
+    if not (need_dy or need_dweights):
+        return None, None
+    if need_dy and dy is None:
+        dy = _empty((T * topk, H), dtype, device, stream)
+    if need_dweights and dweights is None:
+        dweights = _empty((T, topk), torch.float32, device, stream)
+    pdy, lddy = (None, H) if not need_dy else _rows(dy, "dy", dtype, (T * topk, H), device)
+    pdw = None if not need_dweights else _full(dweights, "dweights", torch.float32, (T, topk), device)
+    _run(device, stream, lib.moe_unpermute_backward,
+         pd, ldd, MOE_DT_F32 if dout.dtype is torch.float32 else MOE_DT_BF16, pr, pw, py, ldy,
+         MOE_DT_F32 if dtype is torch.float32 else MOE_DT_BF16, T, topk, H, pdy, lddy, pdw)
+    return dy if need_dy else None, dweights if need_dweights else None
+
+
+class _Dispatch(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, topk_ids, E):
+        out, rows, offsets = moe_permute(x, topk_ids, E)
+        ctx.save_for_backward(rows)
+        ctx.mark_non_differentiable(rows, offsets)
+        ctx.set_materialize_grads(False)
+        return out, rows, offsets
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dout, _rows_grad, _offsets_grad):
+        if dout is None:
+            return None, None, None
+        return moe_unpermute(_dense(dout), ctx.saved_tensors[0]), None, None
+
+
+def moe_dispatch(x, topk_ids, E):
+    """moe_permute as a differentiable function of x (bf16 or fp32) -> (out, rows,
+    expert_offsets)."""
+    return _Dispatch.apply(x, topk_ids, E)
+
+
+class _Combine(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, y, rows, weights, residual):
+        ctx.save_for_backward(y if ctx.needs_input_grad[2] else None, rows, weights)
+        ctx.y_dtype = y.dtype
+        return moe_unpermute(y, rows, weights=weights, residual=residual)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dout):
+        y, rows, weights = ctx.saved_tensors
+        ny, _, nw, nr = ctx.needs_input_grad
+        dy = dweights = None
+        if ny or nw:
+            dy, dweights = moe_unpermute_backward(_dense(dout), rows, y=y, weights=weights, y_dtype=ctx.y_dtype,
+                                                  need_dy=ny, need_dweights=nw)
+        return dy, None, dweights, dout if nr else None
+
+
+def moe_combine(y, rows, weights=None, residual=None):
+    """moe_unpermute as a differentiable function of y, weights and residual (the
+    output has residual's type, or y's)."""
+    return _Combine.apply(y, rows, weights, residual)
+
+
+def moe_linear_workspace_size(T, K, N) -> int:
+    return int(lib.moe_linear_workspace_size(T, K, N))
+
+
+def _linear_sizes(x, w):
+    T, K = _matrix(x, "x")
+    return T, K, _matrix(w, "w")[0]
+
+
+def moe_linear_forward(x, w, bias=None, act=MOE_LINEAR_NONE, addend=None, out_dtype=torch.bfloat16, save_pre=False,
+                       pre=None, out=None, workspace=None, stream=None):
+    """Product with bias, activation and addend: out = act(x w^T + bias) +
+    addend. x bf16 [T, K], w bf16 [N, K], bias bf16 or fp32 [N], addend [T, N] of
+    the output's type (out_dtype: bf16 or fp32); act one of MOE_LINEAR_*.
+    save_pre (or a pre buffer): -> (out, pre bf16 [T, N], the activation's
+    argument, which moe_linear_backward needs), else out. No graph is recorded for
+    gradients: moe_linear does that. out=addend works in place."""
+    T, K, N = _linear_sizes(x, w)
+    device = x.device
+    px, ldx = _rows(x, "x", torch.bfloat16, (T, K), device)
+    pw = _full(w, "w", torch.bfloat16, (N, K), device)
+    pb, f32 = None, False
+    if bias is not None:
+        pb = _full(bias, "bias", _FLOATS, (N,), device)
+        f32 = bias.dtype is torch.float32
+    if out is None:
+        if out_dtype not in _FLOATS:
+            raise ValueError(f"out_dtype must be bfloat16 or float32, got {out_dtype}")
+        out = _empty((T, N), out_dtype, device, stream)
+        po, ldo = out.data_ptr(), N
+    else:
+        po, ldo = _rows(out, "out", _FLOATS, (T, N), device)
+    pa, lda = (None, N) if addend is None else _rows(addend, "addend", out.dtype, (T, N), device)
+    if pre is None and save_pre:
+        pre = _empty((T, N), torch.bfloat16, device, stream)
+    pp = None if pre is None else _full(pre, "pre", torch.bfloat16, (T, N), device)
+    pws, nws, _ws = _workspace(workspace, lib.moe_linear_workspace_size(T, K, N), device, stream)
+    _run(device, stream, lib.moe_linear_forward,
+         px, ldx, pw, pb, MOE_DT_F32 if f32 else MOE_DT_BF16, act, pa, lda, T, K, N, po, ldo,
+         MOE_DT_F32 if out.dtype is torch.float32 else MOE_DT_BF16, pp, pws, nws)
+    return out if pre is None else (out, pre)
+
+
+def moe_linear_backward_workspace_size(T, K, N) -> int:
+    return int(lib.moe_linear_backward_workspace_size(T, K, N))
+
+
+def moe_linear_backward(dout, x, w, pre=None, act=MOE_LINEAR_NONE, need_dx=True, need_dw=True, need_dbias=True,
+                        bias_dtype=torch.bfloat16, dx=None, dw=None, dbias=None, workspace=None, stream=None):
+    """Backward of moe_linear_forward: dout bf16 or fp32 [T, N], pre its saved
+    argument of the activation (not needed for MOE_LINEAR_NONE) -> (dx bf16 [T,
+    K], dw bf16 [N, K], dbias of bias_dtype [N]); a gradient that is not needed is
+    None. The gradient of addend is dout itself."""
+    T, K, N = _linear_sizes(x, w)
+    device = x.device
+    pd, ldd = _rows(dout, "dout", _FLOATS, (T, N), device)
+    px, ldx = _rows(x, "x", torch.bfloat16, (T, K), device)
+    pw = _full(w, "w", torch.bfloat16, (N, K), device)
+    if act != MOE_LINEAR_NONE and pre is None:
+        raise ValueError("pre is needed for the gradient of an activation")
+    pp = None if pre is None else _full(pre, "pre", torch.bfloat16, (T, N), device)
+    if not (need_dx or need_dw or need_dbias):
+        return None, None, None
+    if need_dx and dx is None:
+        dx = _empty((T, K), torch.bfloat16, device, stream)
+    if need_dw and dw is None:
+        dw = _empty((N, K), torch.bfloat16, device, stream)
+    if need_dbias and dbias is None:
+        if bias_dtype not in _FLOATS:
+            raise ValueError(f"bias_dtype must be bfloat16 or float32, got {bias_dtype}")
+        dbias = _empty((N,), bias_dtype, device, stream)
+    pdx, lddx = (None, K) if not need_dx else _rows(dx, "dx", torch.bfloat16, (T, K), device)
+    pdw = None if not need_dw else _full(dw, "dw", torch.bfloat16, (N, K), device)
+    pdb = None if not need_dbias else _full(dbias, "dbias", _FLOATS, (N,), device)
+    pws, nws, _ws = _workspace(workspace, lib.moe_linear_backward_workspace_size(T, K, N), device, stream)
+    _run(device, stream, lib.moe_linear_backward,
+         pd, ldd, MOE_DT_F32 if dout.dtype is torch.float32 else MOE_DT_BF16, px, ldx, pp, pw, act, T, K, N, pdx, lddx,
+         pdw, pdb, MOE_DT_F32 if need_dbias and dbias.dtype is torch.float32 else MOE_DT_BF16, pws, nws)
+    return dx if need_dx else None, dw if need_dw else None, dbias if need_dbias else None
+
+
+class _Linear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, bias, act, addend, out_dtype):
+        needs = act != MOE_LINEAR_NONE and any(ctx.needs_input_grad[:3])
+        r = moe_linear_forward(x, w, bias=bias, act=act, addend=addend, out_dtype=out_dtype, save_pre=needs)
+        out, pre = r if needs else (r, None)
+        ctx.save_for_backward(x, w, pre)
+        ctx.act, ctx.bias_dtype = act, None if bias is None else bias.dtype
+        return out
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dout):
+        x, w, pre = ctx.saved_tensors
+        nx, nw, nb, _, na, _ = ctx.needs_input_grad
+        dx = dw = dbias = None
+        if nx or nw or nb:
+            dx, dw, dbias = moe_linear_backward(_dense(dout), x, w, pre=pre, act=ctx.act, need_dx=nx, need_dw=nw,
+                                                need_dbias=nb, bias_dtype=ctx.bias_dtype)
+        return dx, dw, dbias, None, dout if na else None, None
+
+
+def moe_linear(x, w, bias=None, act=MOE_LINEAR_NONE, addend=None, out_dtype=torch.bfloat16):
+    """moe_linear_forward as a differentiable function of x, w, bias and addend,
+    with moe_linear_backward for the gradients that are asked for. There is no
+    second derivative."""
+    return _Linear.apply(x, w, bias, act, addend, out_dtype)
+
+
 def moe_a16w4_block(x, norm_weight, router_w, w13, w13_scale, w2, w2_scale, topk, residual=None, eps=1e-6,
                     weight_offset=0.0, shared=None, shared_mxfp8=None, lora13=None, lora2=None,
                     renormalize=True, fmt=MOE_W_MXFP4, block_m=None, stream=None, w13_bias=None, w2_bias=None,
-                    swiglu_limit=0.0):
+                    swiglu_limit=0.0, norm_bias=None, router_bias=None):
     """The feed-forward half of a decoder layer on one stream: residual
     addition and norm (moe_rms_norm), router logits (moe_lora_linear in fp32
     with router_w bf16 [E, H]), the routed experts (moe_a16w4_layer, with the
@@ -818,21 +1250,36 @@ def moe_a16w4_block(x, norm_weight, router_w, w13, w13_scale, w2, w2_scale, topk
     The projection computes logits in eights: where E is no multiple of 8,
     router_w is padded in every call, or may be given with its rows padded to
     the next multiple (what these hold does not matter).
+    norm_bias: the norm is a layer norm (moe_layer_norm_forward; no
+    weight_offset, and no MXFP8 output for shared_mxfp8). router_bias bf16 or
+    fp32 [E] is added to the logits (moe_linear_forward).
     -> (out bf16 [T, H], the residual for the next layer), without a graph for
     gradients (of its parts only the bf16 shared expert has one: moe_ffn)."""
     if shared is not None and shared_mxfp8 is not None:
         raise ValueError("shared and shared_mxfp8 exclude each other")
     if shared is None and (lora13 is not None or lora2 is not None):
         raise ValueError("lora13 and lora2 belong to the bf16 shared expert")
+    if norm_bias is not None and (weight_offset or shared_mxfp8 is not None):
+        raise ValueError("norm_bias makes the norm a layer norm, which has no weight_offset and no MXFP8 output")
     E, rows = w13.shape[0], _matrix(router_w, "router_w")[0]
     if rows not in (E, -(-E // 8) * 8):
         raise ValueError(f"router_w has {rows} rows for {E} experts")
     with torch.cuda.device(x.device), _on(stream):
-        y, res, q, qs = moe_rms_norm(x, norm_weight, residual=residual, eps=eps, weight_offset=weight_offset,
-                                     mxfp8=shared_mxfp8 is not None, stream=stream)
+        if norm_bias is not None:
+            y, res, _, _ = moe_layer_norm_forward(x, norm_weight, norm_bias, residual=residual, eps=eps, stream=stream)
+        else:
+            y, res, q, qs = moe_rms_norm(x, norm_weight, residual=residual, eps=eps, weight_offset=weight_offset,
+                                         mxfp8=shared_mxfp8 is not None, stream=stream)
         if rows % 8:
             router_w = torch.nn.functional.pad(router_w, (0, 0, 0, -E % 8))
-        logits = moe_lora_linear(y, router_w, out_dtype=torch.float32, stream=stream)
+        if router_bias is not None:
+            if router_bias.shape != (E,):
+                raise ValueError(f"router_bias must have shape {(E,)}, got {tuple(router_bias.shape)}")
+            if E % 8:
+                router_bias = torch.nn.functional.pad(router_bias, (0, -E % 8))
+            logits = moe_linear_forward(y, router_w, bias=router_bias, out_dtype=torch.float32, stream=stream)
+        else:
+            logits = moe_lora_linear(y, router_w, out_dtype=torch.float32, stream=stream)
         if logits.shape[1] != E:
             logits = logits[:, :E].contiguous()
         out = moe_a16w4_layer(y, logits, w13, w13_scale, w2, w2_scale, topk, fmt=fmt, renormalize=renormalize,

@@ -4,21 +4,17 @@
 #include <cmath>
 #include <cstring>
 
-#include "abi_common.hpp"
+#include "abi_checks.hpp"
 #include "dense.hpp"
+#include "train.hpp"
 
-using moe::abi::align_up;
-using moe::abi::aligned;
-using moe::abi::fail;
-using moe::abi::hip_status;
+using namespace moe::abi;
 
 namespace {
 
 // Tile addressing: a tile's rows (at most 256, or 64 rows of K) lie within
 // 32-bit byte offsets of its first element.
 constexpr int64_t kMaxCols = 1 << 18;
-constexpr int64_t kMaxStride = 1 << 20;
-constexpr int kMaxTokens = 1 << 24;
 constexpr int kMaxRank = 256;
 constexpr int kMaxAdapters = 1 << 24;  // `ranks` has 32-bit offsets
 // Weights that the few-token kernels address with 32-bit offsets.
@@ -28,39 +24,6 @@ moe_status check_size(const char* fn, const char* name, int v, int step) {
     if (v < step || v % step != 0)
         return fail(MOE_ERR_INVALID_ARG, "%s: %s=%d must be a positive multiple of %d", fn, name, v, step);
     if (v > kMaxCols) return fail(MOE_ERR_UNSUPPORTED, "%s: %s=%d > %lld", fn, name, v, (long long)kMaxCols);
-    return MOE_OK;
-}
-
-moe_status check_tokens(const char* fn, int T) {
-    if (T < 0) return fail(MOE_ERR_INVALID_ARG, "%s: T=%d < 0", fn, T);
-    if (T > kMaxTokens) return fail(MOE_ERR_UNSUPPORTED, "%s: T=%d > %d", fn, T, kMaxTokens);
-    return MOE_OK;
-}
-
-moe_status check_stride(const char* fn, const char* name, int64_t stride, int64_t cols, int step) {
-    if (stride < cols || stride % step != 0)
-        return fail(MOE_ERR_INVALID_ARG, "%s: %s=%lld must be at least %lld and a multiple of %d", fn, name,
-                    (long long)stride, (long long)cols, step);
-    if (stride > kMaxStride)
-        return fail(MOE_ERR_UNSUPPORTED, "%s: %s=%lld > %lld", fn, name, (long long)stride, (long long)kMaxStride);
-    return MOE_OK;
-}
-
-template <int N>
-moe_status check_pointers(const char* fn, const void* const (&ptrs)[N], size_t align) {
-    for (const void* p : ptrs)
-        if (!p) return fail(MOE_ERR_INVALID_ARG, "%s: null pointer", fn);
-    for (const void* p : ptrs)
-        if (!aligned(p, align)) return fail(MOE_ERR_INVALID_ARG, "%s: pointer %p not %zu-byte aligned", fn, p, align);
-    return MOE_OK;
-}
-
-moe_status check_workspace(const char* fn, const void* ws, size_t have, int64_t need) {
-    if (need == 0) return MOE_OK;
-    if (!ws) return fail(MOE_ERR_INVALID_ARG, "%s: null workspace", fn);
-    if (!aligned(ws, 256)) return fail(MOE_ERR_INVALID_ARG, "%s: workspace not 256-byte aligned", fn);
-    if ((int64_t)have < need)
-        return fail(MOE_ERR_INVALID_ARG, "%s: workspace %zu bytes < %lld needed", fn, have, (long long)need);
     return MOE_OK;
 }
 
@@ -79,17 +42,6 @@ moe_status check_lora(const char* fn, const char* name, const moe_lora* l, int T
         return fail(MOE_ERR_INVALID_ARG, "%s: %s has a misaligned pointer", fn, name);
     return MOE_OK;
 }
-
-#define CHECK(call)                                    \
-    do {                                               \
-        const moe_status st_ = (call);                 \
-        if (st_ != MOE_OK) return st_;                 \
-    } while (0)
-#define LAUNCH(call, what)                             \
-    do {                                               \
-        const hipError_t e_ = (call);                  \
-        if (e_ != hipSuccess) return hip_status(e_, what); \
-    } while (0)
 
 int vld_of(int rank) { return (int)align_up(rank, 32); }
 
@@ -239,6 +191,45 @@ moe_status check_act(const char* fn, moe_act act) {
 bool valid_sizes(int T, int a, int b, int step) {
     auto ok = [&](int v) { return v >= step && v % step == 0 && v <= kMaxCols; };
     return T >= 0 && T <= kMaxTokens && ok(a) && ok(b);
+}
+
+struct LinearBwdLayout {
+    int64_t sums, partial, total;  // dz at 0
+    int splits_dx;
+};
+
+LinearBwdLayout linear_bwd_layout(int T, int K, int N) {
+    LinearBwdLayout L;
+    const moe::DenseArgs dx = product(nullptr, N, nullptr, K, T, K, N, nullptr, K);
+    L.splits_dx = moe::dense_bwd_splits(dx);
+    L.sums = align_up((int64_t)T * N * 2, 256);
+    L.partial = L.sums + align_up((int64_t)moe::linear_dz_parts(T, N) * N * 4, 256);
+    L.total = L.partial + align_up(moe::dense_partial_bytes(dx, L.splits_dx, moe::kEpiOut, false), 256);
+    return L;
+}
+
+constexpr int kMaxNormed = 65536;  // columns of a norm's row
+
+moe_status check_types(const char* fn, moe_dtype a, moe_dtype b) {
+    if ((a != MOE_DT_BF16 && a != MOE_DT_F32) || (b != MOE_DT_BF16 && b != MOE_DT_F32))
+        return fail(MOE_ERR_UNSUPPORTED, "%s: type %d / %d unknown", fn, (int)a, (int)b);
+    return MOE_OK;
+}
+
+moe_status check_norm(const char* fn, int T, int H, moe_dtype stream_type, moe_dtype weight_type) {
+    CHECK(check_tokens(fn, T));
+    if (H < 1) return fail(MOE_ERR_INVALID_ARG, "%s: H=%d < 1", fn, H);
+    if (H > kMaxNormed) return fail(MOE_ERR_UNSUPPORTED, "%s: H=%d > %d", fn, H, kMaxNormed);
+    return check_types(fn, stream_type, weight_type);
+}
+
+moe_status check_linear(const char* fn, int T, int K, int N, moe_linear_act act, moe_dtype out_type, moe_dtype bias_type) {
+    if ((int)act < MOE_LINEAR_NONE || (int)act > MOE_LINEAR_GELU_TANH)
+        return fail(MOE_ERR_UNSUPPORTED, "%s: activation %d unknown", fn, (int)act);
+    CHECK(check_tokens(fn, T));
+    CHECK(check_size(fn, "K", K, 8));
+    CHECK(check_size(fn, "N", N, 8));
+    return check_types(fn, out_type, bias_type);
 }
 
 bool valid_rank(int r) { return r >= 0 && r % 8 == 0 && r <= kMaxRank; }
@@ -466,6 +457,194 @@ moe_status moe_ffn_backward(const uint16_t* dout, int64_t dout_stride, const uin
     gx.splits = L.splits_dx;
     gx.partial = partial;
     return hip_status(moe::launch_dense_grads(g13, g2, gx, s), "moe_ffn_backward (gradients)");
+}
+
+moe_status moe_layer_norm_forward(const uint16_t* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                                  moe_dtype residual_type, const void* weight, const void* bias,
+                                  moe_dtype weight_type, float eps, int T, int H, void* residual_out,
+                                  int64_t residual_out_stride, uint16_t* y, int64_t y_stride, float* mean, float* rstd,
+                                  void* stream) {
+    const char* fn = "moe_layer_norm_forward";
+    CHECK(check_norm(fn, T, H, residual_type, weight_type));
+    if (!(eps >= 0.0f) || std::isinf(eps)) return fail(MOE_ERR_INVALID_ARG, "%s: eps %g must be >= 0 and finite", fn, (double)eps);
+    CHECK(check_stride(fn, "x_stride", x_stride, H, 1));
+    if (residual) CHECK(check_stride(fn, "residual_stride", residual_stride, H, 1));
+    if (residual_out) CHECK(check_stride(fn, "residual_out_stride", residual_out_stride, H, 1));
+    if (y) CHECK(check_stride(fn, "y_stride", y_stride, H, 1));
+    if (T == 0) return MOE_OK;
+    if ((mean == nullptr) != (rstd == nullptr)) return fail(MOE_ERR_INVALID_ARG, "%s: mean and rstd go together", fn);
+    if (!y && !mean && !residual_out) return fail(MOE_ERR_INVALID_ARG, "%s: no output", fn);
+    if (!x || !weight) return fail(MOE_ERR_INVALID_ARG, "%s: null pointer", fn);
+    const size_t ra = residual_type == MOE_DT_F32 ? 4 : 2, wa = weight_type == MOE_DT_F32 ? 4 : 2;
+    if (!aligned(x, 2) || !aligned(y, 2) || !aligned(residual, ra) || !aligned(residual_out, ra) || !aligned(weight, wa) ||
+        !aligned(bias, wa) || !aligned(mean, 4) || !aligned(rstd, 4))
+        return fail(MOE_ERR_INVALID_ARG, "%s: misaligned pointer", fn);
+    moe::LayerNormArgs a;
+    a.x = x;
+    a.residual = residual;
+    a.weight = weight;
+    a.bias = bias;
+    a.residual_out = residual_out;
+    a.y = y;
+    a.mean = mean;
+    a.rstd = rstd;
+    a.ldx = x_stride;
+    a.ldr = residual_stride;
+    a.ldro = residual_out_stride;
+    a.ldy = y_stride;
+    a.T = T;
+    a.H = H;
+    a.eps = eps;
+    a.res_f32 = residual_type == MOE_DT_F32;
+    a.weight_f32 = weight_type == MOE_DT_F32;
+    return hip_status(moe::launch_layer_norm(a, (hipStream_t)stream), fn);
+}
+
+int64_t moe_layer_norm_backward_workspace_size(int T, int H) {
+    if (T < 0 || T > kMaxTokens || H < 1 || H > kMaxNormed) return -1;
+    return align_up((int64_t)moe::layer_norm_parts(T, H) * 2 * H * 4, 256);
+}
+
+moe_status moe_layer_norm_backward(const uint16_t* dy, int64_t dy_stride, const void* s, int64_t s_stride,
+                                   moe_dtype s_type, const float* mean, const float* rstd, const void* weight,
+                                   moe_dtype weight_type, const void* dresidual_out, int64_t dresidual_out_stride, int T,
+                                   int H, uint16_t* dx, int64_t dx_stride, void* dresidual, int64_t dresidual_stride,
+                                   void* dweight, void* dbias, void* workspace, size_t workspace_bytes, void* stream) {
+    const char* fn = "moe_layer_norm_backward";
+    CHECK(check_norm(fn, T, H, s_type, weight_type));
+    CHECK(check_stride(fn, "dy_stride", dy_stride, H, 1));
+    CHECK(check_stride(fn, "s_stride", s_stride, H, 1));
+    if (dresidual_out) CHECK(check_stride(fn, "dresidual_out_stride", dresidual_out_stride, H, 1));
+    if (dx) CHECK(check_stride(fn, "dx_stride", dx_stride, H, 1));
+    if (dresidual) CHECK(check_stride(fn, "dresidual_stride", dresidual_stride, H, 1));
+    const size_t sa = s_type == MOE_DT_F32 ? 4 : 2, wa = weight_type == MOE_DT_F32 ? 4 : 2;
+    // (Empty tensors may have no address.)
+    if (!dx && !dresidual && !dweight && !dbias)
+        return T == 0 ? MOE_OK : fail(MOE_ERR_INVALID_ARG, "%s: no output", fn);
+    if (!aligned(dx, 2) || !aligned(dresidual, sa) || !aligned(dweight, wa) || !aligned(dbias, wa))
+        return fail(MOE_ERR_INVALID_ARG, "%s: misaligned output", fn);
+    if (T > 0) {
+        if (!dy || !s || !mean || !rstd || !weight) return fail(MOE_ERR_INVALID_ARG, "%s: null pointer", fn);
+        if (!aligned(dy, 2) || !aligned(s, sa) || !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(weight, wa) ||
+            !aligned(dresidual_out, sa))
+            return fail(MOE_ERR_INVALID_ARG, "%s: misaligned pointer", fn);
+        if (dweight || dbias) CHECK(check_workspace(fn, workspace, workspace_bytes, moe_layer_norm_backward_workspace_size(T, H)));
+    }
+    moe::LayerNormBwdArgs a;
+    a.dy = dy;
+    a.s = s;
+    a.mean = mean;
+    a.rstd = rstd;
+    a.weight = weight;
+    a.dres = dresidual_out;
+    a.dx = dx;
+    a.dresidual = dresidual;
+    a.partial = dweight || dbias ? (float*)workspace : nullptr;
+    a.dweight = dweight;
+    a.dbias = dbias;
+    a.lddy = dy_stride;
+    a.lds = s_stride;
+    a.lddr = dresidual_out_stride;
+    a.lddx = dx_stride;
+    a.lddro = dresidual_stride;
+    a.T = T;
+    a.H = H;
+    a.s_f32 = s_type == MOE_DT_F32;
+    a.weight_f32 = weight_type == MOE_DT_F32;
+    return hip_status(moe::launch_layer_norm_bwd(a, (hipStream_t)stream), fn);
+}
+
+int64_t moe_linear_workspace_size(int T, int K, int N) {
+    if (!valid_sizes(T, K, N, 8)) return -1;
+    return partial_bytes(T, N, K, 0, moe::kEpiAct, skinny(T, N, K, 0), 0);
+}
+
+moe_status moe_linear_forward(const uint16_t* x, int64_t x_stride, const uint16_t* w, const void* bias,
+                              moe_dtype bias_type, moe_linear_act act, const void* addend, int64_t addend_stride, int T,
+                              int K, int N, void* out, int64_t out_stride, moe_dtype out_type, uint16_t* pre,
+                              void* workspace, size_t workspace_bytes, void* stream) {
+    const char* fn = "moe_linear_forward";
+    CHECK(check_linear(fn, T, K, N, act, out_type, bias_type));
+    CHECK(check_stride(fn, "x_stride", x_stride, K, 8));
+    CHECK(check_stride(fn, "out_stride", out_stride, N, 8));
+    if (addend) CHECK(check_stride(fn, "addend_stride", addend_stride, N, 8));
+    if (T == 0) return MOE_OK;
+    const void* ptrs[] = {x, w, out};
+    CHECK(check_pointers(fn, ptrs, 16));
+    if (!aligned(bias, 16) || !aligned(addend, 16) || !aligned(pre, 16))
+        return fail(MOE_ERR_INVALID_ARG, "%s: bias, addend and pre must be 16-byte aligned", fn);
+    CHECK(check_workspace(fn, workspace, workspace_bytes, moe_linear_workspace_size(T, K, N)));
+    moe::DenseArgs a = product(x, x_stride, w, K, T, N, K, out, out_stride);
+    a.out_f32 = out_type == MOE_DT_F32;
+    a.bias = bias;
+    a.bias_f32 = bias_type == MOE_DT_F32;
+    a.act = (int)act;
+    a.addend = addend;
+    a.ldadd = addend_stride;
+    a.addend_f32 = addend && a.out_f32;
+    a.pre = pre;
+    return hip_status(run_product(a, 0, moe::kEpiAct, skinny(T, N, K, 0), (float*)workspace, nullptr, (hipStream_t)stream), fn);
+}
+
+int64_t moe_linear_backward_workspace_size(int T, int K, int N) {
+    if (!valid_sizes(T, K, N, 8)) return -1;
+    return linear_bwd_layout(T, K, N).total;
+}
+
+moe_status moe_linear_backward(const void* dout, int64_t dout_stride, moe_dtype dout_type, const uint16_t* x,
+                               int64_t x_stride, const uint16_t* pre, const uint16_t* w, moe_linear_act act, int T, int K,
+                               int N, uint16_t* dx, int64_t dx_stride, uint16_t* dw, void* dbias, moe_dtype bias_type,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+    const char* fn = "moe_linear_backward";
+    CHECK(check_linear(fn, T, K, N, act, dout_type, bias_type));
+    CHECK(check_stride(fn, "dout_stride", dout_stride, N, 8));
+    CHECK(check_stride(fn, "x_stride", x_stride, K, 8));
+    if (dx) CHECK(check_stride(fn, "dx_stride", dx_stride, K, 8));
+    // (An empty dx may have no address.)
+    if (!dx && !dw && !dbias) return T == 0 ? MOE_OK : fail(MOE_ERR_INVALID_ARG, "%s: no output", fn);
+    if (!aligned(dx, 16) || !aligned(dw, 16) || !aligned(dbias, 16))
+        return fail(MOE_ERR_INVALID_ARG, "%s: outputs must be 16-byte aligned", fn);
+    hipStream_t s = (hipStream_t)stream;
+    const LinearBwdLayout L = linear_bwd_layout(T, K, N);
+    const bool f32 = bias_type == MOE_DT_F32;
+    const uint16_t* dz = (const uint16_t*)dout;
+    int64_t lddz = dout_stride;
+    if (T > 0) {
+        if (!dout || (dw && !x) || (dx && !w) || (act != MOE_LINEAR_NONE && !pre))
+            return fail(MOE_ERR_INVALID_ARG, "%s: null pointer", fn);
+        if (!aligned(dout, 16) || !aligned(x, 16) || !aligned(w, 16) || !aligned(pre, 16))
+            return fail(MOE_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", fn);
+        CHECK(check_workspace(fn, workspace, workspace_bytes, L.total));
+        moe::LinearDzArgs z;
+        z.dout = dout;
+        z.pre = pre;
+        // Without an activation dz is dout, if that has its type.
+        z.dz = act == MOE_LINEAR_NONE && dout_type == MOE_DT_BF16 ? nullptr : (uint16_t*)workspace;
+        z.partial = dbias ? (float*)((char*)workspace + L.sums) : nullptr;
+        z.lddo = dout_stride;
+        z.T = T;
+        z.N = N;
+        z.dout_f32 = dout_type == MOE_DT_F32;
+        z.act = (int)act;
+        if (z.dz) {
+            dz = z.dz;
+            lddz = N;
+        }
+        if (dbias || (z.dz && (dx || dw))) LAUNCH(moe::launch_linear_dz(z, s), "moe_linear_backward (dz)");
+        if (dbias)
+            LAUNCH(moe::launch_join_columns(z.partial, moe::linear_dz_parts(T, N), N, N, dbias, nullptr, f32, s),
+                   "moe_linear_backward (bias)");
+    } else if (dbias) {
+        LAUNCH(moe::launch_join_columns(nullptr, 0, N, N, dbias, nullptr, f32, s), "moe_linear_backward (bias)");
+    }
+    if (!dx && !dw) return MOE_OK;
+    // With T == 0 the weights' sum is empty and writes zeros.
+    const moe::DenseArgs gw = product(dz, lddz, x, x_stride, N, K, T, dw, K);
+    moe::DenseArgs gx = product(dz, lddz, w, K, T, K, N, dx, dx_stride);
+    gx.splits = L.splits_dx;
+    gx.partial = (float*)((char*)workspace + L.partial);
+    return hip_status(moe::launch_dense_grads(gw, product(nullptr, 0, nullptr, 0, 0, 0, 0, nullptr, 0), gx, s),
+                      "moe_linear_backward (gradients)");
 }
 
 }  // extern "C"

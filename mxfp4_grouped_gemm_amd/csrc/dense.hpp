@@ -33,6 +33,11 @@ constexpr int kEpiOut = 0;      // out = acc (+ addend), bf16 or fp32
 constexpr int kEpiGated = 1;    // h = silu(gate) * up, bf16; optional gate_up
 constexpr int kEpiGatedMx = 2;  // the same, h in MXFP8
 constexpr int kEpiGatedBwd = 3; // acc = dh: dgate_up and h from the saved gate_up
+constexpr int kEpiAct = 4;      // out = act(acc + bias) (+ addend), optional pre
+constexpr bool epi_gated(int epi) { return epi == kEpiGated || epi == kEpiGatedMx; }
+
+// Activations of kEpiAct.
+constexpr int kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4;
 
 // One product C[m, n] = sum_k X[m, k] W[n, k]. Strides in elements. For the
 // gated epilogues W holds 2N rows (gate rows, then up rows) and n counts pairs.
@@ -46,8 +51,13 @@ struct DenseArgs {
     void* out;              // kEpiOut: C; kEpiGated: h; kEpiGatedMx: h codes; kEpiGatedBwd: dgate_up
     int64_t ldo;
     int out_f32;
-    const uint16_t* addend; // bf16 [M, N], stride ldadd
+    const void* addend;     // [M, N], stride ldadd; bf16, or fp32 with addend_f32
     int64_t ldadd;
+    int addend_f32;
+    const void* bias;       // [N], bf16 or fp32, or null
+    int bias_f32;
+    int act;
+    uint16_t* pre;          // bf16 [M, N]: acc + bias, saved (may be null)
     uint16_t* gate_up;      // kEpiGated: saved (may be null); kEpiGatedBwd: read
     uint16_t* h;            // kEpiGatedBwd: h
     uint8_t* hs;            // kEpiGatedMx: e8m0 scales of h
@@ -61,7 +71,7 @@ struct DenseArgs {
 int dense_splits(const DenseArgs& a, int elt, int epi);
 // (join: the product is joined by a second kernel even if splits == 1).
 inline int64_t dense_partial_bytes(const DenseArgs& a, int splits, int epi, bool join) {
-    return splits <= 1 && !join ? 0 : (int64_t)splits * a.M * a.N * (epi == kEpiOut || epi == kEpiGatedBwd ? 1 : 2) * 4;
+    return splits <= 1 && !join ? 0 : (int64_t)splits * a.M * a.N * (epi_gated(epi) ? 2 : 1) * 4;
 }
 bool dense_big_tiles(const DenseArgs& a, int epi);
 bool dense_one_round(const DenseArgs& a, int epi);

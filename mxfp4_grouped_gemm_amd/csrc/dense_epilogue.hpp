@@ -70,8 +70,82 @@ __device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf
 
 __device__ __forceinline__ u32x2 pack4(f32x4 v) { return u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])}; }
 
+// Four elements of bf16 or fp32 from element `at`, 8-byte (16-byte) aligned.
+__device__ __forceinline__ f32x4 load4(const void* p, int f32, int64_t at) {
+    if (f32) return *(const f32x4*)((const float*)p + at);
+    const u32x2 d = *(const u32x2*)((const uint16_t*)p + at);
+    return f32x4{__uint_as_float(d[0] << 16), __uint_as_float(d[0] & 0xffff0000u), __uint_as_float(d[1] << 16),
+                 __uint_as_float(d[1] & 0xffff0000u)};
+}
+
+constexpr float kLog2e = 1.44269504f, kSqrt2OverPi = 0.797884561f, kInvSqrt2Pi = 0.398942280f;
+
+// Phi(-x) for x >= 0, the normal distribution's tail: erfc(x / sqrt 2) / 2 =
+// exp(-x^2 / 2) P(t) with t = 1 / (1 + 0.36 x) and P the polynomial of degree 7
+// with P(0) = 0 whose largest relative error is least for x in [0, 14], 8.7e-7
+// (beyond, fp32 holds no more of it). z Phi(z) is off by 2e-7 at most; about 16
+// vector instructions, against some 40 of the library's erff.
+__device__ __forceinline__ float normal_tail(float x) {
+    const float t = __builtin_amdgcn_rcpf(fmaf(x, 0.36f, 1.0f));
+    float p = 0.0470560603f;
+    p = fmaf(p, t, -0.179763913f);
+    p = fmaf(p, t, 0.180952996f);
+    p = fmaf(p, t, 0.0265499931f);
+    p = fmaf(p, t, 0.139719039f);
+    p = fmaf(p, t, 0.141772494f);
+    p = fmaf(p, t, 0.143713042f);
+    p *= t;
+    // 2^(-x^2 log2(e) / 2)
+    return p * __builtin_amdgcn_exp2f(x * x * -0.72134752f);
+}
+
+// act(z) for four or eight outputs. The switch is uniform and outside the
+// elements: silu and the tanh form are z / (1 + 2^-u), and z Phi(z) =
+// max(z, 0) - |z| Phi(-|z|).
+template <int V>
+__device__ __forceinline__ void activate(int act, float (&z)[V]) {
+    if (act == kActNone) return;
+    if (act == kActRelu) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) z[e] = z[e] < 0.0f ? 0.0f : z[e];
+    } else if (act == kActGelu) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            const float a = fabsf(z[e]);
+            z[e] = (z[e] < 0.0f ? 0.0f : z[e]) - fminf(a, 40.0f) * normal_tail(a);  // (infinite times 0)
+        }
+    } else {
+        // (Below -200 the quotient is 0, which -inf must not meet.)
+        constexpr float c = 2.0f * kSqrt2OverPi * kLog2e;
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            const float u = act == kActSilu ? z[e] * kLog2e : z[e] * fmaf(z[e] * z[e], c * 0.044715f, c);
+            z[e] = fmaxf(z[e], -200.0f) * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-u));
+        }
+    }
+}
+
+// act'(z); beyond 200 it is the limit, 0 or 1, and a NaN stays one.
+__device__ __forceinline__ float act_slope(int act, float z) {
+    if (act == kActNone) return 1.0f;
+    if (act == kActRelu) return z > 0.0f ? 1.0f : z <= 0.0f ? 0.0f : z;
+    z = fabsf(z) > 200.0f ? copysignf(200.0f, z) : z;
+    if (act == kActGelu) {
+        const float q = normal_tail(fabsf(z));
+        // z phi(z)
+        const float d = z * (kInvSqrt2Pi * __builtin_amdgcn_exp2f(z * z * -0.72134752f));
+        return (z < 0.0f ? q : 1.0f - q) + d;
+    }
+    // p = 1 / (1 + exp(-u)): p + z p (1 - p) u'
+    const float c = act == kActSilu ? 1.0f : 2.0f * kSqrt2OverPi, d = act == kActSilu ? 0.0f : c * 0.044715f;
+    const float u = z * fmaf(z * z, d, c), du = fmaf(z * z, 3.0f * d, c);
+    const float e = __builtin_amdgcn_exp2f(-fabsf(u) * kLog2e), r = __builtin_amdgcn_rcpf(1.0f + e);
+    const float p = u < 0.0f ? e * r : r;
+    return p + z * (e * r * r) * du;
+}
+
 // GATED: v gate, up up (saved to a.gate_up if asked for) -> silu(gate) * up;
-// else v + addend.
+// else act(v + bias) (v + bias saved to a.pre if asked for) + addend.
 //
 // What is rounded to bf16 before its end: h (here and in the tiles), and in the
 // backward dgate, dup and h, once each. They are operands of the next product on
@@ -89,12 +163,15 @@ __device__ __forceinline__ f32x4 finish4(const DenseArgs& a, int64_t token, int 
         }
 #pragma unroll
         for (int r = 0; r < 4; ++r) v[r] = v[r] * sigmoid(v[r]) * up[r];
-    } else if (a.addend) {
-        const u32x2 d = *(const u32x2*)(a.addend + token * a.ldadd + col);
-        v[0] += __uint_as_float(d[0] << 16);
-        v[1] += __uint_as_float(d[0] & 0xffff0000u);
-        v[2] += __uint_as_float(d[1] << 16);
-        v[3] += __uint_as_float(d[1] & 0xffff0000u);
+    } else {
+        if (a.bias) v += load4(a.bias, a.bias_f32, col);
+        if (a.pre) *(u32x2*)(a.pre + token * (int64_t)a.N + col) = pack4(v);
+        if (a.act) {
+            float z[4] = {v[0], v[1], v[2], v[3]};
+            activate<4>(a.act, z);
+            v = f32x4{z[0], z[1], z[2], z[3]};
+        }
+        if (a.addend) v += load4(a.addend, a.addend_f32, token * a.ldadd + col);
     }
     return v;
 }

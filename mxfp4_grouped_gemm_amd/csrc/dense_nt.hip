@@ -54,7 +54,9 @@ hipError_t launch_epi(const DenseArgs& a, hipStream_t s) {
     if (dense_big_tiles(a, EPI))
         return launch_tile<Tile<256, 256, 2, 4, false, false, kEltBf16, EPI, false, LORA>>(a, s);
     if (a.splits > 1) {
-        const hipError_t e = launch_tile<Tile<128, 128, 2, 2, false, false, kEltBf16, EPI, true, false, 4>>(a, s);
+        // (Parts are stored before any epilogue.)
+        constexpr int kPart = EPI == kEpiAct ? kEpiOut : EPI;
+        const hipError_t e = launch_tile<Tile<128, 128, 2, 2, false, false, kEltBf16, kPart, true, false, 4>>(a, s);
         return e != hipSuccess ? e : launch_join(a, EPI, s);
     }
     if (dense_one_round(a, EPI)) return launch_tile<Tile<128, 128, 2, 2, false, false, kEltBf16, EPI, false, LORA, 4>>(a, s);
@@ -66,21 +68,21 @@ hipError_t launch_epi(const DenseArgs& a, hipStream_t s) {
 // 256 x 256 tiles when they come close to filling the 256 compute units, else
 // 128 x 128 ones, which read twice the LDS bytes for a product.
 bool dense_big_tiles(const DenseArgs& a, int epi) {
-    const bool gated = epi == kEpiGated || epi == kEpiGatedMx;
+    const bool gated = epi_gated(epi);
     const int64_t cols = gated ? 2 * (int64_t)a.N : a.N;
     return (int64_t)((a.M + 255) / 256) * ((cols + 255) / 256) >= 160;
 }
 
 // 128 x 128 tiles with at most one workgroup a compute unit.
 bool dense_one_round(const DenseArgs& a, int epi) {
-    const bool gated = epi == kEpiGated || epi == kEpiGatedMx;
+    const bool gated = epi_gated(epi);
     const int64_t cols = gated ? 2 * (int64_t)a.N : a.N;
     return (int64_t)((a.M + 127) / 128) * ((cols + 127) / 128) <= 256;
 }
 
 int dense_splits(const DenseArgs& a, int elt, int epi) {
     if (dense_big_tiles(a, epi)) return 1;
-    const bool gated = epi == kEpiGated || epi == kEpiGatedMx;
+    const bool gated = epi_gated(epi);
     const int64_t cols = gated ? 2 * (int64_t)a.N : a.N;
     const int64_t tiles = (int64_t)((a.M + 127) / 128) * ((cols + 127) / 128);
     if (tiles == 0) return 1;  // no tokens
@@ -97,7 +99,7 @@ hipError_t launch_join(const DenseArgs& a, int epi, hipStream_t s) {
     // Small ones are latency: spread them over the compute units.
     const int size = threads < 256 * 256 ? 64 : 256;
     const dim3 grid((unsigned)((threads + size - 1) / size)), block(size);
-    if (epi == kEpiOut) hipLaunchKernelGGL(join_kernel<kEpiOut>, grid, block, 0, s, a);
+    if (epi == kEpiOut || epi == kEpiAct) hipLaunchKernelGGL(join_kernel<kEpiOut>, grid, block, 0, s, a);
     else if (epi == kEpiGated) hipLaunchKernelGGL(join_kernel<kEpiGated>, grid, block, 0, s, a);
     else if (epi == kEpiGatedMx) hipLaunchKernelGGL(join_kernel<kEpiGatedMx>, grid, block, 0, s, a);
     else hipLaunchKernelGGL(join_kernel<kEpiGatedBwd>, grid, block, 0, s, a);
@@ -105,6 +107,7 @@ hipError_t launch_join(const DenseArgs& a, int epi, hipStream_t s) {
 }
 
 hipError_t launch_dense_nt(const DenseArgs& a, int epi, hipStream_t s) {
+    if (epi == kEpiAct) return launch_epi<kEpiAct, false>(a, s);
     if (epi == kEpiOut) return a.lora.n > 0 ? launch_epi<kEpiOut, true>(a, s) : launch_epi<kEpiOut, false>(a, s);
     return a.lora.n > 0 ? launch_epi<kEpiGated, true>(a, s) : launch_epi<kEpiGated, false>(a, s);
 }

@@ -285,7 +285,7 @@ bool skinny_wide(const DenseArgs& a, bool gated) { return (gated ? 2 * (int64_t)
 int skinny_narrow(const DenseArgs& a) { return a.lora.n > 0 ? a.M * ((a.lora.rank + 15) / 16) : 0; }
 
 int skinny_splits(const DenseArgs& a, int elt, int epi) {
-    const bool gated = epi != kEpiOut;
+    const bool gated = epi_gated(epi);
     const int64_t rows = gated ? 2 * (int64_t)a.N : a.N;
     if (elt != kEltBf16 || one_kernel(a, gated)) return 1;
     const int64_t groups = skinny_wide(a, gated) ? (rows + 63) / 64 : (rows + 15) / 16;
@@ -297,12 +297,12 @@ int skinny_splits(const DenseArgs& a, int elt, int epi) {
 }
 
 bool skinny_joins(const DenseArgs& a, int splits, int elt, int epi) {
-    const bool gated = epi != kEpiOut;
+    const bool gated = epi_gated(epi);
     return elt == kEltBf16 && (a.lora.n > 0 || splits > 1 || (!one_kernel(a, gated) && skinny_wide(a, gated)));
 }
 
 hipError_t launch_skinny(const DenseArgs& a, int elt, int epi, const float* h_f32, hipStream_t s) {
-    const bool gated = epi != kEpiOut;
+    const bool gated = epi_gated(epi);
     if (elt == kEltBf16)
         return gated ? launch_nj<kEltBf16, true, false>(a, nullptr, s) : launch_nj<kEltBf16, false, false>(a, nullptr, s);
     return gated ? launch_nj<kEltMx8, true, false>(a, nullptr, s) : launch_nj<kEltMx8, false, true>(a, h_f32, s);

@@ -760,9 +760,22 @@ __device__ __forceinline__ void dense_tile(const DenseArgs& a, int id, int part,
     // could be to the same place).
     constexpr int V = C::F % 2 ? 4 : 8;          // consecutive outputs of a lane
     constexpr int VN = C::F * 4 / V;             // groups of them
-    constexpr bool kBwd = C::EPI == kEpiGatedBwd, kReads = C::EPI == kEpiOut || kBwd;
-    constexpr int JB = kBwd && C::FM > 4 ? C::FM / 2 : C::FM;  // tokens a batch
-    uint32_t ra[kReads ? JB : 1][VN][V / 2], rb[kBwd ? JB : 1][VN][V / 2];
+    constexpr bool kBwd = C::EPI == kEpiGatedBwd, kAct = C::EPI == kEpiAct, kReads = C::EPI == kEpiOut || kBwd || kAct;
+    constexpr int JB = (kBwd || kAct) && C::FM > 4 ? C::FM / 2 : C::FM;  // tokens a batch
+    uint32_t ra[kReads ? JB : 1][VN][V / 2], rb[kBwd || kAct ? JB : 1][VN][V / 2];
+    float bias[kAct ? VN : 1][V];
+    if constexpr (kAct) {
+#pragma unroll
+        for (int v = 0; v < VN; ++v)
+#pragma unroll
+            for (int e = 0; e < V; e += 4) {
+                const int n = n_of(v * (V / 4)) + e;
+                f32x4 b = {0, 0, 0, 0};
+                if (a.bias && n < a.N) b = load4(a.bias, a.bias_f32, n);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) bias[v][e + k] = b[k];
+            }
+    }
 #pragma unroll
     for (int j = 0; j < C::FM; ++j) {
         const int m = m_of(j);
@@ -779,13 +792,17 @@ __device__ __forceinline__ void dense_tile(const DenseArgs& a, int id, int part,
                             const uint16_t* gu = a.gate_up + mm * 2 * (int64_t)a.N + n;
                             load_words<V / 2>(ra[jj][v], gu);
                             load_words<V / 2>(rb[jj][v], gu + a.N);
+                        } else if (kAct && a.addend_f32) {
+                            const float* d = (const float*)a.addend + mm * a.ldadd + n;
+                            load_words<V / 2>(ra[jj][v], d);
+                            load_words<V / 2>(rb[jj][v], d + V / 2);
                         } else {
-                            load_words<V / 2>(ra[jj][v], a.addend + mm * a.ldadd + n);
+                            load_words<V / 2>(ra[jj][v], (const uint16_t*)a.addend + mm * a.ldadd + n);
                         }
                     }
             }
         }
-        if constexpr (C::EPI == kEpiOut) {
+        if constexpr (C::EPI == kEpiOut || kAct) {
             if (!mok) continue;
 #pragma unroll
             for (int f = 0; f < C::FN; f += V / 4) {
@@ -794,7 +811,17 @@ __device__ __forceinline__ void dense_tile(const DenseArgs& a, int id, int part,
                 float v[V];
 #pragma unroll
                 for (int e = 0; e < V; ++e) v[e] = acc[f + e / 4][j][e % 4];
-                if (a.addend) {
+                if constexpr (kAct) {
+#pragma unroll
+                    for (int e = 0; e < V; ++e) v[e] += bias[f / (V / 4)][e];
+                    if (a.pre) store_bf16<V>(a.pre + m * (int64_t)a.N + n, v);
+                    activate<V>(a.act, v);
+                }
+                if (kAct && a.addend_f32) {
+#pragma unroll
+                    for (int e = 0; e < V; ++e)
+                        v[e] += __uint_as_float(e < V / 2 ? ra[j % JB][f / (V / 4)][e] : rb[j % JB][f / (V / 4)][e - V / 2]);
+                } else if (a.addend) {
                     const auto& d = ra[j % JB][f / (V / 4)];
 #pragma unroll
                     for (int e = 0; e < V; ++e) v[e] += __uint_as_float(e & 1 ? d[e / 2] & 0xffff0000u : d[e / 2] << 16);

@@ -1,0 +1,109 @@
+// Arguments and launchers of the operators of a trainable expert block: layer
+// norm with its backward pass, rows sorted by expert and back, and what the
+// product with bias and activation needs beside the dense tiles.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "dense.hpp"
+
+namespace moe {
+
+struct LayerNormArgs {
+    const uint16_t* x;
+    const void* residual;
+    const void* weight;
+    const void* bias;
+    void* residual_out;
+    uint16_t* y;
+    float* mean;
+    float* rstd;
+    int64_t ldx, ldr, ldro, ldy;
+    int T, H;
+    float eps;
+    int res_f32, weight_f32;
+};
+hipError_t launch_layer_norm(const LayerNormArgs& a, hipStream_t s);
+
+struct LayerNormBwdArgs {
+    const uint16_t* dy;
+    const void* s;
+    const float* mean;
+    const float* rstd;
+    const void* weight;
+    const void* dres;  // gradient that reaches s from elsewhere, or null
+    uint16_t* dx;
+    void* dresidual;  // of s's type
+    float* partial;   // [layer_norm_parts, 2 H], where sums over the rows are asked for
+    void* dweight;
+    void* dbias;
+    int64_t lddy, lds, lddr, lddx, lddro;
+    int T, H;
+    int s_f32, weight_f32;
+};
+// Parts that the sums over the rows are taken in.
+int layer_norm_parts(int T, int H);
+hipError_t launch_layer_norm_bwd(const LayerNormBwdArgs& a, hipStream_t s);
+
+// Sums partial [parts, cols] (fp32) over the parts, in order: columns below
+// `first` go to out0, the others to out1; either may be null.
+hipError_t launch_join_columns(const float* partial, int parts, int cols, int first, void* out0, void* out1, bool f32,
+                               hipStream_t s);
+
+// dz = dout act'(pre) and its sums over the rows. dz may be null (dz == dout).
+struct LinearDzArgs {
+    const void* dout;
+    const uint16_t* pre;
+    uint16_t* dz;
+    float* partial;  // [linear_dz_parts, N] or null
+    int64_t lddo;
+    int T, N;
+    int dout_f32, act;
+};
+int linear_dz_parts(int T, int N);
+hipError_t launch_linear_dz(const LinearDzArgs& a, hipStream_t s);
+
+// Rows of elt bytes an element. `rows` [T, topk]: the sorted row of each pair,
+// -1 - row for a pair of no expert.
+struct PermuteArgs {
+    const void* x;
+    void* out;
+    const int32_t* ids;
+    int32_t* rows;
+    int32_t* offsets;
+    int32_t* counts;  // [permute_chunks, E + 1] (none for few pairs)
+    int64_t ldx, ldo; // bytes
+    int64_t row_bytes;
+    int T, topk, E;
+};
+int64_t permute_workspace_bytes(int64_t pairs, int E);
+hipError_t launch_permute(const PermuteArgs& a, hipStream_t s);
+
+struct UnpermuteArgs {
+    const void* y;
+    const int32_t* rows;
+    const float* weights;  // or null: 1
+    const void* residual;
+    void* out;
+    int64_t ldy, ldr, ldo;
+    int64_t pairs;  // rows of y
+    int T, topk, H;
+    int y_f32, out_f32;
+};
+hipError_t launch_unpermute(const UnpermuteArgs& a, hipStream_t s);
+
+struct UnpermuteBwdArgs {
+    const void* dout;
+    const int32_t* rows;
+    const float* weights;
+    const void* y;
+    void* dy;        // or null
+    float* dweights; // or null (needs y)
+    int64_t lddo, ldy, lddy;
+    int T, topk, H;
+    int y_f32, out_f32;
+};
+hipError_t launch_unpermute_bwd(const UnpermuteBwdArgs& a, hipStream_t s);
+
+}  // namespace moe
