@@ -844,6 +844,21 @@ _DT = {torch.bfloat16: MOE_DT_BF16, torch.float32: MOE_DT_F32, torch.uint8: MOE_
        torch.float8_e8m0fnu: MOE_DT_U8}
 
 
+def _gradient(need, given, name, like, stride, shape, stream):
+    """A gradient of like's type and shape (its row stride, or 0 for a
+    vector), made unless given -> (tensor, address, row stride); None where it
+    is not needed."""
+    cols = shape[-1]
+    if not need:
+        return None, None, cols
+    if given is None:
+        given = _like(like, stride or cols, cols, stream)
+        return given, given.data_ptr(), cols
+    if not stride:
+        return given, _full(given, name, like.dtype, shape, like.device), cols
+    return given, *_rows(given, name, like.dtype, shape, like.device)
+
+
 def moe_layer_norm_forward(x, weight, bias=None, residual=None, eps=1e-5, save_stats=False, y=None, residual_out=None,
                            mean=None, rstd=None, stream=None):
     """Residual addition and layer norm of x bf16 [T, H]: s = x + residual,
@@ -912,26 +927,17 @@ def moe_layer_norm_backward(dy, s, mean, rstd, weight, dresidual_out=None, need_
     pr, ldr = (None, H) if dresidual_out is None else _rows(dresidual_out, "dresidual_out", s.dtype, (T, H), device)
     if not (need_dx or need_dresidual or need_dweight or need_dbias):
         return None, None, None, None
-    if need_dx and dx is None:
-        dx = _empty((T, H), torch.bfloat16, device, stream)
-    if need_dresidual and dresidual is None:
-        dresidual = _empty((T, H), s.dtype, device, stream)
-    if need_dweight and dweight is None:
-        dweight = _empty((H,), weight.dtype, device, stream)
-    if need_dbias and dbias is None:
-        dbias = _empty((H,), weight.dtype, device, stream)
-    px, lddx = (None, H) if not need_dx else _rows(dx, "dx", torch.bfloat16, (T, H), device)
-    po, lddo = (None, H) if not need_dresidual else _rows(dresidual, "dresidual", s.dtype, (T, H), device)
-    pdw = None if not need_dweight else _full(dweight, "dweight", weight.dtype, (H,), device)
-    pdb = None if not need_dbias else _full(dbias, "dbias", weight.dtype, (H,), device)
+    dx, px, lddx = _gradient(need_dx, dx, "dx", dy, ldd, (T, H), stream)
+    dresidual, po, lddo = _gradient(need_dresidual, dresidual, "dresidual", s, lds, (T, H), stream)
+    dweight, pdw, _ = _gradient(need_dweight, dweight, "dweight", weight, 0, (H,), stream)
+    dbias, pdb, _ = _gradient(need_dbias, dbias, "dbias", weight, 0, (H,), stream)
     need = lib.moe_layer_norm_backward_workspace_size(T, H) if need_dweight or need_dbias else 0
     pws, nws, _ws = _workspace(workspace, need, device, stream)
     _run(device, stream, lib.moe_layer_norm_backward,
          pd, ldd, ps, lds, MOE_DT_F32 if s.dtype is torch.float32 else MOE_DT_BF16, pm, pq, pw,
          MOE_DT_F32 if weight.dtype is torch.float32 else MOE_DT_BF16, pr, ldr, T, H, px, lddx, po, lddo, pdw, pdb,
          pws, nws)
-    return (dx if need_dx else None, dresidual if need_dresidual else None, dweight if need_dweight else None,
-            dbias if need_dbias else None)
+    return dx, dresidual, dweight, dbias
 
 
 def _dense(t):
@@ -998,11 +1004,15 @@ def moe_permute(x, topk_ids, E, out=None, rows=None, expert_offsets=None, worksp
     else:
         po, ldo = _rows(out, "out", x.dtype, (T * topk, H), device)
     if rows is None:
-        rows = _empty((T, topk), torch.int32, device, stream)
+        rows = _like(topk_ids, topk, topk, stream)
+        pr = rows.data_ptr()
+    else:
+        pr = _full(rows, "rows", torch.int32, (T, topk), device)
     if expert_offsets is None:
         expert_offsets = _empty((max(E, 0) + 1,), torch.int32, device, stream)
-    pr = _full(rows, "rows", torch.int32, (T, topk), device)
-    pe = _full(expert_offsets, "expert_offsets", torch.int32, (E + 1,), device)
+        pe = expert_offsets.data_ptr()
+    else:
+        pe = _full(expert_offsets, "expert_offsets", torch.int32, (E + 1,), device)
     need = lib.moe_permute_workspace_size(T, topk, E)
     pws, nws, _ws = _workspace(workspace, max(need, 0), device, stream)
     _run(device, stream, lib.moe_permute, px, ldx, _DT[x.dtype], pi, T, topk, E, H, po, ldo, pr, pe, pws, nws)
@@ -1066,12 +1076,17 @@ def moe_unpermute_backward(dout, rows, y=None, weights=None, y_dtype=None, need_
         raise ValueError(f"y_dtype must be bfloat16 or float32, got {dtype}")
     if not (need_dy or need_dweights):
         return None, None
+    pdy, lddy, pdw = None, H, None
     if need_dy and dy is None:
         dy = _empty((T * topk, H), dtype, device, stream)
+        pdy = dy.data_ptr()
+    elif need_dy:
+        pdy, lddy = _rows(dy, "dy", dtype, (T * topk, H), device)
     if need_dweights and dweights is None:
         dweights = _empty((T, topk), torch.float32, device, stream)
-    pdy, lddy = (None, H) if not need_dy else _rows(dy, "dy", dtype, (T * topk, H), device)
-    pdw = None if not need_dweights else _full(dweights, "dweights", torch.float32, (T, topk), device)
+        pdw = dweights.data_ptr()
+    elif need_dweights:
+        pdw = _full(dweights, "dweights", torch.float32, (T, topk), device)
     _run(device, stream, lib.moe_unpermute_backward,
          pd, ldd, MOE_DT_F32 if dout.dtype is torch.float32 else MOE_DT_BF16, pr, pw, py, ldy,
          MOE_DT_F32 if dtype is torch.float32 else MOE_DT_BF16, T, topk, H, pdy, lddy, pdw)
@@ -1189,22 +1204,23 @@ def moe_linear_backward(dout, x, w, pre=None, act=MOE_LINEAR_NONE, need_dx=True,
     pp = None if pre is None else _full(pre, "pre", torch.bfloat16, (T, N), device)
     if not (need_dx or need_dw or need_dbias):
         return None, None, None
-    if need_dx and dx is None:
-        dx = _empty((T, K), torch.bfloat16, device, stream)
-    if need_dw and dw is None:
-        dw = _empty((N, K), torch.bfloat16, device, stream)
+    dx, pdx, lddx = _gradient(need_dx, dx, "dx", x, ldx, (T, K), stream)
+    dw, pdw, _ = _gradient(need_dw, dw, "dw", w, K, (N, K), stream)
+    if need_dw and not dw.is_contiguous():
+        raise ValueError(f"dw must be contiguous, got strides {dw.stride()}")
+    pdb = None
     if need_dbias and dbias is None:
         if bias_dtype not in _FLOATS:
             raise ValueError(f"bias_dtype must be bfloat16 or float32, got {bias_dtype}")
         dbias = _empty((N,), bias_dtype, device, stream)
-    pdx, lddx = (None, K) if not need_dx else _rows(dx, "dx", torch.bfloat16, (T, K), device)
-    pdw = None if not need_dw else _full(dw, "dw", torch.bfloat16, (N, K), device)
-    pdb = None if not need_dbias else _full(dbias, "dbias", _FLOATS, (N,), device)
+        pdb = dbias.data_ptr()
+    elif need_dbias:
+        pdb = _full(dbias, "dbias", _FLOATS, (N,), device)
     pws, nws, _ws = _workspace(workspace, lib.moe_linear_backward_workspace_size(T, K, N), device, stream)
     _run(device, stream, lib.moe_linear_backward,
          pd, ldd, MOE_DT_F32 if dout.dtype is torch.float32 else MOE_DT_BF16, px, ldx, pp, pw, act, T, K, N, pdx, lddx,
          pdw, pdb, MOE_DT_F32 if need_dbias and dbias.dtype is torch.float32 else MOE_DT_BF16, pws, nws)
-    return dx if need_dx else None, dw if need_dw else None, dbias if need_dbias else None
+    return dx, dw, dbias if need_dbias else None
 
 
 class _Linear(torch.autograd.Function):

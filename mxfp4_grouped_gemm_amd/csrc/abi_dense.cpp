@@ -456,7 +456,7 @@ moe_status moe_ffn_backward(const uint16_t* dout, int64_t dout_stride, const uin
     moe::DenseArgs gx = product(dgu, 2 * (int64_t)I, w13, H, T, H, 2 * I, dx, dx_stride);
     gx.splits = L.splits_dx;
     gx.partial = partial;
-    return hip_status(moe::launch_dense_grads(g13, g2, gx, s), "moe_ffn_backward (gradients)");
+    return hip_status(moe::launch_dense_grads(g13, g2, gx, moe::ColumnJoin{}, s), "moe_ffn_backward (gradients)");
 }
 
 moe_status moe_layer_norm_forward(const uint16_t* x, int64_t x_stride, const void* residual, int64_t residual_stride,
@@ -502,7 +502,7 @@ moe_status moe_layer_norm_forward(const uint16_t* x, int64_t x_stride, const voi
 
 int64_t moe_layer_norm_backward_workspace_size(int T, int H) {
     if (T < 0 || T > kMaxTokens || H < 1 || H > kMaxNormed) return -1;
-    return align_up((int64_t)moe::layer_norm_parts(T, H) * 2 * H * 4, 256);
+    return align_up((int64_t)moe::layer_norm_parts(T, H) * 2 * align_up(H, 8) * 4, 256);
 }
 
 moe_status moe_layer_norm_backward(const uint16_t* dy, int64_t dy_stride, const void* s, int64_t s_stride,
@@ -606,7 +606,6 @@ moe_status moe_linear_backward(const void* dout, int64_t dout_stride, moe_dtype 
         return fail(MOE_ERR_INVALID_ARG, "%s: outputs must be 16-byte aligned", fn);
     hipStream_t s = (hipStream_t)stream;
     const LinearBwdLayout L = linear_bwd_layout(T, K, N);
-    const bool f32 = bias_type == MOE_DT_F32;
     const uint16_t* dz = (const uint16_t*)dout;
     int64_t lddz = dout_stride;
     if (T > 0) {
@@ -631,19 +630,16 @@ moe_status moe_linear_backward(const void* dout, int64_t dout_stride, moe_dtype 
             lddz = N;
         }
         if (dbias || (z.dz && (dx || dw))) LAUNCH(moe::launch_linear_dz(z, s), "moe_linear_backward (dz)");
-        if (dbias)
-            LAUNCH(moe::launch_join_columns(z.partial, moe::linear_dz_parts(T, N), N, N, dbias, nullptr, f32, s),
-                   "moe_linear_backward (bias)");
-    } else if (dbias) {
-        LAUNCH(moe::launch_join_columns(nullptr, 0, N, N, dbias, nullptr, f32, s), "moe_linear_backward (bias)");
     }
-    if (!dx && !dw) return MOE_OK;
-    // With T == 0 the weights' sum is empty and writes zeros.
+    // (With T == 0 the sums are empty and write zeros.)
+    const moe::ColumnJoin sums = {(const float*)((char*)workspace + L.sums), dbias, nullptr, T > 0 ? moe::linear_dz_parts(T, N) : 0,
+                                  N, N, 1, bias_type == MOE_DT_F32};
+    if (!dx && !dw) return hip_status(moe::launch_column_join(sums, true, s), "moe_linear_backward (bias)");
     const moe::DenseArgs gw = product(dz, lddz, x, x_stride, N, K, T, dw, K);
     moe::DenseArgs gx = product(dz, lddz, w, K, T, K, N, dx, dx_stride);
     gx.splits = L.splits_dx;
     gx.partial = (float*)((char*)workspace + L.partial);
-    return hip_status(moe::launch_dense_grads(gw, product(nullptr, 0, nullptr, 0, 0, 0, 0, nullptr, 0), gx, s),
+    return hip_status(moe::launch_dense_grads(gw, product(nullptr, 0, nullptr, 0, 0, 0, 0, nullptr, 0), gx, sums, s),
                       "moe_linear_backward (gradients)");
 }
 

@@ -6,6 +6,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "column_join.hpp"
+
 namespace moe {
 
 // A stack of low-rank adapters beside one projection [N, K]: token t adds
@@ -86,7 +88,9 @@ hipError_t launch_dense_mx(const DenseArgs& a, int epi, hipStream_t s);
 // (Their a.splits: dense_bwd_splits, of dh and of dx.)
 int dense_bwd_splits(const DenseArgs& a);
 hipError_t launch_dense_dh(const DenseArgs& a, hipStream_t s);
-hipError_t launch_dense_grads(const DenseArgs& dw13, const DenseArgs& dw2, const DenseArgs& dx, hipStream_t s);
+// (sums: a bias gradient to be joined in the same launch, or no outputs.)
+hipError_t launch_dense_grads(const DenseArgs& dw13, const DenseArgs& dw2, const DenseArgs& dx, const ColumnJoin& sums,
+                              hipStream_t s);
 
 // Up to this many tokens the products stream the weights without LDS tiles.
 // (MXFP8 with H = 3584, I = 2048: 33 us at 64 tokens, 26 in tiles, where h is

@@ -19,6 +19,8 @@ struct GradArgs {
     DenseArgs dw13, dw2, dx;
     int n13, n2, nx;  // tiles of each
     int dx_first;
+    ColumnJoin sums;
+    int nsums;        // its workgroups, ahead of the tiles
 };
 
 // TN: tiles of the weight gradients; NN: of dx. Same buffers.
@@ -26,7 +28,12 @@ template <class TN, class NN>
 __global__ __launch_bounds__(TN::THREADS, 2) void grad_kernel(GradArgs g) {
     static_assert(TN::BUF == NN::BUF && TN::NB == NN::NB && TN::THREADS == NN::THREADS, "one launch");
     MOE_TILE_BUFFERS(s, TN::NB, TN::BUF);
-    int id = (int)blockIdx.x;
+    int id = (int)blockIdx.x - g.nsums;
+    if (id < 0) {
+        static_assert(TN::BUF >= column_join_lds(kFewRuns) && TN::THREADS >= 8 * kFewRuns, "the sums meet in a tile's buffer");
+        column_join<kFewRuns>(g.sums, (int)blockIdx.x, (float*)s[0]);
+        return;
+    }
     if (g.dx_first) {
         id = id < g.nx ? g.n13 + g.n2 + id : id - g.nx;
     }
@@ -47,7 +54,8 @@ hipError_t launch_grad(GradArgs& g, hipStream_t s) {
     g.n2 = g.dw2.out ? (int)tiles_of<TN>(g.dw2) : 0;
     g.nx = g.dx.out ? (int)tiles_of<NN>(g.dx) : 0;
     g.dx_first = g.dx.K > g.dw13.K;
-    const int64_t grid = (int64_t)g.n13 + g.n2 + g.nx;
+    g.nsums = g.sums.out0 ? column_join_groups(g.sums) : 0;
+    const int64_t grid = (int64_t)g.n13 + g.n2 + g.nx + g.nsums;
     if (grid == 0) return hipSuccess;
     hipLaunchKernelGGL((grad_kernel<TN, NN>), dim3((unsigned)grid), dim3(TN::THREADS), 0, s, g);
     return hipGetLastError();
@@ -93,8 +101,10 @@ static hipError_t launch_nn(const DenseArgs& a, hipStream_t s) {
 
 hipError_t launch_dense_dh(const DenseArgs& a, hipStream_t s) { return launch_nn<kEpiGatedBwd>(a, s); }
 
-hipError_t launch_dense_grads(const DenseArgs& dw13, const DenseArgs& dw2, const DenseArgs& dx, hipStream_t s) {
+hipError_t launch_dense_grads(const DenseArgs& dw13, const DenseArgs& dw2, const DenseArgs& dx, const ColumnJoin& sums,
+                              hipStream_t s) {
     GradArgs g;
+    g.sums = sums;
     g.dw13 = dw13;
     g.dw2 = dw2;
     g.dx = dx;

@@ -84,8 +84,8 @@ constexpr float kLog2e = 1.44269504f, kSqrt2OverPi = 0.797884561f, kInvSqrt2Pi =
 // exp(-x^2 / 2) P(t) with t = 1 / (1 + 0.36 x) and P the polynomial of degree 7
 // with P(0) = 0 whose largest relative error is least for x in [0, 14], 8.7e-7
 // (beyond, fp32 holds no more of it). z Phi(z) is off by 2e-7 at most; about 16
-// vector instructions, against some 40 of the library's erff.
-__device__ __forceinline__ float normal_tail(float x) {
+// vector instructions, against some 40 of the library's erff. This is P.
+__device__ __forceinline__ float normal_tail_factor(float x) {
     const float t = __builtin_amdgcn_rcpf(fmaf(x, 0.36f, 1.0f));
     float p = 0.0470560603f;
     p = fmaf(p, t, -0.179763913f);
@@ -94,10 +94,11 @@ __device__ __forceinline__ float normal_tail(float x) {
     p = fmaf(p, t, 0.139719039f);
     p = fmaf(p, t, 0.141772494f);
     p = fmaf(p, t, 0.143713042f);
-    p *= t;
-    // 2^(-x^2 log2(e) / 2)
-    return p * __builtin_amdgcn_exp2f(x * x * -0.72134752f);
+    return p * t;
 }
+
+// exp(-z^2 / 2)
+__device__ __forceinline__ float gauss(float z) { return __builtin_amdgcn_exp2f(z * z * (-0.5f * kLog2e)); }
 
 // act(z) for four or eight outputs. The switch is uniform and outside the
 // elements: silu and the tanh form are z / (1 + 2^-u), and z Phi(z) =
@@ -111,8 +112,9 @@ __device__ __forceinline__ void activate(int act, float (&z)[V]) {
     } else if (act == kActGelu) {
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-            const float a = fabsf(z[e]);
-            z[e] = (z[e] < 0.0f ? 0.0f : z[e]) - fminf(a, 40.0f) * normal_tail(a);  // (infinite times 0)
+            // (Infinite times 0 is not met; a NaN comes through the factor.)
+            const float tail = normal_tail_factor(fabsf(z[e])) * gauss(z[e]);
+            z[e] = fmaf(-__builtin_amdgcn_fmed3f(fabsf(z[e]), 0.0f, 40.0f), tail, __builtin_amdgcn_fmed3f(z[e], 0.0f, __builtin_inff()));
         }
     } else {
         // (Below -200 the quotient is 0, which -inf must not meet.)
@@ -125,23 +127,22 @@ __device__ __forceinline__ void activate(int act, float (&z)[V]) {
     }
 }
 
-// act'(z); beyond 200 it is the limit, 0 or 1, and a NaN stays one.
+// act'(z); far out it is the limit, 0 or 1, and a NaN stays one.
 __device__ __forceinline__ float act_slope(int act, float z) {
     if (act == kActNone) return 1.0f;
     if (act == kActRelu) return z > 0.0f ? 1.0f : z <= 0.0f ? 0.0f : z;
-    z = fabsf(z) > 200.0f ? copysignf(200.0f, z) : z;
+    const float near = __builtin_amdgcn_fmed3f(z, -200.0f, 200.0f);  // what meets a 0
     if (act == kActGelu) {
-        const float q = normal_tail(fabsf(z));
-        // z phi(z)
-        const float d = z * (kInvSqrt2Pi * __builtin_amdgcn_exp2f(z * z * -0.72134752f));
-        return (z < 0.0f ? q : 1.0f - q) + d;
+        // Phi(z) + z phi(z)
+        const float g = gauss(z), q = normal_tail_factor(fabsf(z)) * g;
+        return fmaf(near, kInvSqrt2Pi * g, z < 0.0f ? q : 1.0f - q);
     }
     // p = 1 / (1 + exp(-u)): p + z p (1 - p) u'
     const float c = act == kActSilu ? 1.0f : 2.0f * kSqrt2OverPi, d = act == kActSilu ? 0.0f : c * 0.044715f;
-    const float u = z * fmaf(z * z, d, c), du = fmaf(z * z, 3.0f * d, c);
+    const float u = act == kActSilu ? z : z * fmaf(near * near, d, c);
+    const float du = act == kActSilu ? 1.0f : fmaf(near * near, 3.0f * d, c);
     const float e = __builtin_amdgcn_exp2f(-fabsf(u) * kLog2e), r = __builtin_amdgcn_rcpf(1.0f + e);
-    const float p = u < 0.0f ? e * r : r;
-    return p + z * (e * r * r) * du;
+    return fmaf(near * du, e * r * r, u < 0.0f ? e * r : r);
 }
 
 // GATED: v gate, up up (saved to a.gate_up if asked for) -> silu(gate) * up;

@@ -119,6 +119,24 @@ __device__ __forceinline__ void store_bf16(uint16_t* p, const float* v) {
         *(u32x2*)p = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
 }
 
+// Sixteen consecutive outputs of each lane of a row, whose lanes are 16 apart:
+// the halves trade places between lanes 32 apart, so that a store writes 64
+// bytes of a row in a run. `p`: the row's first output of the wave, n: the
+// columns from there on that exist.
+__device__ __forceinline__ void store_rows16(uint16_t* p, int g, int n, const float* v) {
+    u32x4 a = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+    u32x4 b = {pack_bf16x2(v[8], v[9]), pack_bf16x2(v[10], v[11]), pack_bf16x2(v[12], v[13]), pack_bf16x2(v[14], v[15])};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        auto r = __builtin_amdgcn_permlane32_swap(a[k], b[k], false, false);
+        a[k] = r[0];
+        b[k] = r[1];
+    }
+    const int at = (g & 1) * 16 + (g >> 1) * 8;
+    if (at < n) *(u32x4*)(p + at) = a;
+    if (at + 32 < n) *(u32x4*)(p + at + 32) = b;
+}
+
 // Waits until at most LOADS of this wave's loads are in flight and its LDS
 // reads are done, then for the workgroup. Loads complete in order, so what is
 // left in flight are the latest steps'.
@@ -802,7 +820,35 @@ __device__ __forceinline__ void dense_tile(const DenseArgs& a, int id, int part,
                     }
             }
         }
-        if constexpr (C::EPI == kEpiOut || kAct) {
+        if constexpr (kAct) {
+            static_assert(C::FN == 4, "sixteen outputs a lane");
+            if (!mok) continue;  // (the same in the lanes that trade)
+            float v[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] = acc[e / 4][j][e % 4] + bias[e / 8][e % 8];
+            const int nw = n0 + wn * 64;
+            if (a.pre) store_rows16(a.pre + m * (int64_t)a.N + nw, g, a.N - nw, v);
+            activate<16>(a.act, v);
+            if (a.addend_f32) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) v[e] += __uint_as_float(e % 8 < 4 ? ra[j % JB][e / 8][e % 4] : rb[j % JB][e / 8][e % 4]);
+            } else if (a.addend) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const uint32_t d = ra[j % JB][e / 8][e % 8 / 2];
+                    v[e] += __uint_as_float(e & 1 ? d & 0xffff0000u : d << 16);
+                }
+            }
+            if (a.out_f32) {
+#pragma unroll
+                for (int e = 0; e < 16; e += 4) {
+                    const int n = n_of(e / 4);
+                    if (n < a.N) *(f32x4*)((float*)a.out + m * a.ldo + n) = f32x4{v[e], v[e + 1], v[e + 2], v[e + 3]};
+                }
+            } else {
+                store_rows16((uint16_t*)a.out + m * a.ldo + nw, g, a.N - nw, v);
+            }
+        } else if constexpr (C::EPI == kEpiOut) {
             if (!mok) continue;
 #pragma unroll
             for (int f = 0; f < C::FN; f += V / 4) {
@@ -811,17 +857,7 @@ __device__ __forceinline__ void dense_tile(const DenseArgs& a, int id, int part,
                 float v[V];
 #pragma unroll
                 for (int e = 0; e < V; ++e) v[e] = acc[f + e / 4][j][e % 4];
-                if constexpr (kAct) {
-#pragma unroll
-                    for (int e = 0; e < V; ++e) v[e] += bias[f / (V / 4)][e];
-                    if (a.pre) store_bf16<V>(a.pre + m * (int64_t)a.N + n, v);
-                    activate<V>(a.act, v);
-                }
-                if (kAct && a.addend_f32) {
-#pragma unroll
-                    for (int e = 0; e < V; ++e)
-                        v[e] += __uint_as_float(e < V / 2 ? ra[j % JB][f / (V / 4)][e] : rb[j % JB][f / (V / 4)][e - V / 2]);
-                } else if (a.addend) {
+                if (a.addend) {
                     const auto& d = ra[j % JB][f / (V / 4)];
 #pragma unroll
                     for (int e = 0; e < V; ++e) v[e] += __uint_as_float(e & 1 ? d[e / 2] & 0xffff0000u : d[e / 2] << 16);

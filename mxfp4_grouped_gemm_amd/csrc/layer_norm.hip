@@ -16,7 +16,7 @@ using namespace rows;
 
 // WAVES waves hold a row of at most WAVES * 512 * NC elements. WAVES == 1:
 // four rows a workgroup.
-template <int WAVES, int NC, bool VEC>
+template <int WAVES, int NC, int MODE>
 __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void layer_norm_kernel(LayerNormArgs a) {
     constexpr int kLanes = WAVES * 64;
     const int tid = WAVES == 1 ? (int)threadIdx.x & 63 : (int)threadIdx.x;
@@ -28,21 +28,25 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void layer_norm_kern
     char* ro = (char*)a.residual_out + t * a.ldro * (a.res_f32 ? 4 : 2);
     const int H = a.H;
     auto first = [&](int c) { return (c * kLanes + tid) * 8; };
+    // (A lane past the row's end fetches its first eight, not used.)
+    auto inside = [&](int c) { return first(c) < H ? first(c) : 0; };
     f32x8 s[NC];
     double sum = 0.0, sq = 0.0;
+    Raw8 fx[NC], fr[NC];
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-        const int i = first(c);
-        s[c] = f32x8{0, 0, 0, 0, 0, 0, 0, 0};
-        if (i < H) {
-            s[c] = load8<VEC>(xr, false, i, H);
-            if (a.residual) s[c] += load8<VEC>(rr, a.res_f32, i, H);
-        }
+    for (int c = 0; c < NC; ++c) fx[c] = fetch8<MODE>(xr, false, inside(c), H);
+    if (a.residual) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c) fr[c] = fetch8<MODE>(rr, a.res_f32, inside(c), H);
     }
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
         const int i = first(c);
-        if (a.residual_out && i < H) store8<VEC>(ro, a.res_f32, i, H, s[c]);
+        s[c] = widen8<MODE>(fx[c], false, i, H);
+        if (a.residual) s[c] += widen8<MODE>(fr[c], a.res_f32, i, H);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[c][e] = i < H ? s[c][e] : 0.0f;
+        if (a.residual_out && i < H) put8<MODE>(ro, a.res_f32, i, H, s[c]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const double v = (double)s[c][e];
@@ -82,20 +86,24 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void layer_norm_kern
     for (int c = 0; c < NC; ++c) {
         const int i = first(c);
         if (i >= H) continue;
-        const f32x8 w = load8<VEC>(a.weight, a.weight_f32, i, H);
+        const Raw8 fw = fetch8<MODE>(a.weight, a.weight_f32, i, H);
+        Raw8 fb;
+        if (a.bias) fb = fetch8<MODE>(a.bias, a.weight_f32, i, H);
+        const f32x8 w = widen8<MODE>(fw, a.weight_f32, i, H);
         f32x8 v = {0, 0, 0, 0, 0, 0, 0, 0};
-        if (a.bias) v = load8<VEC>(a.bias, a.weight_f32, i, H);
+        if (a.bias) v = widen8<MODE>(fb, a.weight_f32, i, H);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = fmaf(((s[c][e] - mh) - ml) * rstd, w[e], v[e]);
-        store8<VEC>(a.y + t * a.ldy, false, i, H, v);
+        put8<MODE>(a.y + t * a.ldy, false, i, H, v);
     }
 }
 
 template <int WAVES, int NC>
 static void launch(const LayerNormArgs& a, bool vec, hipStream_t s) {
     const dim3 grid(WAVES == 1 ? (unsigned)((a.T + 3) / 4) : (unsigned)a.T), block(WAVES == 1 ? 256 : WAVES * 64);
-    if (vec) hipLaunchKernelGGL((layer_norm_kernel<WAVES, NC, true>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((layer_norm_kernel<WAVES, NC, false>), grid, block, 0, s, a);
+    if (vec) hipLaunchKernelGGL((layer_norm_kernel<WAVES, NC, kAligned>), grid, block, 0, s, a);
+    else if (a.H >= 8) hipLaunchKernelGGL((layer_norm_kernel<WAVES, NC, kAnywhere>), grid, block, 0, s, a);
+    else if constexpr (WAVES == 1) hipLaunchKernelGGL((layer_norm_kernel<WAVES, NC, kTiny>), grid, block, 0, s, a);
 }
 
 static bool wide(const void* p, int64_t ld, int bytes) {
@@ -136,8 +144,8 @@ hipError_t launch_layer_norm(const LayerNormArgs& a, hipStream_t s) {
 // ------------------------------------------------------------- backward
 // A workgroup goes through rows blockIdx.x, + gridDim.x, ... and keeps its
 // columns' sums of dy n and dy in registers, so the rows are read once.
-template <int WAVES, int NC, bool VEC, bool S32>
-__global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void layer_norm_bwd_kernel(LayerNormBwdArgs a) {
+template <int WAVES, int NC, int MODE, bool S32>
+__device__ __forceinline__ void layer_norm_bwd_rows(const LayerNormBwdArgs& a, int groups) {
     constexpr int kLanes = WAVES * 64, kRows = WAVES == 1 ? 4 : 1;
     const int tid = WAVES == 1 ? (int)threadIdx.x & 63 : (int)threadIdx.x;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -146,37 +154,45 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void layer_norm_bwd_
     __shared__ float part[WAVES > 1 ? 2 : 1][WAVES][2];
     auto first = [&](int c) { return (c * kLanes + tid) * 8; };
     const f32x8 zero = {0, 0, 0, 0, 0, 0, 0, 0};
-    f32x8 w[NC], aw[NC], ab[NC];
+    // (A lane past the row's end fetches its first eight, not used.)
+    auto inside = [&](int c) { return first(c) < H ? first(c) : 0; };
+    f32x8 aw[NC], ab[NC];
+    Raw8 fw[NC];
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-        aw[c] = ab[c] = w[c] = zero;
-        if (first(c) < H) w[c] = load8<VEC>(a.weight, a.weight_f32, first(c), H);
+        aw[c] = ab[c] = zero;
+        fw[c] = fetch8<MODE>(a.weight, a.weight_f32, inside(c), H);
     }
     int flip = 0;
-    for (int64_t t = (int64_t)blockIdx.x * kRows + (WAVES == 1 ? wave : 0); t < a.T; t += (int64_t)gridDim.x * kRows) {
+    const int64_t step = (int64_t)groups * kRows;
+    for (int64_t t = (int64_t)blockIdx.x * kRows + (WAVES == 1 ? wave : 0); t < a.T; t += step) {
         const float mean = a.mean[t], rstd = a.rstd[t];
-        const char* sr = (const char*)a.s + t * a.lds * (S32 ? 4 : 2);
-        f32x8 d[NC], n[NC];
+        Raw8 fd[NC], fs[NC], fr[NC];
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-            const int i = first(c);
-            d[c] = n[c] = zero;
-            if (i < H) {
-                d[c] = load8<VEC>(a.dy + t * a.lddy, false, i, H);
-                n[c] = load8<VEC>(sr, S32, i, H);
-            }
+            fd[c] = fetch8<MODE>(a.dy + t * a.lddy, false, inside(c), H);
+            fs[c] = fetch8<MODE>((const char*)a.s + t * a.lds * (S32 ? 4 : 2), S32, inside(c), H);
         }
+        if (a.dres) {
+#pragma unroll
+            for (int c = 0; c < NC; ++c) fr[c] = fetch8<MODE>((const char*)a.dres + t * a.lddr * (S32 ? 4 : 2), S32, inside(c), H);
+        }
+        f32x8 d[NC], n[NC];
         float sg = 0.0f, sgn = 0.0f;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             const int i = first(c);
+            const f32x8 w = widen8<MODE>(fw[c], a.weight_f32, i, H);
+            d[c] = widen8<MODE>(fd[c], false, i, H);
+            n[c] = widen8<MODE>(fs[c], S32, i, H);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                // (Columns past the row have dy and weight 0.)
-                n[c][e] = (VEC ? i < H : i + e < H) ? (n[c][e] - mean) * rstd : 0.0f;
+                // (Behind the row's last element dy and weight are 0.)
+                d[c][e] = i < H ? d[c][e] : 0.0f;
+                n[c][e] = i < H ? (n[c][e] - mean) * rstd : 0.0f;
                 aw[c][e] = fmaf(d[c][e], n[c][e], aw[c][e]);
                 ab[c][e] += d[c][e];
-                d[c][e] *= w[c][e];
+                d[c][e] *= w[e];
                 sg += d[c][e];
                 sgn = fmaf(d[c][e], n[c][e], sgn);
             }
@@ -206,13 +222,14 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void layer_norm_bwd_
             f32x8 v;
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] = rstd * ((d[c][e] - mg) - n[c][e] * mgn);
-            if (a.dres) v += load8<VEC>((const char*)a.dres + t * a.lddr * (S32 ? 4 : 2), S32, i, H);
-            if (a.dx) store8<VEC>(a.dx + t * a.lddx, false, i, H, v);
-            if (a.dresidual) store8<VEC>((char*)a.dresidual + t * a.lddro * (S32 ? 4 : 2), S32, i, H, v);
+            if (a.dres) v += widen8<MODE>(fr[c], S32, i, H);
+            if (a.dx) put8<MODE>(a.dx + t * a.lddx, false, i, H, v);
+            if (a.dresidual) put8<MODE>((char*)a.dresidual + t * a.lddro * (S32 ? 4 : 2), S32, i, H, v);
         }
     }
     if (!a.partial) return;
-    float* p = a.partial + (int64_t)blockIdx.x * 2 * H;
+    const int ld = (H + 7) & ~7;
+    float* p = a.partial + (int64_t)blockIdx.x * 2 * ld;
     if constexpr (WAVES == 1) {
         __shared__ float sum[4][512];
 #pragma unroll
@@ -221,7 +238,7 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void layer_norm_bwd_
 #pragma unroll
             for (int e = 0; e < 8; ++e) sum[wave][tid * 8 + e] = k ? ab[0][e] : aw[0][e];
             __syncthreads();
-            for (int i = (int)threadIdx.x; i < H; i += 256) p[k * H + i] = (sum[0][i] + sum[1][i]) + (sum[2][i] + sum[3][i]);
+            for (int i = (int)threadIdx.x; i < ld; i += 256) p[k * ld + i] = (sum[0][i] + sum[1][i]) + (sum[2][i] + sum[3][i]);
         }
     } else {
 #pragma unroll
@@ -230,18 +247,77 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void layer_norm_bwd_
             if (i >= H) continue;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
+                // (Columns past the row hold zeros.)
                 const f32x8 v = k ? ab[c] : aw[c];
-                if constexpr (VEC) {
-                    *(f32x4*)(p + k * H + i) = __builtin_shufflevector(v, v, 0, 1, 2, 3);
-                    *(f32x4*)(p + k * H + i + 4) = __builtin_shufflevector(v, v, 4, 5, 6, 7);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (i + e < H) p[k * H + i + e] = v[e];
-                }
+                *(f32x4*)(p + k * ld + i) = __builtin_shufflevector(v, v, 0, 1, 2, 3);
+                *(f32x4*)(p + k * ld + i + 4) = __builtin_shufflevector(v, v, 4, 5, 6, 7);
             }
         }
     }
+}
+
+template <int WAVES, int NC, int MODE, bool S32>
+__global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void layer_norm_bwd_kernel(LayerNormBwdArgs a) {
+    layer_norm_bwd_rows<WAVES, NC, MODE, S32>(a, (int)gridDim.x);
+}
+
+// Few rows: workgroups of a row (four rows for one wave a row) and, in the same
+// launch, workgroups of 32 columns that go through all rows again for the sums,
+// which makes no partial sums and no second launch.
+template <int WAVES, int NC, int MODE, bool S32>
+__global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void layer_norm_bwd_few_kernel(LayerNormBwdArgs a, int row_groups) {
+    constexpr int kThreads = WAVES == 1 ? 256 : WAVES * 64, kRuns = kThreads / 4, kAtOnce = 4;
+    if ((int)blockIdx.x < row_groups) {
+        a.partial = nullptr;
+        layer_norm_bwd_rows<WAVES, NC, MODE, S32>(a, row_groups);
+        return;
+    }
+    // Four lanes a row, eight columns each; the runs of rows meet in LDS.
+    __shared__ float lds[2][kRuns][32 + 1];
+    const int tid = (int)threadIdx.x, q = tid & 3, run = tid >> 2, H = a.H;
+    const int c0 = ((int)blockIdx.x - row_groups) * 32, i = c0 + q * 8, at = i < H ? i : 0;
+    f32x8 aw = {0, 0, 0, 0, 0, 0, 0, 0}, ab = aw;
+    for (int t0 = run; t0 < a.T; t0 += kRuns * kAtOnce) {
+        Raw8 fd[kAtOnce], fs[kAtOnce];
+        float mean[kAtOnce], rstd[kAtOnce];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            // (A row past the end: the first one, not used.)
+            const int64_t t = t0 + k * kRuns < a.T ? t0 + k * kRuns : t0;
+            mean[k] = a.mean[t];
+            rstd[k] = a.rstd[t];
+            fd[k] = fetch8<MODE>(a.dy + t * a.lddy, false, at, H);
+            fs[k] = fetch8<MODE>((const char*)a.s + t * a.lds * (S32 ? 4 : 2), S32, at, H);
+        }
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            if (t0 + k * kRuns >= a.T) continue;
+            const f32x8 d = widen8<MODE>(fd[k], false, at, H), n = widen8<MODE>(fs[k], S32, at, H);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                aw[e] = fmaf(d[e], (n[e] - mean[k]) * rstd[k], aw[e]);
+                ab[e] += d[e];
+            }
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        lds[0][run][q * 8 + e] = aw[e];
+        lds[1][run][q * 8 + e] = ab[e];
+    }
+    // 64 sums (32 columns, two sets) of kRuns runs, four threads each.
+    __syncthreads();
+    const int sum = (tid >> 2) & 63, set = sum >> 5, c = c0 + (sum & 31);
+    float v = 0.0f;
+    if (tid < 256) {
+        for (int k = tid & 3; k < kRuns; k += 4) v += lds[set][k][sum & 31];
+        v += dpp<0xB1>(v);  // (of a quad)
+        v += dpp<0x4E>(v);
+    }
+    void* out = set ? a.dbias : a.dweight;
+    if (tid >= 256 || (tid & 3) || !out || c >= H) return;
+    if (a.weight_f32) ((float*)out)[c] = v;
+    else ((uint16_t*)out)[c] = f32_to_bf16_bits(v);
 }
 
 // Rows that registers do not hold: a workgroup a row, which is read twice (the
@@ -303,67 +379,78 @@ __global__ __launch_bounds__(256) void layer_norm_columns_kernel(LayerNormBwdArg
         const f32x8 n = load8<VEC>((const char*)a.s + t * a.lds * (S32 ? 4 : 2), S32, i, H);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            aw[e] = fmaf(d[e], (n[e] - mean) * rstd, aw[e]);
+            aw[e] = VEC || i + e < H ? fmaf(d[e], (n[e] - mean) * rstd, aw[e]) : 0.0f;
             ab[e] += d[e];
         }
     }
-    float* p = a.partial + (int64_t)blockIdx.y * 2 * H;
+    const int ld = (H + 7) & ~7;
+    float* p = a.partial + (int64_t)blockIdx.y * 2 * ld + i;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        if (!VEC && i + e >= H) continue;
-        p[i + e] = aw[e];
-        p[H + i + e] = ab[e];
+        p[e] = aw[e];
+        p[ld + e] = ab[e];
     }
 }
 
-// 32 columns of 32 runs of parts; the runs' sums meet in LDS.
-__global__ __launch_bounds__(1024) void join_columns_kernel(const float* __restrict__ partial, int parts, int cols, int first,
-                                                            void* __restrict__ out0, void* __restrict__ out1, int f32) {
-    __shared__ float sum[32][33];
-    const int x = (int)threadIdx.x & 31, y = (int)threadIdx.x >> 5;
-    const int c = (int)blockIdx.x * 32 + x;
-    float v = 0.0f;
-    if (c < cols)
-        for (int p = y; p < parts; p += 32) v += partial[(int64_t)p * cols + c];
-    sum[y][x] = v;
-    __syncthreads();
-    if (y != 0 || c >= cols) return;
-    v = 0.0f;
-#pragma unroll
-    for (int k = 0; k < 32; ++k) v += sum[k][x];
-    void* out = c < first ? out0 : out1;
-    const int at = c < first ? c : c - first;
-    if (!out) return;
-    if (f32) ((float*)out)[at] = v;
-    else ((uint16_t*)out)[at] = f32_to_bf16_bits(v);
+template <int RUNS>
+__global__ __launch_bounds__(RUNS * 8) void column_join_kernel(ColumnJoin j) {
+    __shared__ float lds[column_join_lds(RUNS) / 4];
+    column_join<RUNS>(j, (int)blockIdx.x, lds);
 }
 
-hipError_t launch_join_columns(const float* partial, int parts, int cols, int first, void* out0, void* out1, bool f32,
-                               hipStream_t s) {
-    hipLaunchKernelGGL(join_columns_kernel, dim3((unsigned)((cols + 31) / 32)), dim3(1024), 0, s, partial, parts, cols, first,
-                       out0, out1, f32 ? 1 : 0);
+hipError_t launch_column_join(const ColumnJoin& j, bool few, hipStream_t s) {
+    const dim3 grid((unsigned)column_join_groups(j));
+    if (few) hipLaunchKernelGGL(column_join_kernel<kFewRuns>, grid, dim3(kFewRuns * 8), 0, s, j);
+    else hipLaunchKernelGGL(column_join_kernel<128>, grid, dim3(1024), 0, s, j);
     return hipGetLastError();
 }
 
 constexpr int kHeldColumns = 16384;  // of a row in registers, with the sums of its columns
 
-int layer_norm_parts(int T, int H) {
+// Up to so many rows the sums over them are taken in the launch of the rows.
+constexpr int kFewRows = 1024;
+
+// Workgroups of the rows; those of long rows, of the columns' runs of rows.
+static int layer_norm_groups(int T, int H, bool held) {
     const int rows = H <= 512 ? 4 : 1;
     const int64_t groups = ((int64_t)T + rows - 1) / rows;
-    const int most = H <= kHeldColumns ? 1024 : 64;
+    const int most = !held ? 64 : H <= 2048 ? 1024 : 512;
     return (int)(groups < most ? groups : most);
+}
+
+// Whether a row and its columns' sums stay in registers. (Rows of more than
+// 8192 at any address would spill a kilobyte a lane.)
+static bool held_row(int H, bool aligned) { return H <= (aligned ? kHeldColumns : 8192); }
+
+int layer_norm_parts(int T, int H) {
+    return T <= kFewRows && H <= kHeldColumns ? 0 : layer_norm_groups(T, H, held_row(H, true));
+}
+
+// Rows few enough for one launch.
+static bool few_rows(int T, int H) { return T <= kFewRows && H <= kHeldColumns; }
+
+template <int WAVES, int NC, int MODE, bool S32>
+static void launch_bwd_as(const LayerNormBwdArgs& a, hipStream_t s) {
+    const int groups = layer_norm_groups(a.T, a.H, true), threads = WAVES == 1 ? 256 : WAVES * 64;
+    if (few_rows(a.T, a.H)) {
+        const int rows = a.dx || a.dresidual ? groups : 0, cols = a.dweight || a.dbias ? (a.H + 31) / 32 : 0;
+        hipLaunchKernelGGL((layer_norm_bwd_few_kernel<WAVES, NC, MODE, S32>), dim3((unsigned)(rows + cols)), dim3(threads), 0, s, a, rows);
+    } else {
+        hipLaunchKernelGGL((layer_norm_bwd_kernel<WAVES, NC, MODE, S32>), dim3((unsigned)groups), dim3(threads), 0, s, a);
+    }
+}
+
+template <int WAVES, int NC, bool S32>
+static void launch_bwd_mode(const LayerNormBwdArgs& a, bool vec, hipStream_t s) {
+    if (vec) launch_bwd_as<WAVES, NC, kAligned, S32>(a, s);
+    else if (a.H >= 8) launch_bwd_as<WAVES, NC, kAnywhere, S32>(a, s);
+    else if constexpr (WAVES == 1) launch_bwd_as<WAVES, NC, kTiny, S32>(a, s);
 }
 
 template <int WAVES, int NC>
 static void launch_bwd(const LayerNormBwdArgs& a, bool vec, hipStream_t s) {
-    const dim3 grid((unsigned)layer_norm_parts(a.T, a.H)), block(WAVES == 1 ? 256 : WAVES * 64);
-    if (a.s_f32) {
-        if (vec) hipLaunchKernelGGL((layer_norm_bwd_kernel<WAVES, NC, true, true>), grid, block, 0, s, a);
-        else hipLaunchKernelGGL((layer_norm_bwd_kernel<WAVES, NC, false, true>), grid, block, 0, s, a);
-    } else {
-        if (vec) hipLaunchKernelGGL((layer_norm_bwd_kernel<WAVES, NC, true, false>), grid, block, 0, s, a);
-        else hipLaunchKernelGGL((layer_norm_bwd_kernel<WAVES, NC, false, false>), grid, block, 0, s, a);
-    }
+    if (a.s_f32) launch_bwd_mode<WAVES, NC, true>(a, vec, s);
+    else launch_bwd_mode<WAVES, NC, false>(a, vec, s);
 }
 
 template <bool VEC, bool S32>
@@ -387,7 +474,7 @@ static hipError_t launch_long(const LayerNormBwdArgs& a, hipStream_t s) {
         }
     }
     if (a.partial) {
-        const dim3 grid((unsigned)((a.H + 2047) / 2048), (unsigned)layer_norm_parts(a.T, a.H));
+        const dim3 grid((unsigned)((a.H + 2047) / 2048), (unsigned)layer_norm_groups(a.T, a.H, false));
         hipLaunchKernelGGL((layer_norm_columns_kernel<VEC, S32>), grid, dim3(256), 0, s, a);
     }
     return hipGetLastError();
@@ -395,24 +482,26 @@ static hipError_t launch_long(const LayerNormBwdArgs& a, hipStream_t s) {
 
 hipError_t launch_layer_norm_bwd(const LayerNormBwdArgs& a, hipStream_t s) {
     const bool sums = a.dweight || a.dbias;
+    bool held = true;
     if (a.T > 0) {
         const int sb = a.s_f32 ? 4 : 2;
         const bool vec = a.H % 8 == 0 && wide(a.dy, a.lddy, 2) && wide(a.s, a.lds, sb) && wide(a.dres, a.lddr, sb) &&
                          wide(a.dx, a.lddx, 2) && wide(a.dresidual, a.lddro, sb) && wide(a.weight, 0, 4);
+        held = held_row(a.H, vec);
         hipError_t e = hipSuccess;
         if (a.H <= 512) launch_bwd<1, 1>(a, vec, s);
         else if (a.H <= 2048) launch_bwd<4, 1>(a, vec, s);
         else if (a.H <= 4096) launch_bwd<4, 2>(a, vec, s);
         else if (a.H <= 8192) launch_bwd<8, 2>(a, vec, s);
-        else if (a.H <= kHeldColumns) launch_bwd<16, 2>(a, vec, s);
+        else if (held_row(a.H, vec) || few_rows(a.T, a.H)) launch_bwd<16, 2>(a, vec, s);
         else if (a.s_f32) e = vec ? launch_long<true, true>(a, s) : launch_long<false, true>(a, s);
         else e = vec ? launch_long<true, false>(a, s) : launch_long<false, false>(a, s);
         if (e == hipSuccess) e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    if (!sums) return hipSuccess;
-    return launch_join_columns(a.partial, a.T > 0 ? layer_norm_parts(a.T, a.H) : 0, 2 * a.H, a.H, a.dweight, a.dbias,
-                               a.weight_f32, s);
+    if (!sums || (a.T > 0 && few_rows(a.T, a.H))) return hipSuccess;
+    return launch_column_join({a.partial, a.dweight, a.dbias, a.T > 0 ? layer_norm_groups(a.T, a.H, held) : 0, a.H,
+                               (a.H + 7) & ~7, 2, a.weight_f32}, false, s);
 }
 
 }  // namespace moe

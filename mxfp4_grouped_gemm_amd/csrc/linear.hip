@@ -2,8 +2,9 @@
 // rounded to bf16 (it is an operand of the two products that follow), and the
 // bias gradient, the sum of its unrounded values over the rows.
 //
-// A thread goes through rows blockIdx.y, + gridDim.y, ... with eight columns,
-// whose sums stay in registers; the parts are joined by a second kernel.
+// A workgroup takes 512 columns, eight a lane, and its four waves rows w, w + 4,
+// ... of the workgroup's run of rows, four in flight each; the sums of the waves
+// meet in LDS, those of the workgroups in the launch of the products.
 #include "common.hpp"
 #include "dense_epilogue.hpp"
 #include "row_io.hpp"
@@ -13,43 +14,80 @@ namespace moe {
 
 using namespace rows;
 
-template <bool F32>
+namespace {
+constexpr int kAtOnce = 4;           // rows a wave has in flight
+constexpr int kTurn = 4 * kAtOnce;   // rows a workgroup takes in a turn
+}  // namespace
+
+// A kernel an activation: few instructions to fetch for a call of few rows.
+template <bool F32, int ACT>
 __global__ __launch_bounds__(256) void linear_dz_kernel(LinearDzArgs a) {
-    const int n = ((int)blockIdx.x * 256 + (int)threadIdx.x) * 8;
-    if (n >= a.N) return;
+    __shared__ f32x4 part[4][64][2];
+    const int lane = (int)threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int n = ((int)blockIdx.x * 64 + lane) * 8;
+    const int64_t turns = ((int64_t)a.T + kTurn - 1) / kTurn;
+    const int64_t beg = turns * blockIdx.y / gridDim.y * kTurn, stop = turns * (blockIdx.y + 1) / gridDim.y * kTurn;
+    const int64_t end = stop < a.T ? stop : a.T;
     f32x8 sum = {0, 0, 0, 0, 0, 0, 0, 0};
-    for (int64_t t = blockIdx.y; t < a.T; t += gridDim.y) {
-        f32x8 d = load8<true>((const char*)a.dout + t * a.lddo * (F32 ? 4 : 2), F32, n, a.N);
-        if (a.act != kActNone) {
-            const f32x8 z = load8<true>(a.pre + t * a.N, false, n, a.N);
+    if (n < a.N) {
+        for (int64_t t0 = beg + w; t0 < end; t0 += kTurn) {
+            Raw8 fd[kAtOnce], fz[kAtOnce];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) d[e] *= dense::act_slope(a.act, z[e]);
-        }
-        sum += d;
-        if (a.dz) {
-            u32x4 o;
+            for (int i = 0; i < kAtOnce; ++i) {
+                // (A row past the end: the first one, not used.)
+                const int64_t t = t0 + 4 * i < end ? t0 + 4 * i : t0;
+                fd[i] = fetch8<kAligned>((const char*)a.dout + t * a.lddo * (F32 ? 4 : 2), F32, n, a.N);
+                if (ACT != kActNone) fz[i] = fetch8<kAligned>(a.pre + t * a.N, false, n, a.N);
+            }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[e] = pack_bf16x2(d[2 * e], d[2 * e + 1]);
-            *(u32x4*)(a.dz + t * a.N + n) = o;
+            for (int i = 0; i < kAtOnce; ++i) {
+                if (t0 + 4 * i >= end) continue;
+                f32x8 d = widen8<kAligned>(fd[i], F32, n, a.N);
+                if constexpr (ACT != kActNone) {
+                    const f32x8 z = widen8<kAligned>(fz[i], false, n, a.N);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) d[e] *= dense::act_slope(ACT, z[e]);
+                }
+                sum += d;
+                if (a.dz) {
+                    u32x4 o;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[e] = pack_bf16x2(d[2 * e], d[2 * e + 1]);
+                    *(u32x4*)(a.dz + (t0 + 4 * i) * a.N + n) = o;
+                }
+            }
         }
     }
     if (!a.partial) return;
-    float* p = a.partial + (int64_t)blockIdx.y * a.N + n;
-    *(f32x4*)p = __builtin_shufflevector(sum, sum, 0, 1, 2, 3);
-    *(f32x4*)(p + 4) = __builtin_shufflevector(sum, sum, 4, 5, 6, 7);
+    part[w][lane][0] = __builtin_shufflevector(sum, sum, 0, 1, 2, 3);
+    part[w][lane][1] = __builtin_shufflevector(sum, sum, 4, 5, 6, 7);
+    __syncthreads();
+    if (w >= 2 || n >= a.N) return;
+    *(f32x4*)(a.partial + (int64_t)blockIdx.y * a.N + n + 4 * w) =
+        (part[0][lane][w] + part[1][lane][w]) + (part[2][lane][w] + part[3][lane][w]);
 }
 
 int linear_dz_parts(int T, int N) {
-    const int cols = (N + 2047) / 2048;
-    int parts = 1024 / cols;
-    if (parts < 1) parts = 1;
-    return T < parts ? T : parts;
+    // Eight workgroups a compute unit, a turn of rows each at least.
+    const int cols = (N + 511) / 512;
+    const int turns = (int)(((int64_t)T + kTurn - 1) / kTurn);
+    const int parts = 2048 / cols < 1 ? 1 : 2048 / cols < 256 ? 2048 / cols : 256;
+    return turns < parts ? turns : parts;
+}
+
+template <int ACT>
+static void launch_as(const LinearDzArgs& a, hipStream_t s) {
+    const dim3 grid((unsigned)((a.N + 511) / 512), (unsigned)linear_dz_parts(a.T, a.N)), block(256);
+    if (a.dout_f32) hipLaunchKernelGGL((linear_dz_kernel<true, ACT>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((linear_dz_kernel<false, ACT>), grid, block, 0, s, a);
 }
 
 hipError_t launch_linear_dz(const LinearDzArgs& a, hipStream_t s) {
-    const dim3 grid((unsigned)((a.N + 2047) / 2048), (unsigned)linear_dz_parts(a.T, a.N)), block(256);
-    if (a.dout_f32) hipLaunchKernelGGL(linear_dz_kernel<true>, grid, block, 0, s, a);
-    else hipLaunchKernelGGL(linear_dz_kernel<false>, grid, block, 0, s, a);
+    if (a.act == kActNone) launch_as<kActNone>(a, s);
+    else if (a.act == kActRelu) launch_as<kActRelu>(a, s);
+    else if (a.act == kActSilu) launch_as<kActSilu>(a, s);
+    else if (a.act == kActGelu) launch_as<kActGelu>(a, s);
+    else launch_as<kActGeluTanh>(a, s);
     return hipGetLastError();
 }
 

@@ -59,11 +59,20 @@ __device__ __forceinline__ float wave_sum(float v) {
 
 // Eight elements i..i+7 of a row. VEC: all of them are in the row and 16-byte
 // aligned (8 bytes in q); else they are at any element's address, which one
-// wide load or store takes as well, and the row's last eight may be fewer.
+// wide load or store takes as well. The row's last eight may be fewer: they are
+// taken four, two and one at a time, by the bits of H, which all rows share
+// (1531 rows of 2793, layer norm with an fp32 stream: TAILNEW us, TAILOLD element by
+// element).
 typedef f32x4 __attribute__((aligned(4))) f32x4_any;
+typedef f32x2 __attribute__((aligned(4))) f32x2_any;
 typedef u16x8 __attribute__((aligned(2))) u16x8_any;
 typedef u32x4 __attribute__((aligned(2))) u32x4_any;
 typedef u32x2 __attribute__((aligned(1))) u32x2_any;
+typedef u32x2 __attribute__((aligned(2))) u32x2_half;
+typedef uint32_t __attribute__((aligned(2))) u32_half;
+
+__device__ __forceinline__ float low_half(uint32_t d) { return __uint_as_float(d << 16); }
+__device__ __forceinline__ float high_half(uint32_t d) { return __uint_as_float(d & 0xffff0000u); }
 
 template <bool VEC>
 __device__ __forceinline__ f32x8 load8(const void* row, bool f32, int i, int H) {
@@ -80,11 +89,31 @@ __device__ __forceinline__ f32x8 load8(const void* row, bool f32, int i, int H) 
             for (int e = 0; e < 8; ++e) r[e] = bf16_bits_to_f32(u[e]);
         }
     } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int k = i + e;
-            r[e] = k >= H ? 0.0f : f32 ? ((const float*)row)[k] : bf16_bits_to_f32(((const uint16_t*)row)[k]);
+        const bool four = H & 4, two = H & 2, one = H & 1;
+        f32x4 a = {0, 0, 0, 0};
+        f32x2 b = {0, 0};
+        float c = 0.0f;
+        if (f32) {
+            const float* p = (const float*)row + i;
+            if (four) a = *(const f32x4_any*)p;
+            if (two) b = *(const f32x2_any*)(p + (four ? 4 : 0));
+            if (one) c = p[(four ? 4 : 0) + (two ? 2 : 0)];
+        } else {
+            const uint16_t* p = (const uint16_t*)row + i;
+            if (four) {
+                const u32x2 d = *(const u32x2_half*)p;
+                a = f32x4{low_half(d[0]), high_half(d[0]), low_half(d[1]), high_half(d[1])};
+            }
+            if (two) {
+                const uint32_t d = *(const u32_half*)(p + (four ? 4 : 0));
+                b = f32x2{low_half(d), high_half(d)};
+            }
+            if (one) c = bf16_bits_to_f32(p[(four ? 4 : 0) + (two ? 2 : 0)]);
         }
+        // Behind each other.
+        const f32x4 t = two ? f32x4{b[0], b[1], c, 0.0f} : f32x4{c, 0.0f, 0.0f, 0.0f};
+        const f32x4 zero = {0, 0, 0, 0};
+        r = four ? __builtin_shufflevector(a, t, 0, 1, 2, 3, 4, 5, 6, 7) : __builtin_shufflevector(t, zero, 0, 1, 2, 3, 4, 5, 6, 7);
     }
     return r;
 }
@@ -111,14 +140,96 @@ __device__ __forceinline__ void store8(void* row, bool f32, int i, int H, f32x8 
             else *p = o;
         }
     } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int k = i + e;
-            if (k >= H) continue;
-            if (f32) ((float*)row)[k] = v[e];
-            else ((uint16_t*)row)[k] = f32_to_bf16_bits(v[e]);
+        const bool four = H & 4, two = H & 2;
+        const f32x4 t = four ? __builtin_shufflevector(v, v, 4, 5, 6, 7) : __builtin_shufflevector(v, v, 0, 1, 2, 3);
+        const float last = two ? t[2] : t[0];
+        const int b = four ? 4 : 0, c = b + (two ? 2 : 0);
+        if (f32) {
+            float* p = (float*)row + i;
+            if (four) *(f32x4_any*)p = __builtin_shufflevector(v, v, 0, 1, 2, 3);
+            if (two) *(f32x2_any*)(p + b) = f32x2{t[0], t[1]};
+            if (H & 1) p[c] = last;
+        } else {
+            uint16_t* p = (uint16_t*)row + i;
+            if (four) *(u32x2_half*)p = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+            if (two) *(u32_half*)(p + b) = pack_bf16x2(t[0], t[1]);
+            if (H & 1) p[c] = f32_to_bf16_bits(last);
         }
     }
+}
+
+// The same in two halves, so that nothing waits between the loads of a row's
+// several operands: fetch8 loads (what it loads for f32 and for bf16 differs,
+// but no branch holds an arithmetic instruction), widen8 makes numbers of it.
+// MODE kAligned as VEC; kAnywhere: any element's address and H >= 8, where the
+// row's last eight are loaded from H - 8 on and moved down; kTiny: H < 8.
+constexpr int kAligned = 0, kAnywhere = 1, kTiny = 2;
+
+struct Raw8 {
+    u32x4 a, b;
+};
+
+template <int MODE>
+__device__ __forceinline__ Raw8 fetch8(const void* row, bool f32, int i, int H) {
+    Raw8 r;
+    if constexpr (MODE == kTiny) {
+        const f32x8 v = load8<false>(row, f32, i, H);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            r.a[e] = __float_as_uint(v[e]);
+            r.b[e] = __float_as_uint(v[e + 4]);
+        }
+    } else {
+        const int at = MODE == kAligned || i + 8 <= H ? i : H - 8;
+        if (f32) {
+            const float* p = (const float*)row + at;
+            if constexpr (MODE == kAligned) {
+                r.a = ((const u32x4*)p)[0];
+                r.b = ((const u32x4*)p)[1];
+            } else {
+                r.a = __builtin_bit_cast(u32x4, *(const f32x4_any*)p);
+                r.b = __builtin_bit_cast(u32x4, *(const f32x4_any*)(p + 4));
+            }
+        } else {
+            const uint16_t* p = (const uint16_t*)row + at;
+            if constexpr (MODE == kAligned) r.a = *(const u32x4*)p;
+            else r.a = *(const u32x4_any*)p;
+        }
+    }
+    return r;
+}
+
+template <int MODE>
+__device__ __forceinline__ f32x8 widen8(Raw8 r, bool f32, int i, int H) {
+    f32x8 v;
+    if (MODE == kTiny || f32) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            v[e] = __uint_as_float(r.a[e]);
+            v[e + 4] = __uint_as_float(r.b[e]);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            v[2 * e] = low_half(r.a[e]);
+            v[2 * e + 1] = high_half(r.a[e]);
+        }
+    }
+    if constexpr (MODE == kAnywhere) {
+        const int down = i + 8 <= H ? 0 : i + 8 - H;
+        if (__any(down)) {
+#pragma unroll
+            for (int d = 4; d > 0; d /= 2)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = down & d ? (e + d < 8 ? v[e + d] : 0.0f) : v[e];
+        }
+    }
+    return v;
+}
+
+template <int MODE>
+__device__ __forceinline__ void put8(void* row, bool f32, int i, int H, f32x8 v) {
+    store8<MODE == kAligned>(row, f32, i, H, v);
 }
 
 }  // namespace rows

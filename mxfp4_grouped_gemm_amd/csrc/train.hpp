@@ -6,6 +6,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "column_join.hpp"
 #include "dense.hpp"
 
 namespace moe {
@@ -35,21 +36,16 @@ struct LayerNormBwdArgs {
     const void* dres;  // gradient that reaches s from elsewhere, or null
     uint16_t* dx;
     void* dresidual;  // of s's type
-    float* partial;   // [layer_norm_parts, 2 H], where sums over the rows are asked for
+    float* partial;   // [layer_norm_parts, 2, H rounded up to 8], where sums over the rows are asked for
     void* dweight;
     void* dbias;
     int64_t lddy, lds, lddr, lddx, lddro;
     int T, H;
     int s_f32, weight_f32;
 };
-// Parts that the sums over the rows are taken in.
+// Parts that the sums over the rows are taken in (0: no partial sums).
 int layer_norm_parts(int T, int H);
 hipError_t launch_layer_norm_bwd(const LayerNormBwdArgs& a, hipStream_t s);
-
-// Sums partial [parts, cols] (fp32) over the parts, in order: columns below
-// `first` go to out0, the others to out1; either may be null.
-hipError_t launch_join_columns(const float* partial, int parts, int cols, int first, void* out0, void* out1, bool f32,
-                               hipStream_t s);
 
 // dz = dout act'(pre) and its sums over the rows. dz may be null (dz == dout).
 struct LinearDzArgs {
@@ -72,7 +68,7 @@ struct PermuteArgs {
     const int32_t* ids;
     int32_t* rows;
     int32_t* offsets;
-    int32_t* counts;  // [permute_chunks, E + 1] (none for few pairs)
+    int32_t* counts;  // [2, chunks, E + 1] and [chunks, 16] (none for few pairs)
     int64_t ldx, ldo; // bytes
     int64_t row_bytes;
     int T, topk, E;

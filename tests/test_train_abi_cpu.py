@@ -62,9 +62,10 @@ def test_layer_norm_backward_refusals():
     for k in ("dx", "dres", "dw", "db"):
         assert said(norm_bwd(**{k: P + 1}), "misaligned output") == BAD
     assert norm_bwd(s=P + 2, st=1) == BAD and norm_bwd(dr=P + 2, st=1) == BAD and norm_bwd(dw=P + 2, wt=1) == BAD
-    need = moe.moe_layer_norm_backward_workspace_size(4, 64)
+    need = moe.moe_layer_norm_backward_workspace_size(4000, 64)
     assert need > 0 and need % 256 == 0
-    assert said(norm_bwd(wsb=need - 1), "workspace") == BAD and norm_bwd(ws=None) == BAD and norm_bwd(ws=P + 64) == BAD
+    assert said(norm_bwd(T=4000, wsb=need - 1), "workspace") == BAD
+    assert norm_bwd(T=4000, ws=None) == BAD and norm_bwd(T=4000, ws=P + 64) == BAD
     for args in ((-1, 64), (4, 0), (4, 65537), ((1 << 24) + 1, 64)):
         assert moe.moe_layer_norm_backward_workspace_size(*args) == -1
     assert moe.moe_layer_norm_backward_workspace_size(0, 64) == 0
