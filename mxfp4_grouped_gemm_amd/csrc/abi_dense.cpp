@@ -196,12 +196,18 @@ bool valid_sizes(int T, int a, int b, int step) {
 struct LinearBwdLayout {
     int64_t sums, partial, total;  // dz at 0
     int splits_dx;
+    bool few;
 };
 
 LinearBwdLayout linear_bwd_layout(int T, int K, int N) {
     LinearBwdLayout L;
-    const moe::DenseArgs dx = product(nullptr, N, nullptr, K, T, K, N, nullptr, K);
-    L.splits_dx = moe::dense_bwd_splits(dx);
+    // (With addresses, as if all gradients were asked for: a gradient is then the
+    // same alone.)
+    float all;
+    const moe::DenseArgs dw = product(nullptr, N, nullptr, K, N, K, T, &all, K);
+    const moe::DenseArgs dx = product(nullptr, N, nullptr, K, T, K, N, &all, K);
+    L.few = moe::linear_short(dw, dx);
+    L.splits_dx = L.few ? moe::linear_short_splits(dx) : moe::dense_bwd_splits(dx);
     L.sums = align_up((int64_t)T * N * 2, 256);
     L.partial = L.sums + align_up((int64_t)moe::linear_dz_parts(T, N) * N * 4, 256);
     L.total = L.partial + align_up(moe::dense_partial_bytes(dx, L.splits_dx, moe::kEpiOut, false), 256);
@@ -639,6 +645,7 @@ moe_status moe_linear_backward(const void* dout, int64_t dout_stride, moe_dtype 
     moe::DenseArgs gx = product(dz, lddz, w, K, T, K, N, dx, dx_stride);
     gx.splits = L.splits_dx;
     gx.partial = (float*)((char*)workspace + L.partial);
+    if (L.few) return hip_status(moe::launch_linear_short_grads(gw, gx, sums, s), "moe_linear_backward (gradients)");
     return hip_status(moe::launch_dense_grads(gw, product(nullptr, 0, nullptr, 0, 0, 0, 0, nullptr, 0), gx, sums, s),
                       "moe_linear_backward (gradients)");
 }

@@ -88,6 +88,8 @@ hipError_t launch_dense_mx(const DenseArgs& a, int epi, hipStream_t s);
 // (Their a.splits: dense_bwd_splits, of dh and of dx.)
 int dense_bwd_splits(const DenseArgs& a);
 hipError_t launch_dense_dh(const DenseArgs& a, hipStream_t s);
+// Whether launch_dense_grads takes dx in a launch of its own.
+bool dense_dx_alone(const DenseArgs& dw13, const DenseArgs& dw2, const DenseArgs& dx);
 // (sums: a bias gradient to be joined in the same launch, or no outputs.)
 hipError_t launch_dense_grads(const DenseArgs& dw13, const DenseArgs& dw2, const DenseArgs& dx, const ColumnJoin& sums,
                               hipStream_t s);

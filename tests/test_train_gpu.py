@@ -363,7 +363,8 @@ def plan(g, T, k, E=9, how="absent"):
     return ref.permute(torch.zeros(T, 1), routing(g, T, k, E, how), E)[1]
 
 
-COMBINE = [(1, 1, 1), (3, 2, 7), (1, 15, 3584), (37, 4, 1001), (300, 5, 264), (40, 9, 520), (5, 16, 4100), (4, 17, 96),
+COMBINE = [(1, 1, 1), (3, 2, 7), (1, 15, 3584), (37, 4, 1001), (300, 5, 264), (40, 9, 520), (5, 16, 4100), (4, 17, 96), (70, 2, 16),
+           (33, 6, 257),
            (3, 64, 72), (2, 3, 20000)]
 
 
@@ -645,6 +646,22 @@ def test_linear_backward_large_tiles(moe, T, K, N):
     dout, x, pre, w = rnd(g, T, N), rnd(g, T, K), rnd(g, T, N), rnd(g, N, K, scale=1 / math.sqrt(K))
     got = moe.moe_linear_backward(*(cuda(t) for t in (dout, x, w)), pre=cuda(pre), act=ref.GELU)
     check_linear_bwd(ref.GELU, dout, x, pre, w, got)
+
+
+# (sums of few tokens beside weights of many tiles: in one launch, dx in parts
+# and whole)
+@pytest.mark.parametrize("T,K,N", [(1, 4096, 520), (5, 1032, 4104), (33, 8192, 264), (100, 1032, 2056), (128, 2056, 1288),
+                                   (129, 2056, 1288), (300, 1024, 4104), (512, 1024, 4104)])
+@pytest.mark.parametrize("a,dt", [(ref.GELU, BF), (ref.NONE, BF), (ref.SILU, F32)])
+def test_linear_backward_of_few_tokens(moe, T, K, N, a, dt):
+    g = gen(T + K)
+    dout, x, pre, w = rnd(g, T, N + 8, dtype=dt), rnd(g, T, K), rnd(g, T, N), rnd(g, N, K, scale=1 / math.sqrt(K))
+    args = [cuda(dout)[:, 8:], cuda(x), cuda(w)]
+    got = moe.moe_linear_backward(*args, pre=cuda(pre), act=a)
+    check_linear_bwd(a, dout[:, 8:], x, pre, w, got)
+    for k in range(3):
+        one = moe.moe_linear_backward(*args, pre=cuda(pre), act=a, need_dx=k == 0, need_dw=k == 1, need_dbias=k == 2)
+        assert [t is not None for t in one] == [i == k for i in range(3)] and torch.equal(one[k], got[k])
 
 
 @pytest.mark.parametrize("a", [ref.NONE, ref.GELU])
