@@ -561,7 +561,7 @@ def _matrix(t, name):
 def _run(device, stream, fn, *args):
     """fn(*args, stream address) with `device` current, on `stream` or that
     device's current stream."""
-    if torch.cuda.current_device() != device.index:
+    if torch._C._cuda_getDevice() != device.index:
         with torch.cuda.device(device):
             return _run(device, stream, fn, *args)
     if stream is None:
@@ -580,6 +580,13 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _new(t, shape, stream):
+    """A tensor of t's type and device."""
+    if stream is None:
+        return t.new_empty(shape)
+    return _empty(shape, t.dtype, t.device, stream)
 
 
 def _like(t, stride, cols, stream):
@@ -999,7 +1006,7 @@ def moe_permute(x, topk_ids, E, out=None, rows=None, expert_offsets=None, worksp
     px, ldx = _rows(x, "x", tuple(_DT), (T, H), device)
     pi = _full(topk_ids, "topk_ids", torch.int32, (T, topk), device)
     if out is None:
-        out = _empty((T * topk, H), x.dtype, device, stream)
+        out = _new(x, (T * topk, H), stream)
         po, ldo = out.data_ptr(), H
     else:
         po, ldo = _rows(out, "out", x.dtype, (T * topk, H), device)
@@ -1009,7 +1016,7 @@ def moe_permute(x, topk_ids, E, out=None, rows=None, expert_offsets=None, worksp
     else:
         pr = _full(rows, "rows", torch.int32, (T, topk), device)
     if expert_offsets is None:
-        expert_offsets = _empty((max(E, 0) + 1,), torch.int32, device, stream)
+        expert_offsets = _new(topk_ids, (max(E, 0) + 1,), stream)
         pe = expert_offsets.data_ptr()
     else:
         pe = _full(expert_offsets, "expert_offsets", torch.int32, (E + 1,), device)
@@ -1044,7 +1051,8 @@ def moe_unpermute(y, rows, weights=None, residual=None, out_dtype=None, out=None
             raise ValueError(f"out_dtype must be bfloat16 or float32, got {dtype}")
     ps, lds = (None, H) if residual is None else _rows(residual, "residual", dtype, (T, H), device)
     if out is None:
-        out = _empty((T, H), dtype, device, stream)
+        out = _new(y, (T, H), stream) if dtype is y.dtype else _like(residual, lds, H, stream) if residual is not None \
+            else _empty((T, H), dtype, device, stream)
         po, ldo = out.data_ptr(), H
     else:
         po, ldo = _rows(out, "out", _FLOATS, (T, H), device)
@@ -1078,12 +1086,12 @@ def moe_unpermute_backward(dout, rows, y=None, weights=None, y_dtype=None, need_
         return None, None
     pdy, lddy, pdw = None, H, None
     if need_dy and dy is None:
-        dy = _empty((T * topk, H), dtype, device, stream)
+        dy = _new(dout, (T * topk, H), stream) if dtype is dout.dtype else _empty((T * topk, H), dtype, device, stream)
         pdy = dy.data_ptr()
     elif need_dy:
         pdy, lddy = _rows(dy, "dy", dtype, (T * topk, H), device)
     if need_dweights and dweights is None:
-        dweights = _empty((T, topk), torch.float32, device, stream)
+        dweights = _empty((T, topk), torch.float32, device, stream) if weights is None else _like(weights, topk, topk, stream)
         pdw = dweights.data_ptr()
     elif need_dweights:
         pdw = _full(dweights, "dweights", torch.float32, (T, topk), device)
@@ -1169,13 +1177,13 @@ def moe_linear_forward(x, w, bias=None, act=MOE_LINEAR_NONE, addend=None, out_dt
     if out is None:
         if out_dtype not in _FLOATS:
             raise ValueError(f"out_dtype must be bfloat16 or float32, got {out_dtype}")
-        out = _empty((T, N), out_dtype, device, stream)
+        out = _new(x, (T, N), stream) if out_dtype is torch.bfloat16 else _empty((T, N), out_dtype, device, stream)
         po, ldo = out.data_ptr(), N
     else:
         po, ldo = _rows(out, "out", _FLOATS, (T, N), device)
     pa, lda = (None, N) if addend is None else _rows(addend, "addend", out.dtype, (T, N), device)
     if pre is None and save_pre:
-        pre = _empty((T, N), torch.bfloat16, device, stream)
+        pre = _new(x, (T, N), stream)
     pp = None if pre is None else _full(pre, "pre", torch.bfloat16, (T, N), device)
     pws, nws, _ws = _workspace(workspace, lib.moe_linear_workspace_size(T, K, N), device, stream)
     _run(device, stream, lib.moe_linear_forward,

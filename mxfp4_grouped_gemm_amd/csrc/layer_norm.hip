@@ -44,12 +44,11 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void layer_norm_kern
         const int i = first(c);
         s[c] = widen8<MODE>(fx[c], false, i, H);
         if (a.residual) s[c] += widen8<MODE>(fr[c], a.res_f32, i, H);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) s[c][e] = i < H ? s[c][e] : 0.0f;
         if (a.residual_out && i < H) put8<MODE>(ro, a.res_f32, i, H, s[c]);
+        const int skip = i < H ? skip8<MODE>(i, H) : 8;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const double v = (double)s[c][e];
+            const double v = (double)(e >= skip ? s[c][e] : 0.0f);
             sum += v;
             sq = fma(v, v, sq);
         }
@@ -128,7 +127,10 @@ hipError_t launch_layer_norm(const LayerNormArgs& a, hipStream_t s) {
         const bool vec = b.H % 8 == 0 && wide(b.x, b.ldx, 2) && wide(b.residual, b.ldr, (int)rb) &&
                          wide(b.residual_out, b.ldro, (int)rb) && wide(b.y, b.ldy, 2) && wide(b.weight, 0, 4) &&
                          wide(b.bias, 0, 4);
+        // Waves a row that its columns keep busy (1024 columns, 32768 rows: 46 us in
+        // two waves, 61 in four).
         if (b.H <= 512) launch<1, 1>(b, vec, s);
+        else if (b.H <= 1024) launch<2, 1>(b, vec, s);
         else if (b.H <= 2048) launch<4, 1>(b, vec, s);
         else if (b.H <= 4096) launch<4, 2>(b, vec, s);
         else if (b.H <= 8192) launch<4, 4>(b, vec, s);
@@ -181,20 +183,21 @@ __device__ __forceinline__ void layer_norm_bwd_rows(const LayerNormBwdArgs& a, i
         float sg = 0.0f, sgn = 0.0f;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-            const int i = first(c);
+            const int i = first(c), skip = i < H ? skip8<MODE>(i, H) : 8;
             const f32x8 w = widen8<MODE>(fw[c], a.weight_f32, i, H);
             d[c] = widen8<MODE>(fd[c], false, i, H);
             n[c] = widen8<MODE>(fs[c], S32, i, H);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                // (Behind the row's last element dy and weight are 0.)
-                d[c][e] = i < H ? d[c][e] : 0.0f;
-                n[c][e] = i < H ? (n[c][e] - mean) * rstd : 0.0f;
-                aw[c][e] = fmaf(d[c][e], n[c][e], aw[c][e]);
-                ab[c][e] += d[c][e];
+                const float own = e >= skip ? d[c][e] : 0.0f;
+                // (Of a lane past the row, which could be infinite.)
+                n[c][e] = MODE == kAligned && i >= H ? 0.0f : (n[c][e] - mean) * rstd;
+                aw[c][e] = fmaf(own, n[c][e], aw[c][e]);
+                ab[c][e] += own;
                 d[c][e] *= w[e];
-                sg += d[c][e];
-                sgn = fmaf(d[c][e], n[c][e], sgn);
+                const float g = own * w[e];
+                sg += g;
+                sgn = fmaf(g, n[c][e], sgn);
             }
         }
         sg = wave_sum(sg);
@@ -230,27 +233,35 @@ __device__ __forceinline__ void layer_norm_bwd_rows(const LayerNormBwdArgs& a, i
     if (!a.partial) return;
     const int ld = (H + 7) & ~7;
     float* p = a.partial + (int64_t)blockIdx.x * 2 * ld;
+    // (What lies behind the row's last column is not read as numbers.)
     if constexpr (WAVES == 1) {
         __shared__ float sum[4][512];
+        const int i = first(0), skip = i < H ? skip8<MODE>(i, H) : 8, at = i - skip;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             __syncthreads();
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sum[wave][tid * 8 + e] = k ? ab[0][e] : aw[0][e];
+            for (int e = 0; e < 8; ++e)
+                if (e >= skip) sum[wave][at + e] = k ? ab[0][e] : aw[0][e];
             __syncthreads();
-            for (int i = (int)threadIdx.x; i < ld; i += 256) p[k * ld + i] = (sum[0][i] + sum[1][i]) + (sum[2][i] + sum[3][i]);
+            for (int c = (int)threadIdx.x; c < H; c += 256) p[k * ld + c] = (sum[0][c] + sum[1][c]) + (sum[2][c] + sum[3][c]);
         }
     } else {
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-            const int i = first(c);
+            const int i = first(c), skip = skip8<MODE>(i, H);
             if (i >= H) continue;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                // (Columns past the row hold zeros.)
                 const f32x8 v = k ? ab[c] : aw[c];
-                *(f32x4*)(p + k * ld + i) = __builtin_shufflevector(v, v, 0, 1, 2, 3);
-                *(f32x4*)(p + k * ld + i + 4) = __builtin_shufflevector(v, v, 4, 5, 6, 7);
+                if (skip == 0) {
+                    *(f32x4*)(p + k * ld + i) = __builtin_shufflevector(v, v, 0, 1, 2, 3);
+                    *(f32x4*)(p + k * ld + i + 4) = __builtin_shufflevector(v, v, 4, 5, 6, 7);
+                } else {
+#pragma unroll
+                    for (int e = 1; e < 8; ++e)
+                        if (e >= skip) p[k * ld + i - skip + e] = v[e];
+                }
             }
         }
     }
@@ -300,22 +311,23 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void layer_norm_bwd_
             }
         }
     }
+    const int skip = i < H ? skip8<MODE>(i, H) : 8;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        lds[0][run][q * 8 + e] = aw[e];
-        lds[1][run][q * 8 + e] = ab[e];
+        if (e < skip) continue;
+        lds[0][run][q * 8 - skip + e] = aw[e];
+        lds[1][run][q * 8 - skip + e] = ab[e];
     }
-    // 64 sums (32 columns, two sets) of kRuns runs, four threads each.
+    // 64 sums (32 columns, two sets) of kRuns runs, two threads each.
     __syncthreads();
-    const int sum = (tid >> 2) & 63, set = sum >> 5, c = c0 + (sum & 31);
+    const int sum = (tid >> 1) & 63, set = sum >> 5, c = c0 + (sum & 31);
     float v = 0.0f;
-    if (tid < 256) {
-        for (int k = tid & 3; k < kRuns; k += 4) v += lds[set][k][sum & 31];
-        v += dpp<0xB1>(v);  // (of a quad)
-        v += dpp<0x4E>(v);
+    if (tid < 128) {
+        for (int k = tid & 1; k < kRuns; k += 2) v += lds[set][k][sum & 31];
+        v += dpp<0xB1>(v);  // (the neighbour's)
     }
     void* out = set ? a.dbias : a.dweight;
-    if (tid >= 256 || (tid & 3) || !out || c >= H) return;
+    if (tid >= 128 || (tid & 1) || !out || c >= H) return;
     if (a.weight_f32) ((float*)out)[c] = v;
     else ((uint16_t*)out)[c] = f32_to_bf16_bits(v);
 }
@@ -407,14 +419,19 @@ hipError_t launch_column_join(const ColumnJoin& j, bool few, hipStream_t s) {
 
 constexpr int kHeldColumns = 16384;  // of a row in registers, with the sums of its columns
 
-// Up to so many rows the sums over them are taken in the launch of the rows.
+// Up to so many rows the sums over them are taken in the launch of the rows (3584
+// columns: 1024 rows 13.4 us, 1025 rows in two launches 17.7; 8192 columns 24 and
+// 28).
 constexpr int kFewRows = 1024;
 
 // Workgroups of the rows; those of long rows, of the columns' runs of rows.
 static int layer_norm_groups(int T, int H, bool held) {
     const int rows = H <= 512 ? 4 : 1;
     const int64_t groups = ((int64_t)T + rows - 1) / rows;
-    const int most = !held ? 64 : H <= 2048 ? 1024 : 512;
+    // As many as the registers of their waves leave room for, but not so many that
+    // their partial sums count (16384 rows of 3584: 512 workgroups 89 us, 768 96, 1024
+    // 104; 32768 of 1024: 1024 workgroups 54.6, 2048 59; 30000 of 640: 43.6 and 37.2).
+    const int most = !held ? 64 : H <= 512 ? 1024 : H <= 1024 ? 1280 : H <= 2048 ? 1024 : 512;
     return (int)(groups < most ? groups : most);
 }
 
@@ -490,6 +507,7 @@ hipError_t launch_layer_norm_bwd(const LayerNormBwdArgs& a, hipStream_t s) {
         held = held_row(a.H, vec);
         hipError_t e = hipSuccess;
         if (a.H <= 512) launch_bwd<1, 1>(a, vec, s);
+        else if (a.H <= 1024) launch_bwd<2, 1>(a, vec, s);
         else if (a.H <= 2048) launch_bwd<4, 1>(a, vec, s);
         else if (a.H <= 4096) launch_bwd<4, 2>(a, vec, s);
         else if (a.H <= 8192) launch_bwd<8, 2>(a, vec, s);

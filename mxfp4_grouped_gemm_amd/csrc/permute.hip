@@ -24,8 +24,10 @@ typedef uint32_t __attribute__((aligned(1))) u32_byte;
 typedef uint16_t __attribute__((aligned(1))) u16_byte;
 
 constexpr int kMaxTopk = 64;
-// Up to this many pairs each workgroup counts the pairs before its own.
-constexpr int kFewPairs = 2048;
+// Up to this many pairs each wave counts the pairs before its own: one launch (8
+// choices of 112 experts, rows of 3584: 2400 pairs 13.4 us, 18.8 in three launches;
+// 4096 pairs 26.4 and 18.6, 3000 pairs of 128 columns 12.4 and 18.8).
+constexpr int kFewPairs = 2560;
 constexpr int kSlice = 1024;      // pairs ranked at once
 constexpr int kMostChunks = 256;  // of slices; the scan takes them in one workgroup
 constexpr int kKeys = 1025;       // experts, and none
@@ -140,7 +142,7 @@ __global__ __launch_bounds__(256) void permute_few_kernel(PermuteArgs a) {
     const int p = (int)blockIdx.x * 4 + w;
     if (p >= P) return;  // (no barrier follows)
     const char* xr = (const char*)a.x + p / a.topk * a.ldx;
-    constexpr int kBatch = 4;  // pieces of the row, and slices of the ids, in flight
+    constexpr int kBatch = 8;  // pieces of the row, and slices of the ids, in flight
     const int64_t at0 = lane * 16;
     u32x4 v[kBatch];
     auto load = [&](int64_t at) {
@@ -229,7 +231,7 @@ __global__ __launch_bounds__(1024) void permute_rank_kernel(PermuteArgs a) {
 // counts), and the experts' offsets. A workgroup 64 keys: a wave takes a run of
 // chunks; the keys below the workgroup's are summed by each workgroup itself,
 // from the chunks' sums of 64 keys, so that one launch needs no order among
-// workgroups (64 chunks of 897 keys: SCANNEW us; without those sums 10.5; all keys
+// workgroups (64 chunks of 897 keys: 5.0 us; without those sums 10.5; all keys
 // in one workgroup, chunk after chunk, 27).
 __global__ __launch_bounds__(1024) void permute_scan_kernel(PermuteArgs a, int chunks) {
     constexpr int kRun = kMostChunks / 16;
@@ -504,11 +506,12 @@ __global__ __launch_bounds__(512) void unpermute_bwd_kernel(UnpermuteBwdArgs a, 
             }
             const f32x8 d = widen8<MODE>(fd, a.out_f32, i, H);
             if (a.dweights) {
+                const int skip = skip8<MODE>(i, H);
 #pragma unroll
                 for (int j = 0; j < KB; ++j) {
                     const f32x8 v = widen8<MODE>(y[j], Y32, i, H);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) dot[j] = fmaf(d[e], v[e], dot[j]);
+                    for (int e = 0; e < 8; ++e) dot[j] = e >= skip ? fmaf(d[e], v[e], dot[j]) : dot[j];
                 }
             }
             if (a.dy) {

@@ -60,9 +60,7 @@ __device__ __forceinline__ float wave_sum(float v) {
 // Eight elements i..i+7 of a row. VEC: all of them are in the row and 16-byte
 // aligned (8 bytes in q); else they are at any element's address, which one
 // wide load or store takes as well. The row's last eight may be fewer: they are
-// taken four, two and one at a time, by the bits of H, which all rows share
-// (1531 rows of 2793, layer norm with an fp32 stream: TAILNEW us, TAILOLD element by
-// element).
+// taken four, two and one at a time, by the bits of H, which all rows share.
 typedef f32x4 __attribute__((aligned(4))) f32x4_any;
 typedef f32x2 __attribute__((aligned(4))) f32x2_any;
 typedef u16x8 __attribute__((aligned(2))) u16x8_any;
@@ -161,8 +159,11 @@ __device__ __forceinline__ void store8(void* row, bool f32, int i, int H, f32x8 
 // The same in two halves, so that nothing waits between the loads of a row's
 // several operands: fetch8 loads (what it loads for f32 and for bf16 differs,
 // but no branch holds an arithmetic instruction), widen8 makes numbers of it.
-// MODE kAligned as VEC; kAnywhere: any element's address and H >= 8, where the
-// row's last eight are loaded from H - 8 on and moved down; kTiny: H < 8.
+// MODE kAligned as VEC; kTiny: H < 8. kAnywhere: any element's address and H >=
+// 8, where the lane of the row's last elements takes the last eight, from H - 8
+// on: the first skip8 of them are its neighbour's, who sums and stores them.
+// (Moving the lane's own to the front instead took a wave that holds a whole row
+// some half more: 32768 rows of 333, layer norm, 33 us, 22 so.)
 constexpr int kAligned = 0, kAnywhere = 1, kTiny = 2;
 
 struct Raw8 {
@@ -215,21 +216,38 @@ __device__ __forceinline__ f32x8 widen8(Raw8 r, bool f32, int i, int H) {
             v[2 * e + 1] = high_half(r.a[e]);
         }
     }
-    if constexpr (MODE == kAnywhere) {
-        const int down = i + 8 <= H ? 0 : i + 8 - H;
-        if (__any(down)) {
-#pragma unroll
-            for (int d = 4; d > 0; d /= 2)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = down & d ? (e + d < 8 ? v[e + d] : 0.0f) : v[e];
-        }
-    }
     return v;
 }
 
 template <int MODE>
+__device__ __forceinline__ int skip8(int i, int H) {
+    return MODE == kAnywhere && i + 8 > H ? i + 8 - H : 0;
+}
+
+template <int MODE>
 __device__ __forceinline__ void put8(void* row, bool f32, int i, int H, f32x8 v) {
-    store8<MODE == kAligned>(row, f32, i, H, v);
+    if (MODE != kAnywhere || i + 8 <= H) {
+        store8<MODE == kAligned>(row, f32, i, H, v);
+        return;
+    }
+    // The last H % 8 of v, one, two and four from the end.
+    const bool one = H & 1, two = H & 2;
+    const f32x2 b = one ? f32x2{v[5], v[6]} : f32x2{v[6], v[7]};
+    const f32x4 lo = __builtin_shufflevector(v, v, 1, 2, 3, 4), l2 = __builtin_shufflevector(v, v, 2, 3, 4, 5);
+    const f32x4 l3 = __builtin_shufflevector(v, v, 3, 4, 5, 6), l4 = __builtin_shufflevector(v, v, 4, 5, 6, 7);
+    const f32x4 c = one ? (two ? lo : l3) : (two ? l2 : l4);
+    const int at1 = H - 1, at2 = H - (one ? 3 : 2), at4 = i;
+    if (f32) {
+        float* p = (float*)row;
+        if (one) p[at1] = v[7];
+        if (two) *(f32x2_any*)(p + at2) = b;
+        if (H & 4) *(f32x4_any*)(p + at4) = c;
+    } else {
+        uint16_t* p = (uint16_t*)row;
+        if (one) p[at1] = f32_to_bf16_bits(v[7]);
+        if (two) *(u32_half*)(p + at2) = pack_bf16x2(b[0], b[1]);
+        if (H & 4) *(u32x2_half*)(p + at4) = u32x2{pack_bf16x2(c[0], c[1]), pack_bf16x2(c[2], c[3])};
+    }
 }
 
 }  // namespace rows
