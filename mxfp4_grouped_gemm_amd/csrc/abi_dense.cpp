@@ -195,8 +195,8 @@ bool valid_sizes(int T, int a, int b, int step) {
 
 struct LinearBwdLayout {
     int64_t sums, partial, total;  // dz at 0
-    int splits_dx;
-    bool few;
+    int splits_dw, splits_dx;
+    bool own;  // launch_linear_grads
 };
 
 LinearBwdLayout linear_bwd_layout(int T, int K, int N) {
@@ -204,13 +204,16 @@ LinearBwdLayout linear_bwd_layout(int T, int K, int N) {
     // (With addresses, as if all gradients were asked for: a gradient is then the
     // same alone.)
     float all;
-    const moe::DenseArgs dw = product(nullptr, N, nullptr, K, N, K, T, &all, K);
-    const moe::DenseArgs dx = product(nullptr, N, nullptr, K, T, K, N, &all, K);
-    L.few = moe::linear_short(dw, dx);
-    L.splits_dx = L.few ? moe::linear_short_splits(dx) : moe::dense_bwd_splits(dx);
+    moe::DenseArgs dw = product(nullptr, N, nullptr, K, N, K, T, &all, K);
+    moe::DenseArgs dx = product(nullptr, N, nullptr, K, T, K, N, &all, K);
+    L.own = moe::linear_grads_splits(dw, dx);
+    L.splits_dw = dw.splits;
+    L.splits_dx = dx.splits;
     L.sums = align_up((int64_t)T * N * 2, 256);
     L.partial = L.sums + align_up((int64_t)moe::linear_dz_parts(T, N) * N * 4, 256);
-    L.total = L.partial + align_up(moe::dense_partial_bytes(dx, L.splits_dx, moe::kEpiOut, false), 256);
+    // (One of the two is in parts at most.)
+    L.total = L.partial + align_up(moe::dense_partial_bytes(dx, L.splits_dx, moe::kEpiOut, false) +
+                                   moe::dense_partial_bytes(dw, L.splits_dw, moe::kEpiOut, false), 256);
     return L;
 }
 
@@ -641,11 +644,13 @@ moe_status moe_linear_backward(const void* dout, int64_t dout_stride, moe_dtype 
     const moe::ColumnJoin sums = {(const float*)((char*)workspace + L.sums), dbias, nullptr, T > 0 ? moe::linear_dz_parts(T, N) : 0,
                                   N, N, 1, bias_type == MOE_DT_F32};
     if (!dx && !dw) return hip_status(moe::launch_column_join(sums, true, s), "moe_linear_backward (bias)");
-    const moe::DenseArgs gw = product(dz, lddz, x, x_stride, N, K, T, dw, K);
+    moe::DenseArgs gw = product(dz, lddz, x, x_stride, N, K, T, dw, K);
+    gw.splits = L.splits_dw;
+    gw.partial = (float*)((char*)workspace + L.partial);
     moe::DenseArgs gx = product(dz, lddz, w, K, T, K, N, dx, dx_stride);
     gx.splits = L.splits_dx;
     gx.partial = (float*)((char*)workspace + L.partial);
-    if (L.few) return hip_status(moe::launch_linear_short_grads(gw, gx, sums, s), "moe_linear_backward (gradients)");
+    if (L.own) return hip_status(moe::launch_linear_grads(gw, gx, sums, s), "moe_linear_backward (gradients)");
     return hip_status(moe::launch_dense_grads(gw, product(nullptr, 0, nullptr, 0, 0, 0, 0, nullptr, 0), gx, sums, s),
                       "moe_linear_backward (gradients)");
 }

@@ -92,7 +92,10 @@ hipError_t launch_linear_dz(const LinearDzArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
-// Gradients of few tokens (an expert's rows): dw is a sum of one or two steps, bound
+// The products of the backward where the dense block's grid of whole sums leaves
+// compute units idle.
+//
+// Few tokens (an expert's rows): dw is a sum of one or two steps, bound
 // by what it writes, and dx a long sum of few rows. 128 x 128 tiles with two
 // small buffers, so that the loads of some overlap the stores of others (three
 // workgroups a compute unit), in one launch: parts of dx first, then the tiles
@@ -102,37 +105,51 @@ namespace {
 using dense::kEltBf16;
 using dense::Tile;
 
-struct ShortArgs {
+struct GradsArgs {
     DenseArgs dw, dx;
     int nx, nw;  // tiles of each
     ColumnJoin sums;
     int nsums;
 };
 
-using ShortDw = Tile<128, 128, 2, 2, true, true, kEltBf16, kEpiOut, false, false, 2, 64>;
-template <bool SPLIT>
-using ShortDx = Tile<128, 128, 2, 2, false, true, kEltBf16, kEpiOut, SPLIT, false, 2, 64>;
-
-template <bool SPLIT>
-__global__ __launch_bounds__(256, 2) void short_grads_kernel(ShortArgs g) {
-    using NN = ShortDx<SPLIT>;
-    static_assert(ShortDw::BUF == NN::BUF && NN::THREADS == 256, "one launch");
-    MOE_TILE_BUFFERS(s, 2, NN::BUF);
+// TN: tiles of dw; NN: of dx; each of them takes its product's parts first.
+template <class TN, class NN>
+__global__ __launch_bounds__(256, 2) void linear_grads_kernel(GradsArgs g) {
+    static_assert(TN::BUF == NN::BUF && TN::NB == NN::NB && TN::THREADS == 256 && NN::THREADS == 256, "one launch");
+    MOE_TILE_BUFFERS(s, NN::NB, NN::BUF);
     int id = (int)blockIdx.x - g.nsums;
     if (id < 0) {
         static_assert(NN::BUF >= column_join_lds(kFewRuns), "the sums meet in a tile's buffer");
         column_join<kFewRuns>(g.sums, (int)blockIdx.x, (float*)s[0]);
         return;
     }
-    const int parts = SPLIT ? g.dx.splits : 1;
-    if (id < g.nx * parts) {
-        dense::dense_tile<NN>(g.dx, id % g.nx, id / g.nx, s);
-        return;
-    }
-    dense::dense_tile<ShortDw>(g.dw, id - g.nx * parts, 0, s);
+    // The longer sums first.
+    const int first = NN::SPLIT || !TN::SPLIT ? g.nx * g.dx.splits : g.nw * g.dw.splits;
+    const bool later = id >= first;
+    if (later) id -= first;
+    if ((NN::SPLIT || !TN::SPLIT) != later) dense::dense_tile<NN>(g.dx, id % g.nx, id / g.nx, s);
+    else dense::dense_tile<TN>(g.dw, id % g.nw, id / g.nw, s);
 }
 
-int64_t tiles128(int M, int N) { return (int64_t)((M + 127) / 128) * ((N + 127) / 128); }
+template <class TN, class NN>
+hipError_t launch_grads(GradsArgs& g, hipStream_t s) {
+    g.nw = g.dw.out ? (int)dense::tiles_of<TN>(g.dw) : 0;
+    g.nx = g.dx.out ? (int)dense::tiles_of<NN>(g.dx) : 0;
+    g.nsums = g.sums.out0 ? column_join_groups(g.sums) : 0;
+    const unsigned grid = (unsigned)(g.nsums + g.nx * g.dx.splits + g.nw * g.dw.splits);
+    hipLaunchKernelGGL((linear_grads_kernel<TN, NN>), dim3(grid), dim3(256), 0, s, g);
+    hipError_t e = hipGetLastError();
+    if (e == hipSuccess && g.nx && NN::SPLIT) e = launch_join(g.dx, kEpiOut, s);
+    if (e == hipSuccess && g.nw && TN::SPLIT) e = launch_join(g.dw, kEpiOut, s);
+    return e;
+}
+
+template <int EDGE, int NB, int KB, bool SPLIT>
+using DwTile = Tile<EDGE, EDGE, 2, 2, true, true, kEltBf16, kEpiOut, SPLIT, false, NB, KB>;
+template <int EDGE, int NB, int KB, bool SPLIT>
+using DxTile = Tile<EDGE, EDGE, 2, 2, false, true, kEltBf16, kEpiOut, SPLIT, false, NB, KB>;
+
+int64_t tiles_by(int edge, const DenseArgs& a) { return (int64_t)((a.M + edge - 1) / edge) * ((a.N + edge - 1) / edge); }
 
 }  // namespace
 
@@ -142,32 +159,45 @@ int64_t tiles128(int M, int N) { return (int64_t)((M + 127) / 128) * ((N + 127) 
 // 26.6 and 30.6, 128 32.9 and 32.8, 300 43 and 55; K = 2048, N = 1408: 16 tokens
 // 18.8 and 22.2, 256 (not here) 25.3 and 21.1; K = 1024, N = 8192: 256 tokens 33 and
 // 38; K = 8192, N = 1024: 16 tokens 19.0 and 26.2, 256 (not here) 30.9 and 25.1.
-bool linear_short(const DenseArgs& dw, const DenseArgs& dx) {
+static bool few_tokens(const DenseArgs& dw, const DenseArgs& dx) {
     const int T = dx.M;
-    if (T == 0 || T > 512 || tiles128(dw.M, dw.N) < 128) return false;
+    if (T == 0 || T > 512 || tiles_by(128, dw) < 128) return false;
     return T <= 128 || ((int64_t)dw.M * dw.N >= 1 << 22 && dense_dx_alone(dw, DenseArgs{}, dx));
 }
 
-int linear_short_splits(const DenseArgs& dx) {
-    // A workgroup a compute unit, four steps of 64 and more each.
-    const int64_t most = dx.K / 256, room = 256 / tiles128(dx.M, dx.N);
-    const int64_t s = room < most ? room : most;
-    return s < 2 ? 1 : s > 16 ? 16 : (int)s;
+// Weights of few tiles and many tokens: the sum over the tokens in parts, four
+// steps of 64 and more, two workgroups a compute unit. In us, here and in the grid
+// of whole sums: K = N = 512: 8000 tokens 34 and 69, 4000 25 and 40, 2000 (not here)
+// 22 and 17; K = N = 256: 8000 tokens 27 and 68; K = N = 768: 8000 tokens 50 and 71,
+// 3000 28.5 and 35; K = 256, N = 2048: 4000 tokens 33 and 32, 3000 29 and 27; K =
+// N = 896 (196 tiles, not here): 4000 tokens 41 both.
+static bool long_sums(const DenseArgs& dw) { return dw.K >= 3000 && tiles_by(64, dw) <= 160; }
+
+bool linear_grads_splits(DenseArgs& dw, DenseArgs& dx) {
+    auto parts = [](int64_t room, int64_t most) { return (int)(room < most ? (room < 16 ? room : 16) : (most < 16 ? most : 16)); };
+    dw.splits = dx.splits = 1;
+    if (few_tokens(dw, dx)) {
+        // A workgroup a compute unit, four steps of 64 and more each.
+        const int s = parts(256 / tiles_by(128, dx), dx.K / 256);
+        dx.splits = s < 2 ? 1 : s;
+        return true;
+    }
+    if (long_sums(dw)) {
+        dw.splits = parts(512 / tiles_by(64, dw), dw.K / 256);
+        return true;
+    }
+    dx.splits = dense_bwd_splits(dx);
+    return false;
 }
 
-hipError_t launch_linear_short_grads(const DenseArgs& dw, const DenseArgs& dx, const ColumnJoin& sums, hipStream_t s) {
-    ShortArgs g;
+hipError_t launch_linear_grads(const DenseArgs& dw, const DenseArgs& dx, const ColumnJoin& sums, hipStream_t s) {
+    GradsArgs g;
     g.dw = dw;
     g.dx = dx;
     g.sums = sums;
-    g.nw = dw.out ? (int)tiles128(dw.M, dw.N) : 0;
-    g.nx = dx.out ? (int)tiles128(dx.M, dx.N) : 0;
-    g.nsums = sums.out0 ? column_join_groups(sums) : 0;
-    const unsigned grid = (unsigned)(g.nsums + g.nx * dx.splits + g.nw);
-    if (dx.splits > 1) hipLaunchKernelGGL(short_grads_kernel<true>, dim3(grid), dim3(256), 0, s, g);
-    else hipLaunchKernelGGL(short_grads_kernel<false>, dim3(grid), dim3(256), 0, s, g);
-    const hipError_t e = hipGetLastError();
-    return e != hipSuccess || !dx.out || dx.splits == 1 ? e : launch_join(dx, kEpiOut, s);
+    if (dw.splits > 1) return launch_grads<DwTile<64, 4, 128, true>, DxTile<64, 4, 128, false>>(g, s);
+    if (dx.splits > 1) return launch_grads<DwTile<128, 2, 64, false>, DxTile<128, 2, 64, true>>(g, s);
+    return launch_grads<DwTile<128, 2, 64, false>, DxTile<128, 2, 64, false>>(g, s);
 }
 
 }  // namespace moe

@@ -59,11 +59,10 @@ struct LinearDzArgs {
 };
 int linear_dz_parts(int T, int N);
 hipError_t launch_linear_dz(const LinearDzArgs& a, hipStream_t s);
-// dw = dz^T x and dx = dz W of few tokens (linear_short), with the parts of dx
-// that linear_short_splits gives (dx.splits); else launch_dense_grads.
-bool linear_short(const DenseArgs& dw, const DenseArgs& dx);
-int linear_short_splits(const DenseArgs& dx);
-hipError_t launch_linear_short_grads(const DenseArgs& dw, const DenseArgs& dx, const ColumnJoin& sums, hipStream_t s);
+// dw = dz^T x and dx = dz W: the parts of their sums (the products' splits), and
+// whether they are for launch_linear_grads (else launch_dense_grads).
+bool linear_grads_splits(DenseArgs& dw, DenseArgs& dx);
+hipError_t launch_linear_grads(const DenseArgs& dw, const DenseArgs& dx, const ColumnJoin& sums, hipStream_t s);
 
 // Rows of elt bytes an element. `rows` [T, topk]: the sorted row of each pair,
 // -1 - row for a pair of no expert.

@@ -664,6 +664,21 @@ def test_linear_backward_of_few_tokens(moe, T, K, N, a, dt):
         assert [t is not None for t in one] == [i == k for i in range(3)] and torch.equal(one[k], got[k])
 
 
+# (the sum over the tokens in parts)
+@pytest.mark.parametrize("T,K,N", [(3000, 264, 136), (3001, 64, 8), (4100, 520, 264), (3333, 768, 768)])
+@pytest.mark.parametrize("a,dt", [(ref.GELU, BF), (ref.NONE, BF), (ref.RELU, F32)])
+def test_linear_backward_of_many_tokens(moe, T, K, N, a, dt):
+    g = gen(T + K)
+    dout, x, pre = rnd(g, T, N, dtype=dt), rnd(g, T, K + 8), rnd(g, T, N)
+    w = rnd(g, N, K, scale=1 / math.sqrt(K))
+    args = [cuda(dout), cuda(x)[:, :K], cuda(w)]
+    got = moe.moe_linear_backward(*args, pre=cuda(pre), act=a)
+    check_linear_bwd(a, dout, x[:, :K], pre, w, got)
+    for k in range(3):
+        one = moe.moe_linear_backward(*args, pre=cuda(pre), act=a, need_dx=k == 0, need_dw=k == 1, need_dbias=k == 2)
+        assert [t is not None for t in one] == [i == k for i in range(3)] and torch.equal(one[k], got[k])
+
+
 @pytest.mark.parametrize("a", [ref.NONE, ref.GELU])
 def test_linear_backward_strides_and_rows_behind(moe, a):
     g = gen(3)
