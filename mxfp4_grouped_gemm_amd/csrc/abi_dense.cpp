@@ -196,7 +196,7 @@ bool valid_sizes(int T, int a, int b, int step) {
 struct LinearBwdLayout {
     int64_t sums, partial, total;  // dz at 0
     int splits_dw, splits_dx;
-    bool own;  // launch_linear_grads
+    moe::LinearGrads plan;
 };
 
 LinearBwdLayout linear_bwd_layout(int T, int K, int N) {
@@ -206,7 +206,7 @@ LinearBwdLayout linear_bwd_layout(int T, int K, int N) {
     float all;
     moe::DenseArgs dw = product(nullptr, N, nullptr, K, N, K, T, &all, K);
     moe::DenseArgs dx = product(nullptr, N, nullptr, K, T, K, N, &all, K);
-    L.own = moe::linear_grads_splits(dw, dx);
+    L.plan = moe::linear_grads_plan(dw, dx);
     L.splits_dw = dw.splits;
     L.splits_dx = dx.splits;
     L.sums = align_up((int64_t)T * N * 2, 256);
@@ -650,9 +650,7 @@ moe_status moe_linear_backward(const void* dout, int64_t dout_stride, moe_dtype 
     moe::DenseArgs gx = product(dz, lddz, w, K, T, K, N, dx, dx_stride);
     gx.splits = L.splits_dx;
     gx.partial = (float*)((char*)workspace + L.partial);
-    if (L.own) return hip_status(moe::launch_linear_grads(gw, gx, sums, s), "moe_linear_backward (gradients)");
-    return hip_status(moe::launch_dense_grads(gw, product(nullptr, 0, nullptr, 0, 0, 0, 0, nullptr, 0), gx, sums, s),
-                      "moe_linear_backward (gradients)");
+    return hip_status(moe::launch_linear_grads(gw, gx, sums, L.plan, s), "moe_linear_backward (gradients)");
 }
 
 }  // extern "C"

@@ -173,31 +173,43 @@ static bool few_tokens(const DenseArgs& dw, const DenseArgs& dx) {
 // N = 896 (196 tiles, not here): 4000 tokens 41 both.
 static bool long_sums(const DenseArgs& dw) { return dw.K >= 3000 && tiles_by(64, dw) <= 160; }
 
-bool linear_grads_splits(DenseArgs& dw, DenseArgs& dx) {
+LinearGrads linear_grads_plan(DenseArgs& dw, DenseArgs& dx) {
     auto parts = [](int64_t room, int64_t most) { return (int)(room < most ? (room < 16 ? room : 16) : (most < 16 ? most : 16)); };
     dw.splits = dx.splits = 1;
     if (few_tokens(dw, dx)) {
         // A workgroup a compute unit, four steps of 64 and more each.
         const int s = parts(256 / tiles_by(128, dx), dx.K / 256);
         dx.splits = s < 2 ? 1 : s;
-        return true;
+        return kGradsFew;
     }
     if (long_sums(dw)) {
         dw.splits = parts(512 / tiles_by(64, dw), dw.K / 256);
-        return true;
+        return kGradsSmall;
     }
-    dx.splits = dense_bwd_splits(dx);
-    return false;
+    // Small products whose dx would go alone, in parts: with dw in 64 x 64 tiles,
+    // and in parts from 32 steps on (fewer do not pay for the join). 117 tokens, K =
+    // 216, N = 1376: 17.4 us, alone 25.8; 346 tokens, K = 120, N = 2184, in parts:
+    // 19.8 and 24.0; 500 tokens, K = 256, N = 4096: 19.7 and 26.0.
+    const int s = dense_bwd_splits(dx);
+    if (s < 2) return kGradsDense;
+    dx.splits = dx.K >= 2048 ? s : 1;
+    return kGradsSmall;
 }
 
-hipError_t launch_linear_grads(const DenseArgs& dw, const DenseArgs& dx, const ColumnJoin& sums, hipStream_t s) {
+hipError_t launch_linear_grads(const DenseArgs& dw, const DenseArgs& dx, const ColumnJoin& sums, LinearGrads plan,
+                               hipStream_t s) {
     GradsArgs g;
     g.dw = dw;
     g.dx = dx;
     g.sums = sums;
+    if (plan == kGradsDense) return launch_dense_grads(dw, DenseArgs{}, dx, sums, s);
+    if (plan == kGradsFew) {
+        if (dx.splits > 1) return launch_grads<DwTile<128, 2, 64, false>, DxTile<128, 2, 64, true>>(g, s);
+        return launch_grads<DwTile<128, 2, 64, false>, DxTile<128, 2, 64, false>>(g, s);
+    }
     if (dw.splits > 1) return launch_grads<DwTile<64, 4, 128, true>, DxTile<64, 4, 128, false>>(g, s);
-    if (dx.splits > 1) return launch_grads<DwTile<128, 2, 64, false>, DxTile<128, 2, 64, true>>(g, s);
-    return launch_grads<DwTile<128, 2, 64, false>, DxTile<128, 2, 64, false>>(g, s);
+    if (dx.splits > 1) return launch_grads<DwTile<64, 4, 128, false>, DxTile<64, 4, 128, true>>(g, s);
+    return launch_grads<DwTile<64, 4, 128, false>, DxTile<64, 4, 128, false>>(g, s);
 }
 
 }  // namespace moe

@@ -59,10 +59,16 @@ struct LinearDzArgs {
 };
 int linear_dz_parts(int T, int N);
 hipError_t launch_linear_dz(const LinearDzArgs& a, hipStream_t s);
-// dw = dz^T x and dx = dz W: the parts of their sums (the products' splits), and
-// whether they are for launch_linear_grads (else launch_dense_grads).
-bool linear_grads_splits(DenseArgs& dw, DenseArgs& dx);
-hipError_t launch_linear_grads(const DenseArgs& dw, const DenseArgs& dx, const ColumnJoin& sums, hipStream_t s);
+// dw = dz^T x and dx = dz W: how they are launched, which sets the parts of their
+// sums (the products' splits; one of them is in parts at most).
+enum LinearGrads {
+    kGradsDense,  // launch_dense_grads
+    kGradsFew,    // few tokens: 128 x 128 tiles with small buffers
+    kGradsSmall   // 64 x 64 tiles
+};
+LinearGrads linear_grads_plan(DenseArgs& dw, DenseArgs& dx);
+hipError_t launch_linear_grads(const DenseArgs& dw, const DenseArgs& dx, const ColumnJoin& sums, LinearGrads plan,
+                               hipStream_t s);
 
 // Rows of elt bytes an element. `rows` [T, topk]: the sorted row of each pair,
 // -1 - row for a pair of no expert.

@@ -651,7 +651,8 @@ def test_linear_backward_large_tiles(moe, T, K, N):
 # (sums of few tokens beside weights of many tiles: in one launch, dx in parts
 # and whole)
 @pytest.mark.parametrize("T,K,N", [(1, 4096, 520), (5, 1032, 4104), (33, 8192, 264), (100, 1032, 2056), (128, 2056, 1288),
-                                   (129, 2056, 1288), (300, 1024, 4104), (512, 1024, 4104)])
+                                   (129, 2056, 1288), (300, 1024, 4104), (512, 1024, 4104), (117, 216, 1376), (346, 120, 2184),
+                                   (64, 8, 8192)])
 @pytest.mark.parametrize("a,dt", [(ref.GELU, BF), (ref.NONE, BF), (ref.SILU, F32)])
 def test_linear_backward_of_few_tokens(moe, T, K, N, a, dt):
     g = gen(T + K)
