@@ -419,10 +419,10 @@ hipError_t launch_column_join(const ColumnJoin& j, bool few, hipStream_t s) {
 
 constexpr int kHeldColumns = 16384;  // of a row in registers, with the sums of its columns
 
-// Up to so many rows the sums over them are taken in the launch of the rows (3584
-// columns: 1024 rows 13.4 us, 1025 rows in two launches 17.7; 8192 columns 24 and
-// 28).
-constexpr int kFewRows = 1024;
+// Whether the sums over the rows are taken in the launch of the rows (3584
+// columns: 1024 rows 13.4 us, 1025 rows in two launches 17.7, 2048 so 21.2 and in
+// two 18.3; 256 columns: 2048 rows 12.9, in two launches 17.5).
+static bool few_rows(int T, int H) { return H <= kHeldColumns && T <= (H <= 512 ? 2048 : 1024); }
 
 // Workgroups of the rows; those of long rows, of the columns' runs of rows.
 static int layer_norm_groups(int T, int H, bool held) {
@@ -440,11 +440,8 @@ static int layer_norm_groups(int T, int H, bool held) {
 static bool held_row(int H, bool aligned) { return H <= (aligned ? kHeldColumns : 8192); }
 
 int layer_norm_parts(int T, int H) {
-    return T <= kFewRows && H <= kHeldColumns ? 0 : layer_norm_groups(T, H, held_row(H, true));
+    return few_rows(T, H) ? 0 : layer_norm_groups(T, H, held_row(H, true));
 }
-
-// Rows few enough for one launch.
-static bool few_rows(int T, int H) { return T <= kFewRows && H <= kHeldColumns; }
 
 template <int WAVES, int NC, int MODE, bool S32>
 static void launch_bwd_as(const LayerNormBwdArgs& a, hipStream_t s) {

@@ -53,7 +53,8 @@ def near(got, want, tol, what=""):
 # ------------------------------------------------------------------ layer norm
 # (one row to thousands; widths at the borders of the kernels' row sizes, odd ones)
 NORMS = [(1, 1), (3, 7), (1, 3584), (5, 33), (2, 512), (7, 513), (4, 1000), (2050, 520), (2049, 1032), (300, 2793),
-         (9, 4096), (3, 4104), (2, 8192), (5, 8193), (3, 16384), (70, 16390), (2, 20000), (1, 65536)]
+         (9, 4096), (3, 4104), (2, 8192), (5, 8193), (3, 16384), (70, 16390), (2, 20000), (1, 65536), (1024, 530), (1025, 529), (2048, 96),
+         (2049, 99)]
 
 
 @pytest.mark.parametrize("T,H", NORMS)
