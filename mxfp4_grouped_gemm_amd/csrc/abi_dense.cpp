@@ -534,6 +534,10 @@ moe_status moe_layer_norm_backward(const uint16_t* dy, int64_t dy_stride, const 
         return fail(MOE_ERR_INVALID_ARG, "%s: misaligned output", fn);
     if (T > 0) {
         if (!dy || !s || !mean || !rstd || !weight) return fail(MOE_ERR_INVALID_ARG, "%s: null pointer", fn);
+        // (The sums over the rows read dy and s beside the rows' own workgroups.)
+        const void* outs[] = {dx, dresidual};
+        for (const void* o : outs)
+            if (o == dy || o == s) return fail(MOE_ERR_INVALID_ARG, "%s: dx and dresidual must not be dy or s", fn);
         if (!aligned(dy, 2) || !aligned(s, sa) || !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(weight, wa) ||
             !aligned(dresidual_out, sa))
             return fail(MOE_ERR_INVALID_ARG, "%s: misaligned pointer", fn);
@@ -626,8 +630,9 @@ moe_status moe_linear_backward(const void* dout, int64_t dout_stride, moe_dtype 
         moe::LinearDzArgs z;
         z.dout = dout;
         z.pre = pre;
-        // Without an activation dz is dout, if that has its type.
-        z.dz = act == MOE_LINEAR_NONE && dout_type == MOE_DT_BF16 ? nullptr : (uint16_t*)workspace;
+        // Without an activation dz is dout, if that has its type; for dbias alone it
+        // is not kept.
+        z.dz = (act == MOE_LINEAR_NONE && dout_type == MOE_DT_BF16) || (!dx && !dw) ? nullptr : (uint16_t*)workspace;
         z.partial = dbias ? (float*)((char*)workspace + L.sums) : nullptr;
         z.lddo = dout_stride;
         z.T = T;
@@ -638,7 +643,7 @@ moe_status moe_linear_backward(const void* dout, int64_t dout_stride, moe_dtype 
             dz = z.dz;
             lddz = N;
         }
-        if (dbias || (z.dz && (dx || dw))) LAUNCH(moe::launch_linear_dz(z, s), "moe_linear_backward (dz)");
+        if (dbias || z.dz) LAUNCH(moe::launch_linear_dz(z, s), "moe_linear_backward (dz)");
     }
     // (With T == 0 the sums are empty and write zeros.)
     const moe::ColumnJoin sums = {(const float*)((char*)workspace + L.sums), dbias, nullptr, T > 0 ? moe::linear_dz_parts(T, N) : 0,

@@ -43,8 +43,8 @@ def test_layer_norm_refusals():
     assert norm(m=P + 2) == BAD and norm(q=P + 1) == BAD
 
 
-def norm_bwd(dy=P, lddy=64, s=P, lds=64, st=0, m=P, q=P, w=P, wt=0, dr=P, lddr=64, T=4, H=64, dx=P, lddx=64, dres=P,
-             lddres=64, dw=P, db=P, ws=P, wsb=BIG):
+def norm_bwd(dy=P, lddy=64, s=P, lds=64, st=0, m=P, q=P, w=P, wt=0, dr=P, lddr=64, T=4, H=64, dx=2 * P, lddx=64,
+             dres=3 * P, lddres=64, dw=P, db=P, ws=P, wsb=BIG):
     return L.moe_layer_norm_backward(dy, lddy, s, lds, st, m, q, w, wt, dr, lddr, T, H, dx, lddx, dres, lddres, dw, db,
                                      ws, wsb, None)
 
@@ -61,6 +61,8 @@ def test_layer_norm_backward_refusals():
         assert said(norm_bwd(**{k: None}), "null") == BAD and said(norm_bwd(**{k: P + 1}), "misaligned") == BAD
     for k in ("dx", "dres", "dw", "db"):
         assert said(norm_bwd(**{k: P + 1}), "misaligned output") == BAD
+    for k in ("dx", "dres"):
+        assert said(norm_bwd(**{k: P}), "must not be dy or s") == BAD
     assert norm_bwd(s=P + 2, st=1) == BAD and norm_bwd(dr=P + 2, st=1) == BAD and norm_bwd(dw=P + 2, wt=1) == BAD
     need = moe.moe_layer_norm_backward_workspace_size(4000, 64)
     assert need > 0 and need % 256 == 0
