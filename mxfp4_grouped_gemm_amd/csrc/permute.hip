@@ -24,10 +24,13 @@ typedef uint32_t __attribute__((aligned(1))) u32_byte;
 typedef uint16_t __attribute__((aligned(1))) u16_byte;
 
 constexpr int kMaxTopk = 64;
-// Up to this many pairs each wave counts the pairs before its own: one launch (8
-// choices of 112 experts, rows of 3584: 2400 pairs 13.4 us, 18.8 in three launches;
-// 4096 pairs 26.4 and 18.6, 3000 pairs of 128 columns 12.4 and 18.8).
-constexpr int kFewPairs = 2560;
+// Up to so many pairs each wave counts the pairs before its own: one launch, but
+// the counting grows with their square, and the three launches copy wide rows
+// faster (8 choices of 112 experts, one launch and three: rows of 3584, 2400 pairs
+// 13.4 us and 18.8, 4096 pairs 26.4 and 18.6; rows of 1024, 4000 pairs 14.3 and
+// 18.4, 6400 pairs 24.5 and 18.3).
+constexpr int kFewPairs = 2560, kFewNarrowPairs = 4096;
+constexpr int64_t kNarrowRow = 2048;  // bytes
 constexpr int kSlice = 1024;      // pairs ranked at once
 constexpr int kMostChunks = 256;  // of slices; the scan takes them in one workgroup
 constexpr int kKeys = 1025;       // experts, and none
@@ -342,7 +345,7 @@ hipError_t launch_permute(const PermuteArgs& a, hipStream_t s) {
         hipLaunchKernelGGL(clear_kernel, dim3((unsigned)((a.E + 256) / 256)), dim3(256), 0, s, a.offsets, a.E + 1);
         return hipGetLastError();
     }
-    if (P <= kFewPairs) {
+    if (P <= kFewPairs || (P <= kFewNarrowPairs && a.row_bytes <= kNarrowRow)) {
         hipLaunchKernelGGL(permute_few_kernel, dim3((unsigned)(P + 3) / 4 + 1), dim3(256), 0, s, a);
         return hipGetLastError();
     }

@@ -278,7 +278,8 @@ def values(g, T, H, dt):
 # pairs below and above what one launch takes, whole slices of 1024 and one
 # more, more slices than chunks
 PAIRS = [(1, 1, 1), (1, 15, 112), (16, 15, 112), (3, 64, 1000), (128, 16, 64), (2048, 1, 5), (2049, 1, 1024), (1024, 3, 1),
-         (1025, 2, 1023), (700, 8, 257), (5000, 4, 64)]
+         (1025, 2, 1023), (700, 8, 257), (5000, 4, 64), (1365, 3, 70),
+         (4096, 1, 70), (4097, 1, 70)]
 
 
 @pytest.mark.parametrize("T,k,E", PAIRS)
@@ -295,7 +296,7 @@ def test_permute(moe, T, k, E, how):
 
 @pytest.mark.parametrize("H", [1, 3, 7, 8, 15, 64, 100, 2793, 3584, 4097])
 @pytest.mark.parametrize("dt", [BF, F32, U8, torch.uint8])
-@pytest.mark.parametrize("T,k", [(5, 3), (1100, 2)])
+@pytest.mark.parametrize("T,k", [(5, 3), (1100, 2), (1300, 2)])
 def test_permute_widths_and_types(moe, H, dt, T, k):
     g = gen(H + T)
     E = 7
