@@ -49,6 +49,28 @@ __global__ __launch_bounds__(256) void join_kernel(DenseArgs a) {  // 64 or 256 
     }
 }
 
+// The plain product with activation in 64 x 64 tiles: up to two workgroups a
+// compute unit, and for two of them no sum so long that the bytes of LDS that
+// these tiles read twice would count. In us, in 64 x 64 tiles and in the others
+// (with K in parts and a join): K = N = 1024: 65 to 800 tokens 10.7, 13.5 to 20; K =
+// 1024, N = 4096: 128 tokens 10.7 and 16.5, 512 11.6 and 26.3, 800 (832 tiles)
+// 19.9 and 17.5; K = 3584, N = 4096: 128 tokens 15.1 and 22.1, 512 26.7 and 32.8;
+// K = N = 8192: 128 tokens 44.2 both, 200 (512 tiles) 62.9 and 52.5.
+int64_t small_tiles(const DenseArgs& a) { return (int64_t)((a.M + 63) / 64) * ((a.N + 63) / 64); }
+bool small_act(const DenseArgs& a) {
+    const int64_t t = small_tiles(a);
+    return t <= 256 || (t <= 512 && a.K <= 4096);
+}
+
+hipError_t launch_act(const DenseArgs& a, hipStream_t s) {
+    if (a.splits > 1) {
+        const hipError_t e = launch_tile<Tile<64, 64, 2, 2, false, false, kEltBf16, kEpiOut, true, false, 8>>(a, s);
+        return e != hipSuccess ? e : launch_join(a, kEpiAct, s);
+    }
+    if (small_tiles(a) <= 256) return launch_tile<Tile<64, 64, 2, 2, false, false, kEltBf16, kEpiAct, false, false, 8>>(a, s);
+    return launch_tile<Tile<64, 64, 2, 2, false, false, kEltBf16, kEpiAct, false, false, 4>>(a, s);
+}
+
 template <int EPI, bool LORA>
 hipError_t launch_epi(const DenseArgs& a, hipStream_t s) {
     if (dense_big_tiles(a, EPI))
@@ -81,6 +103,12 @@ bool dense_one_round(const DenseArgs& a, int epi) {
 }
 
 int dense_splits(const DenseArgs& a, int elt, int epi) {
+    if (epi == kEpiAct && a.M > 0 && small_act(a)) {
+        // From 64 steps on the sum's parts pay for the join.
+        const int64_t steps = (a.K + 63) / 64, most = steps / 16, room = 256 / small_tiles(a);
+        const int64_t s = room < most ? room : most;
+        return steps < 64 || s < 2 ? 1 : s > 16 ? 16 : (int)s;
+    }
     if (dense_big_tiles(a, epi)) return 1;
     const bool gated = epi_gated(epi);
     const int64_t cols = gated ? 2 * (int64_t)a.N : a.N;
@@ -107,7 +135,7 @@ hipError_t launch_join(const DenseArgs& a, int epi, hipStream_t s) {
 }
 
 hipError_t launch_dense_nt(const DenseArgs& a, int epi, hipStream_t s) {
-    if (epi == kEpiAct) return launch_epi<kEpiAct, false>(a, s);
+    if (epi == kEpiAct) return small_act(a) ? launch_act(a, s) : launch_epi<kEpiAct, false>(a, s);
     if (epi == kEpiOut) return a.lora.n > 0 ? launch_epi<kEpiOut, true>(a, s) : launch_epi<kEpiOut, false>(a, s);
     return a.lora.n > 0 ? launch_epi<kEpiGated, true>(a, s) : launch_epi<kEpiGated, false>(a, s);
 }

@@ -821,32 +821,37 @@ __device__ __forceinline__ void dense_tile(const DenseArgs& a, int id, int part,
             }
         }
         if constexpr (kAct) {
-            static_assert(C::FN == 4, "sixteen outputs a lane");
+            static_assert(C::FN == 4 || C::FN == 2, "sixteen or eight outputs a lane");
             if (!mok) continue;  // (the same in the lanes that trade)
-            float v[16];
+            constexpr int W = C::FN * 4;
+            float v[W];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] = acc[e / 4][j][e % 4] + bias[e / 8][e % 8];
-            const int nw = n0 + wn * 64;
-            if (a.pre) store_rows16(a.pre + m * (int64_t)a.N + nw, g, a.N - nw, v);
-            activate<16>(a.act, v);
+            for (int e = 0; e < W; ++e) v[e] = acc[e / 4][j][e % 4] + bias[e / 8][e % 8];
+            const int nw = n0 + wn * 16 * C::FN;
+            auto store = [&](uint16_t* row) {
+                if constexpr (C::FN == 4) store_rows16(row, g, a.N - nw, v);
+                else if (8 * g < a.N - nw) store_bf16<8>(row + 8 * g, v);
+            };
+            if (a.pre) store(a.pre + m * (int64_t)a.N + nw);
+            activate<W>(a.act, v);
             if (a.addend_f32) {
 #pragma unroll
-                for (int e = 0; e < 16; ++e) v[e] += __uint_as_float(e % 8 < 4 ? ra[j % JB][e / 8][e % 4] : rb[j % JB][e / 8][e % 4]);
+                for (int e = 0; e < W; ++e) v[e] += __uint_as_float(e % 8 < 4 ? ra[j % JB][e / 8][e % 4] : rb[j % JB][e / 8][e % 4]);
             } else if (a.addend) {
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
+                for (int e = 0; e < W; ++e) {
                     const uint32_t d = ra[j % JB][e / 8][e % 8 / 2];
                     v[e] += __uint_as_float(e & 1 ? d & 0xffff0000u : d << 16);
                 }
             }
             if (a.out_f32) {
 #pragma unroll
-                for (int e = 0; e < 16; e += 4) {
+                for (int e = 0; e < W; e += 4) {
                     const int n = n_of(e / 4);
                     if (n < a.N) *(f32x4*)((float*)a.out + m * a.ldo + n) = f32x4{v[e], v[e + 1], v[e + 2], v[e + 3]};
                 }
             } else {
-                store_rows16((uint16_t*)a.out + m * a.ldo + nw, g, a.N - nw, v);
+                store((uint16_t*)a.out + m * a.ldo + nw);
             }
         } else if constexpr (C::EPI == kEpiOut) {
             if (!mok) continue;
