@@ -821,6 +821,9 @@ __device__ __forceinline__ void dense_tile(const DenseArgs& a, int id, int part,
             }
         }
         if constexpr (kAct) {
+            // 8192 tokens, 8192 columns over K = 3584: 384 us without activation,
+            // 411 with GELU, 428 with its argument saved too (the runs of 64 bytes
+            // of store_rows16: 4 us of it).
             static_assert(C::FN == 4 || C::FN == 2, "sixteen or eight outputs a lane");
             if (!mok) continue;  // (the same in the lanes that trade)
             constexpr int W = C::FN * 4;

