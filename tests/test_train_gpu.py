@@ -279,7 +279,7 @@ def values(g, T, H, dt):
 # more, more slices than chunks
 PAIRS = [(1, 1, 1), (1, 15, 112), (16, 15, 112), (3, 64, 1000), (128, 16, 64), (2048, 1, 5), (2049, 1, 1024), (1024, 3, 1),
          (1025, 2, 1023), (700, 8, 257), (5000, 4, 64), (1365, 3, 70),
-         (4096, 1, 70), (4097, 1, 70)]
+         (4096, 1, 70), (4097, 1, 70), (1024, 8, 1024), (8193, 1, 1024)]
 
 
 @pytest.mark.parametrize("T,k,E", PAIRS)
@@ -359,6 +359,50 @@ def test_permute_above_4_gib(moe):
     dy, _ = moe.moe_unpermute_backward(back, rows)
     for c in (0, H - 1):
         assert torch.equal(dy[:, c], back[token, c])
+
+
+def test_layer_norm_above_4_gib(moe):
+    T, H = 300_000, 8192  # 4.6 GiB of bf16, 9.2 of fp32
+    x = torch.empty(T, H, dtype=BF, device="cuda").normal_()
+    r = torch.empty(T, H, device="cuda").normal_()
+    w, b = (torch.empty(H, device="cuda").normal_() for _ in range(2))
+    y, s, mean, rstd = moe.moe_layer_norm_forward(x, w, b, residual=r, save_stats=True)
+    rows = [0, 131071, 262143, 262144, 299_999]
+    s64, v, m, q = ref.layer_norm(dbl(x[rows]), dbl(r[rows]), dbl(w), dbl(b), 1e-5)
+    near(y[rows], v, ref.layer_norm_tol(s64, m, q, dbl(w), v), "y")
+    near(s[rows], s64, F24 * s64.abs(), "s")
+    del r
+    dx, ds, dw, db = moe.moe_layer_norm_backward(x, s, mean, rstd, w, dresidual_out=s, need_dresidual=True)
+    want, tols = ref.layer_norm_backward(dbl(x[rows]), dbl(s[rows]), dbl(mean[rows]), dbl(rstd[rows]), dbl(w), dbl(s[rows]))
+    near(dx[rows], want[0], tols[0], "dx")
+    near(ds[rows], want[0], tols[0], "dresidual")
+    # (T / 512 rows a workgroup, 128 runs of those)
+    for c in (0, H - 1):
+        d = dbl(x[:, c])
+        n = (dbl(s[:, c]) - dbl(mean)) * dbl(rstd)
+        near(db[c:c + 1], d.sum().view(1), (T / 512 + 70) * F24 * d.abs().sum(), "dbias")
+        near(dw[c:c + 1], (d * n).sum().view(1), (T / 512 + 80) * F24 * (d * n).abs().sum(), "dweight")
+
+
+def test_linear_above_4_gib(moe):
+    T, K, N = 300_000, 64, 8192  # out, pre and dout of 4.6 GiB
+    g = gen(9)
+    x = torch.empty(T, K, dtype=BF, device="cuda").normal_()
+    w, b = cuda(rnd(g, N, K, scale=K ** -0.5)), cuda(rnd(g, N))
+    out, pre = moe.moe_linear_forward(x, w, b, act=ref.GELU, save_pre=True)
+    rows = [0, 131071, 262143, 262144, 299_999]
+    check_linear(moe, ref.GELU, x[rows].cpu(), w.cpu(), b.cpu(), None, out[rows], pre[rows])
+    dx, dw, db = moe.moe_linear_backward(out, x, w, pre=pre, act=ref.GELU)
+    check_linear_bwd(ref.GELU, out[rows].cpu(), x[rows].cpu(), pre[rows].cpu(), w.cpu(), (dx[rows], None, None))
+    for c in (0, N - 1):
+        s64, t = ref.slope(ref.GELU, dbl(pre[:, c]))
+        full = dbl(out[:, c]) * s64
+        near(db[c:c + 1], full.sum().view(1), (T / 64 + 300) * F24 * full.abs().sum() + (dbl(out[:, c]).abs() * t).sum(), "dbias")
+        dz = dense_ref.bf16(full)
+        want = dz @ dbl(x)
+        # (sums of T / 8 terms in a row at most, and dz on the other side of a tie)
+        tol = (T / 8 + 64) * F24 * (dz.abs() @ dbl(x).abs()) + dense_ref.FLIPS * want.square().mean().sqrt()
+        near(dw[c], want, tol, "dw")
 
 
 def plan(g, T, k, E=9, how="absent"):
