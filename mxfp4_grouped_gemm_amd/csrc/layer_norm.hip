@@ -339,8 +339,9 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void layer_norm_bwd_
 }
 
 // Rows that registers do not hold: a workgroup a row, which is read twice (the
-// second time from L2).
-template <bool VEC, bool S32>
+// second time from L2). With the columns' sums below, 4000 rows of 12288 with a bf16
+// stream 119 us (491 MB read or written once: 4.1 TB/s); of 10001: 138.
+template <int MODE, bool S32>
 __global__ __launch_bounds__(1024) void layer_norm_bwd_long_kernel(LayerNormBwdArgs a) {
     __shared__ float part[16][2];
     const int tid = (int)threadIdx.x, H = a.H;
@@ -350,10 +351,12 @@ __global__ __launch_bounds__(1024) void layer_norm_bwd_long_kernel(LayerNormBwdA
     const char* sr = (const char*)a.s + t * a.lds * (S32 ? 4 : 2);
     float sg = 0.0f, sgn = 0.0f;
     for (int i = tid * 8; i < H; i += 8192) {
-        const f32x8 d = load8<VEC>(dr, false, i, H), n = load8<VEC>(sr, S32, i, H), w = load8<VEC>(a.weight, a.weight_f32, i, H);
+        const Raw8 fd = fetch8<MODE>(dr, false, i, H), fs = fetch8<MODE>(sr, S32, i, H), fw = fetch8<MODE>(a.weight, a.weight_f32, i, H);
+        const f32x8 d = widen8<MODE>(fd, false, i, H), n = widen8<MODE>(fs, S32, i, H), w = widen8<MODE>(fw, a.weight_f32, i, H);
+        const int skip = skip8<MODE>(i, H);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            if (!VEC && i + e >= H) continue;
+            if (e < skip) continue;
             const float g = d[e] * w[e];
             sg += g;
             sgn = fmaf(g, (n[e] - mean) * rstd, sgn);
@@ -374,37 +377,56 @@ __global__ __launch_bounds__(1024) void layer_norm_bwd_long_kernel(LayerNormBwdA
     }
     const float mg = sg * inv, mgn = sgn * inv;
     for (int i = tid * 8; i < H; i += 8192) {
-        const f32x8 d = load8<VEC>(dr, false, i, H), n = load8<VEC>(sr, S32, i, H), w = load8<VEC>(a.weight, a.weight_f32, i, H);
+        const Raw8 fd = fetch8<MODE>(dr, false, i, H), fs = fetch8<MODE>(sr, S32, i, H), fw = fetch8<MODE>(a.weight, a.weight_f32, i, H);
+        Raw8 fr;
+        if (a.dres) fr = fetch8<MODE>((const char*)a.dres + t * a.lddr * (S32 ? 4 : 2), S32, i, H);
+        const f32x8 d = widen8<MODE>(fd, false, i, H), n = widen8<MODE>(fs, S32, i, H), w = widen8<MODE>(fw, a.weight_f32, i, H);
         f32x8 v;
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = rstd * ((d[e] * w[e] - mg) - (n[e] - mean) * rstd * mgn);
-        if (a.dres) v += load8<VEC>((const char*)a.dres + t * a.lddr * (S32 ? 4 : 2), S32, i, H);
-        if (a.dx) store8<VEC>(a.dx + t * a.lddx, false, i, H, v);
-        if (a.dresidual) store8<VEC>((char*)a.dresidual + t * a.lddro * (S32 ? 4 : 2), S32, i, H, v);
+        if (a.dres) v += widen8<MODE>(fr, S32, i, H);
+        if (a.dx) put8<MODE>(a.dx + t * a.lddx, false, i, H, v);
+        if (a.dresidual) put8<MODE>((char*)a.dresidual + t * a.lddro * (S32 ? 4 : 2), S32, i, H, v);
     }
 }
 
 // The sums over the rows alone: a thread eight columns, rows blockIdx.y, +
-// gridDim.y, ...
-template <bool VEC, bool S32>
+// gridDim.y, ..., four in flight (16000 rows of 10001: 477 us, one at a time 890).
+template <int MODE, bool S32>
 __global__ __launch_bounds__(256) void layer_norm_columns_kernel(LayerNormBwdArgs a) {
+    constexpr int kAtOnce = 4;
     const int i = ((int)blockIdx.x * 256 + (int)threadIdx.x) * 8, H = a.H;
     if (i >= H) return;
     f32x8 aw = {0, 0, 0, 0, 0, 0, 0, 0}, ab = aw;
-    for (int64_t t = (int64_t)blockIdx.y; t < a.T; t += gridDim.y) {
-        const float mean = a.mean[t], rstd = a.rstd[t];
-        const f32x8 d = load8<VEC>(a.dy + t * a.lddy, false, i, H);
-        const f32x8 n = load8<VEC>((const char*)a.s + t * a.lds * (S32 ? 4 : 2), S32, i, H);
+    const int64_t step = (int64_t)gridDim.y;
+    for (int64_t t0 = (int64_t)blockIdx.y; t0 < a.T; t0 += step * kAtOnce) {
+        Raw8 fd[kAtOnce], fs[kAtOnce];
+        float mean[kAtOnce], rstd[kAtOnce];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            aw[e] = VEC || i + e < H ? fmaf(d[e], (n[e] - mean) * rstd, aw[e]) : 0.0f;
-            ab[e] += d[e];
+        for (int k = 0; k < kAtOnce; ++k) {
+            // (A row past the end: the first one, not used.)
+            const int64_t t = t0 + k * step < a.T ? t0 + k * step : t0;
+            mean[k] = a.mean[t];
+            rstd[k] = a.rstd[t];
+            fd[k] = fetch8<MODE>(a.dy + t * a.lddy, false, i, H);
+            fs[k] = fetch8<MODE>((const char*)a.s + t * a.lds * (S32 ? 4 : 2), S32, i, H);
+        }
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            if (t0 + k * step >= a.T) continue;
+            const f32x8 d = widen8<MODE>(fd[k], false, i, H), n = widen8<MODE>(fs[k], S32, i, H);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                aw[e] = fmaf(d[e], (n[e] - mean[k]) * rstd[k], aw[e]);
+                ab[e] += d[e];
+            }
         }
     }
-    const int ld = (H + 7) & ~7;
-    float* p = a.partial + (int64_t)blockIdx.y * 2 * ld + i;
+    const int ld = (H + 7) & ~7, skip = skip8<MODE>(i, H);
+    float* p = a.partial + (int64_t)blockIdx.y * 2 * ld + i - skip;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
+        if (e < skip) continue;
         p[e] = aw[e];
         p[ld + e] = ab[e];
     }
@@ -423,39 +445,39 @@ hipError_t launch_column_join(const ColumnJoin& j, bool few, hipStream_t s) {
     return hipGetLastError();
 }
 
-constexpr int kHeldColumns = 16384;  // of a row in registers, with the sums of its columns
+// Columns of a row in registers with the sums of its columns (4000 rows of 12288 in
+// 16 waves 145 us, read twice 119), and without them, for few rows.
+constexpr int kHeldColumns = 8192, kFewColumns = 16384;
 
 // Whether the sums over the rows are taken in the launch of the rows (3584
 // columns: 1024 rows 13.4 us, 1025 rows in two launches 17.7, 2048 so 21.2 and in
-// two 18.3; 256 columns: 2048 rows 12.9, in two launches 17.5).
-static bool few_rows(int T, int H) { return H <= kHeldColumns && T <= (H <= 512 ? 2048 : 1024); }
+// two 18.3; 256 columns: 2048 rows 12.9, in two launches 17.5; 12288 columns, whose
+// rows spill: 600 rows 26.2, in three launches 29.3, 1000 rows 40.4 and 35.6).
+static bool few_rows(int T, int H) { return H <= kFewColumns && T <= (H <= 512 ? 2048 : H <= kHeldColumns ? 1024 : 640); }
 
 // Workgroups of the rows; those of long rows, of the columns' runs of rows.
-static int layer_norm_groups(int T, int H, bool held) {
+static int layer_norm_groups(int T, int H) {
     const int rows = H <= 512 ? 4 : 1;
     const int64_t groups = ((int64_t)T + rows - 1) / rows;
     // As many as the registers of their waves leave room for, but not so many that
     // their partial sums count (16384 rows of 3584: 512 workgroups 89 us, 768 96, 1024
-    // 104; 32768 of 1024: 1024 workgroups 54.6, 2048 59; 30000 of 640: 43.6 and 37.2).
-    const int most = !held ? 64 : H <= 512 ? 1024 : H <= 1024 ? 1280 : H <= 2048 ? 1024 : 512;
+    // 104; 32768 of 1024: 1024 workgroups 54.6, 2048 59; 30000 of 640: 43.6 and 37.2;
+    // 7000 of 8192: 256 workgroups 90.5, 512 96; 1500 of 8192: 26.6 and 34.3).
+    const int most = H <= 512 ? 1024 : H <= 1024 ? 1280 : H <= 2048 ? 1024 : H <= 4096 ? 512 : H <= kHeldColumns ? 256 : 64;
     return (int)(groups < most ? groups : most);
 }
 
-// Whether a row and its columns' sums stay in registers. (Rows of more than
-// 8192 at any address would spill a kilobyte a lane.)
-static bool held_row(int H, bool aligned) { return H <= (aligned ? kHeldColumns : 8192); }
-
 int layer_norm_parts(int T, int H) {
-    return few_rows(T, H) ? 0 : layer_norm_groups(T, H, held_row(H, true));
+    return few_rows(T, H) ? 0 : layer_norm_groups(T, H);
 }
 
 template <int WAVES, int NC, int MODE, bool S32>
 static void launch_bwd_as(const LayerNormBwdArgs& a, hipStream_t s) {
-    const int groups = layer_norm_groups(a.T, a.H, true), threads = WAVES == 1 ? 256 : WAVES * 64;
+    const int groups = layer_norm_groups(a.T, a.H), threads = WAVES == 1 ? 256 : WAVES * 64;
     if (few_rows(a.T, a.H)) {
         const int rows = a.dx || a.dresidual ? groups : 0, cols = a.dweight || a.dbias ? (a.H + 31) / 32 : 0;
         hipLaunchKernelGGL((layer_norm_bwd_few_kernel<WAVES, NC, MODE, S32>), dim3((unsigned)(rows + cols)), dim3(threads), 0, s, a, rows);
-    } else {
+    } else if constexpr (WAVES < 16) {
         hipLaunchKernelGGL((layer_norm_bwd_kernel<WAVES, NC, MODE, S32>), dim3((unsigned)groups), dim3(threads), 0, s, a);
     }
 }
@@ -473,7 +495,7 @@ static void launch_bwd(const LayerNormBwdArgs& a, bool vec, hipStream_t s) {
     else launch_bwd_mode<WAVES, NC, false>(a, vec, s);
 }
 
-template <bool VEC, bool S32>
+template <int MODE, bool S32>
 static hipError_t launch_long(const LayerNormBwdArgs& a, hipStream_t s) {
     if (a.dx || a.dresidual) {
         constexpr int kMostRows = 1 << 21;  // of 1024 threads: a launch holds fewer than 2^32
@@ -488,40 +510,38 @@ static hipError_t launch_long(const LayerNormBwdArgs& a, hipStream_t s) {
             if (a.dres) b.dres = (const char*)a.dres + t * a.lddr * sb;
             if (a.dx) b.dx = a.dx + t * a.lddx;
             if (a.dresidual) b.dresidual = (char*)a.dresidual + t * a.lddro * sb;
-            hipLaunchKernelGGL((layer_norm_bwd_long_kernel<VEC, S32>), dim3((unsigned)b.T), dim3(1024), 0, s, b);
+            hipLaunchKernelGGL((layer_norm_bwd_long_kernel<MODE, S32>), dim3((unsigned)b.T), dim3(1024), 0, s, b);
             const hipError_t e = hipGetLastError();
             if (e != hipSuccess) return e;
         }
     }
     if (a.partial) {
-        const dim3 grid((unsigned)((a.H + 2047) / 2048), (unsigned)layer_norm_groups(a.T, a.H, false));
-        hipLaunchKernelGGL((layer_norm_columns_kernel<VEC, S32>), grid, dim3(256), 0, s, a);
+        const dim3 grid((unsigned)((a.H + 2047) / 2048), (unsigned)layer_norm_groups(a.T, a.H));
+        hipLaunchKernelGGL((layer_norm_columns_kernel<MODE, S32>), grid, dim3(256), 0, s, a);
     }
     return hipGetLastError();
 }
 
 hipError_t launch_layer_norm_bwd(const LayerNormBwdArgs& a, hipStream_t s) {
     const bool sums = a.dweight || a.dbias;
-    bool held = true;
     if (a.T > 0) {
         const int sb = a.s_f32 ? 4 : 2;
         const bool vec = a.H % 8 == 0 && wide(a.dy, a.lddy, 2) && wide(a.s, a.lds, sb) && wide(a.dres, a.lddr, sb) &&
                          wide(a.dx, a.lddx, 2) && wide(a.dresidual, a.lddro, sb) && wide(a.weight, 0, 4);
-        held = held_row(a.H, vec);
         hipError_t e = hipSuccess;
         if (a.H <= 512) launch_bwd<1, 1>(a, vec, s);
         else if (a.H <= 1024) launch_bwd<2, 1>(a, vec, s);
         else if (a.H <= 2048) launch_bwd<4, 1>(a, vec, s);
         else if (a.H <= 4096) launch_bwd<4, 2>(a, vec, s);
         else if (a.H <= 8192) launch_bwd<8, 2>(a, vec, s);
-        else if (held_row(a.H, vec) || few_rows(a.T, a.H)) launch_bwd<16, 2>(a, vec, s);
-        else if (a.s_f32) e = vec ? launch_long<true, true>(a, s) : launch_long<false, true>(a, s);
-        else e = vec ? launch_long<true, false>(a, s) : launch_long<false, false>(a, s);
+        else if (few_rows(a.T, a.H)) launch_bwd<16, 2>(a, vec, s);
+        else if (a.s_f32) e = vec ? launch_long<kAligned, true>(a, s) : launch_long<kAnywhere, true>(a, s);
+        else e = vec ? launch_long<kAligned, false>(a, s) : launch_long<kAnywhere, false>(a, s);
         if (e == hipSuccess) e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
     if (!sums || (a.T > 0 && few_rows(a.T, a.H))) return hipSuccess;
-    return launch_column_join({a.partial, a.dweight, a.dbias, a.T > 0 ? layer_norm_groups(a.T, a.H, held) : 0, a.H,
+    return launch_column_join({a.partial, a.dweight, a.dbias, a.T > 0 ? layer_norm_groups(a.T, a.H) : 0, a.H,
                                (a.H + 7) & ~7, 2, a.weight_f32}, false, s);
 }
 

@@ -8,7 +8,9 @@ Tolerances, from the arithmetic (F = 2^-24, half a step of fp32):
     r the row's 1 / deviation;
   * its backward: n is off by 3 F |n| + F |s| r, the row's sums have at most 90
     (rows above 16384 columns: 8 a step of 8192) terms in a row; a column's sum has
-    at most T / parts + 70;
+    at most T / parts + 70: a workgroup's rows, its four waves, and a join of 128
+    runs by halves. Few rows: runs of T / 32 at least, and half as many as the runs
+    (128 of more than 8192 columns) behind each other;
   * hardware exp2 and reciprocal are off by about an ulp, 2 F, each; an exponent
     u, itself rounded, by |u| F more (a few of them: 4). So act(z) and act'(z)
     are off by (|u| + 8) 4 F of z p(u) for the sigmoid forms. Phi(-|z|) is off
@@ -55,9 +57,8 @@ def layer_norm_backward(dy, s, mean, rstd, weight, dres=None):
     if dres is not None:
         ds = ds + dres
         tol = tol + 2 * F * (ds.abs() + dres.abs())
-    terms = (T / min(T, 64) if H > 16384 else T / min(T, 1024)) + 70 if T else 1
-    if H <= 512:
-        terms = T / 4096 + 74
+    parts = 4096 if H <= 512 else 1024 if H <= 2048 else 512 if H <= 4096 else 256 if H <= 8192 else 64
+    terms = T / parts + (132 if H > 8192 else 74)
     tw = terms * F * (dy * n).abs().sum(0) + (dy.abs() * dn).sum(0)
     return (ds, (dy * n).sum(0), dy.sum(0)), (tol, tw, terms * F * dy.abs().sum(0))
 
