@@ -340,7 +340,7 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void layer_norm_bwd_
 
 // Rows that registers do not hold: a workgroup a row, which is read twice (the
 // second time from L2). With the columns' sums below, 4000 rows of 12288 with a bf16
-// stream 119 us (491 MB read or written once: 4.1 TB/s); of 10001: 138.
+// stream 119 us (393 MB read or written once: 3.3 TB/s); of 10001: 138.
 template <int MODE, bool S32>
 __global__ __launch_bounds__(1024) void layer_norm_bwd_long_kernel(LayerNormBwdArgs a) {
     __shared__ float part[16][2];
