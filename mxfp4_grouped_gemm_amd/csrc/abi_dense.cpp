@@ -6,6 +6,7 @@
 
 #include "abi_checks.hpp"
 #include "dense.hpp"
+#include "layer_norm_plan.hpp"
 #include "train.hpp"
 
 using namespace moe::abi;

@@ -13,6 +13,7 @@
 // 5.8 TB/s, and 5 for the join of the column sums. Rows that are not 16-byte
 // aligned: 106 and 107 (3583 columns).
 #include "common.hpp"
+#include "layer_norm_plan.hpp"
 #include "row_io.hpp"
 #include "train.hpp"
 
@@ -445,37 +446,12 @@ hipError_t launch_column_join(const ColumnJoin& j, bool few, hipStream_t s) {
     return hipGetLastError();
 }
 
-// Columns of a row in registers with the sums of its columns (4000 rows of 12288 in
-// 16 waves 145 us, read twice 119), and without them, for few rows.
-constexpr int kHeldColumns = 8192, kFewColumns = 16384;
-
-// Whether the sums over the rows are taken in the launch of the rows (3584
-// columns: 1024 rows 13.4 us, 1025 rows in two launches 17.7, 2048 so 21.2 and in
-// two 18.3; 256 columns: 2048 rows 12.9, in two launches 17.5; 12288 columns, whose
-// rows spill: 600 rows 26.2, in three launches 29.3, 1000 rows 40.4 and 35.6).
-static bool few_rows(int T, int H) { return H <= kFewColumns && T <= (H <= 512 ? 2048 : H <= kHeldColumns ? 1024 : 640); }
-
-// Workgroups of the rows; those of long rows, of the columns' runs of rows.
-static int layer_norm_groups(int T, int H) {
-    const int rows = H <= 512 ? 4 : 1;
-    const int64_t groups = ((int64_t)T + rows - 1) / rows;
-    // As many as the registers of their waves leave room for, but not so many that
-    // their partial sums count (16384 rows of 3584: 512 workgroups 89 us, 768 96, 1024
-    // 104; 32768 of 1024: 1024 workgroups 54.6, 2048 59; 30000 of 640: 43.6 and 37.2;
-    // 7000 of 8192: 256 workgroups 90.5, 512 96; 1500 of 8192: 26.6 and 34.3).
-    const int most = H <= 512 ? 1024 : H <= 1024 ? 1280 : H <= 2048 ? 1024 : H <= 4096 ? 512 : H <= kHeldColumns ? 256 : 64;
-    return (int)(groups < most ? groups : most);
-}
-
-int layer_norm_parts(int T, int H) {
-    return few_rows(T, H) ? 0 : layer_norm_groups(T, H);
-}
-
 template <int WAVES, int NC, int MODE, bool S32>
 static void launch_bwd_as(const LayerNormBwdArgs& a, hipStream_t s) {
-    const int groups = layer_norm_groups(a.T, a.H), threads = WAVES == 1 ? 256 : WAVES * 64;
-    if (few_rows(a.T, a.H)) {
-        const int rows = a.dx || a.dresidual ? groups : 0, cols = a.dweight || a.dbias ? (a.H + 31) / 32 : 0;
+    const bool sums = a.dweight || a.dbias;
+    const int groups = layer_norm_row_groups(a.T, a.H, sums), threads = WAVES == 1 ? 256 : WAVES * 64;
+    if (layer_norm_few_rows(a.T, a.H)) {
+        const int rows = a.dx || a.dresidual ? groups : 0, cols = sums ? (a.H + 31) / 32 : 0;
         hipLaunchKernelGGL((layer_norm_bwd_few_kernel<WAVES, NC, MODE, S32>), dim3((unsigned)(rows + cols)), dim3(threads), 0, s, a, rows);
     } else if constexpr (WAVES < 16) {
         hipLaunchKernelGGL((layer_norm_bwd_kernel<WAVES, NC, MODE, S32>), dim3((unsigned)groups), dim3(threads), 0, s, a);
@@ -516,7 +492,7 @@ static hipError_t launch_long(const LayerNormBwdArgs& a, hipStream_t s) {
         }
     }
     if (a.partial) {
-        const dim3 grid((unsigned)((a.H + 2047) / 2048), (unsigned)layer_norm_groups(a.T, a.H));
+        const dim3 grid((unsigned)((a.H + 2047) / 2048), (unsigned)layer_norm_parts(a.T, a.H));
         hipLaunchKernelGGL((layer_norm_columns_kernel<MODE, S32>), grid, dim3(256), 0, s, a);
     }
     return hipGetLastError();
@@ -534,15 +510,15 @@ hipError_t launch_layer_norm_bwd(const LayerNormBwdArgs& a, hipStream_t s) {
         else if (a.H <= 2048) launch_bwd<4, 1>(a, vec, s);
         else if (a.H <= 4096) launch_bwd<4, 2>(a, vec, s);
         else if (a.H <= 8192) launch_bwd<8, 2>(a, vec, s);
-        else if (few_rows(a.T, a.H)) launch_bwd<16, 2>(a, vec, s);
+        else if (layer_norm_few_rows(a.T, a.H)) launch_bwd<16, 2>(a, vec, s);
         else if (a.s_f32) e = vec ? launch_long<kAligned, true>(a, s) : launch_long<kAnywhere, true>(a, s);
         else e = vec ? launch_long<kAligned, false>(a, s) : launch_long<kAnywhere, false>(a, s);
         if (e == hipSuccess) e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    if (!sums || (a.T > 0 && few_rows(a.T, a.H))) return hipSuccess;
-    return launch_column_join({a.partial, a.dweight, a.dbias, a.T > 0 ? layer_norm_groups(a.T, a.H) : 0, a.H,
-                               (a.H + 7) & ~7, 2, a.weight_f32}, false, s);
+    if (!sums || (a.T > 0 && layer_norm_few_rows(a.T, a.H))) return hipSuccess;
+    return launch_column_join({a.partial, a.dweight, a.dbias, layer_norm_parts(a.T, a.H), a.H, (a.H + 7) & ~7, 2, a.weight_f32},
+                              false, s);
 }
 
 }  // namespace moe

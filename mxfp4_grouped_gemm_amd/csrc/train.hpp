@@ -43,8 +43,6 @@ struct LayerNormBwdArgs {
     int T, H;
     int s_f32, weight_f32;
 };
-// Parts that the sums over the rows are taken in (0: no partial sums).
-int layer_norm_parts(int T, int H);
 hipError_t launch_layer_norm_bwd(const LayerNormBwdArgs& a, hipStream_t s);
 
 // dz = dout act'(pre) and its sums over the rows. dz may be null (dz == dout).
