@@ -442,6 +442,7 @@ moe_status moe_layer_norm_forward(const uint16_t* x, int64_t x_stride, const voi
  *   dy       bf16 [T, H];  s [T, H] of s_type (the forward's residual_out, or x).
  *   dresidual_out  [T, H] of s_type: the gradient of residual_out, or NULL.
  *   dx       out bf16 [T, H]: ds, or NULL;  dresidual  out [T, H] of s_type: ds, or NULL.
+ *            Neither may share rows with dy or s: other workgroups read these for the sums.
  *   dweight, dbias  out [H] of weight_type, each may be NULL; overwritten, and
  *            no sum depends on the order of atomics.
  * At least one output is required unless T == 0 (dweight and dbias are then

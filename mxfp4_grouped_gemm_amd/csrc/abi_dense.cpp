@@ -7,6 +7,7 @@
 #include "abi_checks.hpp"
 #include "dense.hpp"
 #include "layer_norm_plan.hpp"
+#include "rows_overlap.hpp"
 #include "train.hpp"
 
 using namespace moe::abi;
@@ -239,6 +240,20 @@ moe_status check_norm(const char* fn, int T, int H, moe_dtype stream_type, moe_d
     if (H < 1) return fail(MOE_ERR_INVALID_ARG, "%s: H=%d < 1", fn, H);
     if (H > kMaxNormed) return fail(MOE_ERR_UNSUPPORTED, "%s: H=%d > %d", fn, H, kMaxNormed);
     return check_types(fn, stream_type, weight_type);
+}
+
+// A matrix's rows: their distance and an element's size.
+struct RowsOf {
+    const void* p;
+    int64_t stride;
+    size_t size;
+};
+
+bool same_rows(const RowsOf& a, const RowsOf& b) { return a.p == b.p && a.stride == b.stride && a.size == b.size; }
+
+bool share_rows(const RowsOf& a, const RowsOf& b, int T, int H) {
+    const int64_t sa = (int64_t)a.size, sb = (int64_t)b.size;
+    return a.p && b.p && rows_overlap((int64_t)a.p, a.stride * sa, H * sa, (int64_t)b.p, b.stride * sb, H * sb, T);
 }
 
 moe_status check_linear(const char* fn, int T, int K, int N, moe_linear_act act, moe_dtype out_type, moe_dtype bias_type) {
@@ -543,10 +558,13 @@ moe_status moe_layer_norm_backward(const uint16_t* dy, int64_t dy_stride, const 
         return fail(MOE_ERR_INVALID_ARG, "%s: misaligned output", fn);
     if (T > 0) {
         if (!dy || !s || !mean || !rstd || !weight) return fail(MOE_ERR_INVALID_ARG, "%s: null pointer", fn);
-        // (The sums over the rows read dy and s beside the rows' own workgroups.)
-        const void* outs[] = {dx, dresidual};
-        for (const void* o : outs)
-            if (o == dy || o == s) return fail(MOE_ERR_INVALID_ARG, "%s: dx and dresidual must not be dy or s", fn);
+        // (The sums over the rows read dy and s beside the rows' own workgroups; a row's
+        // workgroup reads its row of dresidual_out before it writes there.)
+        const RowsOf outs[] = {{dx, dx_stride, 2}, {dresidual, dresidual_stride, sa}}, gy = {dy, dy_stride, 2},
+                     gs = {s, s_stride, sa}, gr = {dresidual_out, dresidual_out_stride, sa};
+        for (const RowsOf& o : outs)
+            if (share_rows(o, gy, T, H) || share_rows(o, gs, T, H) || (!same_rows(o, gr) && share_rows(o, gr, T, H)))
+                return fail(MOE_ERR_INVALID_ARG, "%s: dx and dresidual must not be dy or s or share rows with an input", fn);
         if (!aligned(dy, 2) || !aligned(s, sa) || !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(weight, wa) ||
             !aligned(dresidual_out, sa))
             return fail(MOE_ERR_INVALID_ARG, "%s: misaligned pointer", fn);

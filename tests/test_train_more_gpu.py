@@ -1,9 +1,10 @@
 """More sizes, layouts and far values of the operators of a trainable expert block
 (MI355X); forms and tolerances as in test_train_gpu.py."""
 import pytest
+import torch
 
-from tests import test_train_gpu as base
-from tests.test_train_gpu import BF, F32, moe  # noqa: F401
+from tests import test_train_gpu as base, train_ref as ref
+from tests.test_train_gpu import BF, F32, cuda, dbl, gen, moe, near, rnd  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -13,3 +14,23 @@ pytestmark = pytest.mark.gpu
 @pytest.mark.parametrize("kind", [(BF, True), (F32, False)])
 def test_layer_norm_backward_of_wide_rows(moe, T, H, kind):  # noqa: F811
     base.test_layer_norm_backward(moe, T, H, kind)
+
+
+@pytest.mark.parametrize("T,H", [(6, 7), (40, 301), (1500, 96), (1100, 1032), (1030, 8201), (30, 16400)])
+def test_layer_norm_backward_in_columns_of_its_inputs_buffer(moe, T, H):  # noqa: F811
+    """dx beside dy in one buffer, and dresidual in dresidual_out's own rows; rows of
+    dy or s are refused."""
+    g = gen(T + H)
+    both, s, dr = cuda(rnd(g, T, 2 * H)), cuda(rnd(g, T + 1, H, dtype=F32)), cuda(rnd(g, T, H, dtype=F32))
+    w = cuda(rnd(g, H))
+    _, _, mean, rstd = (cuda(t.float()) for t in ref.layer_norm(dbl(s[:T]), None, torch.ones(H).double(), None, 1e-5))
+    dy, dx = both[:, :H], both[:, H:]
+    keep = dr.clone()
+    want = moe.moe_layer_norm_backward(dy.clone(), s[:T], mean, rstd, w, dresidual_out=keep, need_dresidual=True)
+    got = moe.moe_layer_norm_backward(dy, s[:T], mean, rstd, w, dresidual_out=dr, need_dresidual=True, dx=dx, dresidual=dr)
+    assert got[0].data_ptr() == dx.data_ptr() and got[1].data_ptr() == dr.data_ptr()
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
+    with pytest.raises(moe.MoeError, match="share rows"):
+        moe.moe_layer_norm_backward(dy, s[:T], mean, rstd, w, need_dx=False, need_dresidual=True, dresidual=s[1:])
+    with pytest.raises(moe.MoeError, match="share rows"):
+        moe.moe_layer_norm_backward(dy, s[:T], mean, rstd, w, dx=both[:, H - 1:2 * H - 1])
