@@ -171,8 +171,16 @@ static bool few_tokens(const DenseArgs& dw, const DenseArgs& dx) {
 // of whole sums: K = N = 512: 8000 tokens 34 and 69, 4000 25 and 40, 2000 (not here)
 // 22 and 17; K = N = 256: 8000 tokens 27 and 68; K = N = 768: 8000 tokens 50 and 71,
 // 3000 28.5 and 35; K = 256, N = 2048: 4000 tokens 33 and 32, 3000 29 and 27; K =
-// N = 896 (196 tiles, not here): 4000 tokens 41 both.
-static bool long_sums(const DenseArgs& dw) { return dw.K >= 3000 && tiles_by(64, dw) <= 160; }
+// N = 896 (196 tiles, not here): 4000 tokens 41 both. Where dx's sum is as long and
+// would be left whole on a few compute units, that one is in parts instead (below).
+// dw in parts, dx in parts: 3000 tokens, K = 64, N = 10240 93 and 72, N = 4096 39.3 and
+// 35.8; 5000, K = 8, N = 8192 94.8 and 82.1; 3500, K = 128, N = 5120 61.8 and 51.9; 4000,
+// K = 128, N = 4096 44.8 and 44.0; where it is shorter: 5000, K = 64, N = 4096 52.3 and
+// 54.9, 3000, K = 64, N = 2048 26.6 and 27.4 (6000, K = 64, N = 4096 66.3 and 60.8). Both
+// in parts, and a launch more: 75, 38.0, 84, 55.5, 47.0.
+static bool long_sums(const DenseArgs& dw, const DenseArgs& dx) {
+    return dw.K >= 3000 && tiles_by(64, dw) <= 160 && (dx.K < dw.K || dense_bwd_splits(dx) < 2);
+}
 
 LinearGrads linear_grads_plan(DenseArgs& dw, DenseArgs& dx) {
     auto parts = [](int64_t room, int64_t most) { return (int)(room < most ? (room < 16 ? room : 16) : (most < 16 ? most : 16)); };
@@ -183,7 +191,7 @@ LinearGrads linear_grads_plan(DenseArgs& dw, DenseArgs& dx) {
         dx.splits = s < 2 ? 1 : s;
         return kGradsFew;
     }
-    if (long_sums(dw)) {
+    if (long_sums(dw, dx)) {
         dw.splits = parts(512 / tiles_by(64, dw), dw.K / 256);
         return kGradsSmall;
     }

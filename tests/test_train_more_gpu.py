@@ -34,3 +34,10 @@ def test_layer_norm_backward_in_columns_of_its_inputs_buffer(moe, T, H):  # noqa
         moe.moe_layer_norm_backward(dy, s[:T], mean, rstd, w, need_dx=False, need_dresidual=True, dresidual=s[1:])
     with pytest.raises(moe.MoeError, match="share rows"):
         moe.moe_layer_norm_backward(dy, s[:T], mean, rstd, w, dx=both[:, H - 1:2 * H - 1])
+
+
+# (sums of thousands of tokens beside sums as long over the columns)
+@pytest.mark.parametrize("T,K,N", [(3000, 64, 4096), (3001, 8, 8192), (3500, 136, 4104), (5000, 64, 4096)])
+@pytest.mark.parametrize("a,dt", [(ref.GELU, BF), (ref.NONE, F32)])
+def test_linear_backward_of_two_long_sums(moe, T, K, N, a, dt):  # noqa: F811
+    base.test_linear_backward_of_many_tokens(moe, T, K, N, a, dt)

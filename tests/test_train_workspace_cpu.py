@@ -1,0 +1,39 @@
+"""Workspaces of the operators of a trainable expert block, and what they say of the
+parts that sums are taken in (no GPU; made-up device pointers, as in
+test_train_abi_cpu.py)."""
+import re
+
+import pytest
+import torch
+
+import mxfp4_grouped_gemm_amd as moe
+from tests.test_train_abi_cpu import BAD, linear_bwd
+
+pytestmark = pytest.mark.skipif(torch.cuda.is_available(), reason="host-only checks pass invalid device "
+                                "pointers; never run where a GPU is visible")
+
+
+def needed(call, **kw):
+    """Bytes that a call asks for."""
+    assert call(wsb=0, **kw) == BAD
+    return int(re.search(r"< (\d+) needed", moe.moe_last_error()).group(1))
+
+
+def backward(T, K, N):
+    return needed(linear_bwd, T=T, K=K, N=N, ldd=N, ldx=K, lddx=K)
+
+
+@pytest.mark.parametrize("K,N", [(64, 10240), (128, 5120), (8, 8192), (64, 4096), (128, 4096)])
+def test_long_sums_of_both_products(K, N):
+    """From 3000 tokens on the sum of dw is taken in parts, unless dx's is as long and
+    would be left whole on a few compute units: dx is in parts as with one token fewer
+    (its fp32 parts, T * K each, are in the workspace beside dz and the bias sums)."""
+    parts = lambda T: backward(T, K, N) - 2 * T * N  # noqa: E731
+    assert parts(2999) >= 2 * 2999 * K * 4
+    assert abs(parts(3000) - parts(2999)) <= 16 * K * 4 + N * 4 + 512
+
+
+@pytest.mark.parametrize("T,K,N", [(3000, 64, 2048), (5000, 64, 4096), (8000, 256, 256), (3000, 512, 1280)])
+def test_long_sums_of_dw(T, K, N):
+    """dx's sum is shorter: dw's is in parts (fp32, N * K each)."""
+    assert backward(T, K, N) - 2 * T * N >= 2 * N * K * 4
