@@ -159,11 +159,15 @@ int64_t tiles_by(int edge, const DenseArgs& a) { return (int64_t)((a.M + edge - 
 // and in that grid: K = 3584, N = 4096: 1 token 21.8 and 27.4, 16 24.0 and 29.2, 64
 // 26.6 and 30.6, 128 32.9 and 32.8, 300 43 and 55; K = 2048, N = 1408: 16 tokens
 // 18.8 and 22.2, 256 (not here) 25.3 and 21.1; K = 1024, N = 8192: 256 tokens 33 and
-// 38; K = 8192, N = 1024: 16 tokens 19.0 and 26.2, 256 (not here) 30.9 and 25.1.
+// 38; K = 8192, N = 1024: 16 tokens 19.0 and 26.2, 256 (not here) 30.9 and 25.1. Large
+// weights: K = 2048, N = 2816: 150 tokens 26.3 and 31.9, 256 29.0 and 32.8, 400 31.7 and
+// 31.8; K = 1408, N = 4096: 256 28.8 and 26.5; K = 2560, N = 2560: 150 24.8 and 31.6;
+// K = 2048, N = 2560: 256 29.1 and 31.9; smaller ones (not here): K = N = 2048: 200 26.3 and 23.6, 256 28.3 and 24.2; K = 1024, N
+// = 4096: 256 28.2 and 24.1, 400 29.7 and 26.9.
 static bool few_tokens(const DenseArgs& dw, const DenseArgs& dx) {
     const int T = dx.M;
     if (T == 0 || T > 512 || tiles_by(128, dw) < 128) return false;
-    return T <= 128 || ((int64_t)dw.M * dw.N >= 1 << 22 && dense_dx_alone(dw, DenseArgs{}, dx));
+    return T <= 128 || ((int64_t)dw.M * dw.N >= 5 << 20 && dense_dx_alone(dw, DenseArgs{}, dx));
 }
 
 // Weights of few tiles and many tokens: the sum over the tokens in parts, four

@@ -41,3 +41,9 @@ def test_layer_norm_backward_in_columns_of_its_inputs_buffer(moe, T, H):  # noqa
 @pytest.mark.parametrize("a,dt", [(ref.GELU, BF), (ref.NONE, F32)])
 def test_linear_backward_of_two_long_sums(moe, T, K, N, a, dt):  # noqa: F811
     base.test_linear_backward_of_many_tokens(moe, T, K, N, a, dt)
+
+
+@pytest.mark.parametrize("T,K,N", [(129, 2056, 2816), (300, 2056, 2816), (512, 1408, 4104), (256, 2048, 2048), (400, 1032, 4096)])
+@pytest.mark.parametrize("a,dt", [(ref.GELU, BF), (ref.NONE, BF), (ref.SILU, F32)])
+def test_linear_backward_of_few_tokens_of_large_weights(moe, T, K, N, a, dt):  # noqa: F811
+    base.test_linear_backward_of_few_tokens(moe, T, K, N, a, dt)

@@ -37,3 +37,13 @@ def test_long_sums_of_both_products(K, N):
 def test_long_sums_of_dw(T, K, N):
     """dx's sum is shorter: dw's is in parts (fp32, N * K each)."""
     assert backward(T, K, N) - 2 * T * N >= 2 * N * K * 4
+
+
+@pytest.mark.parametrize("T,K,N,n", [(128, 2048, 2048, 8), (129, 2048, 2048, 0), (256, 2048, 2048, 0), (256, 1024, 4096, 4),
+                                     (300, 1024, 4104, 3), (256, 2048, 2560, 8), (150, 2048, 2816, 8), (256, 3584, 4096, 4)])
+def test_parts_of_few_tokens(T, K, N, n):
+    """dx's parts: of 129 to 512 tokens those beside 128 x 128 tiles of dw only where the
+    weights are large (5 << 20 of them and more), a workgroup of 128 x 128 a compute unit
+    and four steps each at least; else those of 64 x 64 tiles, which leave 256 tokens of
+    2048 columns whole. (The bias sums: a part for 16 tokens.)"""
+    assert backward(T, K, N) - 2 * T * N - -(-T // 16) * N * 4 - n * T * K * 4 in range(0, 768)
