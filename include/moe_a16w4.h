@@ -292,7 +292,9 @@ moe_status mxfp4_to_int4g32_requant(const uint8_t* w, const uint8_t* scale_e8m0,
  * zero weight gradients). Sizes and strides of at most 2^18 columns (2^20 for
  * strides) and 2^24 tokens, else MOE_ERR_UNSUPPORTED. Sums are fp32. Calls
  * that need a workspace take one of the size that their query returns (-1 for
- * invalid sizes), 256-byte aligned; it is scratch for that call alone. Unless
+ * invalid sizes), 256-byte aligned; it is scratch for that call alone. The size
+ * is that of this T: sums of fewer tokens may be taken in more parts, so a buffer
+ * for calls of several sizes is as large as the largest of their queries. Unless
  * stated otherwise, outputs must not overlap inputs or each other.
  * ------------------------------------------------------------------------ */
 typedef enum { MOE_DT_BF16 = 0, MOE_DT_F32 = 1, MOE_DT_U8 = 2 /* bytes; moe_permute alone */ } moe_dtype;
@@ -446,7 +448,8 @@ moe_status moe_layer_norm_forward(const uint16_t* x, int64_t x_stride, const voi
  *   dweight, dbias  out [H] of weight_type, each may be NULL; overwritten, and
  *            no sum depends on the order of atomics.
  * At least one output is required unless T == 0 (dweight and dbias are then
- * zeros). The workspace is needed for dweight or dbias. */
+ * zeros). The workspace is needed for dweight or dbias; the query's size is
+ * enough for any smaller T as well. */
 int64_t moe_layer_norm_backward_workspace_size(int T, int H);
 moe_status moe_layer_norm_backward(const uint16_t* dy, int64_t dy_stride, const void* s,
                                    int64_t s_stride, moe_dtype s_type, const float* mean,
@@ -469,7 +472,8 @@ moe_status moe_layer_norm_backward(const uint16_t* dy, int64_t dy_stride, const 
  * 1 <= E <= 1024, 1 <= topk <= 64, 1 <= H <= 2^18, T <= 2^22. T == 0 writes
  * expert_offsets (zeros). Pointers need their element's alignment only. The
  * gradient of x is moe_unpermute of the gradient of out, without weights; other
- * rows by the same order: moe_unpermute_backward without weights and y. */
+ * rows by the same order: moe_unpermute_backward without weights and y. The
+ * query's size is enough for any smaller T as well. */
 int64_t moe_permute_workspace_size(int T, int topk, int E);
 moe_status moe_permute(const void* x, int64_t x_stride, moe_dtype type, const int32_t* topk_ids,
                        int T, int topk, int E, int H, void* out, int64_t out_stride, int32_t* rows,

@@ -34,7 +34,7 @@ extern "C" {
 
 int64_t moe_permute_workspace_size(int T, int topk, int E) {
     if (T < 0 || T > kMaxRowTokens || topk < 1 || topk > kMaxRowTopk || E < 1 || E > kMaxRowExperts) return -1;
-    return moe::permute_workspace_bytes((int64_t)T * topk, E);
+    return moe::permute_most_workspace_bytes((int64_t)T * topk, E);
 }
 
 moe_status moe_permute(const void* x, int64_t x_stride, moe_dtype type, const int32_t* topk_ids, int T, int topk, int E,
@@ -54,7 +54,7 @@ moe_status moe_permute(const void* x, int64_t x_stride, moe_dtype type, const in
         if (!x || !topk_ids || !out || !rows) return fail(MOE_ERR_INVALID_ARG, "%s: null pointer", fn);
         if (!aligned(x, size) || !aligned(out, size) || !aligned(topk_ids, 4) || !aligned(rows, 4))
             return fail(MOE_ERR_INVALID_ARG, "%s: misaligned pointer", fn);
-        CHECK(check_workspace(fn, workspace, workspace_bytes, moe_permute_workspace_size(T, topk, E)));
+        CHECK(check_workspace(fn, workspace, workspace_bytes, moe::permute_workspace_bytes((int64_t)T * topk, E)));
     }
     moe::PermuteArgs a;
     a.x = x;

@@ -337,8 +337,16 @@ __global__ __launch_bounds__(256) void clear_kernel(int32_t* p, int n) {
 
 }  // namespace
 
+static int64_t chunk_bytes(int64_t chunks, int E) { return (chunks * ((E + 1) * 2 + 16) * 4 + 255) / 256 * 256; }
+
 int64_t permute_workspace_bytes(int64_t pairs, int E) {
-    return pairs <= kFewPairs ? 0 : ((int64_t)chunks_of(pairs) * ((E + 1) * 2 + 16) * 4 + 255) / 256 * 256;
+    return pairs <= kFewPairs ? 0 : chunk_bytes(chunks_of(pairs), E);
+}
+
+// (Chunks of one slice up to the most there are, then fewer of several.)
+int64_t permute_most_workspace_bytes(int64_t pairs, int E) {
+    const int64_t slices = (pairs + kSlice - 1) / kSlice;
+    return pairs <= kFewPairs ? 0 : chunk_bytes(slices < kMostChunks ? slices : kMostChunks, E);
 }
 
 hipError_t launch_permute(const PermuteArgs& a, hipStream_t s) {

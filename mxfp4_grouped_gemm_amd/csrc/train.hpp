@@ -82,6 +82,8 @@ struct PermuteArgs {
     int T, topk, E;
 };
 int64_t permute_workspace_bytes(int64_t pairs, int E);
+// The most that so many pairs or fewer take.
+int64_t permute_most_workspace_bytes(int64_t pairs, int E);
 hipError_t launch_permute(const PermuteArgs& a, hipStream_t s);
 
 struct UnpermuteArgs {

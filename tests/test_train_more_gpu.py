@@ -47,3 +47,23 @@ def test_linear_backward_of_two_long_sums(moe, T, K, N, a, dt):  # noqa: F811
 @pytest.mark.parametrize("a,dt", [(ref.GELU, BF), (ref.NONE, BF), (ref.SILU, F32)])
 def test_linear_backward_of_few_tokens_of_large_weights(moe, T, K, N, a, dt):  # noqa: F811
     base.test_linear_backward_of_few_tokens(moe, T, K, N, a, dt)
+
+
+def test_one_buffer_for_several_sizes(moe):  # noqa: F811
+    """A workspace of the largest batch (of the sort), or of the largest query, for
+    smaller ones."""
+    E = 896
+    ws = torch.empty(moe.moe_permute_workspace_size(262145, 1, E), dtype=torch.uint8, device="cuda")
+    for T in (262145, 262144, 131073, 5000, 2561, 3):
+        x, ids = torch.arange(T, device="cuda", dtype=torch.int32).view(F32).unsqueeze(1), torch.arange(T, device="cuda", dtype=torch.int32) * 7 % (E + 1)
+        out, rows, off = moe.moe_permute(x.contiguous(), ids.unsqueeze(1).contiguous(), E, workspace=ws)
+        order = torch.sort(ids, stable=True).indices
+        n = int((ids < E).sum())
+        assert torch.equal(out.view(torch.int32).flatten()[:n].long(), order[:n]) and int(off[E]) == n
+    g = gen(1)
+    K = N = 512
+    ws = torch.empty(max(moe.moe_linear_backward_workspace_size(T, K, N) for T in (64, 512, 4096)), dtype=torch.uint8, device="cuda")
+    w = cuda(rnd(g, N, K))
+    for T in (4096, 512, 64):
+        d, x = cuda(rnd(g, T, N)), cuda(rnd(g, T, K))
+        assert all(torch.equal(p, q) for p, q in zip(moe.moe_linear_backward(d, x, w, workspace=ws), moe.moe_linear_backward(d, x, w)))

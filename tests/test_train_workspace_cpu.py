@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import mxfp4_grouped_gemm_amd as moe
-from tests.test_train_abi_cpu import BAD, linear_bwd
+from tests.test_train_abi_cpu import BAD, linear_bwd, permute
 
 pytestmark = pytest.mark.skipif(torch.cuda.is_available(), reason="host-only checks pass invalid device "
                                 "pointers; never run where a GPU is visible")
@@ -47,3 +47,27 @@ def test_parts_of_few_tokens(T, K, N, n):
     and four steps each at least; else those of 64 x 64 tiles, which leave 256 tokens of
     2048 columns whole. (The bias sums: a part for 16 tokens.)"""
     assert backward(T, K, N) - 2 * T * N - -(-T // 16) * N * 4 - n * T * K * 4 in range(0, 768)
+
+
+@pytest.mark.parametrize("k,E", [(1, 896), (8, 112), (15, 7), (64, 1024), (3, 1)])
+def test_sort_workspace_does_not_shrink(k, E):
+    """A buffer for the largest batch holds a smaller one's: its query never decreases
+    with T, and no batch asks for more than its own query."""
+    last = 0
+    tokens = sorted({t for n in (1, 2560, 2561, 4096, 262144, 262145, 524288, 1 << 20, 1 << 22) for t in (n // k, n // k + 1, n)
+                     if t <= 1 << 22} | set(range(0, 1 << 22, 99991)))
+    for T in tokens:
+        size = moe.moe_permute_workspace_size(T, k, E)
+        assert size >= last, T
+        last = size
+        if size and T * k > 4096:
+            assert needed(permute, T=T, k=k, E=E) <= size
+
+
+@pytest.mark.parametrize("H", [8, 512, 520, 1024, 4096, 8192, 8200, 16384, 20000])
+def test_layer_norm_workspace_does_not_shrink(H):
+    last = 0
+    for T in list(range(0, 6000, 7)) + [1 << 20, 1 << 24]:
+        size = moe.moe_layer_norm_backward_workspace_size(T, H)
+        assert size >= last, T
+        last = size
