@@ -437,7 +437,9 @@ moe_status moe_layer_norm_forward(const uint16_t* x, int64_t x_stride, const voi
                                   int64_t residual_out_stride, uint16_t* y, int64_t y_stride,
                                   float* mean, float* rstd, void* stream);
 
-/* Its backward from s, mean and rstd, with n as above (of this s) and g = dy * weight:
+/* Its backward from s, mean and rstd, with n = (s - mean) * rstd and g = dy * weight
+ * (the saved mean is fp32, so every n of a row is off by up to 2^-24 |mean| rstd, which
+ * counts where a mean is thousands of deviations; the forward's own mean is not rounded):
  *   ds = rstd * (g - mean(g) - n * mean(g * n)) + dresidual_out
  *   dweight = sum over rows of dy * n;  dbias = sum over rows of dy.
  * ds is the gradient of x and of the residual alike.

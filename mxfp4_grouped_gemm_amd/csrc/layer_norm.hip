@@ -5,7 +5,9 @@
 //   dweight = sum over rows of dy n;  dbias = sum over rows of dy.
 // Forward sums are fp64, s and s^2 in one pass: the variance is their
 // difference, which fp64 holds to 2^-52 (mean / deviation)^2, and squares of an
-// fp32 stream's largest numbers do not overflow. Backward sums are fp32.
+// fp32 stream's largest numbers do not overflow. Backward sums are fp32, and n is of
+// the saved mean, one fp32 number: off by up to 2^-24 |mean| r. (What it lost could be
+// found again only from the whole row, which the workgroups that sum columns do not see.)
 //
 // Both are bound by memory: a row is read once and stays in registers between
 // its sums and its outputs. Forward, 16384 rows of 3584 with a bf16 residual: 81 us,

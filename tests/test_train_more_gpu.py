@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from tests import test_train_gpu as base, train_ref as ref
-from tests.test_train_gpu import BF, F32, cuda, dbl, gen, moe, near, rnd  # noqa: F401
+from tests.test_train_gpu import BF, F24, F32, cuda, dbl, gen, moe, near, rnd  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -67,3 +67,25 @@ def test_one_buffer_for_several_sizes(moe):  # noqa: F811
     for T in (4096, 512, 64):
         d, x = cuda(rnd(g, T, N)), cuda(rnd(g, T, K))
         assert all(torch.equal(p, q) for p, q in zip(moe.moe_linear_backward(d, x, w, workspace=ws), moe.moe_linear_backward(d, x, w)))
+
+
+@pytest.mark.parametrize("T,H", [(40, 264), (300, 4104), (1030, 96), (1100, 1001), (30, 16400)])
+def test_layer_norm_backward_of_far_means(moe, T, H):  # noqa: F811
+    """The forward's statistics and the gradients from them against fp64 with the mean
+    as it is: what the saved mean loses is F |mean| r of n, which train_ref's tolerance
+    has (its F (|s| + |mean|) r), and rstd is within 8 F of itself, as in the forward's
+    test of such rows."""
+    g = gen(T + H)
+    s = rnd(g, T, H, dtype=F32) + torch.tensor([0.0, 1e3, -3e4, 3e4])[torch.arange(T) % 4].unsqueeze(1)
+    dy, w = rnd(g, T, H), rnd(g, H, dtype=F32)
+    zero = torch.zeros(T, H, dtype=BF)
+    _, s2, mean, rstd = moe.moe_layer_norm_forward(cuda(zero), cuda(w), residual=cuda(s), save_stats=True)
+    assert torch.equal(s2.cpu(), s)
+    _, dres, dw, db = moe.moe_layer_norm_backward(cuda(dy), s2, mean, rstd, cuda(w), need_dx=False, need_dresidual=True)
+    _, _, m, q = ref.layer_norm(dbl(s), None, dbl(w), None, 1e-5)
+    want, tols = ref.layer_norm_backward(dbl(dy), dbl(s), m, q, dbl(w))
+    n, gr = (dbl(s) - m.unsqueeze(1)) * q.unsqueeze(1), dbl(dy) * dbl(w)
+    gn = (gr * n).abs().mean(1, keepdim=True)
+    near(dres, want[0], tols[0] + 8 * F24 * (want[0].abs() + 2 * q.unsqueeze(1) * n.abs() * gn), "dresidual")
+    near(dw, want[1], tols[1] + 8 * F24 * (dbl(dy) * n).abs().sum(0), "dweight")
+    near(db, want[2], tols[2], "dbias")
