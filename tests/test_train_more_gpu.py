@@ -89,3 +89,53 @@ def test_layer_norm_backward_of_far_means(moe, T, H):  # noqa: F811
     near(dres, want[0], tols[0] + 8 * F24 * (want[0].abs() + 2 * q.unsqueeze(1) * n.abs() * gn), "dresidual")
     near(dw, want[1], tols[1] + 8 * F24 * (dbl(dy) * n).abs().sum(0), "dweight")
     near(db, want[2], tols[2], "dbias")
+
+
+def test_layer_norm_sums_of_more_rows_than_a_launch_exactly(moe):  # noqa: F811
+    """Sums over more rows than a launch of the forward takes, to the last row: every
+    term and every partial sum is a whole number below 2^24, so fp32 holds them."""
+    T, H = (1 << 21) + 3, 8
+    x = torch.ones(T, H, dtype=BF, device="cuda")
+    x[:, ::2] = -1.0
+    x[-4:] *= 2.0
+    one = torch.ones(H, device="cuda")
+    y, _, mean, rstd = moe.moe_layer_norm_forward(x, one, eps=0.0, save_stats=True)
+    assert torch.equal(y, x.sign()) and not bool(mean.any())
+    assert bool((rstd[:-4] == 1).all()) and bool((rstd[-4:] == 0.5).all())
+    _, _, dw, db = moe.moe_layer_norm_backward(x, x, mean, rstd, one, need_dx=False)
+    # (dy n is 1 a row, 2 in the last four)
+    assert bool((dw == T + 4).all()) and torch.equal(db, x[0].float() * (T + 4))
+
+
+@pytest.mark.parametrize("T,H", [(300_000, 8200), (5001, 9000), (4100, 3000), (1024, 16384), (1030, 300), (100, 520)])
+def test_layer_norm_sums_exactly(moe, T, H):  # noqa: F811
+    """Each row once and no row twice, in the kernels of few, many and wide rows: whole
+    numbers, as above."""
+    x = torch.ones(T, H, dtype=BF, device="cuda")
+    one, mean, rstd = torch.ones(H, device="cuda"), torch.zeros(T, device="cuda"), torch.ones(T, device="cuda")
+    rstd[::7] = 2.0
+    _, _, dw, db = moe.moe_layer_norm_backward(x, x, mean, rstd, one, need_dx=False)
+    assert bool((db == T).all()) and bool((dw == T + -(-T // 7)).all())
+
+
+# (tiles of 128 and 256 columns, whose lanes trade halves of a row before they store)
+@pytest.mark.parametrize("T,K,N", [(1400, 136, 2600), (900, 72, 4104), (4100, 136, 2600), (2048, 520, 5128), (2000, 4104, 1032), (1500, 4104, 1032)])
+@pytest.mark.parametrize("a,dt", [(ref.GELU, BF), (ref.NONE, F32), (ref.SILU, BF), (ref.RELU, F32)])
+def test_linear_large_tiles_strides_in_place_and_rows_behind(moe, T, K, N, a, dt):  # noqa: F811
+    """A strided out in the addend's own rows, and a pre whose rows behind stay."""
+    g = gen(T + N + a)
+    x, w, b, add = base.linear_case(g, T + 3, K + 16, N + 24, F32, dt)
+    w, b = w[:N, :K].contiguous(), b[:N].contiguous()
+    buf = cuda(add)
+    keep, at = buf.clone(), buf[1:1 + T, 16:16 + N]
+    d = at.cpu().clone()
+    pre = torch.full((T + 1, N), 7, dtype=BF, device="cuda")
+    args = cuda(x)[2:2 + T, 8:8 + K], cuda(w), cuda(b)
+    out, _ = moe.moe_linear_forward(*args, act=a, addend=at, out=at, pre=pre[:T])
+    assert out.data_ptr() == at.data_ptr()
+    base.check_linear(moe, a, x[2:2 + T, 8:8 + K], w, b, d, out, pre[:T])
+    keep[1:1 + T, 16:16 + N] = buf[1:1 + T, 16:16 + N]
+    assert torch.equal(keep, buf) and bool((pre[T:] == 7).all())
+    # the same bits apart, and without a saved argument
+    apart = moe.moe_linear_forward(*args, act=a, addend=cuda(d), out_dtype=dt)
+    assert torch.equal(apart, out)
