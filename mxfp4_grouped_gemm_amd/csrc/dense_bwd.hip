@@ -144,8 +144,11 @@ hipError_t launch_dense_grads(const DenseArgs& dw13, const DenseArgs& dw2, const
     if (edge == 256) return launch_grad<256, 2, 4, 4, 64>(g, s);
     if (edge == 128) return launch_grad<128, 2, 2, 4, 128>(g, s);
     // Four buffers where there are more tiles than compute units: two workgroups fit
-    // (777 tokens, K = 1000, N = 520, 352 tiles, backward of the plain product: 21.0
-    // us with eight, 16.9 with four).
+    // (with eight and with four, us: backward of the plain product, 777 tokens, K = 1000,
+    // N = 520, 352 tiles 21.0 and 16.9; of the gated block, 1000 tokens, H = 768, I = 512,
+    // 480 tiles 23.9 and 20.2, 1500 tokens, H = I = 512 23.4 and 20.8, 300 tokens, H =
+    // 1000, I = 400 22.3 and 22.4, 100 tokens, H = 1024, I = 512, whose sums are short,
+    // 28.1 and 28.6).
     if (square_tiles(dw13, 64) + square_tiles(dw2, 64) + square_tiles(g.dx, 64) > 256) return launch_grad<64, 2, 2, 4, 128>(g, s);
     return launch_grad<64, 2, 2, 8, 128>(g, s);
 }

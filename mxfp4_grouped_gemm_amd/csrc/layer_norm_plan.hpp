@@ -41,8 +41,9 @@ inline int layer_norm_row_groups(int T, int H, bool sums) {
 }
 
 // Parts of the sums over the rows that a second launch joins (0: none, few rows). Of
-// rows that are read again for them: runs of rows, 64 of which keep the device busy
-// (128 and 256 take longer to join).
+// rows that are read again for them: 64 runs of rows (us with 32, 64, 128 and 256: 4000
+// rows of 12288 138, 120, 119 and 125; 16000 of 10001 625, 555, 524 and 515; 1100 of
+// 16384 59.1, 57.7, 62.4 and 72.4; 300 of 65536 86, 95, 116 and 155).
 inline int layer_norm_parts(int T, int H) {
     if (T <= 0 || layer_norm_few_rows(T, H)) return 0;
     if (H <= kHeldColumns) return layer_norm_row_groups(T, H, true);

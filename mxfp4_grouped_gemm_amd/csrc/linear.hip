@@ -164,8 +164,8 @@ int64_t tiles_by(int edge, const DenseArgs& a) { return (int64_t)((a.M + edge - 
 // 38; K = 8192, N = 1024: 16 tokens 19.0 and 26.2, 256 (not here) 30.9 and 25.1. Large
 // weights: K = 2048, N = 2816: 150 tokens 26.3 and 31.9, 256 29.0 and 32.8, 400 31.7 and
 // 31.8; K = 1408, N = 4096: 256 28.8 and 26.5; K = 2560, N = 2560: 150 24.8 and 31.6;
-// K = 2048, N = 2560: 256 29.1 and 31.9; smaller ones (not here): K = N = 2048: 200 26.3 and 23.6, 256 28.3 and 24.2; K = 1024, N
-// = 4096: 256 28.2 and 24.1, 400 29.7 and 26.9.
+// K = 2048, N = 2560: 256 29.1 and 31.9; smaller ones (not here): K = N = 2048: 200 26.3
+// and 23.6, 256 28.3 and 24.2; K = 1024, N = 4096: 256 28.2 and 24.1, 400 29.7 and 26.9.
 static bool few_tokens(const DenseArgs& dw, const DenseArgs& dx) {
     const int T = dx.M;
     if (T == 0 || T > 512 || tiles_by(128, dw) < 128) return false;
@@ -189,6 +189,11 @@ static bool long_sums(const DenseArgs& dw, const DenseArgs& dx) {
 }
 
 LinearGrads linear_grads_plan(DenseArgs& dw, DenseArgs& dx) {
+    // 16 parts at most: above, the join's bytes grow with the parts. In us with 8, 16 and
+    // 32: dx of 1 token, K = 1024, N = 8192 25.9, 21.1 and 22.4, 128 tokens 32.5, 28.8 and
+    // 32.8, 16 tokens, N = 16384 42.9, 31.6 and 31.1, K = 512, N = 32768 73, 47 and 38; dw of
+    // 30000 tokens, K = N = 128 41.5, 38.6 and 43.5, 8000 tokens, K = N = 128 20.2, 20.7 and
+    // 24.9, 256 23.4, 27.4 and 31.8 (24.7 with four).
     auto parts = [](int64_t room, int64_t most) { return (int)(room < most ? (room < 16 ? room : 16) : (most < 16 ? most : 16)); };
     dw.splits = dx.splits = 1;
     if (few_tokens(dw, dx)) {
