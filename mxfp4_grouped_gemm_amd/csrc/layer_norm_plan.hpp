@@ -31,11 +31,12 @@ inline int layer_norm_row_groups(int T, int H, bool sums) {
     // 110 and 111; 7000 of 8192: 256 workgroups 90.5, 512 96; 1500 of 8192: 26.6 and
     // 34.3). Few rows of more than 8192 columns: beside the sums, which want the room
     // as well, 64 and 128 workgroups: 400 rows of 12288 16.0 and 19.4, 512 18.7 and 21.1,
-    // 600 22.5 and 23.6, 1000 of 8200 32.5 and 27.0; of an odd width, whose rows take
-    // longer, 300 of 10001 19.6 and 18.8, 512 29.3 and 23.8 (256 workgroups: 400 of 12288
-    // 20.0, 1000 of 8200 30.8); dx alone, 64, 128 and 256: 14.7, 10.6 and 8.8; 19.9, 13.1
-    // and 10.6 (600 of 12288); 28.9, 16.8 and 12.4 (1000 of 8200; 512: 12.8).
-    const int wide = !sums ? 256 : T <= (H % 8 ? 320 : 512) ? 64 : 128;
+    // 600 22.5 and 23.6, 1000 of 8200 32.5 and 27.0; of an odd width, whose loads are at
+    // 2-byte addresses, 300 of 10001 19.6 and 18.8, 512 29.3 and 23.8, but 487 of 10158
+    // 19.5 and 21.0 (256 workgroups: 400 of 12288 20.0, 1000 of 8200 30.8); dx alone, 64,
+    // 128 and 256: 400 of 12288 14.7, 10.6 and 8.8, 600 19.9, 13.1 and 10.6, 1000 of 8200
+    // 28.9, 16.8 and 12.4 (512: 12.8).
+    const int wide = !sums ? 256 : T <= (H % 2 ? 320 : 512) ? 64 : 128;
     const int most = H <= 512 ? 1024 : H <= 1024 ? 1280 : H <= 2048 ? 1024 : H <= 4096 ? 512 : H <= kHeldColumns ? 256 : wide;
     return (int)(groups < most ? groups : most);
 }

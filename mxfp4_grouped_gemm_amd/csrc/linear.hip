@@ -165,7 +165,8 @@ int64_t tiles_by(int edge, const DenseArgs& a) { return (int64_t)((a.M + edge - 
 // weights: K = 2048, N = 2816: 150 tokens 26.3 and 31.9, 256 29.0 and 32.8, 400 31.7 and
 // 31.8; K = 1408, N = 4096: 256 28.8 and 26.5; K = 2560, N = 2560: 150 24.8 and 31.6;
 // K = 2048, N = 2560: 256 29.1 and 31.9; smaller ones (not here): K = N = 2048: 200 26.3
-// and 23.6, 256 28.3 and 24.2; K = 1024, N = 4096: 256 28.2 and 24.1, 400 29.7 and 26.9.
+// and 23.6, 256 28.3 and 24.2; K = 1024, N = 4096: 256 28.2 and 24.1, 400 29.7 and 26.9; K
+// = 512, N = 9000: 150 31.2 and 28.3, but 300 33.5 and 35.9.
 static bool few_tokens(const DenseArgs& dw, const DenseArgs& dx) {
     const int T = dx.M;
     if (T == 0 || T > 512 || tiles_by(128, dw) < 128) return false;
